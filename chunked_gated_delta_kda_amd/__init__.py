@@ -1,15 +1,30 @@
-"""MI355X-native Kimi Delta Attention (KDA) forward.
+"""MI355X-native Kimi Delta Attention (KDA) forward, and the operators a hybrid decoder runs
+beside it: the short causal convolution (``conv_fwd``, ``conv_bwd``, ``conv_decode``).
 
 ``fwd`` marshals torch tensors into the C ABI of libkda.so (include/kda.h).
 PyTorch only allocates device memory and provides the stream; every step of
 the computation runs in the library's HIP kernels.
 """
 import ctypes
+import importlib
 import math
 
 from . import native
 
-__all__ = ["fwd", "fwd_noalloc", "bwd", "decode", "workspace_bytes", "select_variant", "device_errors", "version", "native"]
+__all__ = ["fwd", "fwd_noalloc", "bwd", "decode", "workspace_bytes", "select_variant", "device_errors", "version", "native",
+           "conv_fwd", "conv_bwd", "conv_decode"]
+
+#: the operators beside the delta rule, by the module that is imported on first use (it needs torch)
+_OPERATORS = {"conv_fwd": "short_conv", "conv_bwd": "short_conv", "conv_decode": "short_conv"}
+
+
+def __getattr__(name):
+    if name not in _OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = getattr(importlib.import_module("." + _OPERATORS[name], __name__), name)
+    globals()[name] = value
+    return value
+
 
 HEAD_DIM = 128
 

@@ -1,0 +1,22 @@
+// ops_launch.hpp -- host-side launchers of the operators beside the delta rule (internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda.h"
+
+namespace kda {
+namespace ops {
+
+inline size_t dtype_bytes(int dt) { return dt == KDA_DTYPE_F32 ? 4 : 2; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// short convolution (ops_conv.hip)
+hipError_t launch_conv_fwd(const kda_conv_args &a, int32_t *err, hipStream_t st);
+hipError_t launch_conv_decode(const kda_conv_args &a, hipStream_t st);
+size_t conv_bwd_workspace(int64_t T, int64_t C, int W);
+hipError_t launch_conv_bwd(const kda_conv_args &a, const kda_conv_grads &g, float *ws, int32_t *err, hipStream_t st);
+
+}  // namespace ops
+}  // namespace kda

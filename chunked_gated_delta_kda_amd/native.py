@@ -19,6 +19,7 @@ VARIANTS = {"auto": 0, "split": 1, "fused": 2, "recurrent": 3}
 #: every symbol include/kda.h declares
 EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_noalloc", "kda_workspace_bytes", "kda_select_variant",
            "kda_launch_plan", "kda_decode", "kda_decode_ex", "kda_bwd", "kda_bwd_workspace_bytes",
+           "kda_conv_fwd", "kda_conv_decode", "kda_conv_bwd", "kda_conv_bwd_workspace_bytes",
            "kda_device_errors", "kda_status_string", "kda_version")
 #: KDA_DEVERR_* bits of the device error word
 DEVERR = {1: "fused hand-off wait gave up (outputs invalid)", 2: "malformed cu_seqlens (sanitised)"}
@@ -40,6 +41,24 @@ class KdaLaunchInfo(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("prep_begin", ctypes.c_int32), ("prep_end", ctypes.c_int32),
                 ("recur_begin", ctypes.c_int32), ("recur_end", ctypes.c_int32),
                 ("chunk_len", ctypes.c_int32)]
+
+
+ACT_DTYPES = {"f32": 0, "bf16": 1, "f16": 2}   # KDA_DTYPE_* of the activations of kda_conv_*, kda_ssm_*, kda_attn_*
+CONV_MAX_WIDTH = 8   # KDA_CONV_MAX_WIDTH
+
+
+class KdaConvArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("initial_state", ctypes.c_void_p),
+                ("final_state", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class KdaConvGrads(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("d_final_state", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("d_initial_state", ctypes.c_void_p),
+                ("dy_stride", ctypes.c_int64)]
 
 
 class KdaError(RuntimeError):
@@ -88,6 +107,14 @@ def load_library(path=LIB_PATH):
     lib.kda_bwd.restype = ctypes.c_int
     lib.kda_bwd_workspace_bytes.argtypes = [i32, i32, i32]
     lib.kda_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.kda_conv_fwd.argtypes = [ctypes.POINTER(KdaConvArgs), vp]
+    lib.kda_conv_fwd.restype = ctypes.c_int
+    lib.kda_conv_decode.argtypes = [ctypes.POINTER(KdaConvArgs), vp]
+    lib.kda_conv_decode.restype = ctypes.c_int
+    lib.kda_conv_bwd.argtypes = [ctypes.POINTER(KdaConvArgs), ctypes.POINTER(KdaConvGrads), vp, vp, ctypes.c_size_t]
+    lib.kda_conv_bwd.restype = ctypes.c_int
+    lib.kda_conv_bwd_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.kda_conv_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]
     lib.kda_device_errors.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]

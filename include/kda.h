@@ -77,6 +77,7 @@ typedef enum kda_variant {
 /* Element types of kda_options.g_dtype / state_dtype (and of kda_decode_ex). */
 #define KDA_DTYPE_F32 0
 #define KDA_DTYPE_BF16 1
+#define KDA_DTYPE_F16 2   /* activations of the operators below only (kda_conv_*, kda_ssm_*, kda_attn_*) */
 
 typedef struct kda_options {
     int32_t variant;        /* kda_variant                                              */
@@ -286,6 +287,77 @@ int kda_bwd(const void *q, const void *k, const void *v, const float *g, const f
             int32_t head_dim, const float *initial_state, const float *d_out, const float *d_final_state,
             float *dq, float *dk, float *dv, float *dg, float *dbeta, float *d_initial_state, void *stream,
             void *workspace, size_t workspace_bytes);
+
+/* ------------------------------------------------------------------------------------
+ * Operators beside the delta rule: what a hybrid decoder runs next to it. All of them take
+ * a structure of arguments that the call reads and does not keep. Activations are fp32,
+ * bf16 or fp16 (one dtype per call), parameters, states and their gradients fp32 unless
+ * said otherwise; arithmetic is fp32. A row stride is counted in elements, is at least
+ * the row's own length and need not be a multiple of anything; within a row elements are
+ * contiguous. Base pointers are aligned to their element. Outputs must not overlap inputs
+ * or each other, but where said; KDA_ERR_ALIAS reports an output over an input that the
+ * host can see. Malformed cu_seqlens raise KDA_DEVERR_CU_SEQLENS; every access stays in
+ * bounds, but unlike kda_fwd the call's outputs are then unspecified.
+ */
+
+/* Widest convolution: taps per channel. */
+#define KDA_CONV_MAX_WIDTH 8
+
+typedef struct kda_conv_args {
+    const void *x;            /* [total_tokens, channels], rows x_stride apart            */
+    const float *weight;      /* fp32 [channels, width]; tap width-1 meets the row itself  */
+    const float *bias;        /* fp32 [channels] or NULL                                   */
+    const int32_t *cu_seqlens; /* int32 [num_seqs+1] or NULL (one sequence), as kda_fwd    */
+    const void *initial_state; /* [num_seqs, width-1, channels] of x's dtype: the rows     */
+                              /* before each sequence, oldest first; NULL: zeros           */
+    void *final_state;        /* the same for the rows that follow, or NULL (not written)  */
+    void *out;                /* [total_tokens, channels] of x's dtype, contiguous         */
+    int64_t x_stride;
+    int32_t num_seqs, total_tokens, channels;
+    int32_t width;            /* 2 .. KDA_CONV_MAX_WIDTH                                   */
+    int32_t dtype;            /* KDA_DTYPE_*                                               */
+    int32_t activation;       /* 0: none, 1: SiLU                                          */
+} kda_conv_args;
+
+typedef struct kda_conv_grads {
+    const void *dy;           /* [total_tokens, channels] of x's dtype, rows dy_stride apart */
+    const float *d_final_state; /* fp32 [num_seqs, width-1, channels] or NULL (zeros)      */
+    void *dx;                 /* [total_tokens, channels] of x's dtype, contiguous         */
+    float *dweight;           /* fp32 [channels, width]                                    */
+    float *dbias;             /* fp32 [channels] or NULL (not written)                     */
+    float *d_initial_state;   /* fp32 [num_seqs, width-1, channels] or NULL (not written)  */
+    int64_t dy_stride;
+} kda_conv_grads;
+
+/*
+ * kda_conv_fwd -- the short causal convolution of each channel over a packed batch:
+ *
+ *   p_t = bias + sum_j weight[j] x_{t-width+1+j},   out_t = p_t sigmoid(p_t)   (or p_t)
+ *
+ * Rows before a sequence's first come from initial_state; final_state holds the last
+ * width-1 rows of the sequence (of initial_state and x together where it is shorter), so
+ * that a sequence may be continued. Limits: total_tokens <= 2^27, channels <= 2^20,
+ * num_seqs * channels <= 2^31. final_state must not overlap initial_state.
+ */
+int kda_conv_fwd(const kda_conv_args *args, void *stream);
+
+/*
+ * kda_conv_decode -- one row per sequence: x and out are [num_seqs, channels]
+ * (total_tokens = num_seqs, cu_seqlens NULL), initial_state the rows before it (or NULL:
+ * zeros) and final_state the same moved up by one row. final_state may be the same pointer
+ * as initial_state (updated in place). Limits as kda_conv_fwd.
+ */
+int kda_conv_decode(const kda_conv_args *args, void *stream);
+
+/*
+ * kda_conv_bwd -- gradients of kda_conv_fwd (args->out and args->final_state are ignored).
+ * The sums over tokens run in a fixed order: the same results from run to run. workspace:
+ * kda_conv_bwd_workspace_bytes() bytes of device memory, or NULL: then the library
+ * allocates it stream-ordered on `stream`.
+ */
+size_t kda_conv_bwd_workspace_bytes(int32_t total_tokens, int32_t channels, int32_t width);
+int kda_conv_bwd(const kda_conv_args *args, const kda_conv_grads *grads, void *stream, void *workspace,
+                 size_t workspace_bytes);
 
 /*
  * kda_device_errors -- the device error word of the current device: the OR of the

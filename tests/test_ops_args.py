@@ -1,0 +1,150 @@
+"""Refusals of the operators beside the delta rule, on the CPU: the binding's checks of caller
+tensors, and the C ABI's checks before anything is enqueued."""
+import ctypes
+import os
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from chunked_gated_delta_kda_amd import native  # noqa: E402
+from chunked_gated_delta_kda_amd.short_conv import (check_conv_bwd_args, check_conv_decode_args,  # noqa: E402
+                                                    check_conv_fwd_args)
+
+P = 4096   # never dereferenced: every call below fails validation first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(native.LIB_PATH):
+        pytest.skip("libkda.so not built")
+    return native.load_library()
+
+
+# ---------------------------------------------------------------- short convolution
+T, C, W, N = 20, 12, 4, 3
+
+
+def _conv():
+    return dict(x=torch.zeros(T, C, dtype=torch.bfloat16), weight=torch.zeros(C, W), bias=torch.zeros(C),
+                cu_seqlens=torch.tensor([0, 5, 5, T], dtype=torch.int32),
+                initial_state=torch.zeros(N, W - 1, C, dtype=torch.bfloat16))
+
+
+def test_conv_good_arguments():
+    a = _conv()
+    assert check_conv_fwd_args(**a) == (T, C, W, N, C)
+    a["x"] = torch.zeros(T, 3 * C, dtype=torch.bfloat16)[:, C:2 * C]     # a slice of a projection
+    assert check_conv_fwd_args(**a, out=torch.empty(T, C, dtype=torch.bfloat16)) == (T, C, W, N, 3 * C)
+    assert check_conv_bwd_args(**a, dy=torch.zeros(T, C, dtype=torch.bfloat16))[4:] == (3 * C, C)
+    assert check_conv_fwd_args(torch.zeros(0, C), torch.zeros(C, 2)) == (0, C, 2, 1, C)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("x", lambda: torch.zeros(T, C, dtype=torch.float64)),
+    ("x", lambda: torch.zeros(T, 2, C // 2, dtype=torch.bfloat16)),
+    ("x", lambda: torch.zeros(C, T, dtype=torch.bfloat16).t()),                  # columns contiguous
+    ("x", lambda: torch.zeros(1, C, dtype=torch.bfloat16).expand(T, C)),         # rows overlap
+    ("weight", lambda: torch.zeros(C, W, dtype=torch.bfloat16)),
+    ("weight", lambda: torch.zeros(C, 9)),
+    ("weight", lambda: torch.zeros(C, 1)),
+    ("weight", lambda: torch.zeros(C + 1, W)),
+    ("weight", lambda: torch.zeros(W, C).t()),
+    ("bias", lambda: torch.zeros(C + 1)),
+    ("cu_seqlens", lambda: torch.tensor([0, T])[:1]),
+    ("cu_seqlens", lambda: torch.tensor([0, 5, 5, T])),
+    ("initial_state", lambda: torch.zeros(N, W - 1, C)),
+    ("initial_state", lambda: torch.zeros(N, W, C, dtype=torch.bfloat16)),
+    ("activation", lambda: "gelu"),
+])
+def test_conv_rejects(name, bad):
+    a = _conv()
+    a[name] = bad()
+    with pytest.raises(ValueError, match=name):
+        check_conv_fwd_args(**a)
+
+
+def test_conv_rejects_outputs_and_gradients():
+    a = _conv()
+    with pytest.raises(ValueError, match="out"):
+        check_conv_fwd_args(**a, out=torch.empty(T, C))
+    with pytest.raises(ValueError, match="final_state"):
+        check_conv_fwd_args(**a, final_state=torch.empty(N + 1, W - 1, C, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="dy"):
+        check_conv_bwd_args(**a, dy=torch.zeros(T, C))
+    with pytest.raises(ValueError, match="d_final_state"):
+        check_conv_bwd_args(**a, dy=torch.zeros(T, C, dtype=torch.bfloat16), d_final_state=a["initial_state"])
+    x, w = a["x"], a["weight"]
+    with pytest.raises(ValueError, match="state"):
+        check_conv_decode_args(x, w, None, torch.zeros(T, W - 1, C))
+    with pytest.raises(ValueError, match="state_out"):
+        check_conv_decode_args(x, w, None, None, state_out="elsewhere")
+    with pytest.raises(ValueError, match="x"):
+        check_conv_decode_args(x[:0], w)
+
+
+def test_conv_needs_device_tensors():
+    import chunked_gated_delta_kda_amd as kda
+    a = _conv()
+    with pytest.raises(ValueError, match="device"):
+        kda.conv_fwd(**a)
+    with pytest.raises(ValueError, match="device"):
+        kda.conv_decode(a["x"], a["weight"])
+    with pytest.raises(ValueError, match="device"):
+        kda.conv_bwd(a["x"], a["weight"], a["x"])
+
+
+def conv_args(**over):
+    big = 1 << 30
+    a = dict(x=P, weight=big, bias=None, cu_seqlens=None, initial_state=None, final_state=None, out=2 * big, x_stride=C,
+             num_seqs=1, total_tokens=T, channels=C, width=W, dtype=1, activation=1)
+    a.update(over)
+    return native.KdaConvArgs(**a)
+
+
+def test_conv_abi_refusals(lib):
+    fwd = lambda **kw: lib.kda_conv_fwd(ctypes.byref(conv_args(**kw)), None)  # noqa: E731
+    assert lib.kda_conv_fwd(None, None) == 1
+    for kw in (dict(dtype=3), dict(dtype=-1), dict(width=1), dict(width=9), dict(activation=2)):
+        assert fwd(**kw) == 3, kw
+    for kw in (dict(num_seqs=0), dict(total_tokens=-1), dict(channels=0), dict(x_stride=C - 1), dict(num_seqs=2),
+               dict(total_tokens=(1 << 27) + 1), dict(channels=(1 << 20) + 1, x_stride=1 << 21)):
+        assert fwd(**kw) == 2, kw
+    for kw in (dict(x=None), dict(weight=None), dict(out=None)):
+        assert fwd(**kw) == 1, kw
+    es = 2
+    for kw in (dict(out=P + T * C * es - 2),                                     # out over x's last element
+               dict(initial_state=1 << 20, final_state=1 << 20),                 # in place: a race over tiles
+               dict(final_state=P), dict(out=1 << 20, final_state=1 << 20), dict(out=1 << 20, initial_state=1 << 20)):
+        assert fwd(**kw) == 7, kw
+
+
+def test_conv_decode_abi_refusals(lib):
+    dec = lambda **kw: lib.kda_conv_decode(ctypes.byref(conv_args(num_seqs=T, **kw)), None)  # noqa: E731
+    assert dec(cu_seqlens=P) == 2
+    assert dec(total_tokens=T + 1) == 2
+    assert dec(out=None) == 1
+    state = T * (W - 1) * C * 2
+    assert dec(initial_state=1 << 20, final_state=(1 << 20) + state - 2) == 7
+    assert dec(out=P) == 7
+
+
+def test_conv_bwd_abi_refusals(lib):
+    big = 1 << 30
+
+    def bwd(grads=(), ws=P, nbytes=0, **kw):
+        g = dict(dy=3 * big, d_final_state=None, dx=4 * big, dweight=5 * big, dbias=None, d_initial_state=None, dy_stride=C)
+        g.update(grads)
+        return lib.kda_conv_bwd(ctypes.byref(conv_args(**kw)), ctypes.byref(native.KdaConvGrads(**g)), None, ws, nbytes)
+
+    assert lib.kda_conv_bwd(None, None, None, None, 0) == 1
+    for g in (dict(dy=None), dict(dx=None), dict(dweight=None)):
+        assert bwd(g) == 1, g
+    assert bwd(dict(dy_stride=C - 1)) == 2
+    assert bwd(width=9) == 3
+    assert bwd(num_seqs=2) == 2
+    for g in (dict(dx=P), dict(dx=3 * big), dict(dweight=1 * big), dict(d_initial_state=3 * big)):
+        assert bwd(g) == 7, g
+    need = lib.kda_conv_bwd_workspace_bytes(T, C, W)
+    assert need >= (W + 1) * C * 4 and bwd(nbytes=need - 1) == 4
+    assert lib.kda_conv_bwd_workspace_bytes(-1, C, W) == 0 and lib.kda_conv_bwd_workspace_bytes(T, C, 9) == 0
