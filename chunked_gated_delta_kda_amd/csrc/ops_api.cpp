@@ -79,6 +79,48 @@ int check_conv(const kda_conv_args &a, bool grads) {
     return KDA_OK;
 }
 
+// ---------------------------------------------------------------- selective scan
+bool ssm_sizes_ok(int64_t T, int64_t D, int64_t N, int64_t G) {
+    return T >= 0 && T <= 1 << 27 && D >= 1 && D <= 1 << 20 && N >= 1 && N <= KDA_SSM_MAX_STATE && G >= 1 && G <= D && D % G == 0;
+}
+
+int check_ssm(const kda_ssm_args &a, bool grads) {
+    if (!dtype_ok(a.dtype) || (a.delta_softplus != 0 && a.delta_softplus != 1)) return KDA_ERR_UNSUPPORTED;
+    if (!ssm_sizes_ok(a.total_tokens, a.channels, a.state_size, a.groups) || a.num_seqs < 1 ||
+        (int64_t)a.num_seqs * a.channels > (int64_t)1 << 31)
+        return KDA_ERR_SHAPE;
+    const int64_t bc = (int64_t)a.groups * a.state_size;
+    if (a.u_stride < a.channels || a.delta_stride < a.channels || a.B_stride < bc || a.C_stride < bc ||
+        (a.z && a.z_stride < a.channels))
+        return KDA_ERR_SHAPE;
+    if (!a.A || (a.total_tokens > 0 && (!a.u || !a.delta || !a.B || !a.C || (!grads && !a.out)))) return KDA_ERR_NULL;
+    return KDA_OK;
+}
+
+// the inputs of a scan over `rows` rows
+struct SsmSpans {
+    Span in[9];
+    int64_t state;
+    explicit SsmSpans(const kda_ssm_args &a) {
+        const int64_t es = (int64_t)dtype_bytes(a.dtype), T = a.total_tokens, D = a.channels, N = a.state_size;
+        state = (int64_t)a.num_seqs * D * N * 4;
+        in[0] = span(a.u, rows_bytes(T, a.u_stride, D, es));
+        in[1] = span(a.delta, rows_bytes(T, a.delta_stride, D, es));
+        in[2] = span(a.B, rows_bytes(T, a.B_stride, a.groups * N, es));
+        in[3] = span(a.C, rows_bytes(T, a.C_stride, a.groups * N, es));
+        in[4] = span(a.z, rows_bytes(T, a.z_stride, D, es));
+        in[5] = span(a.A, D * N * 4);
+        in[6] = span(a.D, D * 4);
+        in[7] = span(a.delta_bias, D * 4);
+        in[8] = span(a.initial_state, state);
+    }
+    bool over(Span out, int count = 9) const {
+        for (int i = 0; i < count; ++i)
+            if (meet(in[i], out)) return true;
+        return false;
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -141,6 +183,39 @@ int kda_conv_bwd(const kda_conv_args *args, const kda_conv_grads *grads, void *s
     Workspace ws(workspace, workspace_bytes, kda::ops::conv_bwd_workspace(T, C, a.width), st);
     if (ws.status() != KDA_OK) return ws.status();
     return ws.finish(launched(kda::ops::launch_conv_bwd(a, g, (float *)ws.ptr(), kda::device_error_word(), st)));
+}
+
+size_t kda_ssm_workspace_bytes(int32_t total_tokens, int32_t channels, int32_t state_size, int32_t groups) {
+    if (!ssm_sizes_ok(total_tokens, channels, state_size, groups)) return 0;
+    return kda::ops::ssm_workspace(total_tokens, channels, state_size, groups);
+}
+
+int kda_ssm_fwd(const kda_ssm_args *args, void *stream, void *workspace, size_t workspace_bytes) {
+    if (!args) return KDA_ERR_NULL;
+    const kda_ssm_args &a = *args;
+    if (const int rc = check_ssm(a, false)) return rc;
+    if (!a.cu_seqlens && a.num_seqs != 1) return KDA_ERR_SHAPE;
+    const SsmSpans s(a);
+    const Span out = span(a.out, (int64_t)a.total_tokens * a.channels * (int64_t)dtype_bytes(a.dtype));
+    const Span fin = span(a.final_state, s.state);
+    if (s.over(out) || s.over(fin) || meet(out, fin)) return KDA_ERR_ALIAS;
+    hipStream_t st = (hipStream_t)stream;
+    Workspace ws(workspace, workspace_bytes, kda::ops::ssm_workspace(a.total_tokens, a.channels, a.state_size, a.groups), st);
+    if (ws.status() != KDA_OK) return ws.status();
+    return ws.finish(launched(kda::ops::launch_ssm_fwd(a, (float *)ws.ptr(), kda::device_error_word(), st)));
+}
+
+int kda_ssm_decode(const kda_ssm_args *args, void *stream) {
+    if (!args) return KDA_ERR_NULL;
+    const kda_ssm_args &a = *args;
+    if (const int rc = check_ssm(a, false)) return rc;
+    if (a.cu_seqlens || a.total_tokens != a.num_seqs) return KDA_ERR_SHAPE;
+    const SsmSpans s(a);
+    const Span out = span(a.out, (int64_t)a.total_tokens * a.channels * (int64_t)dtype_bytes(a.dtype));
+    const Span fin = span(a.final_state, s.state);
+    const bool in_place = a.initial_state == a.final_state;
+    if (s.over(out) || s.over(fin, in_place ? 8 : 9) || meet(out, fin)) return KDA_ERR_ALIAS;
+    return launched(kda::ops::launch_ssm_decode(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -20,6 +20,7 @@ VARIANTS = {"auto": 0, "split": 1, "fused": 2, "recurrent": 3}
 EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_noalloc", "kda_workspace_bytes", "kda_select_variant",
            "kda_launch_plan", "kda_decode", "kda_decode_ex", "kda_bwd", "kda_bwd_workspace_bytes",
            "kda_conv_fwd", "kda_conv_decode", "kda_conv_bwd", "kda_conv_bwd_workspace_bytes",
+           "kda_ssm_fwd", "kda_ssm_workspace_bytes", "kda_ssm_decode",
            "kda_device_errors", "kda_status_string", "kda_version")
 #: KDA_DEVERR_* bits of the device error word
 DEVERR = {1: "fused hand-off wait gave up (outputs invalid)", 2: "malformed cu_seqlens (sanitised)"}
@@ -45,6 +46,7 @@ class KdaLaunchInfo(ctypes.Structure):
 
 ACT_DTYPES = {"f32": 0, "bf16": 1, "f16": 2}   # KDA_DTYPE_* of the activations of kda_conv_*, kda_ssm_*, kda_attn_*
 CONV_MAX_WIDTH = 8   # KDA_CONV_MAX_WIDTH
+SSM_MAX_STATE = 256   # KDA_SSM_MAX_STATE
 
 
 class KdaConvArgs(ctypes.Structure):
@@ -59,6 +61,14 @@ class KdaConvGrads(ctypes.Structure):
     _fields_ = [("dy", ctypes.c_void_p), ("d_final_state", ctypes.c_void_p), ("dx", ctypes.c_void_p),
                 ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("d_initial_state", ctypes.c_void_p),
                 ("dy_stride", ctypes.c_int64)]
+
+
+class KdaSsmArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("u", "delta", "A", "B", "C", "D", "z", "delta_bias", "cu_seqlens",
+                                                "initial_state", "final_state", "out")] +
+                [(n, ctypes.c_int64) for n in ("u_stride", "delta_stride", "B_stride", "C_stride", "z_stride")] +
+                [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "channels", "state_size", "groups", "dtype",
+                                               "delta_softplus")])
 
 
 class KdaError(RuntimeError):
@@ -115,6 +125,12 @@ def load_library(path=LIB_PATH):
     lib.kda_conv_bwd.restype = ctypes.c_int
     lib.kda_conv_bwd_workspace_bytes.argtypes = [i32, i32, i32]
     lib.kda_conv_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.kda_ssm_fwd.argtypes = [ctypes.POINTER(KdaSsmArgs), vp, vp, ctypes.c_size_t]
+    lib.kda_ssm_fwd.restype = ctypes.c_int
+    lib.kda_ssm_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.kda_ssm_workspace_bytes.restype = ctypes.c_size_t
+    lib.kda_ssm_decode.argtypes = [ctypes.POINTER(KdaSsmArgs), vp]
+    lib.kda_ssm_decode.restype = ctypes.c_int
     lib.kda_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]
     lib.kda_device_errors.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]

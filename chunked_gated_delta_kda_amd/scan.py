@@ -1,0 +1,139 @@
+"""The selective state space scan: kda_ssm_fwd and kda_ssm_decode of include/kda.h."""
+import ctypes
+
+import torch
+
+from . import native
+from ._args import DTYPES, checked, dense, launch_on, offsets, on_device, ptr, rows
+
+__all__ = ["ssm_fwd", "ssm_decode"]
+
+
+class _Sizes:
+    """What the checks found: T, D, N (states), G, S (sequences) and the row strides."""
+    __slots__ = ("T", "D", "N", "G", "S", "strides")
+
+
+def _check(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state):
+    if u.dtype not in DTYPES or u.dim() != 2:
+        raise ValueError(f"u: expected fp32, bf16 or fp16 [T, D], got {u.dtype} {tuple(u.shape)}")
+    dev, dt = u.device, u.dtype
+    s = _Sizes()
+    s.T, s.D = u.shape
+    if A.dim() != 2 or not 1 <= A.shape[1] <= native.SSM_MAX_STATE:
+        raise ValueError(f"A: expected fp32 [D, N] with N from 1 to {native.SSM_MAX_STATE}, got {tuple(A.shape)}")
+    s.N = A.shape[1]
+    if B.dim() != 3 or B.shape[1] < 1 or s.D % B.shape[1]:
+        raise ValueError(f"B: expected [T, G, N] with G dividing the {s.D} channels, got {tuple(B.shape)}")
+    s.G = B.shape[1]
+    strides = [rows("u", u, dt, (s.T, s.D), dev), rows("delta", delta, dt, (s.T, s.D), dev),
+               rows("B", B, dt, (s.T, s.G, s.N), dev), rows("C", C, dt, (s.T, s.G, s.N), dev), 0]
+    dense("A", A, torch.float32, (s.D, s.N), dev)
+    if D is not None:
+        dense("D", D, torch.float32, (s.D,), dev)
+    if z is not None:
+        strides[4] = rows("z", z, dt, (s.T, s.D), dev)
+    if delta_bias is not None:
+        dense("delta_bias", delta_bias, torch.float32, (s.D,), dev)
+    s.strides = strides
+    s.S = offsets(cu_seqlens, dev)
+    if initial_state is not None:
+        dense("initial_state", initial_state, torch.float32, (s.S, s.D, s.N), dev)
+    return s
+
+
+def check_ssm_fwd_args(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_seqlens=None, initial_state=None, out=None,
+                       final_state=None):
+    """Every check ssm_fwd makes before anything is launched; returns the sizes it found."""
+    s = _check(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state)
+    if out is not None:
+        dense("out", out, u.dtype, (s.T, s.D), u.device)
+    if final_state is not None:
+        dense("final_state", final_state, torch.float32, (s.S, s.D, s.N), u.device)
+    return s
+
+
+def _args(s, u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, final_state, out, softplus):
+    return native.KdaSsmArgs(ptr(u), ptr(delta), ptr(A), ptr(B), ptr(C), ptr(D), ptr(z), ptr(delta_bias), ptr(cu_seqlens),
+                             ptr(initial_state), ptr(final_state), ptr(out), *s.strides, s.S, s.T, s.D, s.N, s.G,
+                             DTYPES[u.dtype], int(bool(softplus)))
+
+
+def scratch(workspace, nbytes, dev):
+    """The caller's workspace, or one of ``nbytes`` (None if none is needed); its pointer and size."""
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace, ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def ssm_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_seqlens=None, initial_state=None,
+            output_final_state=True, *, delta_softplus=True, out=None, final_state=None, workspace=None, stream=None,
+            check=False):
+    """Selective state space scan over a packed batch, on the current HIP device. Per channel c of
+    group g, state n and token t:
+
+        s_t = softplus(delta_t + delta_bias);  h_t[n] = exp(s_t A[n]) h_{t-1}[n] + s_t u_t B_t[g, n]
+        out_t = (sum_n C_t[g, n] h_t[n] + D u_t) * silu(z_t)
+
+    u, delta, z: fp32, bf16 or fp16 [T, D], B, C: [T, G, N] of the same dtype (N up to 256, G
+    dividing D), rows contiguous, any row stride (slices of a projection are read in place); A:
+    fp32 [D, N]; D, delta_bias: fp32 [D] or None; z: None for no gate; cu_seqlens: int32 [S+1] on the
+    device or None (one sequence); initial_state: fp32 [S, D, N] or None (zeros); delta_softplus
+    False: the steps are delta + delta_bias as they are; out, final_state: caller buffers or None.
+    final_state must not overlap initial_state (ssm_decode updates in place). check: as in fwd.
+    Returns (out [T, D] of u's dtype, final_state fp32 [S, D, N] or None). Tensors that the call
+    allocates belong to its stream.
+    """
+    lib = native.load_library()
+    dev = u.device
+    on_device("kda.ssm_fwd", dev)
+    s = check_ssm_fwd_args(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, out, final_state)
+    with launch_on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((s.T, s.D), dtype=u.dtype, device=dev)
+        if not output_final_state:
+            final_state = None
+        elif final_state is None:
+            final_state = torch.empty((s.S, s.D, s.N), dtype=torch.float32, device=dev)
+        workspace, wp, wn = scratch(workspace, lib.kda_ssm_workspace_bytes(s.T, s.D, s.N, s.G), dev)
+        args = _args(s, u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, final_state, out, delta_softplus)
+        call = lambda: native.check(lib.kda_ssm_fwd(ctypes.byref(args), st, wp, wn))  # noqa: E731
+        checked(st, call) if check else call()
+    return out, final_state
+
+
+def check_ssm_decode_args(u, delta, A, B, C, D=None, z=None, delta_bias=None, state=None, out=None, state_out="inplace"):
+    """Every check ssm_decode makes before the launch; returns the sizes it found."""
+    s = _check(u, delta, A, B, C, D, z, delta_bias, None, None)
+    if s.T < 1:
+        raise ValueError("u: expected at least one row")
+    if isinstance(state_out, str) and state_out != "inplace":
+        raise ValueError('state_out: "inplace", None or a tensor')
+    s.S = s.T
+    for name, t in (("state", state), ("state_out", state_out)):
+        if isinstance(t, torch.Tensor):
+            dense(name, t, torch.float32, (s.S, s.D, s.N), u.device)
+    if out is not None:
+        dense("out", out, u.dtype, (s.T, s.D), u.device)
+    return s
+
+
+def ssm_decode(u, delta, A, B, C, D=None, z=None, delta_bias=None, state=None, *, delta_softplus=True, out=None,
+               state_out="inplace", stream=None):
+    """ssm_fwd for one token of each of S sequences: u, delta, z [S, D], B, C [S, G, N]; state fp32
+    [S, D, N] (None: zeros). state_out: "inplace" (update ``state``; a new tensor when state is None),
+    None (not written), or a tensor. Returns (out [S, D], the updated state or None)."""
+    lib = native.load_library()
+    dev = u.device
+    on_device("kda.ssm_decode", dev)
+    s = check_ssm_decode_args(u, delta, A, B, C, D, z, delta_bias, state, out, state_out)
+    with launch_on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((s.T, s.D), dtype=u.dtype, device=dev)
+        if isinstance(state_out, str):
+            state_out = state if state is not None else torch.empty((s.S, s.D, s.N), dtype=torch.float32, device=dev)
+        args = _args(s, u, delta, A, B, C, D, z, delta_bias, None, state, state_out, out, delta_softplus)
+        native.check(lib.kda_ssm_decode(ctypes.byref(args), st))
+    return out, state_out

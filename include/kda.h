@@ -359,6 +359,54 @@ size_t kda_conv_bwd_workspace_bytes(int32_t total_tokens, int32_t channels, int3
 int kda_conv_bwd(const kda_conv_args *args, const kda_conv_grads *grads, void *stream, void *workspace,
                  size_t workspace_bytes);
 
+/* Largest state size of the scan. */
+#define KDA_SSM_MAX_STATE 256
+
+typedef struct kda_ssm_args {
+    const void *u;            /* [total_tokens, channels], rows u_stride apart              */
+    const void *delta;        /* [total_tokens, channels], rows delta_stride apart          */
+    const float *A;           /* fp32 [channels, state_size]                                */
+    const void *B;            /* [total_tokens, groups, state_size], rows B_stride apart     */
+    const void *C;            /* [total_tokens, groups, state_size], rows C_stride apart     */
+    const float *D;           /* fp32 [channels] or NULL (no skip)                          */
+    const void *z;            /* [total_tokens, channels], rows z_stride apart, or NULL (no gate) */
+    const float *delta_bias;  /* fp32 [channels] or NULL                                    */
+    const int32_t *cu_seqlens; /* int32 [num_seqs+1] or NULL (one sequence), as kda_fwd      */
+    const float *initial_state; /* fp32 [num_seqs, channels, state_size] or NULL (zeros)     */
+    float *final_state;       /* fp32 [num_seqs, channels, state_size] or NULL (not written) */
+    void *out;                /* [total_tokens, channels], contiguous                       */
+    int64_t u_stride, delta_stride, B_stride, C_stride, z_stride;
+    int32_t num_seqs, total_tokens, channels;
+    int32_t state_size;       /* 1 .. KDA_SSM_MAX_STATE                                     */
+    int32_t groups;           /* divides channels; channel c reads group c / (channels / groups) */
+    int32_t dtype;            /* KDA_DTYPE_* of u, delta, B, C, z and out                    */
+    int32_t delta_softplus;   /* 1: steps are softplus(delta + delta_bias), 0: delta + delta_bias */
+} kda_ssm_args;
+
+/*
+ * kda_ssm_fwd -- the selective state space scan over a packed batch. Per sequence, channel
+ * c of group g, state n and token t in order:
+ *
+ *   s_t = softplus(delta_t[c] + delta_bias[c])
+ *   h_t[n] = exp(s_t A[c][n]) h_{t-1}[n] + s_t u_t[c] B_t[g][n]
+ *   out_t[c] = (sum_n C_t[g][n] h_t[n] + D[c] u_t[c]) * z_t[c] sigmoid(z_t[c])
+ *
+ * with h from initial_state (zeros when NULL) and final_state the last h. The time axis is
+ * scanned in tiles whose states are joined in the workspace: kda_ssm_workspace_bytes() bytes
+ * of device memory, or NULL: then the library allocates it stream-ordered on `stream`. The
+ * same results from run to run. Limits: total_tokens <= 2^27, channels <= 2^20,
+ * num_seqs * channels <= 2^31. final_state must not overlap initial_state.
+ */
+size_t kda_ssm_workspace_bytes(int32_t total_tokens, int32_t channels, int32_t state_size, int32_t groups);
+int kda_ssm_fwd(const kda_ssm_args *args, void *stream, void *workspace, size_t workspace_bytes);
+
+/*
+ * kda_ssm_decode -- one token per sequence: u, delta, z and out are [num_seqs, channels],
+ * B and C [num_seqs, groups, state_size] (total_tokens = num_seqs, cu_seqlens NULL).
+ * final_state may be the same pointer as initial_state (updated in place). No workspace.
+ */
+int kda_ssm_decode(const kda_ssm_args *args, void *stream);
+
 /*
  * kda_device_errors -- the device error word of the current device: the OR of the
  * KDA_DEVERR_* bits that kernels of every call on this device (any variant, with or

@@ -68,3 +68,47 @@ def check(name, got, ref, size, kind, steps):
     worst = np.unravel_index(np.argmax(off), off.shape) if off.size else None
     assert not off.size or off[worst] <= 1.0, \
         f"{name}: {off[worst]:.3g} times the tolerance at {worst}: got {got[worst]!r}, want {ref[worst]!r}"
+
+
+def softplus(x):
+    return np.logaddexp(x, 0.0)
+
+
+def scan(u, delta, A, B, C, D, z, bias, lengths, init=None, use_softplus=True):
+    """The selective scan and, beside each result, a bound on its fp32 rounding errors in units of 2^-24.
+
+    Roundings, relative: the step s from x = delta + bias: 3 |x| + 12 (the sum, the exponential's
+    argument and value, the odd series); the decay e^{sA}: |sA| times (the step's + 4), and 7 (its
+    value, its product with h, the sum, and what a tile's summed steps add: at most its length
+    spread over its tokens); the input s u B: the step's + 3. They are carried by the recurrence
+    itself. The output: a rounding per term of the sum over states, the skip's and the gate's."""
+    T, ch = u.shape
+    N, G = A.shape[1], B.shape[1]
+    x = delta + (0.0 if bias is None else bias)
+    s = softplus(x) if use_softplus else x
+    rs = 3 * np.abs(x) + 12 if use_softplus else np.ones_like(x)
+    spread = lambda v: np.repeat(v, ch // G, axis=0)  # noqa: E731
+    y, ye = np.zeros((T, ch)), np.zeros((T, ch))
+    fin, fe = np.zeros((len(lengths), ch, N)), np.zeros((len(lengths), ch, N))
+    skip = np.zeros(ch) if D is None else D
+    at = 0
+    for i, n in enumerate(lengths):
+        h = init[i].copy() if init is not None else np.zeros((ch, N))
+        size, err = np.abs(h), np.zeros((ch, N))
+        for t in range(at, at + n):
+            a = np.exp(s[t][:, None] * A)
+            inp = (s[t] * u[t])[:, None] * spread(B[t])
+            dec = (rs[t][:, None] + 4) * np.abs(s[t][:, None] * A) + 7
+            err = a * (err + size * dec) + (rs[t][:, None] + 3) * np.abs(inp)
+            h, size = a * h + inp, a * size + np.abs(inp)
+            Ct = np.abs(spread(C[t]))
+            y[t] = (spread(C[t]) * h).sum(1)
+            ye[t] = (Ct * err).sum(1) + (N + 6) * (Ct * size).sum(1)
+        fin[i], fe[i] = h, err
+        at += n
+    y, ye = y + skip * u, ye + 3 * np.abs(skip * u)
+    if z is not None:
+        gate = z * sigmoid(z)
+        ye = np.abs(gate) * (ye + (3 * np.abs(z) + 8) * np.abs(y))
+        y = y * gate
+    return y, ye, fin, fe

@@ -148,3 +148,116 @@ def test_conv_bwd_abi_refusals(lib):
     need = lib.kda_conv_bwd_workspace_bytes(T, C, W)
     assert need >= (W + 1) * C * 4 and bwd(nbytes=need - 1) == 4
     assert lib.kda_conv_bwd_workspace_bytes(-1, C, W) == 0 and lib.kda_conv_bwd_workspace_bytes(T, C, 9) == 0
+
+
+# ---------------------------------------------------------------- selective scan
+Dn, Ns, G = 12, 5, 3
+
+
+def _ssm():
+    bf = torch.bfloat16
+    return dict(u=torch.zeros(T, Dn, dtype=bf), delta=torch.zeros(T, Dn, dtype=bf), A=torch.zeros(Dn, Ns),
+                B=torch.zeros(T, G, Ns, dtype=bf), C=torch.zeros(T, G, Ns, dtype=bf), D=torch.zeros(Dn),
+                z=torch.zeros(T, Dn, dtype=bf), delta_bias=torch.zeros(Dn),
+                cu_seqlens=torch.tensor([0, 5, 5, T], dtype=torch.int32), initial_state=torch.zeros(N, Dn, Ns))
+
+
+def test_ssm_good_arguments():
+    from chunked_gated_delta_kda_amd.scan import check_ssm_decode_args, check_ssm_fwd_args
+    a = _ssm()
+    s = check_ssm_fwd_args(**a)
+    assert (s.T, s.D, s.N, s.G, s.S, s.strides) == (T, Dn, Ns, G, N, [Dn, Dn, G * Ns, G * Ns, Dn])
+    proj = torch.zeros(T, 2 * Dn + 2 * G * Ns, dtype=torch.bfloat16)       # slices of one projection
+    a.update(u=proj[:, :Dn], z=proj[:, Dn:2 * Dn], B=proj[:, 2 * Dn:2 * Dn + G * Ns].unflatten(1, (G, Ns)),
+             C=proj[:, 2 * Dn + G * Ns:].unflatten(1, (G, Ns)))
+    w = proj.shape[1]
+    assert check_ssm_fwd_args(**a).strides == [w, Dn, w, w, w]
+    a.update(D=None, z=None, delta_bias=None, cu_seqlens=None, initial_state=None)
+    assert check_ssm_fwd_args(**a).S == 1
+    del a["cu_seqlens"], a["initial_state"]
+    assert check_ssm_decode_args(**a, state=torch.zeros(T, Dn, Ns)).S == T
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("u", lambda: torch.zeros(T, Dn, dtype=torch.float64)),
+    ("u", lambda: torch.zeros(T, G, 4, dtype=torch.bfloat16)),
+    ("delta", lambda: torch.zeros(T, Dn)),
+    ("delta", lambda: torch.zeros(T, 1, dtype=torch.bfloat16)),
+    ("A", lambda: torch.zeros(Dn, 257)),
+    ("A", lambda: torch.zeros(Dn, 0)),
+    ("A", lambda: torch.zeros(Ns, Dn).t()),
+    ("A", lambda: torch.zeros(Dn, Ns, dtype=torch.bfloat16)),
+    ("B", lambda: torch.zeros(T, Ns, dtype=torch.bfloat16)),
+    ("B", lambda: torch.zeros(T, 5, Ns, dtype=torch.bfloat16)),              # 5 groups do not divide 12 channels
+    ("B", lambda: torch.zeros(T, Ns, G, dtype=torch.bfloat16).transpose(1, 2)),
+    ("C", lambda: torch.zeros(T, 1, Ns, dtype=torch.bfloat16)),
+    ("D", lambda: torch.zeros(Dn, dtype=torch.bfloat16)),
+    ("z", lambda: torch.zeros(T - 1, Dn, dtype=torch.bfloat16)),
+    ("delta_bias", lambda: torch.zeros(1)),
+    ("initial_state", lambda: torch.zeros(N, Dn, Ns, dtype=torch.bfloat16)),
+    ("initial_state", lambda: torch.zeros(N, Ns, Dn)),
+])
+def test_ssm_rejects(name, bad):
+    from chunked_gated_delta_kda_amd.scan import check_ssm_fwd_args
+    a = _ssm()
+    a[name] = bad()
+    with pytest.raises(ValueError, match=f"{name}:"):
+        check_ssm_fwd_args(**a)
+
+
+def test_ssm_rejects_outputs():
+    from chunked_gated_delta_kda_amd.scan import check_ssm_decode_args, check_ssm_fwd_args
+    import chunked_gated_delta_kda_amd as kda
+    a = _ssm()
+    with pytest.raises(ValueError, match="out"):
+        check_ssm_fwd_args(**a, out=torch.empty(T, Dn))
+    with pytest.raises(ValueError, match="final_state"):
+        check_ssm_fwd_args(**a, final_state=torch.empty(N, Dn, Ns + 1))
+    with pytest.raises(ValueError, match="device"):
+        kda.ssm_fwd(**a)
+    del a["cu_seqlens"], a["initial_state"]
+    with pytest.raises(ValueError, match="state"):
+        check_ssm_decode_args(**a, state=torch.zeros(N, Dn, Ns))
+    with pytest.raises(ValueError, match="state_out"):
+        check_ssm_decode_args(**a, state_out="new")
+    with pytest.raises(ValueError, match="device"):
+        kda.ssm_decode(**a)
+
+
+def ssm_args(**over):
+    names = ("u", "delta", "A", "B", "C", "D", "z", "delta_bias")
+    a = {n: (i + 1) << 20 for i, n in enumerate(names)}
+    a.update(cu_seqlens=None, initial_state=16 << 20, final_state=17 << 20, out=18 << 20, u_stride=Dn, delta_stride=Dn,
+             B_stride=G * Ns, C_stride=G * Ns, z_stride=Dn, num_seqs=1, total_tokens=T, channels=Dn, state_size=Ns, groups=G,
+             dtype=1, delta_softplus=1)
+    a.update(over)
+    return native.KdaSsmArgs(**a)
+
+
+def test_ssm_abi_refusals(lib):
+    fwd = lambda ws=P, n=0, **kw: lib.kda_ssm_fwd(ctypes.byref(ssm_args(**kw)), None, ws, n)  # noqa: E731
+    assert lib.kda_ssm_fwd(None, None, None, 0) == 1
+    for kw in (dict(dtype=3), dict(delta_softplus=2)):
+        assert fwd(**kw) == 3, kw
+    for kw in (dict(num_seqs=0), dict(num_seqs=2), dict(total_tokens=-1), dict(channels=0), dict(state_size=0),
+               dict(state_size=257), dict(groups=5), dict(groups=0), dict(u_stride=Dn - 1), dict(B_stride=G * Ns - 1),
+               dict(z_stride=0), dict(total_tokens=(1 << 27) + 1)):
+        assert fwd(**kw) == 2, kw
+    for kw in (dict(u=None), dict(delta=None), dict(A=None), dict(B=None), dict(C=None), dict(out=None)):
+        assert fwd(**kw) == 1, kw
+    for kw in (dict(out=1 << 20), dict(out=7 << 20), dict(final_state=16 << 20), dict(final_state=3 << 20),
+               dict(final_state=18 << 20)):
+        assert fwd(**kw) == 7, kw
+    need = lib.kda_ssm_workspace_bytes(T, Dn, Ns, G)
+    assert need > 0 and fwd(n=need - 1) == 4
+    assert lib.kda_ssm_workspace_bytes(16, Dn, Ns, G) == 0            # one tile needs none
+    assert lib.kda_ssm_workspace_bytes(T, Dn, Ns, 5) == 0             # not a valid shape
+
+
+def test_ssm_decode_abi_refusals(lib):
+    dec = lambda **kw: lib.kda_ssm_decode(ctypes.byref(ssm_args(num_seqs=T, **kw)), None)  # noqa: E731
+    assert dec(cu_seqlens=P) == 2 and dec(total_tokens=T - 1) == 2
+    assert dec(out=None) == 1
+    state = T * Dn * Ns * 4
+    assert dec(final_state=(16 << 20) + state - 4) == 7
+    assert dec(out=2 << 20) == 7
