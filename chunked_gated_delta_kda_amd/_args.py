@@ -64,6 +64,15 @@ def ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def scratch(workspace, nbytes, dev):
+    """The caller's workspace, or one of ``nbytes`` (None if none is needed); its pointer and size."""
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace, ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
 @contextlib.contextmanager
 def _elsewhere(dev, stream):
     with torch.cuda.device(dev):

@@ -121,6 +121,17 @@ struct SsmSpans {
     }
 };
 
+// ---------------------------------------------------------------- paged token attention
+// 0, or the status of sizes that the kernels do not take
+int check_attn_sizes(int64_t B, int64_t hq, int64_t hkv, int64_t dh, int64_t width, int64_t page) {
+    if (dh != 64 && dh != 128 && dh != 256) return KDA_ERR_UNSUPPORTED;
+    if (B < 1 || hkv < 1 || hq < hkv || hq % hkv || hq > 65535 || width < 1 || page < 1 || width > (1 << 30) / page) return KDA_ERR_SHAPE;
+    if ((B + 1) * hkv * ((hq / hkv + 15) / 16) > 1 << 22) return KDA_ERR_SHAPE;
+    return KDA_OK;
+}
+
+bool by16(const void *p) { return (uintptr_t)p % 16 == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -216,6 +227,46 @@ int kda_ssm_decode(const kda_ssm_args *args, void *stream) {
     const bool in_place = a.initial_state == a.final_state;
     if (s.over(out) || s.over(fin, in_place ? 8 : 9) || meet(out, fin)) return KDA_ERR_ALIAS;
     return launched(kda::ops::launch_ssm_decode(a, (hipStream_t)stream));
+}
+
+size_t kda_attn_workspace_bytes(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                int32_t table_width, int32_t page_size) {
+    if (check_attn_sizes(num_seqs, q_heads, kv_heads, head_dim, table_width, page_size) != KDA_OK) return 0;
+    return kda::ops::attn_workspace(num_seqs, q_heads, kv_heads, head_dim, table_width, page_size);
+}
+
+int kda_attn_decode(const kda_attn_args *args, void *stream, void *workspace, size_t workspace_bytes) {
+    if (!args) return KDA_ERR_NULL;
+    const kda_attn_args &a = *args;
+    if (a.dtype != KDA_DTYPE_BF16 && a.dtype != KDA_DTYPE_F16) return KDA_ERR_UNSUPPORTED;
+    if (!std::isfinite(a.scale)) return KDA_ERR_UNSUPPORTED;
+    if (const int rc = check_attn_sizes(a.num_seqs, a.q_heads, a.kv_heads, a.head_dim, a.table_width, a.page_size)) return rc;
+    if (a.num_pages < 1 || a.table_stride < 0 || (a.num_seqs > 1 && a.table_stride < a.table_width)) return KDA_ERR_SHAPE;
+    const int64_t strides[] = {a.q_stride, a.q_head_stride, a.k_page_stride, a.k_token_stride,
+                               a.k_head_stride, a.v_page_stride, a.v_token_stride, a.v_head_stride};
+    for (const int64_t s : strides)
+        if (s < 0) return KDA_ERR_SHAPE;
+    for (const int64_t s : strides)
+        if (s % 8) return KDA_ERR_UNSUPPORTED;
+    if (!a.q || !a.k_cache || !a.v_cache || !a.block_table || !a.seq_lens || !a.out) return KDA_ERR_NULL;
+    if (!by16(a.q) || !by16(a.k_cache) || !by16(a.v_cache)) return KDA_ERR_UNSUPPORTED;
+    const int64_t es = 2, B = a.num_seqs;
+    auto cache = [&](const void *p, int64_t page, int64_t token, int64_t head) {
+        return span(p, ((a.num_pages - 1) * page + (a.page_size - 1) * token + (a.kv_heads - 1) * head + a.head_dim) * es);
+    };
+    const Span in[] = {span(a.q, ((B - 1) * a.q_stride + (a.q_heads - 1) * a.q_head_stride + a.head_dim) * es),
+                       cache(a.k_cache, a.k_page_stride, a.k_token_stride, a.k_head_stride),
+                       cache(a.v_cache, a.v_page_stride, a.v_token_stride, a.v_head_stride),
+                       span(a.block_table, ((B - 1) * a.table_stride + a.table_width) * 4), span(a.seq_lens, B * 4)};
+    const Span out = span(a.out, B * a.q_heads * a.head_dim * es), lse = span(a.lse, B * a.q_heads * 4);
+    if (meet(out, lse)) return KDA_ERR_ALIAS;
+    for (const Span &i : in)
+        if (meet(i, out) || meet(i, lse)) return KDA_ERR_ALIAS;
+    hipStream_t st = (hipStream_t)stream;
+    Workspace ws(workspace, workspace_bytes,
+                 kda::ops::attn_workspace(B, a.q_heads, a.kv_heads, a.head_dim, a.table_width, a.page_size), st);
+    if (ws.status() != KDA_OK) return ws.status();
+    return ws.finish(launched(kda::ops::launch_attn_decode(a, (float *)ws.ptr(), kda::device_error_word(), st)));
 }
 
 }  // extern "C"

@@ -1,0 +1,423 @@
+// ops_attn.hip -- attention of one new token per sequence over a paged key-value cache, split
+// over the cache's length and joined.
+//
+//   out[h] = sum_t softmax_t(scale q[h].k_t) v_t over the len cached tokens of the sequence, in
+//   one pass with the running maximum and sum; lse[h] = log sum_t e^{scale q[h].k_t}
+//
+// Bound by the bytes of the cache, each read once. A wave takes 32 tokens of one key-value head at
+// a time, for up to 16 query heads that share it:
+//  * S^T = K Q^T (v_mfma_f32_16x16x32: rows tokens, columns heads). A lane holds the scores of one
+//    head for 8 tokens, so maxima and sums are lane-local but for two exchanges between the
+//    wave's four 16-lane rows.
+//  * O^T = V^T P^T. P leaves S^T in the very lanes its operand wants (the 32 tokens of the
+//    contraction are relabelled: slot 8 g + i is token 4 g + i for i < 4, 16 + 4 g + i - 4 else), split
+//    into a rounded part and the rest, two products, so that P does not lose what the output
+//    keeps. V's operand holds 8 tokens of one element: a lane loads DV neighbouring elements
+//    of 8 tokens (whole rows of the cache per instruction) and pairs the tokens' halves up with
+//    byte permutes. Neither K nor V passes through LDS.
+//  * The result has a head's elements in its own lanes, so rescaling needs no exchange.
+// Blocks take chunks of one sequence's tokens. Every block works the chunk length out from all
+// lengths (on the device: the host does not know them), so that skewed batches spread evenly and a
+// captured launch stays right when lengths change. Chunks' partial results go to the workspace;
+// attn_join_kernel joins them in their order. A sequence of one chunk is written at once.
+#include "ops_common.hpp"
+#include "ops_launch.hpp"
+
+namespace kda {
+namespace ops {
+namespace attn {
+namespace {
+
+constexpr int WAVES = 4;
+constexpr int TILE = 32;                  // tokens of a wave at a time
+constexpr int ROUND = WAVES * TILE;       // tokens of a block at a time
+constexpr float NEG_INF = -__builtin_inff();
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <int DT> struct Ops;
+template <> struct Ops<KDA_DTYPE_BF16> {
+    typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+    typedef __bf16 x2 __attribute__((ext_vector_type(2)));
+    using E = __bf16;
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+    }
+};
+template <> struct Ops<KDA_DTYPE_F16> {
+    typedef _Float16 x8 __attribute__((ext_vector_type(8)));
+    typedef _Float16 x2 __attribute__((ext_vector_type(2)));
+    using E = _Float16;
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+    }
+};
+
+// Two probabilities to a rounded pair and the pair of what rounding left.
+template <int DT> __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
+    using x2 = typename Ops<DT>::x2;
+    using E = typename Ops<DT>::E;
+    const x2 h = {(E)a, (E)b};
+    const x2 l = {(E)(a - (float)h[0]), (E)(b - (float)h[1])};
+    hi = __builtin_bit_cast(uint32_t, h);
+    lo = __builtin_bit_cast(uint32_t, l);
+}
+
+// maximum and sum over a lane's column (its four 16-lane rows)
+__device__ __forceinline__ float column_max(float x) {
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float column_sum(float x) {
+    x = swap16_add(x, x);
+    return swap32_add(x, x);
+}
+
+// What a sequence holds: its length, at most what its row of the table can address.
+__device__ __forceinline__ int seq_len(const kda_attn_args &a, int s) {
+    const int64_t most = (int64_t)a.table_width * a.page_size;
+    const int n = a.seq_lens[s];
+    return n < 0 ? 0 : n > most ? (int)most : n;
+}
+
+__device__ __forceinline__ int64_t wave_sum64(int64_t x) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+
+struct Work {
+    int seq, part, parts, slot;   // slot: index of the chunk among all chunks
+    int begin, end;               // its tokens
+};
+
+// Tokens of a chunk: all tokens over `spread` chunks, whole rounds, at least min_chunk.
+__device__ __forceinline__ int chunk_len(int64_t total, int spread, int min_chunk) {
+    const int64_t c = (total + spread - 1) / spread;
+    const int64_t r = (c + ROUND - 1) / ROUND * ROUND;
+    return r < min_chunk ? min_chunk : (int)(r < (1 << 30) ? r : 1 << 30);
+}
+__device__ __forceinline__ int parts_of(int len, int chunk) { return len > chunk ? (len + chunk - 1) / chunk : 1; }
+
+// The chunk of index `slot`, found by every wave for itself; false past the last.
+__device__ __forceinline__ bool find_work(const kda_attn_args &a, int slot, int spread, int min_chunk, Work &w) {
+    const int lane = threadIdx.x & 63;
+    int64_t total = 0;
+    for (int s = lane; s < a.num_seqs; s += 64) total += seq_len(a, s);
+    const int chunk = chunk_len(wave_sum64(total), spread, min_chunk);
+    int before = 0;
+    for (int s0 = 0; s0 < a.num_seqs; s0 += 64) {
+        const int s = s0 + lane;
+        const int len = s < a.num_seqs ? seq_len(a, s) : 0;
+        const int mine = s < a.num_seqs ? parts_of(len, chunk) : 0;
+        int upto = mine;      // inclusive sum over lanes
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int v = __shfl_up(upto, d);
+            if (lane >= d) upto += v;
+        }
+        const int all = __shfl(upto, 63);
+        if (slot < before + all) {
+            const uint64_t at = __ballot(before + upto > slot);
+            const int l = __builtin_ctzll(at);
+            w.seq = s0 + l;
+            w.parts = __shfl(mine, l);
+            w.part = slot - (before + __shfl(upto, l) - w.parts);
+            w.slot = slot;
+            const int n = __shfl(len, l);
+            w.begin = w.part * chunk;
+            w.end = w.parts == 1 || n - w.begin < chunk ? n : w.begin + chunk;
+            return true;
+        }
+        before += all;
+    }
+    return false;
+}
+
+// Row offsets (elements, from the caches' bases) of 32 tokens, and which of them are there.
+struct Rows {
+    int64_t k[TILE], v[TILE];
+};
+
+template <int DT, int DH>
+__global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_args a, float *acc_out, float *ml_out,
+                                                                int32_t *err, int spread, int min_chunk, int tiles_h) {
+    using O = Ops<DT>;
+    using E = typename O::E;
+    constexpr int KD = DH / 32;      // 32-element steps of a score
+    constexpr int DV = DH / 16;      // elements of a lane in O^T's operand rows
+    __shared__ Rows rows[WAVES];
+    __shared__ float join[WAVES][16 * (DH + 4)];
+    __shared__ float stat[WAVES][16][2];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int per = a.kv_heads * tiles_h;
+    const int slot = blockIdx.x / per, rest = blockIdx.x - slot * per;
+    const int kvh = rest / tiles_h, ht = rest - kvh * tiles_h;
+    Work w;
+    if (!find_work(a, slot, spread, min_chunk, w)) return;
+    const int seq = __builtin_amdgcn_readfirstlane(w.seq);
+    const int begin = __builtin_amdgcn_readfirstlane(w.begin), end = __builtin_amdgcn_readfirstlane(w.end);
+    if (err && w.part == 0 && rest == 0 && threadIdx.x == 0) {
+        const int n = a.seq_lens[seq];
+        if (n < 0 || n > (int64_t)a.table_width * a.page_size) atomicOr(err, KDA_DEVERR_PAGES);
+    }
+    const int group = a.q_heads / a.kv_heads;
+    const int heads = group - ht * 16 < 16 ? group - ht * 16 : 16;      // of this block
+    const int head0 = kvh * group + ht * 16;
+    u32x4 q[KD];
+#pragma unroll
+    for (int k = 0; k < KD; ++k) {
+        q[k] = u32x4{0, 0, 0, 0};
+        if (i < heads)
+            q[k] = *reinterpret_cast<const u32x4 *>((const E *)a.q + seq * a.q_stride + (int64_t)(head0 + i) * a.q_head_stride +
+                                                    32 * k + 8 * g);
+    }
+    const float scale = a.scale * LOG2E_F;
+    f32x4 acc[DV];
+#pragma unroll
+    for (int d = 0; d < DV; ++d) acc[d] = f32x4{0, 0, 0, 0};
+    float m = NEG_INF, l = 0.0f;
+    const int32_t *table = a.block_table + (int64_t)seq * a.table_stride;
+    const E *kc = (const E *)a.k_cache + (int64_t)kvh * a.k_head_stride;
+    const E *vc = (const E *)a.v_cache + (int64_t)kvh * a.v_head_stride;
+    Rows &R = rows[wave];
+    bool bad = false;
+
+    for (int t0 = begin + wave * TILE; t0 < end; t0 += ROUND) {
+        // every lane one token (the upper half of the wave repeats the lower): its page, checked
+        const int t = t0 + (lane & 31);
+        const int tc = t < end ? t : end - 1;
+        const int pg = tc / a.page_size, at = tc - pg * a.page_size;
+        int page = table[pg];
+        bool there = t < end;
+        if (page < 0 || page >= a.num_pages) {
+            bad = true, there = false;
+            page = 0;
+        }
+        if (lane < 32) R.k[lane] = (int64_t)page * a.k_page_stride + (int64_t)at * a.k_token_stride;
+        else R.v[lane - 32] = (int64_t)page * a.v_page_stride + (int64_t)at * a.v_token_stride;
+        const uint32_t seen = (uint32_t)__ballot(there);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        u32x4 kr[2][KD];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const E *row = kc + R.k[16 * h + i] + 8 * g;
+#pragma unroll
+            for (int k = 0; k < KD; ++k) kr[h][k] = *reinterpret_cast<const u32x4 *>(row + 32 * k);
+        }
+        uint32_t vr[8][DV / 2];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const int tok = (s < 4 ? 0 : 12) + 4 * g + s;
+            const E *row = vc + R.v[tok] + DV * i;
+            if constexpr (DV == 4) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(row);
+                vr[s][0] = x.x, vr[s][1] = x.y;
+            } else {
+#pragma unroll
+                for (int c = 0; c < DV / 8; ++c) {
+                    const u32x4 x = *reinterpret_cast<const u32x4 *>(row + 8 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) vr[s][4 * c + e] = x[e];
+                }
+            }
+        }
+        f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int k = 0; k < KD; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) st[h] = O::mma(kr[h][k], q[k], st[h]);
+        // this lane's tokens: 4 g + j and 16 + 4 g + j
+        float sc[8], top = NEG_INF;
+        const uint32_t mine = (seen >> (4 * g)) & 0xf000f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const bool on = (mine >> ((s < 4 ? 0 : 12) + s)) & 1;
+            sc[s] = on ? st[s >> 2][s & 3] * scale : NEG_INF;
+            top = __builtin_fmaxf(top, sc[s]);
+        }
+        const float mn = __builtin_fmaxf(m, column_max(top));
+        if (__any(mn > m)) {
+            const float f = mn > m ? exp2_f(m - mn) : 1.0f;      // m may be -inf: 0
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DV; ++d) acc[d] *= f;
+            m = mn;
+        }
+        const float ref = m == NEG_INF ? 0.0f : m;
+        float p[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            p[s] = exp2_f(sc[s] - ref);
+            l += p[s];
+        }
+        u32x4 hi, lo;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            uint32_t x, y;
+            split_pair<DT>(p[2 * s], p[2 * s + 1], x, y);
+            hi[s] = x, lo[s] = y;
+        }
+        if (seen != 0xffffffffu) {          // rows that are not there may hold anything: 0 x NaN
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const bool on = (mine >> ((s < 4 ? 0 : 12) + s)) & 1;
+#pragma unroll
+                for (int e = 0; e < DV / 2; ++e) vr[s][e] = on ? vr[s][e] : 0u;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < DV / 2; ++e) {
+            u32x4 even, odd;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                even[s] = __builtin_amdgcn_perm(vr[2 * s + 1][e], vr[2 * s][e], 0x05040100);
+                odd[s] = __builtin_amdgcn_perm(vr[2 * s + 1][e], vr[2 * s][e], 0x07060302);
+            }
+            acc[2 * e] = O::mma(even, hi, acc[2 * e]);
+            acc[2 * e + 1] = O::mma(odd, hi, acc[2 * e + 1]);
+            acc[2 * e] = O::mma(even, lo, acc[2 * e]);
+            acc[2 * e + 1] = O::mma(odd, lo, acc[2 * e + 1]);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+    if (err && __any(bad) && lane == 0) atomicOr(err, KDA_DEVERR_PAGES);
+    l = column_sum(l);
+
+    // the waves' results, against the block's largest maximum
+    if (g == 0) stat[wave][i][0] = m, stat[wave][i][1] = l;
+    __syncthreads();
+    float M = NEG_INF, L = 0.0f;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) M = __builtin_fmaxf(M, stat[v][i][0]);
+    const float ref = M == NEG_INF ? 0.0f : M;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) L += stat[v][i][1] * exp2_f(stat[v][i][0] - ref);
+    const float f = exp2_f(m - ref);
+    // O^T: element DV (4 g + j) + d of head i
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int d = 0; d < DV; ++d) join[wave][i * (DH + 4) + DV * (4 * g + j) + d] = acc[d][j] * f;
+    __syncthreads();
+    const bool whole = w.parts == 1;
+    for (int x = threadIdx.x; x < heads * DH; x += 64 * WAVES) {
+        const int h = x / DH, d = x - h * DH;
+        float o = 0.0f;
+#pragma unroll
+        for (int v = 0; v < WAVES; ++v) o += join[v][h * (DH + 4) + d];
+        if (whole) {
+            float hm = NEG_INF, hl = 0.0f;
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v) hm = __builtin_fmaxf(hm, stat[v][h][0]);
+            const float hr = hm == NEG_INF ? 0.0f : hm;
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v) hl += stat[v][h][1] * exp2_f(stat[v][h][0] - hr);
+            reinterpret_cast<E *>(a.out)[((int64_t)seq * a.q_heads + head0 + h) * DH + d] = (E)(hl == 0.0f ? 0.0f : o / hl);
+        } else acc_out[((int64_t)w.slot * a.q_heads + head0 + h) * DH + d] = o;
+    }
+    if (threadIdx.x < heads) {      // wave 0: lane i is head i
+        if (whole) {
+            if (a.lse) a.lse[(int64_t)seq * a.q_heads + head0 + i] = L == 0.0f ? NEG_INF : (ref + __builtin_log2f(L)) * LN2_F;
+        } else {
+            float *ml = ml_out + ((int64_t)w.slot * a.q_heads + head0 + i) * 2;
+            ml[0] = M, ml[1] = L;
+        }
+    }
+}
+
+// Joins the chunks of one (sequence, head), in their order, where there are several.
+template <int DT>
+__global__ __launch_bounds__(256) void attn_join_kernel(const kda_attn_args a, const float *acc, const float *ml, int spread,
+                                                        int min_chunk) {
+    using E = typename Ops<DT>::E;
+    __shared__ float part[256];
+    const int s = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63;
+    int64_t total = 0;
+    for (int q = lane; q < a.num_seqs; q += 64) total += seq_len(a, q);
+    const int chunk = chunk_len(wave_sum64(total), spread, min_chunk);
+    const int parts = parts_of(seq_len(a, s), chunk);
+    if (parts == 1) return;
+    int64_t first = 0;
+    for (int q = lane; q < s; q += 64) first += parts_of(seq_len(a, q), chunk);
+    first = wave_sum64(first);
+    const float *st = ml + (first * a.q_heads + h) * 2;
+    const int64_t step = (int64_t)a.q_heads * 2;
+    float M = NEG_INF;
+    for (int p = lane; p < parts; p += 64) M = __builtin_fmaxf(M, st[p * step]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) M = __builtin_fmaxf(M, __shfl_xor(M, d));
+    const float ref = M == NEG_INF ? 0.0f : M;
+    const int dh = a.head_dim, lanes = dh < 256 ? dh : 256, groups = 256 / lanes;
+    const int grp = threadIdx.x / lanes, d = threadIdx.x - grp * lanes;
+    float o = 0.0f, L = 0.0f;
+    for (int p = 0; p < parts; ++p) L += st[p * step + 1] * exp2_f(st[p * step] - ref);
+    if (grp < groups)
+        for (int p = grp; p < parts; p += groups)
+            o += acc[((first + p) * a.q_heads + h) * dh + d] * exp2_f(st[p * step] - ref);
+    part[threadIdx.x] = o;
+    __syncthreads();
+    if (threadIdx.x < dh) {
+        for (int q = 1; q < groups; ++q) o += part[q * lanes + d];
+        reinterpret_cast<E *>(a.out)[((int64_t)s * a.q_heads + h) * dh + d] = (E)(L == 0.0f ? 0.0f : o / L);
+    }
+    if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)s * a.q_heads + h] = L == 0.0f ? NEG_INF : (ref + __builtin_log2f(L)) * LN2_F;
+}
+
+// The host's part of the plan: how many chunks all tokens are spread over, how many there can be,
+// and whether any sequence can have more than one.
+struct Plan {
+    int spread, slots, min_chunk, tiles_h;
+    bool join;
+};
+Plan plan(int64_t B, int64_t hq, int64_t hkv, int64_t width, int64_t page) {
+    Plan p;
+    p.tiles_h = (int)ceil_div(hq / hkv, 16);
+    const int64_t per = hkv * p.tiles_h;
+    p.min_chunk = 2 * ROUND;
+    const int64_t most = width * page;
+    int64_t spread = ceil_div(1024, per);
+    p.spread = (int)spread;
+    p.join = most > p.min_chunk;
+    // sum of ceil(len / chunk) <= spread + B, and no sequence has more than its table allows
+    const int64_t by_len = B * ceil_div(most > 0 ? most : 1, p.min_chunk);
+    p.slots = (int)(spread + B < by_len ? spread + B : by_len);
+    return p;
+}
+
+template <int DT, int DH>
+hipError_t run(const kda_attn_args &a, const Plan &p, float *acc, float *ml, int32_t *err, hipStream_t st) {
+    const int64_t blocks = (int64_t)p.slots * a.kv_heads * p.tiles_h;
+    attn_chunk_kernel<DT, DH><<<dim3((unsigned)blocks), 64 * WAVES, 0, st>>>(a, acc, ml, err, p.spread, p.min_chunk, p.tiles_h);
+    if (hipError_t e = hipGetLastError()) return e;
+    if (p.join) attn_join_kernel<DT><<<dim3((unsigned)a.num_seqs, (unsigned)a.q_heads), 256, 0, st>>>(a, acc, ml, p.spread, p.min_chunk);
+    return hipGetLastError();
+}
+
+template <int DT> hipError_t run_dt(const kda_attn_args &a, const Plan &p, float *acc, float *ml, int32_t *err, hipStream_t st) {
+    if (a.head_dim == 64) return run<DT, 64>(a, p, acc, ml, err, st);
+    if (a.head_dim == 128) return run<DT, 128>(a, p, acc, ml, err, st);
+    return run<DT, 256>(a, p, acc, ml, err, st);
+}
+
+}  // namespace
+}  // namespace attn
+
+size_t attn_workspace(int64_t B, int64_t hq, int64_t hkv, int64_t dh, int64_t width, int64_t page) {
+    const attn::Plan p = attn::plan(B, hq, hkv, width, page);
+    return p.join ? (size_t)p.slots * hq * (dh + 2) * sizeof(float) : 0;
+}
+
+hipError_t launch_attn_decode(const kda_attn_args &a, float *ws, int32_t *err, hipStream_t st) {
+    const attn::Plan p = attn::plan(a.num_seqs, a.q_heads, a.kv_heads, a.table_width, a.page_size);
+    float *ml = ws ? ws + (size_t)p.slots * a.q_heads * a.head_dim : nullptr;
+    if (a.dtype == KDA_DTYPE_BF16) return attn::run_dt<KDA_DTYPE_BF16>(a, p, ws, ml, err, st);
+    return attn::run_dt<KDA_DTYPE_F16>(a, p, ws, ml, err, st);
+}
+
+}  // namespace ops
+}  // namespace kda

@@ -21,9 +21,11 @@ EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_noalloc", "kda_workspace_bytes", "k
            "kda_launch_plan", "kda_decode", "kda_decode_ex", "kda_bwd", "kda_bwd_workspace_bytes",
            "kda_conv_fwd", "kda_conv_decode", "kda_conv_bwd", "kda_conv_bwd_workspace_bytes",
            "kda_ssm_fwd", "kda_ssm_workspace_bytes", "kda_ssm_decode",
+           "kda_attn_decode", "kda_attn_workspace_bytes",
            "kda_device_errors", "kda_status_string", "kda_version")
 #: KDA_DEVERR_* bits of the device error word
-DEVERR = {1: "fused hand-off wait gave up (outputs invalid)", 2: "malformed cu_seqlens (sanitised)"}
+DEVERR = {1: "fused hand-off wait gave up (outputs invalid)", 2: "malformed cu_seqlens (sanitised)",
+          4: "block table entry or length outside the cache (left out)"}
 STATE_DTYPES = {"f32": 0, "bf16": 1}
 DTYPES = STATE_DTYPES   # KDA_DTYPE_* of kda_options.g_dtype / state_dtype
 SEGMENT_ONE = 65536   # KDA_SEGMENT_ONE: unit of the launch plan's segment fractions
@@ -69,6 +71,15 @@ class KdaSsmArgs(ctypes.Structure):
                 [(n, ctypes.c_int64) for n in ("u_stride", "delta_stride", "B_stride", "C_stride", "z_stride")] +
                 [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "channels", "state_size", "groups", "dtype",
                                                "delta_softplus")])
+
+
+class KdaAttnArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k_cache", "v_cache", "block_table", "seq_lens", "out", "lse")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "q_head_stride", "k_page_stride", "k_token_stride",
+                                               "k_head_stride", "v_page_stride", "v_token_stride", "v_head_stride",
+                                               "table_stride")] +
+                [(n, ctypes.c_int32) for n in ("num_seqs", "q_heads", "kv_heads", "head_dim", "num_pages", "page_size",
+                                               "table_width", "dtype")] + [("scale", ctypes.c_float)])
 
 
 class KdaError(RuntimeError):
@@ -131,6 +142,10 @@ def load_library(path=LIB_PATH):
     lib.kda_ssm_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_ssm_decode.argtypes = [ctypes.POINTER(KdaSsmArgs), vp]
     lib.kda_ssm_decode.restype = ctypes.c_int
+    lib.kda_attn_decode.argtypes = [ctypes.POINTER(KdaAttnArgs), vp, vp, ctypes.c_size_t]
+    lib.kda_attn_decode.restype = ctypes.c_int
+    lib.kda_attn_workspace_bytes.argtypes = [i32] * 6
+    lib.kda_attn_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]
     lib.kda_device_errors.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]

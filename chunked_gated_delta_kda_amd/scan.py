@@ -4,7 +4,7 @@ import ctypes
 import torch
 
 from . import native
-from ._args import DTYPES, checked, dense, launch_on, offsets, on_device, ptr, rows
+from ._args import DTYPES, checked, dense, launch_on, offsets, on_device, ptr, rows, scratch
 
 __all__ = ["ssm_fwd", "ssm_decode"]
 
@@ -57,15 +57,6 @@ def _args(s, u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, fin
     return native.KdaSsmArgs(ptr(u), ptr(delta), ptr(A), ptr(B), ptr(C), ptr(D), ptr(z), ptr(delta_bias), ptr(cu_seqlens),
                              ptr(initial_state), ptr(final_state), ptr(out), *s.strides, s.S, s.T, s.D, s.N, s.G,
                              DTYPES[u.dtype], int(bool(softplus)))
-
-
-def scratch(workspace, nbytes, dev):
-    """The caller's workspace, or one of ``nbytes`` (None if none is needed); its pointer and size."""
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace, ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def ssm_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_seqlens=None, initial_state=None,

@@ -5,7 +5,7 @@ import ctypes
 import torch
 
 from . import native
-from ._args import DTYPES, checked, dense, launch_on, offsets, on_device, ptr, rows
+from ._args import DTYPES, checked, dense, launch_on, offsets, on_device, ptr, rows, scratch
 
 __all__ = ["conv_fwd", "conv_bwd", "conv_decode"]
 
@@ -138,14 +138,10 @@ def conv_bwd(x, weight, dy, bias=None, cu_seqlens=None, initial_state=None, d_fi
         gr = dict(dx=torch.empty((T, C), dtype=x.dtype, device=dev), dweight=torch.empty((C, W), **f32),
                   dbias=torch.empty((C,), **f32) if bias is not None else None,
                   d_initial_state=torch.empty((N, W - 1, C), **f32) if need_d_initial_state else None)
-        if workspace is None:
-            workspace = torch.empty(lib.kda_conv_bwd_workspace_bytes(T, C, W), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+        workspace, wp, wn = scratch(workspace, lib.kda_conv_bwd_workspace_bytes(T, C, W), dev)
         args = native.KdaConvArgs(ptr(x), ptr(weight), ptr(bias), ptr(cu_seqlens), ptr(initial_state), None, None, stride,
                                   N, T, C, W, DTYPES[x.dtype], _ACTIVATIONS[activation])
         grads = native.KdaConvGrads(ptr(dy), ptr(d_final_state), ptr(gr["dx"]), ptr(gr["dweight"]), ptr(gr["dbias"]),
                                     ptr(gr["d_initial_state"]), dy_stride)
-        native.check(lib.kda_conv_bwd(ctypes.byref(args), ctypes.byref(grads), st, ptr(workspace),
-                                      workspace.numel() * workspace.element_size()))
+        native.check(lib.kda_conv_bwd(ctypes.byref(args), ctypes.byref(grads), st, wp, wn))
     return gr

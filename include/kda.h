@@ -64,6 +64,9 @@ typedef enum kda_variant {
                                      call's outputs and final_state are not valid        */
 #define KDA_DEVERR_CU_SEQLENS 2   /* cu_seqlens was not 0 = c_0 <= ... <= c_N = T; the
                                      offsets were sanitised before use (see kda_fwd)     */
+#define KDA_DEVERR_PAGES 4        /* kda_attn_decode: a page number outside the cache, whose
+                                     tokens were left out, or a length outside its row of
+                                     the block table, which was clamped to it             */
 
 /* Kernel kinds reported by kda_launch_plan (profiling). */
 #define KDA_KERNEL_CHUNK_MAP 0
@@ -406,6 +409,48 @@ int kda_ssm_fwd(const kda_ssm_args *args, void *stream, void *workspace, size_t 
  * final_state may be the same pointer as initial_state (updated in place). No workspace.
  */
 int kda_ssm_decode(const kda_ssm_args *args, void *stream);
+
+typedef struct kda_attn_args {
+    const void *q;            /* [num_seqs, q_heads, head_dim]                              */
+    const void *k_cache;      /* [num_pages, page_size, kv_heads, head_dim], any strides      */
+    const void *v_cache;      /* [num_pages, page_size, kv_heads, head_dim], any strides      */
+    const int32_t *block_table; /* int32 [num_seqs, table_width], rows table_stride apart: the */
+                              /* pages of each sequence in order; entries past its length   */
+                              /* are not read                                               */
+    const int32_t *seq_lens;  /* int32 [num_seqs]: cached tokens, the new one's included; 0: none */
+    void *out;                /* [num_seqs, q_heads, head_dim], contiguous                  */
+    float *lse;               /* fp32 [num_seqs, q_heads] or NULL (not written)             */
+    int64_t q_stride, q_head_stride;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    int64_t table_stride;
+    int32_t num_seqs;
+    int32_t q_heads, kv_heads; /* kv_heads divides q_heads; query head h reads key-value head */
+                              /* h / (q_heads / kv_heads)                                   */
+    int32_t head_dim;         /* 64, 128 or 256                                             */
+    int32_t num_pages, page_size, table_width;
+    int32_t dtype;            /* KDA_DTYPE_BF16 or KDA_DTYPE_F16: q, the caches and out       */
+    float scale;              /* finite                                                     */
+} kda_attn_args;
+
+/*
+ * kda_attn_decode -- attention of one new token per sequence over a paged key-value cache:
+ *
+ *   out[h] = sum_t softmax_t(scale q[h].k_t) v_t,   lse[h] = log sum_t exp(scale q[h].k_t)
+ *
+ * over the sequence's cached tokens, split over their length and joined. A sequence without
+ * tokens gives zeros and lse = -infinity. Rows of q and of the caches are read 16 bytes at a
+ * time: their base pointers are aligned to 16 bytes and their strides are multiples of 8
+ * elements, else KDA_ERR_UNSUPPORTED. What a page holds past a sequence's length is not used,
+ * whatever it is. workspace: kda_attn_workspace_bytes() bytes of device memory, or NULL: then
+ * the library allocates it stream-ordered on `stream`. The launches depend on the sizes in
+ * args alone: a captured call stays right when lengths, pages and table entries change. The
+ * same results from run to run. Limits: table_width * page_size <= 2^30, q_heads <= 65535,
+ * (num_seqs + 1) * kv_heads * ceil(q_heads / kv_heads / 16) <= 2^22.
+ */
+size_t kda_attn_workspace_bytes(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                int32_t table_width, int32_t page_size);
+int kda_attn_decode(const kda_attn_args *args, void *stream, void *workspace, size_t workspace_bytes);
 
 /*
  * kda_device_errors -- the device error word of the current device: the OR of the

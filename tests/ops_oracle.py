@@ -112,3 +112,37 @@ def scan(u, delta, A, B, C, D, z, bias, lengths, init=None, use_softplus=True):
         ye = np.abs(gate) * (ye + (3 * np.abs(z) + 8) * np.abs(y))
         y = y * gate
     return y, ye, fin, fe
+
+
+def attention(q, k, v, table, lens, scale, kind):
+    """Attention of one token per sequence, lse, and bounds on their rounding errors (absolute, but for
+    the rounding of the output). A score: a product sum of Dh terms in fp32 and three roundings; a
+    probability: the score's error twice (its own and the sum's), exponential and arguments; its
+    split into two 16-bit parts leaves 2^-16 (bf16), or 2^-22 and an absolute 2^-25 (fp16, whose
+    small values are subnormal); sums over n tokens in fp32, 32 at a time and in pieces."""
+    B, hq, dh = q.shape
+    hkv, page = k.shape[2], k.shape[1]
+    out, oe = np.zeros((B, hq, dh)), np.zeros((B, hq, dh))
+    lse, le = np.full((B, hq), -np.inf), np.zeros((B, hq))
+    rel, sub = (2.0 ** -16, 0.0) if kind == "bf16" else (2.0 ** -22, 2.0 ** -25)
+    for b in range(B):
+        n = lens[b]
+        if n == 0:
+            continue
+        t = np.arange(n)
+        kk, vv = k[table[b, t // page], t % page], v[table[b, t // page], t % page]
+        for h in range(hq):
+            kh, vh = kk[:, h // (hq // hkv)], vv[:, h // (hq // hkv)]
+            s = scale * (kh @ q[b, h])
+            es = U * (dh + 4) * abs(scale) * (np.abs(kh) @ np.abs(q[b, h]))
+            m = s.max()
+            p = np.exp(s - m)
+            L = p.sum()
+            ep = 2 * es.max() + U * (4 * np.abs(s - m) + 2 * np.abs(s) + 8)
+            out[b, h] = p @ vh / L
+            size = (p[:, None] * np.abs(vh)).sum(0) / L
+            oe[b, h] = ((p * ep)[:, None] * np.abs(vh)).sum(0) / L + size * ((p * ep).sum() / L + rel + U * (n / 16 + 200)) \
+                + sub * np.abs(vh).sum(0) / L
+            lse[b, h] = m + np.log(L)
+            le[b, h] = (p * ep).sum() / L + U * (n / 16 + 200 + 4 * abs(lse[b, h]))
+    return out, oe, lse, le

@@ -261,3 +261,86 @@ def test_ssm_decode_abi_refusals(lib):
     state = T * Dn * Ns * 4
     assert dec(final_state=(16 << 20) + state - 4) == 7
     assert dec(out=2 << 20) == 7
+
+
+# ---------------------------------------------------------------- paged token attention
+def _attn(dt=torch.bfloat16):
+    return dict(q=torch.zeros(3, 8, 128, dtype=dt), k_cache=torch.zeros(10, 16, 2, 128, dtype=dt),
+                v_cache=torch.zeros(10, 16, 2, 128, dtype=dt), block_table=torch.zeros(3, 4, dtype=torch.int32),
+                seq_lens=torch.zeros(3, dtype=torch.int32))
+
+
+def test_attn_good_arguments():
+    from chunked_gated_delta_kda_amd.paged_attention import check_attn_decode_args
+    a = _attn()
+    assert check_attn_decode_args(**a) == (3, 8, 2, 128, 10, 16, 4)
+    joint = torch.zeros(10, 2, 2, 16, 128, dtype=torch.bfloat16)       # keys and values side by side, heads first
+    a.update(k_cache=joint[:, 0].transpose(1, 2), v_cache=joint[:, 1].transpose(1, 2))
+    assert check_attn_decode_args(**a)[2] == 2
+    a["block_table"] = torch.zeros(3, 9, dtype=torch.int32)[:, :4]
+    assert check_attn_decode_args(**a)[6] == 4
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("q", lambda: torch.zeros(3, 8, 128)),
+    ("q", lambda: torch.zeros(3, 8, 96, dtype=torch.bfloat16)),
+    ("q", lambda: torch.zeros(0, 8, 128, dtype=torch.bfloat16)),
+    ("q", lambda: torch.zeros(3, 7, 128, dtype=torch.bfloat16)),
+    ("q", lambda: torch.zeros(3, 8, 132, dtype=torch.bfloat16)[..., :128]),             # strides not multiples of 8
+    ("q", lambda: torch.zeros(3 * 8 * 128 + 1, dtype=torch.bfloat16)[1:].view(3, 8, 128)),  # base not aligned
+    ("k_cache", lambda: torch.zeros(10, 16, 2, 128, dtype=torch.float16)),
+    ("k_cache", lambda: torch.zeros(10, 16, 2, 64, dtype=torch.bfloat16)),
+    ("k_cache", lambda: torch.zeros(0, 16, 2, 128, dtype=torch.bfloat16)),
+    ("v_cache", lambda: torch.zeros(10, 8, 2, 128, dtype=torch.bfloat16)),
+    ("v_cache", lambda: torch.zeros(10, 16, 128, 2, dtype=torch.bfloat16).transpose(2, 3)),
+    ("block_table", lambda: torch.zeros(3, 4, dtype=torch.int64)),
+    ("block_table", lambda: torch.zeros(2, 4, dtype=torch.int32)),
+    ("block_table", lambda: torch.zeros(4, 3, dtype=torch.int32).t()),
+    ("block_table", lambda: torch.zeros(3, 0, dtype=torch.int32)),
+    ("seq_lens", lambda: torch.zeros(3, dtype=torch.int64)),
+    ("seq_lens", lambda: torch.zeros(4, dtype=torch.int32)),
+    ("scale", lambda: float("nan")),
+    ("out", lambda: torch.zeros(3, 8, 128)),
+    ("lse", lambda: torch.zeros(3, 8, dtype=torch.bfloat16)),
+])
+def test_attn_rejects(name, bad):
+    from chunked_gated_delta_kda_amd.paged_attention import check_attn_decode_args
+    a = _attn()
+    a[name] = bad()
+    with pytest.raises(ValueError, match=f"{name}:"):
+        check_attn_decode_args(**a)
+
+
+def test_attn_needs_device_tensors():
+    import chunked_gated_delta_kda_amd as kda
+    with pytest.raises(ValueError, match="device"):
+        kda.attn_decode(**_attn())
+
+
+def test_attn_abi_refusals(lib):
+    def call(ws=P, n=1 << 40, **over):
+        mb = 1 << 20
+        a = dict(q=mb, k_cache=16 * mb, v_cache=32 * mb, block_table=48 * mb, seq_lens=49 * mb, out=50 * mb, lse=None,
+                 q_stride=1024, q_head_stride=128, k_page_stride=4096, k_token_stride=256, k_head_stride=128,
+                 v_page_stride=4096, v_token_stride=256, v_head_stride=128, table_stride=4, num_seqs=3, q_heads=8, kv_heads=2,
+                 head_dim=128, num_pages=10, page_size=16, table_width=64, dtype=1, scale=0.1)
+        a["table_stride"] = 64
+        a.update(over)
+        return lib.kda_attn_decode(ctypes.byref(native.KdaAttnArgs(**a)), None, ws, n)
+
+    assert lib.kda_attn_decode(None, None, None, 0) == 1
+    for kw in (dict(dtype=0), dict(dtype=3), dict(head_dim=96), dict(scale=float("inf")), dict(k_token_stride=252),
+               dict(q_stride=1020), dict(q=(1 << 20) + 8), dict(v_cache=(32 << 20) + 2)):
+        assert call(**kw) == 3, kw
+    for kw in (dict(num_seqs=0), dict(q_heads=7), dict(kv_heads=0), dict(num_pages=0), dict(page_size=0), dict(table_width=0),
+               dict(table_stride=63), dict(k_head_stride=-8), dict(table_width=1 << 27, table_stride=1 << 27),
+               dict(num_seqs=1 << 22)):
+        assert call(**kw) == 2, kw
+    for name in ("q", "k_cache", "v_cache", "block_table", "seq_lens", "out"):
+        assert call(**{name: None}) == 1, name
+    for kw in (dict(out=1 << 20), dict(out=16 << 20), dict(lse=50 << 20), dict(lse=49 << 20), dict(out=48 << 20)):
+        assert call(**kw) == 7, kw
+    need = lib.kda_attn_workspace_bytes(3, 8, 2, 128, 64, 16)
+    assert need > 0 and call(n=need - 1) == 4
+    assert lib.kda_attn_workspace_bytes(3, 8, 2, 128, 1, 16) == 0        # one chunk each: none needed
+    assert lib.kda_attn_workspace_bytes(3, 7, 2, 128, 1, 16) == 0
