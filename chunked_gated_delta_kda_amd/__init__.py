@@ -1,6 +1,6 @@
 """MI355X-native Kimi Delta Attention (KDA) forward, and the operators a hybrid decoder runs
 beside it: the short causal convolution (``conv_fwd``, ``conv_bwd``, ``conv_decode``), the
-selective state space scan (``ssm_fwd``, ``ssm_decode``) and the attention of one new token over a
+selective state space scan (``ssm_fwd``, ``ssm_bwd``, ``ssm_decode``) and the attention of one new token over a
 paged key-value cache (``attn_decode``).
 
 ``fwd`` marshals torch tensors into the C ABI of libkda.so (include/kda.h).
@@ -14,11 +14,12 @@ import math
 from . import native
 
 __all__ = ["fwd", "fwd_noalloc", "bwd", "decode", "workspace_bytes", "select_variant", "device_errors", "version", "native",
-           "conv_fwd", "conv_bwd", "conv_decode", "ssm_fwd", "ssm_decode", "attn_decode"]
+           "conv_fwd", "conv_bwd", "conv_decode", "ssm_fwd", "ssm_bwd", "ssm_decode",
+           "attn_decode"]
 
 #: the operators beside the delta rule, by the module that is imported on first use (it needs torch)
 _OPERATORS = {"conv_fwd": "short_conv", "conv_bwd": "short_conv", "conv_decode": "short_conv",
-              "ssm_fwd": "scan", "ssm_decode": "scan", "attn_decode": "paged_attention"}
+              "ssm_fwd": "scan", "ssm_bwd": "scan", "ssm_decode": "scan", "attn_decode": "paged_attention"}
 
 
 def __getattr__(name):

@@ -229,6 +229,39 @@ int kda_ssm_decode(const kda_ssm_args *args, void *stream) {
     return launched(kda::ops::launch_ssm_decode(a, (hipStream_t)stream));
 }
 
+size_t kda_ssm_bwd_workspace_bytes(int32_t total_tokens, int32_t channels, int32_t state_size, int32_t groups) {
+    if (!ssm_sizes_ok(total_tokens, channels, state_size, groups)) return 0;
+    return kda::ops::ssm_bwd_workspace(total_tokens, channels, state_size, groups);
+}
+
+int kda_ssm_bwd(const kda_ssm_args *args, const kda_ssm_grads *grads, void *stream, void *workspace,
+                size_t workspace_bytes) {
+    if (!args || !grads) return KDA_ERR_NULL;
+    kda_ssm_args a = *args;
+    a.out = nullptr, a.final_state = nullptr;
+    const kda_ssm_grads &g = *grads;
+    if (const int rc = check_ssm(a, true)) return rc;
+    if (!a.cu_seqlens && a.num_seqs != 1) return KDA_ERR_SHAPE;
+    if (g.dy_stride < a.channels) return KDA_ERR_SHAPE;
+    if (!g.dA || (a.total_tokens > 0 && (!g.dy || !g.du || !g.ddelta || !g.dB || !g.dC || (a.z && !g.dz)))) return KDA_ERR_NULL;
+    const SsmSpans s(a);
+    const int64_t es = (int64_t)dtype_bytes(a.dtype), T = a.total_tokens, D = a.channels, N = a.state_size;
+    const Span dy = span(g.dy, rows_bytes(T, g.dy_stride, D, es)), dfin = span(g.d_final_state, s.state);
+    const Span out[] = {span(g.du, T * D * es), span(g.ddelta, T * D * es), span(g.dB, T * a.groups * N * es),
+                        span(g.dC, T * a.groups * N * es), span(a.z ? g.dz : nullptr, T * D * es), span(g.dA, D * N * 4),
+                        span(g.dD, D * 4), span(g.ddelta_bias, D * 4), span(g.d_initial_state, s.state)};
+    constexpr int outs = sizeof(out) / sizeof(out[0]);
+    for (int i = 0; i < outs; ++i) {
+        if (s.over(out[i]) || meet(dy, out[i]) || meet(dfin, out[i])) return KDA_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return KDA_ERR_ALIAS;
+    }
+    hipStream_t st = (hipStream_t)stream;
+    Workspace ws(workspace, workspace_bytes, kda::ops::ssm_bwd_workspace(T, D, N, a.groups), st);
+    if (ws.status() != KDA_OK) return ws.status();
+    return ws.finish(launched(kda::ops::launch_ssm_bwd(a, g, (float *)ws.ptr(), kda::device_error_word(), st)));
+}
+
 size_t kda_attn_workspace_bytes(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                 int32_t table_width, int32_t page_size) {
     if (check_attn_sizes(num_seqs, q_heads, kv_heads, head_dim, table_width, page_size) != KDA_OK) return 0;

@@ -22,6 +22,9 @@ hipError_t launch_conv_bwd(const kda_conv_args &a, const kda_conv_grads &g, floa
 size_t ssm_workspace(int64_t T, int64_t D, int64_t N, int64_t G);
 hipError_t launch_ssm_fwd(const kda_ssm_args &a, float *ws, int32_t *err, hipStream_t st);
 hipError_t launch_ssm_decode(const kda_ssm_args &a, hipStream_t st);
+// its gradients (ops_ssm_bwd.hip)
+size_t ssm_bwd_workspace(int64_t T, int64_t D, int64_t N, int64_t G);
+hipError_t launch_ssm_bwd(const kda_ssm_args &a, const kda_ssm_grads &g, float *ws, int32_t *err, hipStream_t st);
 
 // paged token attention (ops_attn.hip)
 size_t attn_workspace(int64_t B, int64_t hq, int64_t hkv, int64_t dh, int64_t width, int64_t page);

@@ -42,6 +42,7 @@ struct Place {
     int group;         // of B and C
     int ch;            // natural channel, clamped to the group's last
     bool mine;         // natural channel exists and this lane is the one that stores it
+    bool dup;          // natural channel lies past the group's last, which it repeats
     int base, last;    // first channel of the wave, last channel of the group
     int N;
     __device__ __forceinline__ Place(const kda_ssm_args &a, int block) {
@@ -54,7 +55,8 @@ struct Place {
         last = group * per + per - 1;
         const int want = base + 16 * (g % CB) + i;
         ch = want < last ? want : last;
-        mine = want <= last && g < CB;
+        dup = want > last;
+        mine = !dup && g < CB;
     }
     // state held by register 4 b + j of product m; channel of block b
     __device__ __forceinline__ int state(int m, int b, int j) const { return 16 * (b / CB + m * NB) + 4 * g + j; }

@@ -21,6 +21,7 @@ EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_noalloc", "kda_workspace_bytes", "k
            "kda_launch_plan", "kda_decode", "kda_decode_ex", "kda_bwd", "kda_bwd_workspace_bytes",
            "kda_conv_fwd", "kda_conv_decode", "kda_conv_bwd", "kda_conv_bwd_workspace_bytes",
            "kda_ssm_fwd", "kda_ssm_workspace_bytes", "kda_ssm_decode",
+           "kda_ssm_bwd", "kda_ssm_bwd_workspace_bytes",
            "kda_attn_decode", "kda_attn_workspace_bytes",
            "kda_device_errors", "kda_status_string", "kda_version")
 #: KDA_DEVERR_* bits of the device error word
@@ -71,6 +72,11 @@ class KdaSsmArgs(ctypes.Structure):
                 [(n, ctypes.c_int64) for n in ("u_stride", "delta_stride", "B_stride", "C_stride", "z_stride")] +
                 [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "channels", "state_size", "groups", "dtype",
                                                "delta_softplus")])
+
+
+class KdaSsmGrads(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dy", "d_final_state", "du", "ddelta", "dB", "dC", "dz", "dA", "dD",
+                                                "ddelta_bias", "d_initial_state")] + [("dy_stride", ctypes.c_int64)])
 
 
 class KdaAttnArgs(ctypes.Structure):
@@ -142,6 +148,10 @@ def load_library(path=LIB_PATH):
     lib.kda_ssm_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_ssm_decode.argtypes = [ctypes.POINTER(KdaSsmArgs), vp]
     lib.kda_ssm_decode.restype = ctypes.c_int
+    lib.kda_ssm_bwd.argtypes = [ctypes.POINTER(KdaSsmArgs), ctypes.POINTER(KdaSsmGrads), vp, vp, ctypes.c_size_t]
+    lib.kda_ssm_bwd.restype = ctypes.c_int
+    lib.kda_ssm_bwd_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.kda_ssm_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_attn_decode.argtypes = [ctypes.POINTER(KdaAttnArgs), vp, vp, ctypes.c_size_t]
     lib.kda_attn_decode.restype = ctypes.c_int
     lib.kda_attn_workspace_bytes.argtypes = [i32] * 6

@@ -1,4 +1,4 @@
-"""The selective state space scan: kda_ssm_fwd and kda_ssm_decode of include/kda.h."""
+"""The selective state space scan: kda_ssm_fwd, kda_ssm_decode and kda_ssm_bwd of include/kda.h."""
 import ctypes
 
 import torch
@@ -6,7 +6,7 @@ import torch
 from . import native
 from ._args import DTYPES, checked, dense, launch_on, offsets, on_device, ptr, rows, scratch
 
-__all__ = ["ssm_fwd", "ssm_decode"]
+__all__ = ["ssm_fwd", "ssm_bwd", "ssm_decode"]
 
 
 class _Sizes:
@@ -128,3 +128,41 @@ def ssm_decode(u, delta, A, B, C, D=None, z=None, delta_bias=None, state=None, *
         args = _args(s, u, delta, A, B, C, D, z, delta_bias, None, state, state_out, out, delta_softplus)
         native.check(lib.kda_ssm_decode(ctypes.byref(args), st))
     return out, state_out
+
+
+def check_ssm_bwd_args(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, cu_seqlens=None, initial_state=None,
+                       d_final_state=None):
+    """Every check ssm_bwd makes before anything is launched; returns the sizes it found and dy's row stride."""
+    s = _check(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state)
+    stride = rows("dy", dy, u.dtype, (s.T, s.D), u.device)
+    if d_final_state is not None:
+        dense("d_final_state", d_final_state, torch.float32, (s.S, s.D, s.N), u.device)
+    return s, stride
+
+
+def ssm_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, cu_seqlens=None, initial_state=None,
+            d_final_state=None, *, delta_softplus=True, need_d_initial_state=True, workspace=None, stream=None):
+    """Gradients of ssm_fwd: given dy = dL/d(out) ([T, D] of u's dtype, any row stride) and optionally
+    d_final_state = dL/d(final_state) (fp32 [S, D, N]), returns a dict of du, ddelta, dz ([T, D]), dB, dC
+    ([T, G, N]) of u's dtype, and fp32 dA ([D, N]), dD, ddelta_bias ([D]) and d_initial_state ([S, D, N], or None
+    when need_d_initial_state is False); dz, dD and ddelta_bias are None without z, D and delta_bias. Needs
+    nothing that the forward computed. The same results from run to run."""
+    lib = native.load_library()
+    dev = u.device
+    on_device("kda.ssm_bwd", dev)
+    s, dy_stride = check_ssm_bwd_args(u, delta, A, B, C, dy, D, z, delta_bias, cu_seqlens, initial_state, d_final_state)
+    f32 = dict(dtype=torch.float32, device=dev)
+    with launch_on(dev, stream) as st:
+        act = lambda *shape: torch.empty(shape, dtype=u.dtype, device=dev)  # noqa: E731
+        gr = dict(du=act(s.T, s.D), ddelta=act(s.T, s.D), dA=torch.empty((s.D, s.N), **f32), dB=act(s.T, s.G, s.N),
+                  dC=act(s.T, s.G, s.N), dD=torch.empty((s.D,), **f32) if D is not None else None,
+                  dz=act(s.T, s.D) if z is not None else None,
+                  ddelta_bias=torch.empty((s.D,), **f32) if delta_bias is not None else None,
+                  d_initial_state=torch.empty((s.S, s.D, s.N), **f32) if need_d_initial_state else None)
+        workspace, wp, wn = scratch(workspace, lib.kda_ssm_bwd_workspace_bytes(s.T, s.D, s.N, s.G), dev)
+        args = _args(s, u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, None, None, delta_softplus)
+        grads = native.KdaSsmGrads(ptr(dy), ptr(d_final_state), ptr(gr["du"]), ptr(gr["ddelta"]), ptr(gr["dB"]), ptr(gr["dC"]),
+                                   ptr(gr["dz"]), ptr(gr["dA"]), ptr(gr["dD"]), ptr(gr["ddelta_bias"]),
+                                   ptr(gr["d_initial_state"]), dy_stride)
+        native.check(lib.kda_ssm_bwd(ctypes.byref(args), ctypes.byref(grads), st, wp, wn))
+    return gr

@@ -410,6 +410,31 @@ int kda_ssm_fwd(const kda_ssm_args *args, void *stream, void *workspace, size_t 
  */
 int kda_ssm_decode(const kda_ssm_args *args, void *stream);
 
+typedef struct kda_ssm_grads {
+    const void *dy;           /* [total_tokens, channels] of args' dtype, rows dy_stride apart */
+    const float *d_final_state; /* fp32 [num_seqs, channels, state_size] or NULL (zeros)      */
+    void *du, *ddelta;        /* [total_tokens, channels] of args' dtype, contiguous          */
+    void *dB, *dC;            /* [total_tokens, groups, state_size] of args' dtype, contiguous */
+    void *dz;                 /* [total_tokens, channels] of args' dtype; required with z      */
+    float *dA;                /* fp32 [channels, state_size]                                  */
+    float *dD;                /* fp32 [channels] or NULL (not written)                        */
+    float *ddelta_bias;       /* fp32 [channels] or NULL (not written)                        */
+    float *d_initial_state;   /* fp32 [num_seqs, channels, state_size] or NULL (not written)  */
+    int64_t dy_stride;
+} kda_ssm_grads;
+
+/*
+ * kda_ssm_bwd -- gradients of kda_ssm_fwd with respect to every input, from dy, the gradient of
+ * out, and d_final_state (args->out and args->final_state are ignored). Needs nothing that
+ * the forward computed. Sums run in a fixed order: the same results from run to run. workspace:
+ * kda_ssm_bwd_workspace_bytes() bytes of device memory, or NULL: then the library allocates it
+ * stream-ordered on `stream`; it holds, above all, a state per channel for every 4 tokens (2 from
+ * state sizes over 64, 1 over 128).
+ */
+size_t kda_ssm_bwd_workspace_bytes(int32_t total_tokens, int32_t channels, int32_t state_size, int32_t groups);
+int kda_ssm_bwd(const kda_ssm_args *args, const kda_ssm_grads *grads, void *stream, void *workspace,
+                size_t workspace_bytes);
+
 typedef struct kda_attn_args {
     const void *q;            /* [num_seqs, q_heads, head_dim]                              */
     const void *k_cache;      /* [num_pages, page_size, kv_heads, head_dim], any strides      */

@@ -146,3 +146,84 @@ def attention(q, k, v, table, lens, scale, kind):
             lse[b, h] = m + np.log(L)
             le[b, h] = (p * ep).sum() / L + U * (n / 16 + 200 + 4 * abs(lse[b, h]))
     return out, oe, lse, le
+
+
+def scan_grads(u, delta, A, B, C, D, z, bias, lengths, init, use_softplus, dy, dfin):
+    """Gradients of the selective scan by the chain rule, token by token from the end, and beside each
+    a bound on its fp32 rounding errors in units of 2^-24, carried as in ``scan``: a product's error
+    is each factor's times the other's size; a sum adds a rounding per term to the terms' sizes."""
+    T, ch = u.shape
+    N, G = A.shape[1], B.shape[1]
+    per = ch // G
+    x = delta + (0.0 if bias is None else bias)
+    s = softplus(x) if use_softplus else x
+    sig = sigmoid(x) if use_softplus else np.ones_like(x)
+    rs = 3 * np.abs(x) + 12 if use_softplus else np.ones_like(x)
+    spread = lambda v: np.repeat(v, per, axis=0)  # noqa: E731
+    gather = lambda v: v.reshape(G, per, N).sum(1)  # noqa: E731
+    skip = np.zeros(ch) if D is None else D
+    z0 = np.zeros_like(u) if z is None else z
+    gate = z * sigmoid(z) if z is not None else np.ones_like(u)
+    rg = 3 * np.abs(z0) + 10                      # of the gate, relative
+    g = dy * gate
+    names = ("du", "ddelta", "dz", "dA", "dB", "dC", "dD", "ddelta_bias", "d_initial_state")
+    shapes = ((T, ch), (T, ch), (T, ch), (ch, N), (T, G, N), (T, G, N), (ch,), (ch,), (len(lengths), ch, N))
+    out = {n: np.zeros(sh) for n, sh in zip(names, shapes)}
+    err = {n: np.zeros(sh) for n, sh in zip(names, shapes)}
+    chsum = 20 + ch / G / 32                      # roundings of a sum over a group's channels
+    at = 0
+    for i, n in enumerate(lengths):
+        h = init[i].copy() if init is not None else np.zeros((ch, N))
+        size, e = np.abs(h), np.zeros((ch, N))
+        trail = []
+        for t in range(at, at + n):
+            a = np.exp(s[t][:, None] * A)
+            inp = (s[t] * u[t])[:, None] * spread(B[t])
+            dec = (rs[t][:, None] + 4) * np.abs(s[t][:, None] * A) + 7
+            ah, sah, eah = a * h, a * size, a * (e + size * dec)
+            h, size, e = ah + inp, sah + np.abs(inp), eah + (rs[t][:, None] + 3) * np.abs(inp)
+            trail.append((a, dec, ah, sah, eah, h, size, e))
+        dh = dfin[i].copy() if dfin is not None else np.zeros((ch, N))
+        ds, de = np.abs(dh), np.zeros((ch, N))
+        for t in range(at + n - 1, at - 1, -1):
+            a, dec, ah, sah, eah, h, size, e = trail[t - at]
+            Bt, Ct = spread(B[t]), spread(C[t])
+            gt = g[t][:, None]
+            dh, ds, de = dh + Ct * gt, ds + np.abs(Ct * gt), de + (rg[t][:, None] + 3) * np.abs(Ct * gt)
+            out["dC"][t] = gather(gt * h)
+            err["dC"][t] = gather(np.abs(gt) * (e + (rg[t][:, None] + chsum) * size))
+            su = (s[t] * u[t])[:, None]
+            out["dB"][t] = gather(dh * su)
+            err["dB"][t] = gather(np.abs(su) * (de + (rs[t][:, None] + chsum) * ds))
+            y = (Ct * h).sum(1) + skip * u[t]
+            ey = (np.abs(Ct) * (e + (N + 6) * size)).sum(1) + 3 * np.abs(skip * u[t])
+            if z is not None:
+                f = dy[t] * silu_grad(z[t])
+                sf = np.abs(dy[t]) * sigmoid(z[t]) * (1 + np.abs(z[t]))     # before its terms cancel
+                out["dz"][t], err["dz"][t] = f * y, np.abs(f) * ey + rg[t] * sf * np.abs(y)
+            into, si = (dh * Bt).sum(1), (ds * np.abs(Bt)).sum(1)
+            ei = (de * np.abs(Bt)).sum(1) + (N + 6) * si
+            out["du"][t] = s[t] * into + skip * g[t]
+            err["du"][t] = np.abs(s[t]) * (ei + (rs[t] + 2) * si) + (rg[t] + 3) * np.abs(skip * g[t])
+            q, sq = dh * ah, ds * sah
+            eq = de * sah + ds * eah
+            through = (q * A).sum(1) + u[t] * into
+            out["ddelta"][t] = through * sig[t]
+            sizes = (sq * np.abs(A)).sum(1) + np.abs(u[t]) * si
+            err["ddelta"][t] = sig[t] * ((np.abs(A) * (eq + (N + 8) * sq)).sum(1) + np.abs(u[t]) * ei
+                                         + (3 * np.abs(x[t]) + 12) * sizes)
+            out["dA"] += q * s[t][:, None]
+            err["dA"] += np.abs(s[t][:, None]) * (eq + (rs[t][:, None] + 4) * sq)
+            out["dD"] += g[t] * u[t]
+            err["dD"] += (rg[t] + 2) * np.abs(g[t] * u[t])
+            out["ddelta_bias"] += out["ddelta"][t]
+            err["ddelta_bias"] += err["ddelta"][t]
+            # sums over tokens: a rounding per token of a tile and per tile, of what they add up
+            many = T / 16 + 160
+            err["dA"] += many * np.abs(s[t][:, None]) * sq
+            err["dD"] += many * np.abs(g[t] * u[t])
+            err["ddelta_bias"] += many * sizes * sig[t]
+            dh, ds, de = dh * a, ds * a, a * (de + ds * dec)
+        out["d_initial_state"][i], err["d_initial_state"][i] = dh, de + ds
+        at += n
+    return out, err

@@ -211,3 +211,138 @@ def test_another_stream_and_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, ref) and torch.equal(f, fin)
+
+
+def grads_of(d, lengths, seed, kind, wide=1):
+    g = torch.Generator().manual_seed(seed)
+    T, D = d["u"].shape
+    return dict(dy=torch.randn(T, wide * D, generator=g).to(TYPES[kind]).cuda()[:, :D],
+                d_final_state=(0.2 * torch.randn(len(lengths), D, d["A"].shape[1], generator=g)).cuda())
+
+
+def compare_grads(got, d, g, lengths, kind, softplus=True):
+    ref, err = oo.scan_grads(*(np64(d[k]) for k in ("u", "delta", "A", "B", "C", "D", "z", "delta_bias")), lengths,
+                             np64(d["initial_state"]), softplus, np64(g["dy"]), np64(g["d_final_state"]))
+    for name in ("du", "ddelta", "dz", "dA", "dB", "dC", "dD", "ddelta_bias", "d_initial_state"):
+        of = dict(dz="z", dD="D", ddelta_bias="delta_bias").get(name)
+        if of and d[of] is None:
+            assert got[name] is None
+            continue
+        t = kind if name in ("du", "ddelta", "dz", "dB", "dC") else "fp32"
+        oo.check(name, np64(got[name]), ref[name], err[name] + 2 * np.abs(ref[name]), t, 1)
+
+
+@pytest.mark.parametrize("case", CASES, ids=ident)
+def test_gradients(case):
+    import chunked_gated_delta_kda_amd as kda
+
+    lengths, D, N, kind, groups, init, gate, wide, skip, bias = case
+    d = make(lengths, D, N, kind, 11, groups, init, gate, wide, skip, bias)
+    g = grads_of(d, lengths, 12, kind, wide)
+    got = kda.ssm_bwd(**d, **g)
+    compare_grads(got, d, g, lengths, kind)
+    again = kda.ssm_bwd(**d, **g)
+    assert all(torch.equal(got[k], again[k]) for k in got if got[k] is not None)
+
+
+def test_gradients_without_softplus_or_final_gradient():
+    import chunked_gated_delta_kda_amd as kda
+
+    lengths = [70, 9]
+    d = make(lengths, 40, 16, "fp32", 13)
+    d["delta"] = (d["delta"].abs() * 0.1).contiguous()
+    d["delta_bias"] = d["delta_bias"].abs() * 0.01
+    g = grads_of(d, lengths, 14, "fp32")
+    g["d_final_state"] = None
+    got = kda.ssm_bwd(**d, **g, delta_softplus=False, need_d_initial_state=False)
+    assert got["d_initial_state"] is None
+    got["d_initial_state"] = kda.ssm_bwd(**d, **g, delta_softplus=False)["d_initial_state"]
+    compare_grads(got, d, g, lengths, "fp32", False)
+
+
+def test_gradients_against_differences():
+    """Central differences of the forward in fp32 with a step of 1/32: the third derivative's h^2/6 and the
+    roundings of the loss (values of a few, over h) stay within 2e-2 of each input's largest gradient."""
+    import chunked_gated_delta_kda_amd as kda
+
+    lengths = [5, 1, 19]
+    d = make(lengths, 3, 5, "fp32", 15)
+    g = grads_of(d, lengths, 16, "fp32")
+    got = kda.ssm_bwd(**d, **g)
+    dyc, dfc = np64(g["dy"]), np64(g["d_final_state"])
+
+    def loss(e):
+        y, fin = kda.ssm_fwd(**e)
+        return float((np64(y) * dyc).sum() + (np64(fin) * dfc).sum())
+
+    for name, key in (("u", "du"), ("delta", "ddelta"), ("A", "dA"), ("B", "dB"), ("C", "dC"), ("D", "dD"), ("z", "dz"),
+                      ("delta_bias", "ddelta_bias"), ("initial_state", "d_initial_state")):
+        flat = d[name].contiguous().reshape(-1)
+        want = got[key].double().reshape(-1).cpu().numpy()
+        for i in range(0, flat.numel(), 1 + flat.numel() // 12):
+            side = []
+            for sign in (1, -1):
+                moved = flat.clone()
+                moved[i] += sign / 32
+                side.append(loss({**d, name: moved.reshape(d[name].shape)}))
+            assert abs((side[0] - side[1]) * 16 - want[i]) <= 2e-2 * max(1.0, np.abs(want).max()), (name, i)
+
+
+def test_gradients_stay_in_their_sequences():
+    import chunked_gated_delta_kda_amd as kda
+
+    lengths = [21, 13, 30]
+    d = make(lengths, 20, 16, "fp32", 17)
+    g = grads_of(d, lengths, 18, "fp32")
+    ref = kda.ssm_bwd(**d, **g)
+    for name in ("u", "B", "C", "delta", "z", "dy"):
+        e, f = dict(d), dict(g)
+        src = f if name == "dy" else e
+        src[name] = src[name].clone()
+        src[name][21:34] = float("nan")
+        got = kda.ssm_bwd(**e, **f)
+        for k in ("du", "ddelta", "dB", "dC", "dz"):
+            assert torch.equal(got[k][:21], ref[k][:21]) and torch.equal(got[k][34:], ref[k][34:]), (name, k)
+        assert torch.equal(got["d_initial_state"][::2], ref["d_initial_state"][::2]), name
+
+
+def test_gradients_on_a_stream_in_a_graph_and_within_their_buffers():
+    import chunked_gated_delta_kda_amd as kda
+
+    lengths = [70, 0, 3, 200]
+    d = make(lengths, 100, 16, "bf16", 19)
+    g = grads_of(d, lengths, 20, "bf16")
+    need = kda.native.load_library().kda_ssm_bwd_workspace_bytes(273, 100, 16, 1)
+    ws = torch.full((need + 512,), 7, dtype=torch.uint8, device="cuda")
+    ref = kda.ssm_bwd(**d, **g, workspace=ws[256:256 + need])
+    assert (ws[:256] == 7).all() and (ws[256 + need:] == 7).all()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = kda.ssm_bwd(**d, **g, stream=side)
+    side.synchronize()
+    assert all(torch.equal(got[k], ref[k]) for k in ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = kda.ssm_bwd(**d, **g)
+    for _ in range(3):
+        for t in got.values():
+            t.zero_()
+        e = make([50, 9], 64, 16, "bf16", 9)
+        kda.ssm_bwd(**e, **grads_of(e, [50, 9], 3, "bf16"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], ref[k]) for k in ref)
+
+
+def test_gradients_of_malformed_offsets_stay_in_bounds():
+    import chunked_gated_delta_kda_amd as kda
+
+    for T in (12, 64):
+        d = make([T // 2, T // 4, T - T // 2 - T // 4], 24, 16, "bf16", 21)
+        g = grads_of(d, [1, 1, 1], 22, "bf16")
+        for bad in ([0, T - 1, 3, T], [5, 6, 8, T], [0, 4, 6, T - 1], [0, -9, 900, T]):
+            d["cu_seqlens"] = torch.tensor(bad, dtype=torch.int32, device="cuda")
+            kda.device_errors()
+            kda.ssm_bwd(**d, **g)
+            assert kda.device_errors() == 2

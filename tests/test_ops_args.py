@@ -344,3 +344,40 @@ def test_attn_abi_refusals(lib):
     assert need > 0 and call(n=need - 1) == 4
     assert lib.kda_attn_workspace_bytes(3, 8, 2, 128, 1, 16) == 0        # one chunk each: none needed
     assert lib.kda_attn_workspace_bytes(3, 7, 2, 128, 1, 16) == 0
+
+
+def test_ssm_bwd_rejects():
+    from chunked_gated_delta_kda_amd.scan import check_ssm_bwd_args
+    import chunked_gated_delta_kda_amd as kda
+    a = _ssm()
+    dy = torch.zeros(T, 2 * Dn, dtype=torch.bfloat16)[:, :Dn]
+    s, stride = check_ssm_bwd_args(**a, dy=dy, d_final_state=torch.zeros(N, Dn, Ns))
+    assert (s.T, stride) == (T, 2 * Dn)
+    with pytest.raises(ValueError, match="dy"):
+        check_ssm_bwd_args(**a, dy=torch.zeros(T, Dn))
+    with pytest.raises(ValueError, match="d_final_state"):
+        check_ssm_bwd_args(**a, dy=dy, d_final_state=torch.zeros(N, Dn, Ns, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="device"):
+        kda.ssm_bwd(**a, dy=dy)
+
+
+def test_ssm_bwd_abi_refusals(lib):
+    def bwd(grads=(), ws=P, nbytes=0, **kw):
+        names = ("dy", "d_final_state", "du", "ddelta", "dB", "dC", "dz", "dA", "dD", "ddelta_bias", "d_initial_state")
+        g = {n: (32 + i) << 20 for i, n in enumerate(names)}
+        g["dy_stride"] = Dn
+        g.update(grads)
+        return lib.kda_ssm_bwd(ctypes.byref(ssm_args(**kw)), ctypes.byref(native.KdaSsmGrads(**g)), None, ws, nbytes)
+
+    assert lib.kda_ssm_bwd(None, None, None, None, 0) == 1
+    for g in (dict(dy=None), dict(du=None), dict(ddelta=None), dict(dB=None), dict(dC=None), dict(dz=None), dict(dA=None)):
+        assert bwd(g) == 1, g
+    assert bwd(dict(dy_stride=Dn - 1)) == 2 and bwd(num_seqs=2) == 2 and bwd(state_size=257) == 2
+    assert bwd(dtype=7) == 3
+    for g in (dict(du=1 << 20), dict(dA=3 << 20), dict(d_initial_state=16 << 20), dict(dB=36 << 20, dC=36 << 20),
+              dict(dz=32 << 20), dict(d_initial_state=33 << 20)):
+        assert bwd(g) == 7, g
+    need = lib.kda_ssm_bwd_workspace_bytes(T, Dn, Ns, G)
+    assert need > 0 and bwd(nbytes=need - 1) == 4
+    assert bwd(dict(dz=None), z=None, nbytes=need - 1) == 4       # no gate, no gradient of one
+    assert lib.kda_ssm_bwd_workspace_bytes(T, Dn, Ns, 5) == 0
