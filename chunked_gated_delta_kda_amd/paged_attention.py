@@ -15,45 +15,59 @@ HEAD_DIMS = (64, 128, 256)
 
 def _strides(t):
     """Strides but the last; those of dimensions of one entry do not matter."""
-    return [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride())]
+    shape, stride = t.shape, t.stride()
+    return [stride[i] if shape[i] > 1 else 0 for i in range(len(shape) - 1)]
 
 
 def _by8(name, t, dev):
-    """Rows read 16 bytes at a time: the last dimension contiguous, other strides multiples of 8."""
-    if t.device != dev or t.stride(-1) != 1 or any(s % 8 for s in _strides(t)) or t.data_ptr() % 16:
+    """Rows read 16 bytes at a time: the last dimension contiguous, other strides multiples of 8. Returns
+    those strides."""
+    strides = _strides(t)
+    off = 0
+    for s in strides:
+        off |= s
+    if off % 8 or t.stride(-1) != 1 or t.data_ptr() % 16 or t.device != dev:
         fail(name, t, "rows of contiguous elements, strides that are multiples of 8, a base aligned to 16 bytes", dev)
+    return strides
+
+
+def _check(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse):
+    dev, dt, shape = q.device, q.dtype, q.shape
+    if dt not in (torch.bfloat16, torch.float16) or len(shape) != 3 or shape[0] < 1:
+        raise ValueError(f"q: expected bf16 or fp16 [B, Hq, Dh], got {dt} {tuple(shape)}")
+    B, hq, dh = shape
+    if dh not in HEAD_DIMS:
+        raise ValueError(f"q: head dimension {dh}; expected one of {HEAD_DIMS}")
+    cache = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != dt or len(cache) != 4 or t.shape != cache or cache[3] != dh or min(cache) < 1:
+            raise ValueError(f"{name}: expected {dt} [pages, page size, Hkv, {dh}], one shape for both, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+    strides = _by8("q", q, dev) + _by8("k_cache", k_cache, dev) + _by8("v_cache", v_cache, dev)
+    pages, page, hkv, _ = cache
+    if hq % hkv:
+        raise ValueError(f"q: {hq} heads are not a multiple of the cache's {hkv}")
+    table = block_table.shape
+    if block_table.dtype != torch.int32 or len(table) != 2 or table[0] != B or table[1] < 1 or block_table.device != dev:
+        fail("block_table", block_table, f"int32 [{B}, pages of the longest]", dev)
+    rows, inner = block_table.stride()
+    if (table[1] > 1 and inner != 1) or (B > 1 and rows < table[1]):
+        fail("block_table", block_table, f"int32 [{B}, pages of the longest] with contiguous rows", dev)
+    strides.append(rows if B > 1 else table[1])
+    dense("seq_lens", seq_lens, torch.int32, (B,), dev)
+    if scale is not None and not math.isfinite(scale):
+        raise ValueError("scale: expected a finite number")
+    if out is not None:
+        dense("out", out, dt, (B, hq, dh), dev)
+    if lse is not None:
+        dense("lse", lse, torch.float32, (B, hq), dev)
+    return B, hq, hkv, dh, pages, page, table[1], strides
 
 
 def check_attn_decode_args(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None, lse=None):
     """Every check attn_decode makes before anything is launched; returns (B, Hq, Hkv, Dh, pages, page
     size, table width)."""
-    dev = q.device
-    if q.dtype not in (torch.bfloat16, torch.float16) or q.dim() != 3 or q.shape[0] < 1:
-        raise ValueError(f"q: expected bf16 or fp16 [B, Hq, Dh], got {q.dtype} {tuple(q.shape)}")
-    B, hq, dh = q.shape
-    if dh not in HEAD_DIMS:
-        raise ValueError(f"q: head dimension {dh}; expected one of {HEAD_DIMS}")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != q.dtype or t.dim() != 4 or t.shape != k_cache.shape or t.shape[3] != dh or min(t.shape) < 1:
-            raise ValueError(f"{name}: expected {q.dtype} [pages, page size, Hkv, {dh}], one shape for both, got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        _by8(name, t, dev)
-    _by8("q", q, dev)
-    pages, page, hkv, _ = k_cache.shape
-    if hq % hkv:
-        raise ValueError(f"q: {hq} heads are not a multiple of the cache's {hkv}")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1 \
-            or block_table.device != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1) \
-            or (B > 1 and block_table.stride(0) < block_table.shape[1]):
-        fail("block_table", block_table, f"int32 [{B}, pages of the longest] with contiguous rows", dev)
-    dense("seq_lens", seq_lens, torch.int32, (B,), dev)
-    if scale is not None and not math.isfinite(scale):
-        raise ValueError("scale: expected a finite number")
-    if out is not None:
-        dense("out", out, q.dtype, (B, hq, dh), dev)
-    if lse is not None:
-        dense("lse", lse, torch.float32, (B, hq), dev)
-    return B, hq, hkv, dh, pages, page, block_table.shape[1]
+    return _check(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse)[:7]
 
 
 def attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, *, return_lse=False, out=None, lse=None,
@@ -75,7 +89,7 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, *, retur
     lib = native.load_library()
     dev = q.device
     on_device("kda.attn_decode", dev)
-    B, hq, hkv, dh, pages, page, width = check_attn_decode_args(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse)
+    B, hq, hkv, dh, pages, page, width, strides = _check(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse)
     with launch_on(dev, stream) as st:
         if out is None:
             out = torch.empty((B, hq, dh), dtype=q.dtype, device=dev)
@@ -83,8 +97,7 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, *, retur
             lse = torch.empty((B, hq), dtype=torch.float32, device=dev)
         workspace, wp, wn = scratch(workspace, lib.kda_attn_workspace_bytes(B, hq, hkv, dh, width, page), dev)
         args = native.KdaAttnArgs(ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_table), ptr(seq_lens), ptr(out), ptr(lse),
-                                  *_strides(q), *_strides(k_cache), *_strides(v_cache),
-                                  max(block_table.stride(0), width), B, hq, hkv, dh, pages, page, width, DTYPES[q.dtype],
+                                  *strides, B, hq, hkv, dh, pages, page, width, DTYPES[q.dtype],
                                   1.0 / math.sqrt(dh) if scale is None else scale)
         call = lambda: native.check(lib.kda_attn_decode(ctypes.byref(args), st, wp, wn))  # noqa: E731
         checked(st, call) if check else call()
