@@ -93,6 +93,8 @@ int check_ssm(const kda_ssm_args &a, bool grads) {
     if (a.u_stride < a.channels || a.delta_stride < a.channels || a.B_stride < bc || a.C_stride < bc ||
         (a.z && a.z_stride < a.channels))
         return KDA_ERR_SHAPE;
+    for (const int64_t s : {a.u_stride, a.delta_stride, a.B_stride, a.C_stride, a.z ? a.z_stride : 0})
+        if (s > KDA_SSM_MAX_STRIDE) return KDA_ERR_SHAPE;
     if (!a.A || (a.total_tokens > 0 && (!a.u || !a.delta || !a.B || !a.C || (!grads && !a.out)))) return KDA_ERR_NULL;
     return KDA_OK;
 }
@@ -196,9 +198,10 @@ int kda_conv_bwd(const kda_conv_args *args, const kda_conv_grads *grads, void *s
     return ws.finish(launched(kda::ops::launch_conv_bwd(a, g, (float *)ws.ptr(), kda::device_error_word(), st)));
 }
 
-size_t kda_ssm_workspace_bytes(int32_t total_tokens, int32_t channels, int32_t state_size, int32_t groups) {
-    if (!ssm_sizes_ok(total_tokens, channels, state_size, groups)) return 0;
-    return kda::ops::ssm_workspace(total_tokens, channels, state_size, groups);
+size_t kda_ssm_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t channels, int32_t state_size,
+                               int32_t groups) {
+    if (num_seqs < 1 || !ssm_sizes_ok(total_tokens, channels, state_size, groups)) return 0;
+    return kda::ops::ssm_workspace(total_tokens, channels, state_size, groups, num_seqs);
 }
 
 int kda_ssm_fwd(const kda_ssm_args *args, void *stream, void *workspace, size_t workspace_bytes) {
@@ -211,7 +214,7 @@ int kda_ssm_fwd(const kda_ssm_args *args, void *stream, void *workspace, size_t 
     const Span fin = span(a.final_state, s.state);
     if (s.over(out) || s.over(fin) || meet(out, fin)) return KDA_ERR_ALIAS;
     hipStream_t st = (hipStream_t)stream;
-    Workspace ws(workspace, workspace_bytes, kda::ops::ssm_workspace(a.total_tokens, a.channels, a.state_size, a.groups), st);
+    Workspace ws(workspace, workspace_bytes, kda::ops::ssm_workspace(a.total_tokens, a.channels, a.state_size, a.groups, a.num_seqs), st);
     if (ws.status() != KDA_OK) return ws.status();
     return ws.finish(launched(kda::ops::launch_ssm_fwd(a, (float *)ws.ptr(), kda::device_error_word(), st)));
 }

@@ -108,5 +108,14 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+// Barrier of a block over its LDS traffic alone: unlike __syncthreads it does not wait for global
+// loads in flight, so what is loaded ahead stays in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_waitcnt(0xc07f);     // lgkmcnt(0), the others open
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 }  // namespace ops
 }  // namespace kda

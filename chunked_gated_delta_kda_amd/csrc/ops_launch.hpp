@@ -19,7 +19,7 @@ size_t conv_bwd_workspace(int64_t T, int64_t C, int W);
 hipError_t launch_conv_bwd(const kda_conv_args &a, const kda_conv_grads &g, float *ws, int32_t *err, hipStream_t st);
 
 // selective state space scan (ops_ssm.hip)
-size_t ssm_workspace(int64_t T, int64_t D, int64_t N, int64_t G);
+size_t ssm_workspace(int64_t T, int64_t D, int64_t N, int64_t G, int64_t S);
 hipError_t launch_ssm_fwd(const kda_ssm_args &a, float *ws, int32_t *err, hipStream_t st);
 hipError_t launch_ssm_decode(const kda_ssm_args &a, hipStream_t st);
 // its gradients (ops_ssm_bwd.hip)

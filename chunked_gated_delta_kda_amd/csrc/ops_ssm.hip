@@ -1,17 +1,22 @@
 // ops_ssm.hip -- the selective state space scan: prompts (over a packed batch) and one token of
 // each sequence. The mathematics and the register layout are in ops_ssm.hpp.
 //
-// Prompts. The time axis is cut into tiles of consecutive packed tokens, whatever sequences start
-// or end in them, so that few channels still fill the card:
+// Prompts go one of two ways (by_blocks): in one launch, a block of waves per 16 channels walking the
+// tokens (ssm_scan_kernel), or by waves. Then the time axis is cut into tiles of consecutive packed
+// tokens, whatever sequences start or end in them, so that few channels still fill the card:
 //   1. ssm_tile_kernel: each tile from a zero state: its end state E and the sum S of its
 //      step sizes, so that the tile maps a state h to e^{A S} h + E (to E alone where a sequence
 //      starts in it);
 //   2. ssm_join_kernel: those maps one after another per (channel, state): the state each tile
 //      starts from, in E's place;
-//   3. ssm_scan_kernel: the scan itself, from that state.
-// One tile needs the last step only. Bound by vector issue: a (token, channel, state) costs two
-// multiplications, an exponential and the product with C, and steps 1 and 3 both pay the first
-// three.
+//   3. ssm_wide_kernel: the scan itself, from that state.
+// Bound by vector issue: a (token, channel, state) costs two multiplications, an exponential and the
+// product with C, and steps 1 and 3 both pay the first three.
+#include <atomic>
+#include <cmath>
+#include <type_traits>
+
+#include "kda_launch.hpp"
 #include "ops_ssm.hpp"
 
 namespace kda {
@@ -19,24 +24,30 @@ namespace ops {
 namespace ssm {
 namespace {
 
+constexpr int K_TILE = 8, K_SCAN = 4;   // tokens a wave stages at a time
+
 // K tokens' activations of a wave, one element a lane, in flight while the tokens before are
 // computed.
-template <int DT, int CB, int M, bool OUT> struct Raw {
+template <int DT, int K, int M, bool OUT> struct Raw {
     using E = typename Elem<DT>::type;
     E delta[K], u[K], z[K], B[K][M], C[K][M];
+    template <int CB>
     __device__ __forceinline__ void load(const kda_ssm_args &a, const Place<CB, M> &p, int t, int stop) {
+        const uint32_t ch = (uint32_t)p.ch * sizeof(E);
+        const char *u0 = (const char *)a.u, *d0 = (const char *)a.delta, *z0 = (const char *)a.z;
+        const char *B0 = (const char *)a.B + (int64_t)p.group * p.N * sizeof(E), *C0 = (const char *)a.C + (int64_t)p.group * p.N * sizeof(E);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t r = t + k < stop ? t + k : stop - 1;   // past the end: the last row again
-            delta[k] = reinterpret_cast<const E *>(a.delta)[r * a.delta_stride + p.ch];
-            u[k] = reinterpret_cast<const E *>(a.u)[r * a.u_stride + p.ch];
-            if (OUT && a.z) z[k] = reinterpret_cast<const E *>(a.z)[r * a.z_stride + p.ch];
+            const int64_t r = (int64_t)(t + k < stop ? t + k : stop - 1) * sizeof(E);   // past the end: the last row again
+            delta[k] = at<DT>(d0 + r * a.delta_stride, ch);
+            u[k] = at<DT>(u0 + r * a.u_stride, ch);
+            if (OUT && a.z) z[k] = at<DT>(z0 + r * a.z_stride, ch);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const int n = p.nat_state(m);
-                const int64_t at = (int64_t)p.group * p.N + n;
-                B[k][m] = n < p.N ? reinterpret_cast<const E *>(a.B)[r * a.B_stride + at] : (E)0.0f;
-                if (OUT) C[k][m] = n < p.N ? reinterpret_cast<const E *>(a.C)[r * a.C_stride + at] : (E)0.0f;
+                const uint32_t st = (uint32_t)(n < p.N ? n : p.N - 1) * sizeof(E);
+                B[k][m] = at<DT>(B0 + r * a.B_stride, st);
+                if (OUT) C[k][m] = at<DT>(C0 + r * a.C_stride, st);
             }
         }
     }
@@ -58,6 +69,7 @@ __device__ __forceinline__ void advance(f32x16 (&h)[M], const f32x16 (&A2)[M], c
 template <int DT, int CB, int M>
 __global__ __launch_bounds__(64 * WAVES) void ssm_tile_kernel(const kda_ssm_args a, float *ws, float *sums, int32_t *resets,
                                                               int32_t *err, int L, int tiles, int blocks) {
+    constexpr int K = K_TILE;
     __shared__ __align__(16) float lds[WAVES][K * 16 * CB];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t unit = (int64_t)blockIdx.x * WAVES + wave;
@@ -80,21 +92,22 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_tile_kernel(const kda_ssm_args
     float sum = 0.0f;
     float *steps = lds[wave];
     int t = reset ? start : t0;
-    Raw<DT, CB, M, false> raw;
+    Raw<DT, K, M, false> raw;
     raw.load(a, p, t, t1);
     while (t < t1) {
-        float s[K], x[K], B[K][M];
+        float x[K], B[K][M];
+        const int count = t1 - t;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const float d = (float)raw.delta[k] + bias;
-            s[k] = a.delta_softplus ? softplus_f(d) : d;
-            x[k] = s[k] * (float)raw.u[k];
-            const bool step = t + k < t1;
-            if (step) sum += s[k];
-            else s[k] = 0.0f, x[k] = 0.0f;      // no step: e^0 h + 0 (B too: what is repeated may be infinite)
-            steps[k * 16 * CB + CB * p.i + p.g % CB] = s[k];
+            float s = a.delta_softplus ? softplus_f(d) : d;
+            x[k] = s * (float)raw.u[k];
+            const bool step = k < count;
+            s = step ? s : 0.0f, x[k] = step ? x[k] : 0.0f;    // no step: e^0 h + 0 (B too: what is repeated may be infinite)
+            sum += s;
+            steps[k * 16 * CB + CB * p.i + p.g % CB] = s;
 #pragma unroll
-            for (int m = 0; m < M; ++m) B[k][m] = step ? (float)raw.B[k][m] : 0.0f;
+            for (int m = 0; m < M; ++m) B[k][m] = step && p.nat_state(m) < p.N ? (float)raw.B[k][m] : 0.0f;
         }
         wave_fence();
         t += K;
@@ -152,10 +165,13 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const kda_ssm_args a, flo
     }
 }
 
+// The scan for state sizes over 32 and for short sequences: a wave by itself, all states of its channels
+// in its registers, from the joined states of its tile.
 template <int DT, int CB, int M>
-__global__ __launch_bounds__(64 * WAVES) void ssm_scan_kernel(const kda_ssm_args a, const float *ws, int32_t *err, int L,
+__global__ __launch_bounds__(64 * WAVES) void ssm_wide_kernel(const kda_ssm_args a, const float *ws, int32_t *err, int L,
                                                               int tiles, int blocks) {
     using E = typename Elem<DT>::type;
+    constexpr int K = K_SCAN;
     constexpr int NS = 64 / CB * M;            // states of a staged C row
     __shared__ __align__(16) float lds[WAVES][K * (16 * CB + NS)];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -182,27 +198,28 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_scan_kernel(const kda_ssm_args
     } else load_state<CB, M>(a.initial_state, n, a, p, h);
     const float bias = a.delta_bias ? a.delta_bias[p.ch] : 0.0f, skip = a.D ? a.D[p.ch] : 0.0f;
     float *steps = lds[wave], *rows = lds[wave] + K * 16 * CB;
+    const bool every = __all(!p.dup);          // lanes of one channel store the same
+    const uint32_t ch = (uint32_t)p.ch * sizeof(E);
     int t = t0;
-    Raw<DT, CB, M, true> raw;
+    Raw<DT, K, M, true> raw;
     raw.load(a, p, t, t1);
-    while (true) {
-        // one sequence's tokens of this tile, or what of them fits a stage
-        const int stop = end < t1 ? end : t1;
-        float s[K], x[K], u[K], z[K], B[K][M], y[K];
-        const int count = stop - t < K ? stop - t : K;
+    // `count` tokens of one sequence
+    auto stage = [&](int count, auto whole) {
+        float x[K], u[K], z[K], B[K][M], y[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            const bool on = whole || k < count;     // the next sequence's rows stay out of this state
             const float d = (float)raw.delta[k] + bias;
-            s[k] = a.delta_softplus ? softplus_f(d) : d;
+            const float s = a.delta_softplus ? softplus_f(d) : d;
             u[k] = (float)raw.u[k];
-            x[k] = s[k] * u[k];
-            if (k >= count) s[k] = 0.0f, x[k] = 0.0f;
+            x[k] = on ? s * u[k] : 0.0f;
             z[k] = a.z ? (float)raw.z[k] : 0.0f;
-            steps[k * 16 * CB + CB * p.i + p.g % CB] = s[k];
+            steps[k * 16 * CB + CB * p.i + p.g % CB] = on ? s : 0.0f;
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                B[k][m] = k < count ? (float)raw.B[k][m] : 0.0f;   // the next sequence's rows stay out of this state
-                rows[k * NS + p.nat_state(m)] = (float)raw.C[k][m];
+                const bool in = p.nat_state(m) < p.N;
+                B[k][m] = on && in ? (float)raw.B[k][m] : 0.0f;
+                rows[k * NS + p.nat_state(m)] = in ? (float)raw.C[k][m] : 0.0f;
             }
         }
         wave_fence();
@@ -229,21 +246,287 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_scan_kernel(const kda_ssm_args
             y[k] = to_natural<CB>(r);
         }
         wave_fence();
+        char *out = (char *)a.out + (int64_t)from * a.channels * sizeof(E);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float v = __builtin_fmaf(skip, u[k], y[k]);
             if (a.z) v *= z[k] * sigmoid_f(z[k]);
-            if (k < count && p.mine) reinterpret_cast<E *>(a.out)[(int64_t)(from + k) * a.channels + p.ch] = (E)v;
+            if (whole || (k < count && p.mine)) *reinterpret_cast<E *>(out + (int64_t)k * a.channels * sizeof(E) + ch) = (E)v;
         }
-        if (t < end) {
-            if (t < t1) continue;
-            break;
+    };
+    while (true) {
+        const int stop = end < t1 ? end : t1;
+        if (every)
+            while (stop - t >= K) stage(K, std::true_type{});
+        if (t < stop) {
+            stage(stop - t < K ? stop - t : K, std::false_type{});
+            if (t < stop) continue;
         }
+        if (t < end) break;             // the sequence goes on in the next tile
         store_state<CB, M>(a.final_state, n, a, p, h);
         for (++n; n < a.num_seqs && off.at(n + 1) <= t; ++n) pass_state<CB, M>(a.final_state, a.initial_state, n, a, p);
         if (t >= t1 || n >= a.num_seqs) break;
         end = off.at(n + 1);
         load_state<CB, M>(a.initial_state, n, a, p, h);
+    }
+}
+
+// The scan in one launch, for state sizes up to 32 where the channels alone fill the card or the batch is
+// short (by_blocks): a block of W = 12 waves owns 16 channels and walks all tokens in steps of up to W KT of
+// one sequence, each wave KT of them. The exponential of a (token, channel, state) is formed once and
+// one pass over the inputs is enough. Per step:
+//   1. a wave forms its tokens' decays and inputs, kept in registers, and runs them from a zero
+//      state: E; with P = e^{A sum s} that is the wave's map h -> P h + E;
+//   2. the block's first threads, one per (channel, state), run the state through the W maps in LDS,
+//      leaving each wave's input state there, while every wave stages its tokens of the next step;
+//   3. a wave runs its tokens again from its input state, for y.
+// NB: 16-state blocks. The four blocks of a product are TP = 4/NB tokens by NB blocks of states; product
+// q holds tokens TP q + b / NB, states 16 (b % NB) + 4 g + j, channel i.
+template <int NB> struct Scan {
+    static constexpr int W = 12, KT = 8 / NB, TP = 4 / NB, Q = 2;   // waves, tokens of a wave, of a product, products
+    static constexpr int NS = 16 * NB, PAIRS = 256 * NB, SROW = KT + 4, STEP = W * KT;
+};
+template <int NB> struct ScanLds {
+    using S = Scan<NB>;
+    float E[S::W][S::PAIRS], P[S::W][S::PAIRS], h[S::W][S::PAIRS];
+    float steps[S::W][16 * S::SROW], C[S::W][2][S::KT * S::NS];
+};
+
+// From one value per token of a product (sums over j) to the lane that carries the token: TP q + g / NB.
+template <int TP> __device__ __forceinline__ float token_lane(const float (&r)[TP]) {
+    if constexpr (TP == 4) return swap16_add(swap32_add(r[0], r[2]), swap32_add(r[1], r[3]));
+    else {
+        const float s = swap32_add(r[0], r[TP - 1]);
+        return swap16_add(s, s);
+    }
+}
+
+// A step: its first token, how many, and the sequence they belong to.
+struct Step {
+    int t, count, n, end;
+    template <int STEP> __device__ __forceinline__ void size(int T) {
+        const int stop = end < T ? end : T;
+        count = stop - t < STEP ? stop - t : STEP;
+    }
+    // the step after this one
+    template <int STEP> __device__ __forceinline__ Step next(const Offsets &off, int T) const {
+        Step s{t + count, 0, n, end};
+        if (s.t == s.end && s.t < T) {
+            for (++s.n; s.n < off.N - 1 && off.at(s.n + 1) <= s.t; ++s.n) {}
+            s.end = off.at(s.n + 1);
+        }
+        s.template size<STEP>(T);
+        return s;
+    }
+};
+
+template <int DT, int NB>
+__global__ __launch_bounds__(64 * Scan<NB>::W) void ssm_scan_kernel(const kda_ssm_args a, int32_t *err, int blocks, int xcds) {
+    using E = typename Elem<DT>::type;
+    using Z = Scan<NB>;
+    constexpr int KT = Z::KT, TP = Z::TP, Q = Z::Q, NS = Z::NS, SROW = Z::SROW, W = Z::W, STEP = Z::STEP;
+    constexpr uint32_t es = sizeof(E);
+    extern __shared__ __align__(16) char lds_raw[];
+    ScanLds<NB> &lds = *reinterpret_cast<ScanLds<NB> *>(lds_raw);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    // Blocks go to the XCDs in turn: neighbouring channels (of one memory line) to one XCD.
+    const int id = blockIdx.x, block = xcds > 1 ? (id % xcds) * (blocks / xcds) + id / xcds : id;
+    const Offsets off{a.cu_seqlens, a.num_seqs, a.total_tokens};
+    if (id == 0) check_offsets(off, err, threadIdx.x, 64 * W);
+    const int N = a.state_size, per = a.channels / a.groups, pb = (per + 15) / 16;
+    const int group = block / pb, base = group * per + (block - group * pb) * 16, last = group * per + per - 1;
+    const int c = base + i, cc = c <= last ? c : last;
+    const int T = a.total_tokens;
+
+    // The block's state, one (channel, state) a thread: pair 4 lane + j of state block b, as E and P lie.
+    const int op = threadIdx.x & 255, ob = threadIdx.x >> 8;
+    const int oc = base + ((op >> 2) & 15), on = 16 * ob + 4 * (op >> 6) + (op & 3);
+    const bool owner = threadIdx.x < Z::PAIRS, holds = owner && oc <= last && on < N;
+    const int64_t own_at = (int64_t)oc * N + on, own_step = (int64_t)a.channels * N;
+    auto first_state = [&](int seq) { return holds && a.initial_state ? a.initial_state[seq * own_step + own_at] : 0.0f; };
+    auto last_state = [&](int seq, float h) {
+        if (holds && a.final_state) a.final_state[seq * own_step + own_at] = h;
+    };
+    if (T == 0) {
+        for (int q = 0; q < a.num_seqs; ++q) last_state(q, first_state(q));
+        return;
+    }
+    Step cur{0, 0, off.find(0), 0};
+    cur.end = off.at(cur.n + 1);
+    cur.size<STEP>(T);
+    float state = first_state(cur.n);
+    for (int q = 0; q < cur.n; ++q) last_state(q, first_state(q));
+
+    float A2[NB][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = 16 * b + 4 * g + j;
+            A2[b][j] = c <= last && n < N ? a.A[(int64_t)c * N + n] * LOG2E_F : 0.0f;
+        }
+    const float bias = a.delta_bias ? a.delta_bias[cc] : 0.0f, skip = a.D ? a.D[cc] : 0.0f;
+    // A lane's place in a product's rows: its token of the product, its channel and its state.
+    const int nat_st = 16 * (g % NB) + i, tl = g / NB;
+    const bool state_in = nat_st < N;
+    const uint32_t ch = (uint32_t)cc * es, st = (uint32_t)(state_in ? nat_st : N - 1) * es;
+    const uint32_t od = (uint32_t)(tl * a.delta_stride) * es + ch, ou = (uint32_t)(tl * a.u_stride) * es + ch;
+    const uint32_t oz = (uint32_t)(tl * a.z_stride) * es + ch, oo = (uint32_t)(tl * a.channels) * es + ch;
+    const uint32_t oB = (uint32_t)(tl * a.B_stride) * es + st, oC = (uint32_t)(tl * a.C_stride) * es + st;
+    const char *const u0 = (const char *)a.u, *const d0 = (const char *)a.delta, *const z0 = (const char *)a.z;
+    const char *const B0 = (const char *)a.B + (int64_t)group * N * es, *const C0 = (const char *)a.C + (int64_t)group * N * es;
+    const bool has_z = a.z != nullptr;
+    E rdelta[Q], ru[Q], rz[Q], rB[Q], rC[Q];
+    auto load = [&](const Step &s) {
+        const int t = s.t + w * KT;
+        if (t + KT <= T) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int64_t r = (int64_t)(t + TP * q) * es;
+                rdelta[q] = at<DT>(d0 + r * a.delta_stride, od);
+                ru[q] = at<DT>(u0 + r * a.u_stride, ou);
+                if (has_z) rz[q] = at<DT>(z0 + r * a.z_stride, oz);
+                rB[q] = at<DT>(B0 + r * a.B_stride, oB);
+                rC[q] = at<DT>(C0 + r * a.C_stride, oC);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {     // rows past the batch's end: its last one again
+                const int tq = t + TP * q + tl;
+                const int64_t r = (int64_t)(tq < T ? tq : T - 1) * es;
+                rdelta[q] = at<DT>(d0 + r * a.delta_stride, ch);
+                ru[q] = at<DT>(u0 + r * a.u_stride, ch);
+                if (has_z) rz[q] = at<DT>(z0 + r * a.z_stride, ch);
+                rB[q] = at<DT>(B0 + r * a.B_stride, st);
+                rC[q] = at<DT>(C0 + r * a.C_stride, st);
+            }
+        }
+    };
+    float u[Q], gate[Q], x[Q], Bq[Q];
+    auto stage = [&](const Step &sp, int turn) {
+        const int left = sp.count - w * KT;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int k = TP * q + tl;
+            const bool is = k < left;         // past the step's end: no step, nothing in (B too: what lies there may be infinite)
+            const float d = (float)rdelta[q] + bias;
+            float s = a.delta_softplus ? softplus_f(d) : d;
+            s = is ? s : 0.0f;
+            u[q] = is ? (float)ru[q] : 0.0f;
+            x[q] = s * u[q];
+            gate[q] = has_z ? (float)rz[q] * sigmoid_f((float)rz[q]) : 1.0f;
+            Bq[q] = is && state_in ? (float)rB[q] : 0.0f;
+            lds.steps[w][i * SROW + k] = s;
+            lds.C[w][turn][k * NS + nat_st] = state_in ? (float)rC[q] : 0.0f;
+        }
+        wave_fence();
+    };
+    load(cur);
+    stage(cur, 0);
+    Step nxt = cur.next<STEP>(off, T);
+    if (nxt.t < T) load(nxt);
+    for (int turn = 0;; turn ^= 1) {
+        float step[KT], e[KT][NB][4], in_[KT][NB][4], sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KT; k += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(&lds.steps[w][i * SROW + k]);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) step[k + b] = v[b];
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            f32x16 zero;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
+            const f32x16 v = __builtin_amdgcn_mfma_f32_16x16x1f32(Bq[q], x[q], zero, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int k = TP * q + (r / 4) / NB, b = (r / 4) % NB, j = r % 4;
+                in_[k][b][j] = v[r];
+                e[k][b][j] = exp2_f(A2[b][j] * step[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KT; ++k) sum += step[k];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            f32x4 ve, vp;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ve[j] = in_[0][b][j];
+#pragma unroll
+                for (int k = 1; k < KT; ++k) ve[j] = __builtin_fmaf(e[k][b][j], ve[j], in_[k][b][j]);
+                vp[j] = exp2_f(A2[b][j] * sum);
+            }
+            *reinterpret_cast<f32x4 *>(&lds.E[w][256 * b + 4 * lane]) = ve;
+            *reinterpret_cast<f32x4 *>(&lds.P[w][256 * b + 4 * lane]) = vp;
+        }
+        float uc[Q], gc[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) uc[q] = u[q], gc[q] = gate[q];
+        lds_barrier();
+        const bool more = nxt.t < T;
+        if (owner) {
+#pragma unroll
+            for (int v0 = 0; v0 < W; v0 += 4) {
+                float me[4], mp[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) me[v] = lds.E[v0 + v][threadIdx.x], mp[v] = lds.P[v0 + v][threadIdx.x];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    lds.h[v0 + v][threadIdx.x] = state;
+                    state = __builtin_fmaf(mp[v], state, me[v]);
+                }
+            }
+        }
+        if (cur.t + cur.count == cur.end) {      // the sequence's last token; empty ones may follow, and the next one begins
+            last_state(cur.n, state);
+            for (int q = cur.n + 1; q < a.num_seqs && off.at(q + 1) <= cur.end; ++q) last_state(q, first_state(q));
+            if (more) state = first_state(nxt.n);
+        }
+        Step after = nxt;
+        if (more) {
+            stage(nxt, turn ^ 1);
+            after = nxt.next<STEP>(off, T);
+            if (after.t < T) load(after);
+        }
+        lds_barrier();
+        float own[NB][4], y[Q];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(&lds.h[w][256 * b + 4 * lane]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) own[b][j] = v[j];
+        }
+        const float *Cr = lds.C[w][turn];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            float r[TP];
+#pragma unroll
+            for (int b0 = 0; b0 < TP; ++b0) {
+                const int k = TP * q + b0;
+                r[b0] = 0.0f;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const f32x4 c4 = *reinterpret_cast<const f32x4 *>(Cr + k * NS + 16 * b + 4 * g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        own[b][j] = __builtin_fmaf(e[k][b][j], own[b][j], in_[k][b][j]);
+                        r[b0] = __builtin_fmaf(c4[j], own[b][j], r[b0]);
+                    }
+                }
+            }
+            y[q] = token_lane<TP>(r);
+        }
+        const int left = c <= last ? cur.count - w * KT : 0;
+        char *out = (char *)a.out + (int64_t)(cur.t + w * KT) * a.channels * es;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const float v = __builtin_fmaf(skip, uc[q], y[q]) * gc[q];
+            if (TP * q + tl < left) *reinterpret_cast<E *>(out + (int64_t)(TP * q) * a.channels * es + oo) = (E)v;
+        }
+        if (!more) break;
+        cur = nxt, nxt = after;
     }
 }
 
@@ -311,33 +594,59 @@ __global__ __launch_bounds__(256) void ssm_decode_kernel(const kda_ssm_args a) {
 }
 
 // ------------------------------------------------------------------------------ launches
+// Whether the scan by blocks takes a batch. Its blocks of 16 channels run one to a CU, ceil(blocks / 256)
+// rounds of 32 ns a token; the scan by waves costs 35 ns a token and 256 blocks' channels, spread over the card
+// at any count, and 12 us for its three launches and joined states. A step of a block is one sequence's:
+// sequences that are short on average go to the waves. Measured (us, blocks | waves): 8192 x 4096 x 16 275 | 290,
+// 65536 x 1024 x 16 2030 | 535, 256 x 256 x 16 9 | 17 (bf16, gate).
+bool by_blocks(int64_t T, int64_t S, int64_t D, int64_t N, int64_t G) {
+    if (N > 32 || T < 64 * S) return false;
+    const double blocks = (double)(G * ceil_div(D / G, 16));
+    return std::ceil(blocks / 256.0) * (double)T * 0.032 <= blocks / 256.0 * (double)T * 0.035 + 12.0;
+}
+
 template <int DT, int CB, int M>
-hipError_t fwd_form(const kda_ssm_args &a, float *ws, int32_t *err, hipStream_t st) {
-    const Form f{CB, M};
-    const int64_t T = a.total_tokens, blocks = blocks_of(f, a.channels, a.groups);
-    const int L = tile_len(T, blocks);
-    const int64_t tiles = T ? ceil_div(T, L) : 1, units = tiles * blocks;
-    const dim3 grid((unsigned)ceil_div(units, WAVES));
-    if (tiles > 1) {
-        float *sums = ws + units * 1024 * M;
-        int32_t *resets = (int32_t *)(sums + tiles * a.channels);
-        ssm_tile_kernel<DT, CB, M><<<grid, 64 * WAVES, 0, st>>>(a, ws, sums, resets, err, L, (int)tiles, (int)blocks);
-        if (hipError_t e = hipGetLastError()) return e;
-        ssm_join_kernel<CB, M><<<dim3((unsigned)ceil_div(blocks * 16 * M, 4)), 256, 0, st>>>(a, ws, sums, resets, (int)tiles,
+hipError_t join_tiles(const kda_ssm_args &a, float *ws, int32_t *err, int L, int64_t tiles, int64_t blocks, hipStream_t st) {
+    const int64_t units = tiles * blocks;
+    float *sums = ws + units * 1024 * M;
+    int32_t *resets = (int32_t *)(sums + tiles * a.channels);
+    ssm_tile_kernel<DT, CB, M><<<dim3((unsigned)ceil_div(units, WAVES)), 64 * WAVES, 0, st>>>(a, ws, sums, resets, err, L, (int)tiles,
                                                                                              (int)blocks);
-        if (hipError_t e = hipGetLastError()) return e;
-    }
-    ssm_scan_kernel<DT, CB, M><<<grid, 64 * WAVES, 0, st>>>(a, ws, err, L, (int)tiles, (int)blocks);
+    if (hipError_t e = hipGetLastError()) return e;
+    ssm_join_kernel<CB, M><<<dim3((unsigned)ceil_div(blocks * 16 * M, 4)), 256, 0, st>>>(a, ws, sums, resets, (int)tiles, (int)blocks);
+    return hipGetLastError();
+}
+
+template <int DT, int NB> hipError_t fwd_block(const kda_ssm_args &a, int32_t *err, hipStream_t st) {
+    const int64_t blocks = a.groups * ceil_div(a.channels / a.groups, 16);
+    static std::atomic<uint64_t> done;
+    constexpr int bytes = (int)sizeof(ScanLds<NB>);
+    if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void *>(ssm_scan_kernel<DT, NB>), bytes, done)) return e;
+    ssm_scan_kernel<DT, NB><<<dim3((unsigned)blocks), 64 * Scan<NB>::W, bytes, st>>>(a, err, (int)blocks, blocks % 8 == 0 ? 8 : 1);
+    return hipGetLastError();
+}
+
+template <int DT, int CB, int M>
+hipError_t fwd_wide(const kda_ssm_args &a, float *ws, int32_t *err, hipStream_t st) {
+    const int64_t T = a.total_tokens, blocks = blocks_of(Form{CB, M}, a.channels, a.groups);
+    const int L = tile_len(T, blocks);
+    const int64_t tiles = T ? ceil_div(T, L) : 1;
+    if (tiles > 1)
+        if (hipError_t e = join_tiles<DT, CB, M>(a, ws, err, L, tiles, blocks, st)) return e;
+    ssm_wide_kernel<DT, CB, M><<<dim3((unsigned)ceil_div(tiles * blocks, WAVES)), 64 * WAVES, 0, st>>>(a, ws, err, L, (int)tiles,
+                                                                                                      (int)blocks);
     return hipGetLastError();
 }
 
 template <int DT> hipError_t fwd_dt(const kda_ssm_args &a, float *ws, int32_t *err, hipStream_t st) {
     const Form f = form_of(a.state_size);
-    if (f.cb == 4) return fwd_form<DT, 4, 1>(a, ws, err, st);
-    if (f.cb == 2) return fwd_form<DT, 2, 1>(a, ws, err, st);
-    if (f.m == 1) return fwd_form<DT, 1, 1>(a, ws, err, st);
-    if (f.m == 2) return fwd_form<DT, 1, 2>(a, ws, err, st);
-    return fwd_form<DT, 1, 4>(a, ws, err, st);
+    if (by_blocks(a.total_tokens, a.num_seqs, a.channels, a.state_size, a.groups))
+        return f.cb == 4 ? fwd_block<DT, 1>(a, err, st) : fwd_block<DT, 2>(a, err, st);
+    if (f.cb == 4) return fwd_wide<DT, 4, 1>(a, ws, err, st);
+    if (f.cb == 2) return fwd_wide<DT, 2, 1>(a, ws, err, st);
+    if (f.m == 1) return fwd_wide<DT, 1, 1>(a, ws, err, st);
+    if (f.m == 2) return fwd_wide<DT, 1, 2>(a, ws, err, st);
+    return fwd_wide<DT, 1, 4>(a, ws, err, st);
 }
 
 template <int DT, int NL> hipError_t decode_nl(const kda_ssm_args &a, hipStream_t st) {
@@ -365,16 +674,18 @@ template <int DT> hipError_t decode_dt(const kda_ssm_args &a, hipStream_t st) {
 int tile_len(int64_t T, int64_t blocks) {
     int64_t L = T * blocks / 4096;
     L = L < 16 ? 16 : L > T ? T : L;
-    return (int)((L + K - 1) / K * K);
+    return (int)((L + 7) / 8 * 8);
 }
 
 }  // namespace ssm
 
-size_t ssm_workspace(int64_t T, int64_t D, int64_t N, int64_t G) {
+size_t ssm_workspace(int64_t T, int64_t D, int64_t N, int64_t G, int64_t S) {
     using namespace ssm;
     const Form f = form_of((int)N);
-    const int64_t blocks = blocks_of(f, D, G), tiles = T ? ceil_div(T, tile_len(T, blocks)) : 1;
-    return tiles > 1 ? (size_t)(tiles * blocks * 1024 * f.m + tiles * D + tiles) * 4 : 0;
+    const int64_t blocks = blocks_of(f, D, G);
+    const int64_t tiles = T ? ceil_div(T, tile_len(T, blocks)) : 1;
+    if (tiles <= 1 || by_blocks(T, S, D, N, G)) return 0;
+    return (size_t)(tiles * blocks * 1024 * f.m + tiles * D + tiles) * 4;
 }
 
 hipError_t launch_ssm_fwd(const kda_ssm_args &a, float *ws, int32_t *err, hipStream_t st) {

@@ -26,8 +26,12 @@ namespace kda {
 namespace ops {
 namespace ssm {
 
-constexpr int K = 8;          // tokens staged at a time
 constexpr int WAVES = 4;      // independent waves of a block
+
+// One element of a row, from the row's uniform address and the lane's own offset in bytes.
+template <int DT> __device__ __forceinline__ typename Elem<DT>::type at(const char *row, uint32_t bytes) {
+    return *reinterpret_cast<const typename Elem<DT>::type *>(row + bytes);
+}
 
 template <int DT> __device__ __forceinline__ float load1(const void *p, int64_t off) {
     return (float)reinterpret_cast<const typename Elem<DT>::type *>(p)[off];

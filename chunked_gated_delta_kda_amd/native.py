@@ -144,7 +144,7 @@ def load_library(path=LIB_PATH):
     lib.kda_conv_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_ssm_fwd.argtypes = [ctypes.POINTER(KdaSsmArgs), vp, vp, ctypes.c_size_t]
     lib.kda_ssm_fwd.restype = ctypes.c_int
-    lib.kda_ssm_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.kda_ssm_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     lib.kda_ssm_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_ssm_decode.argtypes = [ctypes.POINTER(KdaSsmArgs), vp]
     lib.kda_ssm_decode.restype = ctypes.c_int

@@ -88,7 +88,7 @@ def ssm_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_seqlens=None,
             final_state = None
         elif final_state is None:
             final_state = torch.empty((s.S, s.D, s.N), dtype=torch.float32, device=dev)
-        workspace, wp, wn = scratch(workspace, lib.kda_ssm_workspace_bytes(s.T, s.D, s.N, s.G), dev)
+        workspace, wp, wn = scratch(workspace, lib.kda_ssm_workspace_bytes(s.S, s.T, s.D, s.N, s.G), dev)
         args = _args(s, u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, final_state, out, delta_softplus)
         call = lambda: native.check(lib.kda_ssm_fwd(ctypes.byref(args), st, wp, wn))  # noqa: E731
         checked(st, call) if check else call()

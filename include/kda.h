@@ -362,8 +362,9 @@ size_t kda_conv_bwd_workspace_bytes(int32_t total_tokens, int32_t channels, int3
 int kda_conv_bwd(const kda_conv_args *args, const kda_conv_grads *grads, void *stream, void *workspace,
                  size_t workspace_bytes);
 
-/* Largest state size of the scan. */
+/* Largest state size and row stride (elements) of the scan. */
 #define KDA_SSM_MAX_STATE 256
+#define KDA_SSM_MAX_STRIDE (1 << 27)
 
 typedef struct kda_ssm_args {
     const void *u;            /* [total_tokens, channels], rows u_stride apart              */
@@ -400,7 +401,8 @@ typedef struct kda_ssm_args {
  * same results from run to run. Limits: total_tokens <= 2^27, channels <= 2^20,
  * num_seqs * channels <= 2^31. final_state must not overlap initial_state.
  */
-size_t kda_ssm_workspace_bytes(int32_t total_tokens, int32_t channels, int32_t state_size, int32_t groups);
+size_t kda_ssm_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t channels, int32_t state_size,
+                               int32_t groups);
 int kda_ssm_fwd(const kda_ssm_args *args, void *stream, void *workspace, size_t workspace_bytes);
 
 /*

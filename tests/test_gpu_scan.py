@@ -70,6 +70,10 @@ CASES = [
     ([60], 32, 16, "fp32", 1, True, True, 1, False, False),
     ([0, 0], 20, 16, "bf16", 1, True, True, 1, True, True),
     ([1200, 1, 700, 0, 99], 1030, 16, "bf16", 1, True, True, 2, True, True),
+    ([700, 0, 200, 97], 70, 30, "fp32", 2, True, True, 1, True, True),
+    ([96, 192, 1, 0, 95, 400], 33, 16, "bf16", 1, True, True, 1, True, True),
+    ([3] * 40, 50, 16, "fp32", 1, True, True, 1, True, True),
+    ([2] * 30 + [50], 36, 25, "bf16", 3, True, True, 2, True, True),
 ]
 
 
@@ -167,11 +171,12 @@ def test_prompt_then_tokens_is_the_whole():
 def test_nothing_is_written_beside_the_outputs():
     import chunked_gated_delta_kda_amd as kda
 
-    lengths, D, N = [9, 0, 30], 50, 13
+    lengths, D, N = [9, 0, 30], 50, 50      # over 32 states: tiles joined in the workspace
     d = make(lengths, D, N, "bf16", 6)
     out = torch.full((41, D), 7.0, dtype=torch.bfloat16, device="cuda")
     fin = torch.full((5, D, N), 7.0, device="cuda")
-    need = kda.native.load_library().kda_ssm_workspace_bytes(39, D, N, 1)
+    need = kda.native.load_library().kda_ssm_workspace_bytes(3, 39, D, N, 1)
+    assert need > 0
     ws = torch.full((need + 512,), 7, dtype=torch.uint8, device="cuda")
     kda.ssm_fwd(**d, out=out[1:40], final_state=fin[1:4], workspace=ws[256:256 + need])
     for t in (out[0], out[40], fin[0], fin[4], ws[:256], ws[256 + need:]):

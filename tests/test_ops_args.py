@@ -241,17 +241,20 @@ def test_ssm_abi_refusals(lib):
         assert fwd(**kw) == 3, kw
     for kw in (dict(num_seqs=0), dict(num_seqs=2), dict(total_tokens=-1), dict(channels=0), dict(state_size=0),
                dict(state_size=257), dict(groups=5), dict(groups=0), dict(u_stride=Dn - 1), dict(B_stride=G * Ns - 1),
-               dict(z_stride=0), dict(total_tokens=(1 << 27) + 1)):
+               dict(z_stride=0), dict(total_tokens=(1 << 27) + 1), dict(C_stride=(1 << 27) + 1)):
         assert fwd(**kw) == 2, kw
     for kw in (dict(u=None), dict(delta=None), dict(A=None), dict(B=None), dict(C=None), dict(out=None)):
         assert fwd(**kw) == 1, kw
     for kw in (dict(out=1 << 20), dict(out=7 << 20), dict(final_state=16 << 20), dict(final_state=3 << 20),
                dict(final_state=18 << 20)):
         assert fwd(**kw) == 7, kw
-    need = lib.kda_ssm_workspace_bytes(T, Dn, Ns, G)
-    assert need > 0 and fwd(n=need - 1) == 4
-    assert lib.kda_ssm_workspace_bytes(16, Dn, Ns, G) == 0            # one tile needs none
-    assert lib.kda_ssm_workspace_bytes(T, Dn, Ns, 5) == 0             # not a valid shape
+    long = 1 << 20
+    need = lib.kda_ssm_workspace_bytes(1, long, Dn, Ns, G)
+    far = {n: (i + 1) << 40 for i, n in enumerate(("u", "delta", "B", "C", "z", "out"))}
+    assert need > 0 and fwd(n=need - 1, total_tokens=long, **far) == 4
+    assert lib.kda_ssm_workspace_bytes(1, 16, Dn, Ns, G) == 0         # one launch needs none
+    assert lib.kda_ssm_workspace_bytes(1, T, Dn, Ns, 5) == 0          # not a valid shape
+    assert lib.kda_ssm_workspace_bytes(0, T, Dn, Ns, G) == 0
 
 
 def test_ssm_decode_abi_refusals(lib):
