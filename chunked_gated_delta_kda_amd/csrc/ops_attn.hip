@@ -148,7 +148,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
     using E = typename O::E;
     constexpr int KD = DH / 32;      // 32-element steps of a score
     constexpr int DV = DH / 16;      // elements of a lane in O^T's operand rows
-    __shared__ Rows rows[WAVES];
+    __shared__ Rows rows[WAVES][2];
     __shared__ float join[WAVES][16 * (DH + 4)];
     __shared__ float stat[WAVES][16][2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -182,38 +182,44 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
     const int32_t *table = a.block_table + (int64_t)seq * a.table_stride;
     const E *kc = (const E *)a.k_cache + (int64_t)kvh * a.k_head_stride;
     const E *vc = (const E *)a.v_cache + (int64_t)kvh * a.v_head_stride;
-    Rows &R = rows[wave];
+    Rows *const R = rows[wave];
     bool bad = false;
 
-    for (int t0 = begin + wave * TILE; t0 < end; t0 += ROUND) {
-        // every lane one token (the upper half of the wave repeats the lower): its page, checked
-        const int t = t0 + (lane & 31);
-        const int tc = t < end ? t : end - 1;
-        const int pg = tc / a.page_size, at = tc - pg * a.page_size;
-        int page = table[pg];
+    u32x4 kr[2][KD];
+    uint32_t vr[8][DV / 2];
+    // Page numbers are fetched two tiles ahead, a tile's rows are placed one tile ahead; its keys are
+    // loaded once the scores before them have used theirs, its values likewise: the registers that a
+    // tile leaves carry the loads of the next.
+    auto page_of = [&](int t0) {
+        const int t = t0 + (lane & 31), tc = t < end ? t : end - 1;
+        return table[tc / a.page_size];
+    };
+    // every lane one token (the upper half of the wave repeats the lower): its page, checked
+    auto place = [&](int t0, int page, int turn) {
+        const int t = t0 + (lane & 31), tc = t < end ? t : end - 1;
+        const int at = tc - tc / a.page_size * a.page_size;
         bool there = t < end;
-        if (page < 0 || page >= a.num_pages) {
-            bad = true, there = false;
-            page = 0;
-        }
-        if (lane < 32) R.k[lane] = (int64_t)page * a.k_page_stride + (int64_t)at * a.k_token_stride;
-        else R.v[lane - 32] = (int64_t)page * a.v_page_stride + (int64_t)at * a.v_token_stride;
-        const uint32_t seen = (uint32_t)__ballot(there);
+        if (page < 0 || page >= a.num_pages) bad = true, there = false, page = 0;
+        if (lane < 32) R[turn].k[lane] = (int64_t)page * a.k_page_stride + (int64_t)at * a.k_token_stride;
+        else R[turn].v[lane - 32] = (int64_t)page * a.v_page_stride + (int64_t)at * a.v_token_stride;
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        u32x4 kr[2][KD];
+        return (uint32_t)__ballot(there);
+    };
+    auto load_k = [&](int turn) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const E *row = kc + R.k[16 * h + i] + 8 * g;
+            const E *row = kc + R[turn].k[16 * h + i] + 8 * g;
 #pragma unroll
             for (int k = 0; k < KD; ++k) kr[h][k] = *reinterpret_cast<const u32x4 *>(row + 32 * k);
         }
-        uint32_t vr[8][DV / 2];
+    };
+    auto load_v = [&](int turn) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
             const int tok = (s < 4 ? 0 : 12) + 4 * g + s;
-            const E *row = vc + R.v[tok] + DV * i;
+            const E *row = vc + R[turn].v[tok] + DV * i;
             if constexpr (DV == 4) {
                 const uint2 x = *reinterpret_cast<const uint2 *>(row);
                 vr[s][0] = x.x, vr[s][1] = x.y;
@@ -226,11 +232,28 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
                 }
             }
         }
+    };
+    int t0 = begin + wave * TILE, turn = 0, ahead = 0;
+    uint32_t seen = 0;
+    if (t0 < end) {
+        seen = place(t0, page_of(t0), 0);
+        load_k(0);
+        load_v(0);
+        if (t0 + ROUND < end) ahead = page_of(t0 + ROUND);
+    }
+    for (; t0 < end; t0 += ROUND, turn ^= 1) {
+        const bool more = t0 + ROUND < end;
+        uint32_t then = 0;
+        if (more) {
+            then = place(t0 + ROUND, ahead, turn ^ 1);
+            if (t0 + 2 * ROUND < end) ahead = page_of(t0 + 2 * ROUND);
+        }
         f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int k = 0; k < KD; ++k)
 #pragma unroll
             for (int h = 0; h < 2; ++h) st[h] = O::mma(kr[h][k], q[k], st[h]);
+        if (more) load_k(turn ^ 1);
         // this lane's tokens: 4 g + j and 16 + 4 g + j
         float sc[8], top = NEG_INF;
         const uint32_t mine = (seen >> (4 * g)) & 0xf000f;
@@ -283,7 +306,8 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
             acc[2 * e] = O::mma(even, lo, acc[2 * e]);
             acc[2 * e + 1] = O::mma(odd, lo, acc[2 * e + 1]);
         }
-        __builtin_amdgcn_wave_barrier();
+        if (more) load_v(turn ^ 1);
+        seen = then;
     }
     if (err && __any(bad) && lane == 0) atomicOr(err, KDA_DEVERR_PAGES);
     l = column_sum(l);
@@ -330,12 +354,19 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
     }
 }
 
-// Joins the chunks of one (sequence, head), in their order, where there are several.
-template <int DT>
+// Joins the chunks of one (sequence, head), in their order, where there are several: threads take four
+// elements each, groups of threads every GROUPS-th chunk.
+#ifndef SPREAD
+#define SPREAD 1024
+#endif
+constexpr int MAX_SPREAD = 1024;
+template <int DT, int DH>
 __global__ __launch_bounds__(256) void attn_join_kernel(const kda_attn_args a, const float *acc, const float *ml, int spread,
                                                         int min_chunk) {
     using E = typename Ops<DT>::E;
-    __shared__ float part[256];
+    constexpr int LANES = DH / 4, GROUPS = 256 / LANES;
+    __shared__ float weight[MAX_SPREAD];
+    __shared__ f32x4 part[256];
     const int s = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63;
     int64_t total = 0;
     for (int q = lane; q < a.num_seqs; q += 64) total += seq_len(a, q);
@@ -347,23 +378,34 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const kda_attn_args a, c
     first = wave_sum64(first);
     const float *st = ml + (first * a.q_heads + h) * 2;
     const int64_t step = (int64_t)a.q_heads * 2;
-    float M = NEG_INF;
+    float M = NEG_INF, L = 0.0f;
     for (int p = lane; p < parts; p += 64) M = __builtin_fmaxf(M, st[p * step]);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) M = __builtin_fmaxf(M, __shfl_xor(M, d));
     const float ref = M == NEG_INF ? 0.0f : M;
-    const int dh = a.head_dim, lanes = dh < 256 ? dh : 256, groups = 256 / lanes;
-    const int grp = threadIdx.x / lanes, d = threadIdx.x - grp * lanes;
-    float o = 0.0f, L = 0.0f;
-    for (int p = 0; p < parts; ++p) L += st[p * step + 1] * exp2_f(st[p * step] - ref);
-    if (grp < groups)
-        for (int p = grp; p < parts; p += groups)
-            o += acc[((first + p) * a.q_heads + h) * dh + d] * exp2_f(st[p * step] - ref);
+    for (int p = lane; p < parts; p += 64) {       // every wave the whole sum, the first one the weights
+        const float w = exp2_f(st[p * step] - ref);
+        if (threadIdx.x < 64) weight[p] = w;
+        L += st[p * step + 1] * w;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) L += __shfl_xor(L, d);
+    __syncthreads();
+    const int grp = threadIdx.x / LANES, x = threadIdx.x % LANES;
+    const f32x4 *from = reinterpret_cast<const f32x4 *>(acc + (first * a.q_heads + h) * DH) + x;
+    const int64_t row = (int64_t)a.q_heads * LANES;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int p = grp; p < parts; p += GROUPS) o += from[p * row] * weight[p];
     part[threadIdx.x] = o;
     __syncthreads();
-    if (threadIdx.x < dh) {
-        for (int q = 1; q < groups; ++q) o += part[q * lanes + d];
-        reinterpret_cast<E *>(a.out)[((int64_t)s * a.q_heads + h) * dh + d] = (E)(L == 0.0f ? 0.0f : o / L);
+    if (threadIdx.x < LANES) {
+#pragma unroll
+        for (int q = 1; q < GROUPS; ++q) o += part[q * LANES + x];
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        E *to = reinterpret_cast<E *>(a.out) + ((int64_t)s * a.q_heads + h) * DH + 4 * x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = (E)(o[e] * inv);
     }
     if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)s * a.q_heads + h] = L == 0.0f ? NEG_INF : (ref + __builtin_log2f(L)) * LN2_F;
 }
@@ -380,7 +422,7 @@ Plan plan(int64_t B, int64_t hq, int64_t hkv, int64_t width, int64_t page) {
     const int64_t per = hkv * p.tiles_h;
     p.min_chunk = 2 * ROUND;
     const int64_t most = width * page;
-    int64_t spread = ceil_div(1024, per);
+    const int64_t spread = ceil_div(SPREAD, per);
     p.spread = (int)spread;
     p.join = most > p.min_chunk;
     // sum of ceil(len / chunk) <= spread + B, and no sequence has more than its table allows
@@ -394,7 +436,7 @@ hipError_t run(const kda_attn_args &a, const Plan &p, float *acc, float *ml, int
     const int64_t blocks = (int64_t)p.slots * a.kv_heads * p.tiles_h;
     attn_chunk_kernel<DT, DH><<<dim3((unsigned)blocks), 64 * WAVES, 0, st>>>(a, acc, ml, err, p.spread, p.min_chunk, p.tiles_h);
     if (hipError_t e = hipGetLastError()) return e;
-    if (p.join) attn_join_kernel<DT><<<dim3((unsigned)a.num_seqs, (unsigned)a.q_heads), 256, 0, st>>>(a, acc, ml, p.spread, p.min_chunk);
+    if (p.join) attn_join_kernel<DT, DH><<<dim3((unsigned)a.num_seqs, (unsigned)a.q_heads), 256, 0, st>>>(a, acc, ml, p.spread, p.min_chunk);
     return hipGetLastError();
 }
 
