@@ -89,8 +89,9 @@ __device__ __forceinline__ int64_t wave_sum64(int64_t x) {
 }
 
 struct Work {
-    int seq, part, parts, slot;   // slot: index of the chunk among all chunks
-    int begin, end;               // its tokens
+    int seq, slot;        // slot: where the chunk's partial result lies
+    bool whole;           // the sequence's only chunk
+    int begin, end;       // its tokens
 };
 
 // Tokens of a chunk: all tokens over `spread` chunks, whole rounds, at least min_chunk.
@@ -99,40 +100,46 @@ __device__ __forceinline__ int chunk_len(int64_t total, int spread, int min_chun
     const int64_t r = (c + ROUND - 1) / ROUND * ROUND;
     return r < min_chunk ? min_chunk : (int)(r < (1 << 30) ? r : 1 << 30);
 }
-__device__ __forceinline__ int parts_of(int len, int chunk) { return len > chunk ? (len + chunk - 1) / chunk : 1; }
+// A sequence's full chunks; what is left (or all of a sequence without any) is one chunk more.
+__device__ __forceinline__ int full_of(int len, int chunk) { return len / chunk; }
+__device__ __forceinline__ bool rest_of(int len, int chunk) { return len % chunk != 0 || len == 0; }
 
-// The chunk of index `slot`, found by every wave for itself; false past the last.
+// The chunk of index `slot`, found by every wave for itself; false past the last. Indexes count the full
+// chunks of all sequences in order, then the rests: blocks start in that order, the short ones last.
 __device__ __forceinline__ bool find_work(const kda_attn_args &a, int slot, int spread, int min_chunk, Work &w) {
     const int lane = threadIdx.x & 63;
     int64_t total = 0;
     for (int s = lane; s < a.num_seqs; s += 64) total += seq_len(a, s);
     const int chunk = chunk_len(wave_sum64(total), spread, min_chunk);
+    w.slot = slot;
     int before = 0;
-    for (int s0 = 0; s0 < a.num_seqs; s0 += 64) {
-        const int s = s0 + lane;
-        const int len = s < a.num_seqs ? seq_len(a, s) : 0;
-        const int mine = s < a.num_seqs ? parts_of(len, chunk) : 0;
-        int upto = mine;      // inclusive sum over lanes
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass)
+        for (int s0 = 0; s0 < a.num_seqs; s0 += 64) {
+            const int s = s0 + lane;
+            const int len = s < a.num_seqs ? seq_len(a, s) : 0;
+            const int full = full_of(len, chunk);
+            const int mine = s >= a.num_seqs ? 0 : pass == 0 ? full : rest_of(len, chunk);
+            int upto = mine;      // inclusive sum over lanes
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int v = __shfl_up(upto, d);
-            if (lane >= d) upto += v;
+            for (int d = 1; d < 64; d *= 2) {
+                const int v = __shfl_up(upto, d);
+                if (lane >= d) upto += v;
+            }
+            const int all = __shfl(upto, 63);
+            if (slot < before + all) {
+                const uint64_t at = __ballot(before + upto > slot);
+                const int l = __builtin_ctzll(at);
+                const int n = __shfl(len, l), f = __shfl(full, l);
+                const int part = pass == 0 ? slot - (before + __shfl(upto, l) - f) : f;
+                w.seq = s0 + l;
+                w.whole = f + (rest_of(n, chunk) ? 1 : 0) == 1;
+                w.begin = part * chunk;
+                w.end = pass == 0 ? w.begin + chunk : n;
+                return true;
+            }
+            before += all;
         }
-        const int all = __shfl(upto, 63);
-        if (slot < before + all) {
-            const uint64_t at = __ballot(before + upto > slot);
-            const int l = __builtin_ctzll(at);
-            w.seq = s0 + l;
-            w.parts = __shfl(mine, l);
-            w.part = slot - (before + __shfl(upto, l) - w.parts);
-            w.slot = slot;
-            const int n = __shfl(len, l);
-            w.begin = w.part * chunk;
-            w.end = w.parts == 1 || n - w.begin < chunk ? n : w.begin + chunk;
-            return true;
-        }
-        before += all;
-    }
     return false;
 }
 
@@ -153,13 +160,17 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
     __shared__ float stat[WAVES][16][2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
     const int per = a.kv_heads * tiles_h;
+#ifdef SLOTFAST
+    const int slots = gridDim.x / per, rest = blockIdx.x / slots, slot = blockIdx.x - rest * slots;
+#else
     const int slot = blockIdx.x / per, rest = blockIdx.x - slot * per;
+#endif
     const int kvh = rest / tiles_h, ht = rest - kvh * tiles_h;
     Work w;
     if (!find_work(a, slot, spread, min_chunk, w)) return;
     const int seq = __builtin_amdgcn_readfirstlane(w.seq);
     const int begin = __builtin_amdgcn_readfirstlane(w.begin), end = __builtin_amdgcn_readfirstlane(w.end);
-    if (err && w.part == 0 && rest == 0 && threadIdx.x == 0) {
+    if (err && w.begin == 0 && rest == 0 && threadIdx.x == 0) {
         const int n = a.seq_lens[seq];
         if (n < 0 || n > (int64_t)a.table_width * a.page_size) atomicOr(err, KDA_DEVERR_PAGES);
     }
@@ -328,7 +339,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
 #pragma unroll
         for (int d = 0; d < DV; ++d) join[wave][i * (DH + 4) + DV * (4 * g + j) + d] = acc[d][j] * f;
     __syncthreads();
-    const bool whole = w.parts == 1;
+    const bool whole = w.whole;
     for (int x = threadIdx.x; x < heads * DH; x += 64 * WAVES) {
         const int h = x / DH, d = x - h * DH;
         float o = 0.0f;
@@ -356,47 +367,58 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
 
 // Joins the chunks of one (sequence, head), in their order, where there are several: threads take four
 // elements each, groups of threads every GROUPS-th chunk.
-#ifndef SPREAD
-#define SPREAD 1024
+// Blocks that all tokens are spread over. Measured on MI355X (us, 512 | 768 | 1024 | 1536): 1 x 65536 tokens, 32 heads over 8,
+// 58.2 | 62.4 | 61.6 | 66.2; 64 skewed sequences fp16, 32 heads over 4, 93.6 | 86.0 | 89.4 | 87.0.
+#ifndef SPR
+#define SPR 768
 #endif
-constexpr int MAX_SPREAD = 1024;
+#ifndef MC
+#define MC 2
+#endif
+constexpr int SPREAD = SPR, MAX_PARTS = SPREAD + 1;
 template <int DT, int DH>
 __global__ __launch_bounds__(256) void attn_join_kernel(const kda_attn_args a, const float *acc, const float *ml, int spread,
                                                         int min_chunk) {
     using E = typename Ops<DT>::E;
     constexpr int LANES = DH / 4, GROUPS = 256 / LANES;
-    __shared__ float weight[MAX_SPREAD];
+    __shared__ float weight[MAX_PARTS];
     __shared__ f32x4 part[256];
     const int s = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63;
     int64_t total = 0;
     for (int q = lane; q < a.num_seqs; q += 64) total += seq_len(a, q);
     const int chunk = chunk_len(wave_sum64(total), spread, min_chunk);
-    const int parts = parts_of(seq_len(a, s), chunk);
+    const int len = seq_len(a, s), full = full_of(len, chunk), parts = full + (rest_of(len, chunk) ? 1 : 0);
     if (parts == 1) return;
-    int64_t first = 0;
-    for (int q = lane; q < s; q += 64) first += parts_of(seq_len(a, q), chunk);
-    first = wave_sum64(first);
-    const float *st = ml + (first * a.q_heads + h) * 2;
+    // where its full chunks begin, and its rest: after everyone's full chunks and the rests before it
+    int64_t first = 0, rest = 0;
+    for (int q = lane; q < a.num_seqs; q += 64) {
+        const int n = seq_len(a, q), f = full_of(n, chunk);
+        first += q < s ? f : 0;
+        rest += f + (q < s && rest_of(n, chunk) ? 1 : 0);
+    }
+    first = wave_sum64(first), rest = wave_sum64(rest);
     const int64_t step = (int64_t)a.q_heads * 2;
+    auto stat_of = [&](int p) { return ml + (p < full ? first + p : rest) * step + 2 * h; };
     float M = NEG_INF, L = 0.0f;
-    for (int p = lane; p < parts; p += 64) M = __builtin_fmaxf(M, st[p * step]);
+    for (int p = lane; p < parts; p += 64) M = __builtin_fmaxf(M, stat_of(p)[0]);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) M = __builtin_fmaxf(M, __shfl_xor(M, d));
     const float ref = M == NEG_INF ? 0.0f : M;
     for (int p = lane; p < parts; p += 64) {       // every wave the whole sum, the first one the weights
-        const float w = exp2_f(st[p * step] - ref);
+        const float *st = stat_of(p);
+        const float w = exp2_f(st[0] - ref);
         if (threadIdx.x < 64) weight[p] = w;
-        L += st[p * step + 1] * w;
+        L += st[1] * w;
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) L += __shfl_xor(L, d);
     __syncthreads();
     const int grp = threadIdx.x / LANES, x = threadIdx.x % LANES;
-    const f32x4 *from = reinterpret_cast<const f32x4 *>(acc + (first * a.q_heads + h) * DH) + x;
+    const f32x4 *from = reinterpret_cast<const f32x4 *>(acc) + (int64_t)h * LANES + x;
     const int64_t row = (int64_t)a.q_heads * LANES;
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll 8
-    for (int p = grp; p < parts; p += GROUPS) o += from[p * row] * weight[p];
+    for (int p = grp; p < parts; p += GROUPS) o += from[(p < full ? first + p : rest) * row] * weight[p];
     part[threadIdx.x] = o;
     __syncthreads();
     if (threadIdx.x < LANES) {
@@ -420,7 +442,7 @@ Plan plan(int64_t B, int64_t hq, int64_t hkv, int64_t width, int64_t page) {
     Plan p;
     p.tiles_h = (int)ceil_div(hq / hkv, 16);
     const int64_t per = hkv * p.tiles_h;
-    p.min_chunk = 2 * ROUND;
+    p.min_chunk = MC * ROUND;
     const int64_t most = width * page;
     const int64_t spread = ceil_div(SPREAD, per);
     p.spread = (int)spread;

@@ -11,6 +11,8 @@
 // last W-1 rows in registers, so a row is read once (and W-1 rows again at a tile's start). The
 // tile is uniform over the block; the sequences that start or end in it are found from the
 // offsets by a search at the tile's start, so no map of the batch is built beforehand.
+#include <type_traits>
+
 #include "ops_common.hpp"
 #include "ops_launch.hpp"
 
@@ -28,14 +30,20 @@ template <int DT> struct Vec<DT, 1> {
 };
 
 template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const void *base, int64_t off, float *out) {
-    using V = typename Vec<DT, VEC>::type;
-    const V v = *reinterpret_cast<const V *>(reinterpret_cast<const typename Elem<DT>::type *>(base) + off);
+__device__ __forceinline__ typename Vec<DT, VEC>::type load_raw(const void *base, int64_t off) {
+    return *reinterpret_cast<const typename Vec<DT, VEC>::type *>(reinterpret_cast<const typename Elem<DT>::type *>(base) + off);
+}
+template <int DT, int VEC>
+__device__ __forceinline__ void to_float(const typename Vec<DT, VEC>::type &v, float *out) {
     if constexpr (VEC == 1) out[0] = (float)v;
     else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) out[i] = (float)v[i];
     }
+}
+template <int DT, int VEC>
+__device__ __forceinline__ void load_vec(const void *base, int64_t off, float *out) {
+    to_float<DT, VEC>(load_raw<DT, VEC>(base, off), out);
 }
 
 template <int DT, int VEC>
@@ -51,14 +59,28 @@ __device__ __forceinline__ void store_vec(void *base, int64_t off, const float *
     *reinterpret_cast<V *>(reinterpret_cast<E *>(base) + off) = v;
 }
 
-// the taps of VEC channels, fp32 [C][W]
+// The taps of VEC channels, fp32 [C][W]: contiguous, four at a time where VEC W is a multiple of four (the
+// weight is then aligned to 16 bytes).
 template <int W, int VEC>
 __device__ __forceinline__ void load_taps(const float *w, const float *b, int c, float (&tap)[W][VEC], float (&bias)[VEC]) {
+    float flat[VEC * W];
+    const float *from = w + (int64_t)c * W;
+    if constexpr (VEC > 1 && VEC * W % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC * W; i += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(from + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) flat[i + j] = v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC * W; ++i) flat[i] = from[i];
+    }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         bias[i] = b ? b[c + i] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < W; ++j) tap[j][i] = w[(int64_t)(c + i) * W + j];
+        for (int j = 0; j < W; ++j) tap[j][i] = flat[i * W + j];
     }
 }
 
@@ -91,8 +113,9 @@ __device__ __forceinline__ void empty_final(const kda_conv_args &a, int n, int c
     store_final<DT, W, VEC>(a, n, c, hist);
 }
 
-// Rows loaded ahead of their use (in flight together).
-constexpr int AHEAD = 8;
+// Rows in flight ahead of their use, forward and backward. Measured on MI355X (us, forward of 8192 x 4096 bf16 with
+// 4 | 8 rows): 26.0 | 27.3; more rows only cost registers (8 rows: 224, two waves a SIMD).
+constexpr int AHEAD = 4, BWD_AHEAD = 4;
 
 template <int DT, int W, int VEC>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(const kda_conv_args a, int32_t *err, int L) {
@@ -119,34 +142,45 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const kda_conv_args a, in
     for (int j = 0; j < W - 1; ++j) load_row<DT, W, VEC>(a, n, start, t0 - (W - 1) + j, c, hist[j]);
     const bool act = a.activation != 0;
     int t = t0;
+    // rows of the tile, AHEAD at a time, the next ones in flight while these are computed (rows past
+    // the last are read again from the last)
+    typename Vec<DT, VEC>::type next[AHEAD];
+    auto fetch = [&](int from) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            next[k] = load_raw<DT, VEC>(a.x, (int64_t)(from + k < t1 ? from + k : t1 - 1) * a.x_stride + c);
+    };
+    fetch(t);
     while (true) {
         const int stop = end < t1 ? end : t1;
         while (t < stop) {
             const int m = stop - t < AHEAD ? stop - t : AHEAD;
-            float row[AHEAD][VEC];
+            typename Vec<DT, VEC>::type row[AHEAD];
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {   // rows past the last are read again from the last
-                const int tk = k < m ? t + k : stop - 1;
-                load_vec<DT, VEC>(a.x, (int64_t)tk * a.x_stride + c, row[k]);
-            }
+            for (int k = 0; k < AHEAD; ++k) row[k] = next[k];
+            if (t + m < t1) fetch(t + m);
+            auto rows = [&](auto whole) {
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                if (k < m) {
-                    float y[VEC];
+                for (int k = 0; k < AHEAD; ++k)
+                    if (whole || k < m) {
+                        float x[VEC], y[VEC];
+                        to_float<DT, VEC>(row[k], x);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        float p = bias[i];
+                        for (int i = 0; i < VEC; ++i) {
+                            float p = bias[i];
 #pragma unroll
-                        for (int j = 0; j < W - 1; ++j) p = __builtin_fmaf(tap[j][i], hist[j][i], p);
-                        p = __builtin_fmaf(tap[W - 1][i], row[k][i], p);
-                        y[i] = act ? p * sigmoid_f(p) : p;
+                            for (int j = 0; j < W - 1; ++j) p = __builtin_fmaf(tap[j][i], hist[j][i], p);
+                            p = __builtin_fmaf(tap[W - 1][i], x[i], p);
+                            y[i] = act ? p * sigmoid_f(p) : p;
 #pragma unroll
-                        for (int j = 0; j + 1 < W - 1; ++j) hist[j][i] = hist[j + 1][i];
-                        hist[W - 2][i] = row[k][i];
+                            for (int j = 0; j + 1 < W - 1; ++j) hist[j][i] = hist[j + 1][i];
+                            hist[W - 2][i] = x[i];
+                        }
+                        store_vec<DT, VEC>(a.out, (int64_t)(t + k) * a.channels + c, y);
                     }
-                    store_vec<DT, VEC>(a.out, (int64_t)(t + k) * a.channels + c, y);
-                }
-            }
+            };
+            if (m == AHEAD) rows(std::true_type{});
+            else rows(std::false_type{});
             t += m;
         }
         if (t < end) break;              // the sequence goes on in the next tile
@@ -199,10 +233,11 @@ struct BwdWalk {
     float tap[W][VEC], bias[VEC], hist[W - 1][VEC], e[W][VEC], dw[W][VEC], db[VEC];
     int c, n, start, t0, t1;
 
-    // the gradient of row s: of x, or of the initial state where s lies before the sequence
-    __device__ __forceinline__ void emit(int s, const float *extra) {
-        const bool row = s >= start && s >= t0 && s < t1;
-        const bool init = s < start && start >= t0 && g.d_initial_state;
+    // the gradient of row s: of x, or of the initial state where s lies before the sequence; plain: of a row
+    // that this tile owns
+    template <bool PLAIN> __device__ __forceinline__ void emit(int s, const float *extra) {
+        const bool row = PLAIN || (s >= start && s >= t0 && s < t1);
+        const bool init = !PLAIN && s < start && start >= t0 && g.d_initial_state;
         if (!row && !init) return;
         float d[VEC];
 #pragma unroll
@@ -227,7 +262,7 @@ struct BwdWalk {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) e[j][i] = 0.0f;
     }
-    __device__ __forceinline__ void step(int t, const float *x, const float *dy, bool mine) {
+    template <bool PLAIN> __device__ __forceinline__ void step(int t, const float *x, const float *dy, bool mine) {
         shift();
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
@@ -250,7 +285,7 @@ struct BwdWalk {
             for (int j = 0; j + 1 < W - 1; ++j) hist[j][i] = hist[j + 1][i];
             hist[W - 2][i] = x[i];
         }
-        emit(t - (W - 1), nullptr);
+        emit<PLAIN>(t - (W - 1), nullptr);
     }
     // past the sequence's end: no further e, and the final state's gradient joins its rows
     __device__ __forceinline__ void finish(int end) {
@@ -266,7 +301,7 @@ struct BwdWalk {
             const int s = end + k - (W - 1);
             if (g.d_final_state && (s < start || s < t1))
                 load_vec<KDA_DTYPE_F32, VEC>(g.d_final_state, ((int64_t)n * (W - 1) + k) * a.channels + c, extra);
-            emit(s, extra);
+            emit<false>(s, extra);
         }
     }
 };
@@ -314,29 +349,45 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const kda_conv_args a, co
         if (tile == 0)
             for (int i = 0; i < k.n; ++i) empty_grad<DT, VEC, W>(a, g, i, c);
         int t = k.t0;
+        const int last = T - k.t1 < W - 1 ? T : k.t1 + W - 1;       // rows that this tile reads
+        typename Vec<DT, VEC>::type nx[BWD_AHEAD], ndy[BWD_AHEAD];
+        auto fetch = [&](int from) {
+#pragma unroll
+            for (int q = 0; q < BWD_AHEAD; ++q) {
+                const int64_t r = from + q < last ? from + q : last - 1;
+                nx[q] = load_raw<DT, VEC>(a.x, r * a.x_stride + c);
+                ndy[q] = load_raw<DT, VEC>(g.dy, r * g.dy_stride + c);
+            }
+        };
+        fetch(t);
         while (true) {
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) load_row<DT, W, VEC>(a, k.n, k.start, t - (W - 1) + j, c, k.hist[j]);
             k.begin();
-            const int halo = T - k.t1 < W - 1 ? T : k.t1 + W - 1;
-            const int stop = end < halo ? end : halo;
+            const int stop = end < last ? end : last;
             while (t < stop) {
-                constexpr int A = 4;
-                float x[A][VEC], dy[A][VEC];
+                typename Vec<DT, VEC>::type x[BWD_AHEAD], dy[BWD_AHEAD];
 #pragma unroll
-                for (int q = 0; q < A; ++q) {
-                    const int tq = t + q < stop ? t + q : stop - 1;
-                    load_vec<DT, VEC>(a.x, (int64_t)tq * a.x_stride + c, x[q]);
-                    load_vec<DT, VEC>(g.dy, (int64_t)tq * g.dy_stride + c, dy[q]);
-                }
+                for (int q = 0; q < BWD_AHEAD; ++q) x[q] = nx[q], dy[q] = ndy[q];
+                const int then = t + BWD_AHEAD < stop ? t + BWD_AHEAD : stop;
+                if (then < last) fetch(then);
+                auto steps = [&](auto plain) {
 #pragma unroll
-                for (int q = 0; q < A; ++q)
-                    if (t + q < stop) k.step(t + q, x[q], dy[q], t + q < k.t1);
-                t += A;
+                    for (int q = 0; q < BWD_AHEAD; ++q)
+                        if (plain || t + q < stop) {
+                            float xf[VEC], dyf[VEC];
+                            to_float<DT, VEC>(x[q], xf);
+                            to_float<DT, VEC>(dy[q], dyf);
+                            k.template step<decltype(plain)::value>(t + q, xf, dyf, plain || t + q < k.t1);
+                        }
+                };
+                const int lo = k.start > k.t0 ? k.start : k.t0;
+                if (t - (W - 1) >= lo && t + BWD_AHEAD <= (stop < k.t1 ? stop : k.t1)) steps(std::true_type{});
+                else steps(std::false_type{});
+                t = then;
             }
             if (stop < end) break;       // the sequence goes on past this tile's last row
             k.finish(end);
-            t = end;
             int n = k.n + 1;
             if (end > k.t1) break;       // what follows belongs to the next tile
             for (; n < a.num_seqs && off.at(n + 1) <= end; ++n) empty_grad<DT, VEC, W>(a, g, n, c);
@@ -378,7 +429,7 @@ bool aligned(const void *p, int64_t bytes) { return ((uintptr_t)p % bytes) == 0;
 int conv_vec(const kda_conv_args &a, int full) {
     const int64_t es = (int64_t)dtype_bytes(a.dtype);
     const bool ok = a.channels % full == 0 && a.x_stride % full == 0 && aligned(a.x, full * es) && aligned(a.out, full * es) &&
-                    aligned(a.initial_state, full * es) && aligned(a.final_state, full * es);
+                    aligned(a.initial_state, full * es) && aligned(a.final_state, full * es) && aligned(a.weight, 16);
     return ok ? full : 1;
 }
 
@@ -396,18 +447,22 @@ Shape conv_shape(int64_t tiles, int C, int vec) {
     return s;
 }
 
-// Rows per tile: short enough that the batch fills the card (about 16 waves a CU), at least 8
-// and at most 64.
-int conv_tile(int64_t T, int64_t C, int vec, int lo, int hi) {
+// Rows per tile: as many tiles as give the card `target` waves, lo to hi rows each. Short tiles read the taps and
+// the rows before them (and, backward, behind them) too often, long ones leave the card idle. Measured on MI355X
+// (us): forward, 8192 x 4096 bf16, 8 channels a thread, target 1024 | 2048 | 4096 | 8192 waves: 29.5 | 26.0 | 32.2 |
+// 33.0; gradients, 8 x 1024 x 2048 bf16, 2 channels a thread, target (of one channel a thread) 4096 | 8192 waves 32.2 |
+// 33.8, and with 4 channels a thread 37.6 | 33.6.
+int conv_tile(int64_t T, int64_t C, int vec, int lo, int hi, int target) {
     const int64_t waves = ceil_div(ceil_div(C, vec), 64);
-    int64_t L = T * waves / 4096;
+    int64_t L = T * waves / target;
     L = L < lo ? lo : L > hi ? hi : L;
     return (int)(L / 8 * 8);
 }
-constexpr int BWD_MIN = 32, BWD_MAX = 128;
+int fwd_tile(int64_t T, int64_t C, int vec) { return conv_tile(T, C, vec, 8, 64, 2048); }
+int bwd_tile(int64_t T, int64_t C) { return conv_tile(T, C, 1, 32, 128, 4096); }
 
 template <int DT, int W, int VEC> hipError_t fwd_at(const kda_conv_args &a, int32_t *err, hipStream_t st) {
-    const int L = conv_tile(a.total_tokens, a.channels, VEC, 8, 64);
+    const int L = fwd_tile(a.total_tokens, a.channels, VEC);
     const int64_t tiles = a.total_tokens ? ceil_div(a.total_tokens, L) : 1;
     const Shape s = conv_shape(tiles, a.channels, VEC);
     conv_fwd_kernel<DT, W, VEC><<<s.grid, s.block, 0, st>>>(a, err, L);
@@ -420,7 +475,7 @@ template <int DT, int W, int VEC> hipError_t decode_at(const kda_conv_args &a, h
 }
 template <int DT, int W, int VEC>
 hipError_t bwd_at(const kda_conv_args &a, const kda_conv_grads &g, float *ws, int32_t *err, hipStream_t st) {
-    const int L = conv_tile(a.total_tokens, a.channels, 1, BWD_MIN, BWD_MAX);
+    const int L = bwd_tile(a.total_tokens, a.channels);
     const int64_t tiles = a.total_tokens ? ceil_div(a.total_tokens, L) : 1;
     const Shape s = conv_shape(tiles, a.channels, VEC);
     conv_bwd_kernel<DT, W, VEC><<<s.grid, s.block, 0, st>>>(a, g, ws, err, L);
@@ -488,7 +543,7 @@ hipError_t launch_conv_decode(const kda_conv_args &a, hipStream_t st) {
     return decode_dt<KDA_DTYPE_F16>(a, st);
 }
 size_t conv_bwd_workspace(int64_t T, int64_t C, int W) {
-    const int64_t tiles = T ? ceil_div(T, conv_tile(T, C, 1, BWD_MIN, BWD_MAX)) : 1;
+    const int64_t tiles = T ? ceil_div(T, bwd_tile(T, C)) : 1;
     return (size_t)tiles * (W + 1) * C * sizeof(float);
 }
 hipError_t launch_conv_bwd(const kda_conv_args &a, const kda_conv_grads &g, float *ws, int32_t *err, hipStream_t st) {
