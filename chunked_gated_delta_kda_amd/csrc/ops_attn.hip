@@ -94,10 +94,10 @@ struct Work {
     int begin, end;       // its tokens
 };
 
-// Tokens of a chunk: all tokens over `spread` chunks, whole rounds, at least min_chunk.
+// Tokens of a chunk: all tokens over `spread` chunks, whole tiles, at least min_chunk.
 __device__ __forceinline__ int chunk_len(int64_t total, int spread, int min_chunk) {
     const int64_t c = (total + spread - 1) / spread;
-    const int64_t r = (c + ROUND - 1) / ROUND * ROUND;
+    const int64_t r = (c + TILE - 1) / TILE * TILE;
     return r < min_chunk ? min_chunk : (int)(r < (1 << 30) ? r : 1 << 30);
 }
 // A sequence's full chunks; what is left (or all of a sequence without any) is one chunk more.
@@ -160,11 +160,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
     __shared__ float stat[WAVES][16][2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
     const int per = a.kv_heads * tiles_h;
-#ifdef SLOTFAST
-    const int slots = gridDim.x / per, rest = blockIdx.x / slots, slot = blockIdx.x - rest * slots;
-#else
     const int slot = blockIdx.x / per, rest = blockIdx.x - slot * per;
-#endif
     const int kvh = rest / tiles_h, ht = rest - kvh * tiles_h;
     Work w;
     if (!find_work(a, slot, spread, min_chunk, w)) return;
@@ -368,14 +364,8 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
 // Joins the chunks of one (sequence, head), in their order, where there are several: threads take four
 // elements each, groups of threads every GROUPS-th chunk.
 // Blocks that all tokens are spread over. Measured on MI355X (us, 512 | 768 | 1024 | 1536): 1 x 65536 tokens, 32 heads over 8,
-// 58.2 | 62.4 | 61.6 | 66.2; 64 skewed sequences fp16, 32 heads over 4, 93.6 | 86.0 | 89.4 | 87.0.
-#ifndef SPR
-#define SPR 768
-#endif
-#ifndef MC
-#define MC 2
-#endif
-constexpr int SPREAD = SPR, MAX_PARTS = SPREAD + 1;
+// 58.6 | 62.5 | 62.4 | 66; 64 skewed sequences fp16, 32 heads over 4, 93.0 | 90.0 | 87.8 | 87.
+constexpr int SPREAD = 768, MAX_PARTS = SPREAD + 1;
 template <int DT, int DH>
 __global__ __launch_bounds__(256) void attn_join_kernel(const kda_attn_args a, const float *acc, const float *ml, int spread,
                                                         int min_chunk) {
@@ -442,7 +432,7 @@ Plan plan(int64_t B, int64_t hq, int64_t hkv, int64_t width, int64_t page) {
     Plan p;
     p.tiles_h = (int)ceil_div(hq / hkv, 16);
     const int64_t per = hkv * p.tiles_h;
-    p.min_chunk = MC * ROUND;
+    p.min_chunk = 2 * ROUND;
     const int64_t most = width * page;
     const int64_t spread = ceil_div(SPREAD, per);
     p.spread = (int)spread;

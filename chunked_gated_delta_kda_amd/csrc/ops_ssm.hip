@@ -139,10 +139,8 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const kda_ssm_args a, flo
     const int block = unit / (16 * M), r = unit - block * (16 * M);
     const Place<CB, M> p(a, block);
     const int m = r / 16, b = (r % 16) / 4, j = r % 4;
-    const int c = p.channel(b), n = p.state(m, b, j);
-    const bool in = c <= p.last && n < p.N;
-    const int cc = c <= p.last ? c : p.last;
-    const float A2 = in ? a.A[(int64_t)c * p.N + n] * LOG2E_F : 0.0f;
+    const int c = p.copied(b), n = p.state(m, b, j);
+    const float A2 = n < p.N ? a.A[(int64_t)c * p.N + n] * LOG2E_F : 0.0f;
     const int64_t step = (int64_t)blocks * 1024 * M;
     float *at = tile_state<M>(ws, 0, blocks, block) + r * 64 + p.lane;
     float h = 0.0f;
@@ -153,7 +151,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const kda_ssm_args a, flo
         for (int q = 0; q < AHEAD; ++q) {
             const int k = k0 + q < tiles ? k0 + q : tiles - 1;
             E[q] = at[k * step];
-            S[q] = sums[(int64_t)k * a.channels + cc];
+            S[q] = sums[(int64_t)k * a.channels + c];
             reset[q] = resets[k];
         }
 #pragma unroll
@@ -199,7 +197,6 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_wide_kernel(const kda_ssm_args
     } else load_state<CB, M>(a.initial_state, n, a, p, h);
     const float bias = a.delta_bias ? a.delta_bias[p.ch] : 0.0f, skip = a.D ? a.D[p.ch] : 0.0f;
     float *steps = lds[wave], *rows = lds[wave] + K * 16 * CB;
-    const bool every = __all(!p.dup);          // lanes of one channel store the same
     const uint32_t ch = (uint32_t)p.ch * sizeof(E);
     int t = t0;
     Raw<DT, K, M, true> raw;
@@ -252,13 +249,12 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_wide_kernel(const kda_ssm_args
         for (int k = 0; k < K; ++k) {
             float v = __builtin_fmaf(skip, u[k], y[k]);
             if (a.z) v *= z[k] * sigmoid_f(z[k]);
-            if (whole || (k < count && p.mine)) *reinterpret_cast<E *>(out + (int64_t)k * a.channels * sizeof(E) + ch) = (E)v;
+            if (whole || k < count) *reinterpret_cast<E *>(out + (int64_t)k * a.channels * sizeof(E) + ch) = (E)v;
         }
     };
     while (true) {
         const int stop = end < t1 ? end : t1;
-        if (every)
-            while (stop - t >= K) stage(K, std::true_type{});
+        while (stop - t >= K) stage(K, std::true_type{});     // lanes of one channel store the same
         if (t < stop) {
             stage(stop - t < K ? stop - t : K, std::false_type{});
             if (t < stop) continue;

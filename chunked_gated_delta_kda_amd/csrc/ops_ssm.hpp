@@ -44,9 +44,9 @@ struct Place {
     static constexpr int CHANNELS = 16 * CB;
     int lane, i, g;
     int group;         // of B and C
-    int ch;            // natural channel, clamped to the group's last
-    bool mine;         // natural channel exists and this lane is the one that stores it
-    bool dup;          // natural channel lies past the group's last, which it repeats
+    int ch;            // natural channel; past the group's last one, that one again: everything about
+                       // such a channel is a copy, and what its lane stores is the same value
+    bool mine;         // natural channel exists and this is the one lane that stores it
     int base, last;    // first channel of the wave, last channel of the group
     int N;
     __device__ __forceinline__ Place(const kda_ssm_args &a, int block) {
@@ -59,12 +59,12 @@ struct Place {
         last = group * per + per - 1;
         const int want = base + 16 * (g % CB) + i;
         ch = want < last ? want : last;
-        dup = want > last;
-        mine = !dup && g < CB;
+        mine = want <= last && g < CB;
     }
     // state held by register 4 b + j of product m; channel of block b
     __device__ __forceinline__ int state(int m, int b, int j) const { return 16 * (b / CB + m * NB) + 4 * g + j; }
     __device__ __forceinline__ int channel(int b) const { return base + 16 * (b % CB) + i; }
+    __device__ __forceinline__ int copied(int b) const { return channel(b) <= last ? channel(b) : last; }
     // state of this lane's element of the instruction's B-row operand of product m
     __device__ __forceinline__ int nat_state(int m) const { return 16 * (g / CB + m * NB) + i; }
 };
@@ -77,12 +77,12 @@ __device__ __forceinline__ void load_decay(const kda_ssm_args &a, const Place<CB
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int c = p.channel(b), n = p.state(m, b, j);
-                A2[m][4 * b + j] = c <= p.last && n < p.N ? a.A[(int64_t)c * p.N + n] * LOG2E_F : 0.0f;
+                const int n = p.state(m, b, j);
+                A2[m][4 * b + j] = n < p.N ? a.A[(int64_t)p.copied(b) * p.N + n] * LOG2E_F : 0.0f;
             }
 }
 
-// State [seq][channel][state] of fp32 memory to registers; zeros where `s` is NULL or outside.
+// State [seq][channel][state] of fp32 memory to registers; zeros where `s` is NULL or the state lies past the last.
 template <int CB, int M>
 __device__ __forceinline__ void load_state(const float *s, int64_t seq, const kda_ssm_args &a, const Place<CB, M> &p,
                                            f32x16 (&h)[M]) {
@@ -90,12 +90,11 @@ __device__ __forceinline__ void load_state(const float *s, int64_t seq, const kd
     for (int m = 0; m < M; ++m)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int c = p.channel(b);
-            const float *row = s ? s + (seq * a.channels + (c <= p.last ? c : p.last)) * p.N : nullptr;
+            const float *row = s ? s + (seq * a.channels + p.copied(b)) * p.N : nullptr;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n = p.state(m, b, j);
-                h[m][4 * b + j] = row && c <= p.last && n < p.N ? row[n] : 0.0f;
+                h[m][4 * b + j] = row && n < p.N ? row[n] : 0.0f;
             }
         }
 }

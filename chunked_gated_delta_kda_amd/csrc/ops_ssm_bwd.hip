@@ -9,12 +9,17 @@
 //      the gradient G that it sends to the state before it (sum_t P_t C_t dy'_t, P_t the product of
 //      the decays so far: one exponential serves both), the local states before every KR-th token
 //   2. ssm_bwd_join_kernel: states forward and gradients backward over the tiles
-//   3. ssm_bwd_kernel: each tile from its end, KR tokens at a time: their decays and decayed states
-//      again from the stored state (completed by e^{A S} times the tile's first state), kept in
-//      registers, then the gradients
+//   3. ssm_bwd_kernel: each tile from its end, KR tokens at a time: their decayed states again from the
+//      stored state (completed by e^{A S} times the tile's first state), kept in registers, then the
+//      gradients. Decays are formed again on the way back: the registers that would keep them cost
+//      more than the exponential.
 //   4. ssm_bwd_rows_kernel, ssm_bwd_params_kernel: the sums over channel blocks (dB, dC) and over
 //      tiles (dA, dD, dbias), in a fixed order.
+// A cell is KR tokens of the tiles' grid, a group what one sequence has of a cell: the kernels go from group to
+// group, the cell's other tokens masked (no step, nothing in, nothing out; what they would store goes to a
+// place that nobody reads), so that the code of the tokens knows no borders.
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_ssm.hpp"
 
@@ -23,14 +28,14 @@ namespace ops {
 namespace ssm {
 namespace {
 
-constexpr int KB = 4;                       // tokens staged at a time
-template <int M> constexpr int KR_OF = 4 / M;   // tokens whose decays and states are held: 128 registers
+template <int M> constexpr int KR_OF = 4 / M;   // tokens of a cell, whose decayed states are held: 64 registers
 
 // Where the workspace keeps what, in floats.
 struct Layout {
     int64_t units, subs;                    // (tile, block) pairs; stored states of a tile
-    int64_t end_state, grad, local, sums, first_sums, dA, drow, rows, flags, total;
-    Layout(int64_t T, int64_t D, int64_t N, int64_t tiles, int64_t blocks, int L, int M) {
+    int64_t end_state, grad, local, sums, first_sums, dA, drow, rows, flags, none, total;
+    // NP: states of a wave, 16 to a state block
+    Layout(int64_t T, int64_t D, int64_t NP, int64_t tiles, int64_t blocks, int L, int M) {
         const int KR = 4 / M;
         units = tiles * blocks, subs = L / KR;
         const int64_t state = units * 1024 * M;
@@ -41,30 +46,35 @@ struct Layout {
         first_sums = sums + tiles * subs * D;        // [tile][D]: of the whole tile
         dA = first_sums + tiles * D;
         drow = dA + state;                           // [tile][2][D]: dD, dbias
-        rows = drow + 2 * tiles * D;                 // [block][T][2][N]: dB, dC
-        flags = rows + blocks * T * 2 * N;           // [tile][2]
-        total = flags + 2 * tiles;
+        rows = drow + 2 * tiles * D;                 // [block][T][2][NP]: dB, dC, NP the padded state size
+        flags = rows + blocks * T * 2 * NP;          // [tile][2]
+        none = flags + 2 * tiles + (-(flags + 2 * tiles) & 3);   // [2 NP or D]: where masked tokens store
+        total = none + std::max(2 * NP, D);
     }
 };
 
 template <int DT, int M> struct RawBwd {
     using E = typename Elem<DT>::type;
+    static constexpr int KB = KR_OF<M>;
     E delta[KB], u[KB], z[KB], dy[KB], B[KB][M], C[KB][M];
     template <int CB>
     __device__ __forceinline__ void load(const kda_ssm_args &a, const kda_ssm_grads &d, const Place<CB, M> &p, int t, int stop) {
+        const uint32_t ch = (uint32_t)p.ch * sizeof(E);
+        const char *u0 = (const char *)a.u, *d0 = (const char *)a.delta, *z0 = (const char *)a.z, *y0 = (const char *)d.dy;
+        const char *B0 = (const char *)a.B + (int64_t)p.group * p.N * sizeof(E), *C0 = (const char *)a.C + (int64_t)p.group * p.N * sizeof(E);
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-            const int64_t r = t + k < stop ? t + k : stop - 1;
-            delta[k] = reinterpret_cast<const E *>(a.delta)[r * a.delta_stride + p.ch];
-            u[k] = reinterpret_cast<const E *>(a.u)[r * a.u_stride + p.ch];
-            dy[k] = reinterpret_cast<const E *>(d.dy)[r * d.dy_stride + p.ch];
-            if (a.z) z[k] = reinterpret_cast<const E *>(a.z)[r * a.z_stride + p.ch];
+            const int64_t r = (int64_t)(t + k < stop ? t + k : stop - 1) * sizeof(E);
+            delta[k] = at<DT>(d0 + r * a.delta_stride, ch);
+            u[k] = at<DT>(u0 + r * a.u_stride, ch);
+            dy[k] = at<DT>(y0 + r * d.dy_stride, ch);
+            if (a.z) z[k] = at<DT>(z0 + r * a.z_stride, ch);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const int n = p.nat_state(m);
-                const int64_t at = (int64_t)p.group * p.N + n;
-                B[k][m] = n < p.N ? reinterpret_cast<const E *>(a.B)[r * a.B_stride + at] : (E)0.0f;
-                C[k][m] = n < p.N ? reinterpret_cast<const E *>(a.C)[r * a.C_stride + at] : (E)0.0f;
+                const uint32_t st = (uint32_t)(n < p.N ? n : p.N - 1) * sizeof(E);
+                B[k][m] = at<DT>(B0 + r * a.B_stride, st);
+                C[k][m] = at<DT>(C0 + r * a.C_stride, st);
             }
         }
     }
@@ -72,19 +82,20 @@ template <int DT, int M> struct RawBwd {
 
 // Staged tokens of a wave in LDS: per channel (natural lane l at CB i + g % CB) and per state.
 template <int CB, int M> struct StageBwd {
-    static constexpr int CH = 16 * CB, NS = 64 / CB * M;
+    static constexpr int CH = 16 * CB, NS = 64 / CB * M, KB = KR_OF<M>;
     float s[KB][CH], x[KB][CH], dy[KB][CH];       // step, step times input, dy'
     float u[KB][CH], sig[KB][CH], dz[KB][CH];     // input, sigmoid(delta + bias), dy silu'(z)
     float B[KB][NS], C[KB][NS];
 };
 
+// Tokens lo to hi - 1 of a cell are staged, the others masked.
 template <int DT, int CB, int M>
 __device__ __forceinline__ void stage(StageBwd<CB, M> &S, const RawBwd<DT, M> &raw, const kda_ssm_args &a, const Place<CB, M> &p,
-                                      float bias, int count, float (&step)[KB]) {
+                                      float bias, int lo, int hi, float &steps) {
     const int at = CB * p.i + p.g % CB;
 #pragma unroll
-    for (int k = 0; k < KB; ++k) {
-        const bool on = k < count, in = on && !p.dup;
+    for (int k = 0; k < KR_OF<M>; ++k) {
+        const bool on = k >= lo && k < hi;
         const float d = (float)raw.delta[k] + bias, u = (float)raw.u[k], dy = (float)raw.dy[k];
         float s = d, sig = 1.0f, g = dy, dz = 0.0f;
         if (a.delta_softplus) s = softplus_f(d), sig = sigmoid_f(d);
@@ -93,18 +104,18 @@ __device__ __forceinline__ void stage(StageBwd<CB, M> &S, const RawBwd<DT, M> &r
             g = dy * z * sz;
             dz = dy * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
         }
-        // past the tile's end no step, nothing in, nothing out; a channel past the group's last, which
-        // repeats it, adds nothing to the sums over channels
         s = on ? s : 0.0f;
-        step[k] = s;
-        S.s[k][at] = s, S.x[k][at] = in ? s * u : 0.0f, S.dy[k][at] = in ? g : 0.0f;
-        S.u[k][at] = u, S.sig[k][at] = sig, S.dz[k][at] = dz;
+        steps += s;
+        S.s[k][at] = s, S.x[k][at] = on ? s * u : 0.0f, S.dy[k][at] = on ? g : 0.0f;
+        S.u[k][at] = on ? u : 0.0f, S.sig[k][at] = on ? sig : 0.0f, S.dz[k][at] = dz;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            S.B[k][p.nat_state(m)] = on ? (float)raw.B[k][m] : 0.0f;
-            S.C[k][p.nat_state(m)] = on ? (float)raw.C[k][m] : 0.0f;
+            const bool is = on && p.nat_state(m) < p.N;
+            S.B[k][p.nat_state(m)] = is ? (float)raw.B[k][m] : 0.0f;
+            S.C[k][p.nat_state(m)] = is ? (float)raw.C[k][m] : 0.0f;
         }
     }
+    wave_fence();
 }
 
 template <int CB, int M>
@@ -149,37 +160,36 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_tile_kernel(const kda_s
 #pragma unroll
         for (int r = 0; r < 16; ++r) P[m][r] = 1.0f, G[m][r] = 0.0f, zero[m][r] = 0.0f;
     const float bias = a.delta_bias ? a.delta_bias[p.ch] : 0.0f;
+    const int nat = CB * p.i + p.g % CB;
     float sum = 0.0f;
     StageBwd<CB, M> &S = stages[wave];
+    float *const grad = ws + lay.grad + unit * (1024 * M);
+    auto store_grad = [&] {
+#pragma unroll
+        for (int r = 0; r < 16 * M; ++r) grad[r * 64 + p.lane] = G[r / 16][r % 16];
+    };
     RawBwd<DT, M> raw;
     raw.template load<CB>(a, d, p, t0, t1);
-    for (int t = t0; t < t1; t += KB) {
-        float step[KB];
-        stage<DT, CB, M>(S, raw, a, p, bias, t1 - t, step);
-        wave_fence();
-        if (t + KB < t1) raw.template load<CB>(a, d, p, t + KB, t1);
+    int gs = t0;                                    // the group's first token
+    while (gs < t1) {
+        const int tb = t0 + (gs - t0) / KR * KR, cell_end = tb + KR < t1 ? tb + KR : t1, ge = end < cell_end ? end : cell_end;
+        if (gs == tb) {                             // the state before the cell, and the steps so far
+            const int64_t sub = (tb - t0) / KR;
+            float *to = ws + lay.local + (unit * lay.subs + sub) * (1024 * M);
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            if (t + k == end && t + k < t1) {           // the next sequence starts with this token
-                if (first) add_state<CB, M>(G, P, d.d_final_state, n, a, p);
-                first = false, reset = true;
-                for (++n; n < a.num_seqs - 1 && off.at(n + 1) <= t + k; ++n) {}
-                end = off.at(n + 1);
-                load_state<CB, M>(a.initial_state, n, a, p, h);
-            }
-            if (k % KR == 0) {                          // the state before this token, and the steps so far
-                const int64_t sub = (t - t0 + k) / KR;
-                float *to = ws + lay.local + (unit * lay.subs + sub) * (1024 * M);
+            for (int r = 0; r < 16 * M; r += 4)
+                *reinterpret_cast<f32x4 *>(to + r * 64 + 4 * p.lane) =
+                    f32x4{h[r / 16][r % 16], h[r / 16][r % 16 + 1], h[r / 16][r % 16 + 2], h[r / 16][r % 16 + 3]};
+            if (p.mine) ws[lay.sums + ((int64_t)tile * lay.subs + sub) * a.channels + p.ch] = sum;
+        }
+        stage<DT, CB, M>(S, raw, a, p, bias, gs - tb, ge - tb, sum);
+        if (ge == cell_end && ge < t1) raw.template load<CB>(a, d, p, ge, t1);
 #pragma unroll
-                for (int r = 0; r < 16 * M; ++r) to[r * 64 + p.lane] = h[r / 16][r % 16];
-                if (p.mine) ws[lay.sums + ((int64_t)tile * lay.subs + sub) * a.channels + p.ch] = sum;
-            }
-            sum += step[k];
+        for (int k = 0; k < KR; ++k) {
             float sc[CB], B[M], C[M];
             read_steps<CB>(S.s[k], p.i, sc);
             operands<CB, M>(S.B[k], p, B);
             operands<CB, M>(S.C[k], p, C);
-            const int nat = CB * p.i + p.g % CB;
             const float x = S.x[k][nat], dy = S.dy[k][nat];
 #pragma unroll
             for (int m = 0; m < M; ++m) {
@@ -189,31 +199,39 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_tile_kernel(const kda_s
 #pragma unroll
                 for (int r = 0; r < 16; ++r) h[m][r] *= e[r];
                 h[m] = __builtin_amdgcn_mfma_f32_16x16x1f32(B[m], x, h[m], 0, 0, 0);
-                if (first) {
-                    const f32x16 w = __builtin_amdgcn_mfma_f32_16x16x1f32(C[m], dy, zero[m], 0, 0, 0);
+                const f32x16 w = __builtin_amdgcn_mfma_f32_16x16x1f32(C[m], dy, zero[m], 0, 0, 0);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        P[m][r] *= e[r];
-                        G[m][r] = __builtin_fmaf(P[m][r], w[r], G[m][r]);
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    P[m][r] *= e[r];
+                    G[m][r] = __builtin_fmaf(P[m][r], w[r], G[m][r]);
                 }
             }
         }
         wave_fence();
+        gs = ge;
+        if (gs == end) {                            // the sequence ends: with the first one G is complete
+            if (first) {
+                add_state<CB, M>(G, P, d.d_final_state, n, a, p);
+                store_grad();
+            }
+            first = false;
+            if (gs < t1) {
+                reset = true;
+                for (++n; n < a.num_seqs - 1 && off.at(n + 1) <= gs; ++n) {}
+                end = off.at(n + 1);
+                load_state<CB, M>(a.initial_state, n, a, p, h);
+            }
+        }
     }
-    const bool ends = end == t1;            // the last token's sequence
-    if (first && ends) add_state<CB, M>(G, P, d.d_final_state, n, a, p);
-    float *to = ws + lay.end_state + unit * (1024 * M), *tg = ws + lay.grad + unit * (1024 * M);
+    if (first) store_grad();
+    float *to = ws + lay.end_state + unit * (1024 * M);
 #pragma unroll
-    for (int r = 0; r < 16 * M; ++r) {
-        to[r * 64 + p.lane] = h[r / 16][r % 16];
-        tg[r * 64 + p.lane] = G[r / 16][r % 16];
-    }
+    for (int r = 0; r < 16 * M; ++r) to[r * 64 + p.lane] = h[r / 16][r % 16];
     if (p.mine) ws[lay.first_sums + (int64_t)tile * a.channels + p.ch] = sum;
     if (block == 0 && p.lane == 0) {
         int32_t *f = reinterpret_cast<int32_t *>(ws + lay.flags) + 2 * tile;
         f[0] = reset;                       // a sequence starts in the tile: its end state stands alone
-        f[1] = !first || ends;              // one ends in it: nothing of what lies behind reaches back
+        f[1] = !first;                      // one ends in it: nothing of what lies behind reaches back
     }
 }
 
@@ -228,9 +246,8 @@ __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(const kda_ssm_args a,
     const int block = unit / (16 * M), r = unit - block * (16 * M);
     const Place<CB, M> p(a, block);
     const int m = r / 16, b = (r % 16) / 4, j = r % 4;
-    const int c = p.channel(b), n = p.state(m, b, j);
-    const int cc = c <= p.last ? c : p.last;
-    const float A2 = c <= p.last && n < p.N ? a.A[(int64_t)c * p.N + n] * LOG2E_F : 0.0f;
+    const int c = p.copied(b), n = p.state(m, b, j);
+    const float A2 = n < p.N ? a.A[(int64_t)c * p.N + n] * LOG2E_F : 0.0f;
     const bool back = blockIdx.y == 1;
     const int64_t step = (int64_t)blocks * 1024 * M;
     float *at = ws + (back ? lay.grad : lay.end_state) + (int64_t)block * (1024 * M) + r * 64 + p.lane;
@@ -244,7 +261,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(const kda_ssm_args a,
         for (int q = 0; q < AHEAD; ++q) {
             const int f = k0 + q < tiles ? k0 + q : tiles - 1, k = back ? tiles - 1 - f : f;
             E[q] = at[k * step];
-            S[q] = sums[(int64_t)k * a.channels + cc];
+            S[q] = sums[(int64_t)k * a.channels + c];
             alone[q] = flags[2 * k];
         }
 #pragma unroll
@@ -258,12 +275,23 @@ __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(const kda_ssm_args a,
     }
 }
 
+// Sums of four values over the 16 lanes of a row: in lane i that of v[i % 4].
+__device__ __forceinline__ float row_sum4(float v0, float v1, float v2, float v3, bool odd, bool upper) {
+    const float a = (odd ? v1 : v0) + dpp_f<0xb1>(odd ? v0 : v1);       // quad_perm [1,0,3,2]
+    const float b = (odd ? v3 : v2) + dpp_f<0xb1>(odd ? v2 : v3);
+    float c = (upper ? b : a) + dpp_f<0x4e>(upper ? a : b);             // quad_perm [2,3,0,1]
+    c += dpp_f<0x124>(c);                                               // row_ror:4
+    c += dpp_f<0x128>(c);                                               // row_ror:8
+    return c;
+}
+
 template <int DT, int CB, int M>
 __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_args a, const kda_ssm_grads d, float *ws,
                                                                 const Layout lay, int L, int tiles, int blocks) {
     using E = typename Elem<DT>::type;
-    constexpr int KR = KR_OF<M>, NB = 4 / CB;
+    constexpr int KR = KR_OF<M>, NB = 4 / CB, NP = 16 * NB * M;
     __shared__ __align__(16) StageBwd<CB, M> stages[WAVES];
+    __shared__ __align__(16) float entry[WAVES][1024 * M];       // the state before the tile
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t unit = (int64_t)blockIdx.x * WAVES + wave;
     if (unit >= (int64_t)tiles * blocks) return;
@@ -279,166 +307,176 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_ar
     if (end == t1)          // empty sequences at the tile's end are this tile's
         for (int q = n + 1; q < a.num_seqs && off.at(q + 1) <= t1; ++q)
             pass_state<CB, M>(d.d_initial_state, d.d_final_state, q, a, p);
-    f32x16 A2[M], g[M], dA[M], first[M];
+    f32x16 A2[M], g[M], dA[M];
     load_decay<CB, M>(a, p, A2);
     {
         const float *fg = ws + lay.grad + unit * (1024 * M), *fh = ws + lay.end_state + unit * (1024 * M);
 #pragma unroll
         for (int r = 0; r < 16 * M; ++r) {
             g[r / 16][r % 16] = fg[r * 64 + p.lane];
-            first[r / 16][r % 16] = fh[r * 64 + p.lane];
+            entry[wave][r / 4 * 256 + 4 * p.lane + r % 4] = fh[r * 64 + p.lane];
             dA[r / 16][r % 16] = 0.0f;
         }
     }
     const float bias = a.delta_bias ? a.delta_bias[p.ch] : 0.0f, skip = a.D ? a.D[p.ch] : 0.0f;
+    const bool odd = p.i & 1, upper = p.i & 2;
+    float real[CB];         // copies of a channel do not count in sums over channels
+#pragma unroll
+    for (int b = 0; b < CB; ++b) real[b] = p.channel(b) <= p.last ? 1.0f : 0.0f;
+    const uint32_t ch = (uint32_t)p.ch * sizeof(E), srow = (uint32_t)(4 * p.g + (p.i & 3)) * 4;
     float dD = 0.0f, dbias = 0.0f;
     StageBwd<CB, M> &S = stages[wave];
     const int nat = CB * p.i + p.g % CB;
+    char *const none = (char *)(ws + lay.none);
     RawBwd<DT, M> raw;
-    int t = t0 + (t1 - t0 - 1) / KB * KB;
-    raw.template load<CB>(a, d, p, t, t1);
-    for (; t >= t0; t -= KB) {
-        float step[KB];
-        const int count = t1 - t < KB ? t1 - t : KB;
-        stage<DT, CB, M>(S, raw, a, p, bias, count, step);
-        wave_fence();
-        if (t > t0) raw.template load<CB>(a, d, p, t - KB, t1);
-#pragma unroll 1
-        for (int ks = KB - KR; ks >= 0; ks -= KR) {
-            const int tb = t + ks;
-            if (tb >= t1) continue;
-            // the state before token tb
-            const bool mixed = start > tb || end < (tb + KR < t1 ? tb + KR : t1);   // sequences meet among these tokens
-            int fn = n, fstart = start, fend = end;
-            if (start > tb) fn = off.find(tb), fstart = off.at(fn), fend = off.at(fn + 1);
-            f32x16 h[M], e[KR][M], ah[KR][M];
-            if (fstart == tb) load_state<CB, M>(a.initial_state, fn, a, p, h);
-            else {
-                const int64_t sub = (tb - t0) / KR;
-                const float *from = ws + lay.local + (unit * lay.subs + sub) * (1024 * M);
+    f32x16 local[M];            // the stored state before the next cell, and the steps up to it
+    float lsum[CB];
+    auto fetch = [&](int tb) {
+        const int64_t sub = (tb - t0) / KR;
+        const float *from = ws + lay.local + (unit * lay.subs + sub) * (1024 * M);
 #pragma unroll
-                for (int r = 0; r < 16 * M; ++r) h[r / 16][r % 16] = from[r * 64 + p.lane];
-                if (fstart < t0) {
-                    const float *sums = ws + lay.sums + ((int64_t)tile * lay.subs + sub) * a.channels;
-                    float sc[CB];
+        for (int r = 0; r < 16 * M; r += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(from + r * 64 + 4 * p.lane);
 #pragma unroll
-                    for (int b = 0; b < CB; ++b) sc[b] = sums[p.channel(b) <= p.last ? p.channel(b) : p.last];
+            for (int j = 0; j < 4; ++j) local[r / 16][r % 16 + j] = v[j];
+        }
+        const float *sums = ws + lay.sums + ((int64_t)tile * lay.subs + sub) * a.channels;
 #pragma unroll
-                    for (int m = 0; m < M; ++m)
+        for (int b = 0; b < CB; ++b) lsum[b] = sums[p.copied(b)];
+    };
+    int ge = t1;                                    // the token after the group
+    {
+        const int tb = t0 + (t1 - 1 - t0) / KR * KR;
+        raw.template load<CB>(a, d, p, tb, t1);
+        fetch(tb);
+    }
+    while (ge > t0) {
+        const int tb = t0 + (ge - 1 - t0) / KR * KR, gs = start > tb ? start : tb;
+        const bool opens = gs == start;             // the group starts its sequence
+        float steps = 0.0f;
+        stage<DT, CB, M>(S, raw, a, p, bias, gs - tb, ge - tb, steps);
+        f32x16 h[M], ah[KR][M];
+        if (opens) load_state<CB, M>(a.initial_state, n, a, p, h);
+        else {
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            h[m][r] = __builtin_fmaf(exp2_f(A2[m][r] * sc[(r / 4) % CB]), first[m][r], h[m][r]);
-                }
-            }
-            // forward over these tokens: decays, decayed states; y for dz, dC
+            for (int m = 0; m < M; ++m) h[m] = local[m];
+            if (start < t0) {
 #pragma unroll
-            for (int k = 0; k < KR; ++k) {
-                const int kk = ks + k;
-                if (mixed && k > 0 && tb + k == fend && tb + k < t1) {
-                    for (++fn; fn < a.num_seqs - 1 && off.at(fn + 1) <= tb + k; ++fn) {}
-                    fend = off.at(fn + 1);
-                    load_state<CB, M>(a.initial_state, fn, a, p, h);
-                }
-                float sc[CB], dyc[CB], B[M], r[CB];
-                read_steps<CB>(S.s[kk], p.i, sc);
-                read_steps<CB>(S.dy[kk], p.i, dyc);
-                operands<CB, M>(S.B[kk], p, B);
-                const float x = S.x[kk][nat];
+                for (int r = 0; r < 16 * M; r += 4) {
+                    const f32x4 f = *reinterpret_cast<const f32x4 *>(&entry[wave][r / 4 * 256 + 4 * p.lane]);
+                    const int m = r / 16, q = r % 16;
 #pragma unroll
-                for (int b = 0; b < CB; ++b) r[b] = 0.0f;
-                float *rows = ws + lay.rows + (((int64_t)block * T + tb + k) * 2 + 1) * p.N;
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) e[k][m][q] = exp2_f(A2[m][q] * sc[(q / 4) % CB]);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) ah[k][m][q] = e[k][m][q] * h[m][q];
-                    h[m] = __builtin_amdgcn_mfma_f32_16x16x1f32(B[m], x, ah[k][m], 0, 0, 0);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        const f32x4 c4 = *reinterpret_cast<const f32x4 *>(&S.C[kk][p.state(m, nb * CB, 0)]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float dC = 0.0f;
-#pragma unroll
-                            for (int b = 0; b < CB; ++b) {
-                                const float hv = h[m][4 * (nb * CB + b) + j];
-                                r[b] = __builtin_fmaf(c4[j], hv, r[b]);
-                                dC = __builtin_fmaf(dyc[b], hv, dC);
-                            }
-                            dC = row_sum(dC);
-                            const int st = p.state(m, nb * CB, j);
-                            if (p.i == j && st < p.N && tb + k < t1) rows[st] = dC;
-                        }
-                    }
-                }
-                if (a.z && tb + k < t1) {
-                    const float y = __builtin_fmaf(skip, S.u[kk][nat], to_natural<CB>(r));
-                    if (p.mine) reinterpret_cast<E *>(d.dz)[(int64_t)(tb + k) * a.channels + p.ch] = (E)(S.dz[kk][nat] * y);
-                }
-            }
-            // and back
-#pragma unroll
-            for (int k = KR - 1; k >= 0; --k) {
-                const int kk = ks + k, tk = tb + k;
-                if (tk >= t1) continue;
-                if (tk + 1 == end) load_state<CB, M>(d.d_final_state, n, a, p, g);
-                float sc[CB], xc[CB], C[M], r1[CB], r2[CB];
-                read_steps<CB>(S.s[kk], p.i, sc);
-                read_steps<CB>(S.x[kk], p.i, xc);
-                operands<CB, M>(S.C[kk], p, C);
-                const float dy = S.dy[kk][nat];
-#pragma unroll
-                for (int b = 0; b < CB; ++b) r1[b] = 0.0f, r2[b] = 0.0f;
-                float *rows = ws + lay.rows + ((int64_t)block * T + tk) * 2 * p.N;
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    g[m] = __builtin_amdgcn_mfma_f32_16x16x1f32(C[m], dy, g[m], 0, 0, 0);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        const f32x4 b4 = *reinterpret_cast<const f32x4 *>(&S.B[kk][p.state(m, nb * CB, 0)]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float dB = 0.0f;
-#pragma unroll
-                            for (int b = 0; b < CB; ++b) {
-                                const int q = 4 * (nb * CB + b) + j;
-                                const float dh = g[m][q];
-                                r1[b] = __builtin_fmaf(b4[j], dh, r1[b]);
-                                dB = __builtin_fmaf(xc[b], dh, dB);
-                                const float v = dh * ah[k][m][q];
-                                r2[b] = __builtin_fmaf(A2[m][q], v, r2[b]);
-                                dA[m][q] = __builtin_fmaf(sc[b], v, dA[m][q]);
-                                g[m][q] = dh * e[k][m][q];
-                            }
-                            dB = row_sum(dB);
-                            const int st = p.state(m, nb * CB, j);
-                            if (p.i == j && st < p.N) rows[st] = dB;
-                        }
-                    }
-                }
-                const float into = to_natural<CB>(r1), dec = to_natural<CB>(r2) * LN2_F;
-                const float u = S.u[kk][nat], s = S.s[kk][nat];
-                const float ddelta = __builtin_fmaf(u, into, dec) * S.sig[kk][nat];
-                if (p.mine) {
-                    const int64_t o = (int64_t)tk * a.channels + p.ch;
-                    reinterpret_cast<E *>(d.du)[o] = (E)__builtin_fmaf(s, into, skip * dy);
-                    reinterpret_cast<E *>(d.ddelta)[o] = (E)ddelta;
-                }
-                dD = __builtin_fmaf(dy, u, dD);
-                dbias += ddelta;
-                if (tk == start) {      // a sequence's first token: what is left belongs to its initial state
-                    store_state<CB, M>(d.d_initial_state, n, a, p, g);
-                    if (tk > t0 || tk == 0) {
-                        for (--n; n >= 0 && off.at(n) >= tk; --n)
-                            pass_state<CB, M>(d.d_initial_state, d.d_final_state, n, a, p);
-                        n = n < 0 ? 0 : n;
-                        start = off.at(n), end = tk;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        h[m][q + j] = __builtin_fmaf(exp2_f(A2[m][q + j] * lsum[(q / 4) % CB]), f[j], h[m][q + j]);
                 }
             }
         }
+        if (ge == end) load_state<CB, M>(d.d_final_state, n, a, p, g);
+        // forward over the cell: decayed states; y for dz, dC
+        float *const rows = ws + lay.rows + ((int64_t)block * T + tb) * (2 * NP);
+#pragma unroll
+        for (int k = 0; k < KR; ++k) {
+            const bool on = tb + k >= gs && tb + k < ge;
+            char *const row = on ? (char *)(rows + k * 2 * NP) : none;
+            float sc[CB], dyc[CB], B[M], r[CB];
+            read_steps<CB>(S.s[k], p.i, sc);
+            read_steps<CB>(S.dy[k], p.i, dyc);
+            operands<CB, M>(S.B[k], p, B);
+            const float x = S.x[k][nat];
+#pragma unroll
+            for (int b = 0; b < CB; ++b) r[b] = 0.0f, dyc[b] *= real[b];
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) ah[k][m][q] = exp2_f(A2[m][q] * sc[(q / 4) % CB]) * h[m][q];
+                h[m] = __builtin_amdgcn_mfma_f32_16x16x1f32(B[m], x, ah[k][m], 0, 0, 0);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const f32x4 c4 = *reinterpret_cast<const f32x4 *>(&S.C[k][p.state(m, nb * CB, 0)]);
+                    float dC[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        dC[j] = 0.0f;
+#pragma unroll
+                        for (int b = 0; b < CB; ++b) {
+                            const float hv = h[m][4 * (nb * CB + b) + j];
+                            r[b] = __builtin_fmaf(c4[j], hv, r[b]);
+                            dC[j] = __builtin_fmaf(dyc[b], hv, dC[j]);
+                        }
+                    }
+                    *reinterpret_cast<float *>(row + (NP + 16 * (nb + m * NB)) * 4 + srow) =
+                        row_sum4(dC[0], dC[1], dC[2], dC[3], odd, upper);
+                }
+            }
+            if (a.z) {
+                const float y = __builtin_fmaf(skip, S.u[k][nat], to_natural<CB>(r));
+                char *const out = on ? (char *)d.dz + (int64_t)(tb + k) * a.channels * sizeof(E) : none;
+                *reinterpret_cast<E *>(out + ch) = (E)(S.dz[k][nat] * y);
+            }
+        }
+        // and back; what the next cell needs is fetched half way, when registers have come free
+#pragma unroll
+        for (int k = KR - 1; k >= 0; --k) {
+            const bool on = tb + k >= gs && tb + k < ge;
+            if (k == (KR - 1) / 2) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (gs == tb && tb > t0) {
+                    fetch(tb - KR);
+                    raw.template load<CB>(a, d, p, tb - KR, t1);
+                }
+            }
+            char *const row = on ? (char *)(rows + k * 2 * NP) : none;
+            float sc[CB], xc[CB], C[M], r1[CB], r2[CB];
+            read_steps<CB>(S.s[k], p.i, sc);
+            read_steps<CB>(S.x[k], p.i, xc);
+            operands<CB, M>(S.C[k], p, C);
+            const float dy = S.dy[k][nat];
+#pragma unroll
+            for (int b = 0; b < CB; ++b) r1[b] = 0.0f, r2[b] = 0.0f, xc[b] *= real[b];
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                g[m] = __builtin_amdgcn_mfma_f32_16x16x1f32(C[m], dy, g[m], 0, 0, 0);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const f32x4 b4 = *reinterpret_cast<const f32x4 *>(&S.B[k][p.state(m, nb * CB, 0)]);
+                    float dB[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        dB[j] = 0.0f;
+#pragma unroll
+                        for (int b = 0; b < CB; ++b) {
+                            const int q = 4 * (nb * CB + b) + j;
+                            const float dh = g[m][q];
+                            r1[b] = __builtin_fmaf(b4[j], dh, r1[b]);
+                            dB[j] = __builtin_fmaf(xc[b], dh, dB[j]);
+                            const float v = dh * ah[k][m][q];
+                            r2[b] = __builtin_fmaf(A2[m][q], v, r2[b]);
+                            dA[m][q] = __builtin_fmaf(sc[b], v, dA[m][q]);
+                            g[m][q] = dh * exp2_f(A2[m][q] * sc[b]);
+                        }
+                    }
+                    *reinterpret_cast<float *>(row + 16 * (nb + m * NB) * 4 + srow) = row_sum4(dB[0], dB[1], dB[2], dB[3], odd, upper);
+                }
+            }
+            const float into = to_natural<CB>(r1), dec = to_natural<CB>(r2) * LN2_F;
+            const float u = S.u[k][nat], s = S.s[k][nat];
+            const float ddelta = __builtin_fmaf(u, into, dec) * S.sig[k][nat];
+            const int64_t o = (int64_t)(tb + k) * a.channels * sizeof(E);
+            *reinterpret_cast<E *>((on ? (char *)d.du + o : none) + ch) = (E)__builtin_fmaf(s, into, skip * dy);
+            *reinterpret_cast<E *>((on ? (char *)d.ddelta + o : none) + ch) = (E)ddelta;
+            dD = __builtin_fmaf(dy, u, dD);
+            dbias += on ? ddelta : 0.0f;
+        }
         wave_fence();
+        ge = gs;
+        if (opens) {        // what is left belongs to the initial state
+            store_state<CB, M>(d.d_initial_state, n, a, p, g);
+            if (gs > t0 || gs == 0) {
+                for (--n; n >= 0 && off.at(n) >= gs; --n) pass_state<CB, M>(d.d_initial_state, d.d_final_state, n, a, p);
+                n = n < 0 ? 0 : n;
+                start = off.at(n), end = gs;
+            }
+        }
     }
     float *to = ws + lay.dA + unit * (1024 * M);
 #pragma unroll
@@ -451,21 +489,23 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_ar
 
 // dB and dC of every (token, group, state): the sums over the group's channel blocks.
 template <int DT>
-__global__ __launch_bounds__(256) void ssm_bwd_rows_kernel(const kda_ssm_args a, const kda_ssm_grads d, const float *rows, int per_group) {
+__global__ __launch_bounds__(256) void ssm_bwd_rows_kernel(const kda_ssm_args a, const kda_ssm_grads d, const float *rows, int per_group,
+                                                           int NP) {
     using E = typename Elem<DT>::type;
     const int N = a.state_size, G = a.groups;
-    const int64_t line = (int64_t)a.total_tokens * 2 * N;            // of one block
+    const int64_t line = (int64_t)a.total_tokens * 2 * NP;           // of one block
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;      // (token, which, state)
     const int grp = blockIdx.y;
     if (id >= line) return;
+    const int64_t t = id / (2 * NP);
+    const int r = (int)(id - t * 2 * NP), n = r < NP ? r : r - NP;
+    if (n >= N) return;
     const float *from = rows + (int64_t)grp * per_group * line + id;
     float s = 0.0f;
 #pragma unroll 8
     for (int b = 0; b < per_group; ++b) s += from[b * line];
-    const int64_t t = id / (2 * N);
-    const int r = (int)(id - t * 2 * N);
-    E *to = reinterpret_cast<E *>(r < N ? d.dB : d.dC);
-    to[(t * G + grp) * N + (r < N ? r : r - N)] = (E)s;
+    E *to = reinterpret_cast<E *>(r < NP ? d.dB : d.dC);
+    to[(t * G + grp) * N + n] = (E)s;
 }
 
 // dA (blockIdx.y 0 .. 16 M - 1: a register of every block's lanes), dD and dbias (the last): sums over tiles.
@@ -501,7 +541,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_params_kernel(const kda_ssm_args 
 int bwd_tile_len(int64_t T, int64_t blocks) {
     int64_t L = T * blocks / 2048;
     L = L < 16 ? 16 : L > T ? T : L;
-    return (int)((L + KB - 1) / KB * KB);
+    return (int)((L + 3) / 4 * 4);
 }
 
 template <int DT, int CB, int M>
@@ -509,7 +549,7 @@ hipError_t bwd_form(const kda_ssm_args &a, const kda_ssm_grads &d, float *ws, in
     const int64_t T = a.total_tokens, blocks = blocks_of(Form{CB, M}, a.channels, a.groups);
     const int L = bwd_tile_len(T, blocks);
     const int64_t tiles = T ? ceil_div(T, L) : 1;
-    const Layout lay(T, a.channels, a.state_size, tiles, blocks, L, M);
+    const Layout lay(T, a.channels, 64 / CB * M, tiles, blocks, L, M);
     const dim3 grid((unsigned)ceil_div(lay.units, WAVES));
     if (T) {
         ssm_bwd_tile_kernel<DT, CB, M><<<grid, 64 * WAVES, 0, st>>>(a, d, ws, lay, err, L, (int)tiles, (int)blocks);
@@ -520,9 +560,9 @@ hipError_t bwd_form(const kda_ssm_args &a, const kda_ssm_grads &d, float *ws, in
     ssm_bwd_kernel<DT, CB, M><<<grid, 64 * WAVES, 0, st>>>(a, d, ws, lay, L, (int)tiles, (int)blocks);
     if (hipError_t e = hipGetLastError()) return e;
     if (T) {
-        const int64_t line = T * 2 * a.state_size;
+        const int64_t line = T * 2 * (64 / CB * M);
         ssm_bwd_rows_kernel<DT><<<dim3((unsigned)ceil_div(line, 256), (unsigned)a.groups), 256, 0, st>>>(
-            a, d, ws + lay.rows, (int)(blocks / a.groups));
+            a, d, ws + lay.rows, (int)(blocks / a.groups), 64 / CB * M);
         if (hipError_t e = hipGetLastError()) return e;
     }
     const int64_t wide = std::max<int64_t>(blocks * 64, 2 * (int64_t)a.channels);
@@ -548,7 +588,7 @@ size_t ssm_bwd_workspace(int64_t T, int64_t D, int64_t N, int64_t G) {
     const Form f = form_of((int)N);
     const int64_t blocks = blocks_of(f, D, G);
     const int L = bwd_tile_len(T, blocks);
-    return (size_t)Layout(T, D, N, T ? ceil_div(T, L) : 1, blocks, L, f.m).total * sizeof(float);
+    return (size_t)Layout(T, D, 64 / f.cb * f.m, T ? ceil_div(T, L) : 1, blocks, L, f.m).total * sizeof(float);
 }
 
 hipError_t launch_ssm_bwd(const kda_ssm_args &a, const kda_ssm_grads &d, float *ws, int32_t *err, hipStream_t st) {
