@@ -16,75 +16,81 @@ DTYPES = {torch.float32: native.ACT_DTYPES["f32"], torch.bfloat16: native.ACT_DT
           torch.float16: native.ACT_DTYPES["f16"]}
 
 
-def fail(name, t, want, dev):
-    raise ValueError(f"{name}: expected {want} on {dev}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} "
-                     f"on {t.device}")
+def _place(index):
+    return "the CPU" if index < 0 else f"cuda:{index}"
 
 
-def dense(name, t, dtype, shape, dev):
-    """A contiguous ``dtype`` tensor of ``shape`` on ``dev``."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
-        fail(name, t, f"contiguous {dtype} {tuple(shape)}", dev)
+def fail(name, t, want, index):
+    raise ValueError(f"{name}: expected {want} on {_place(index)}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} "
+                     f"on {_place(t.get_device())}")
 
 
-def rows(name, t, dtype, shape, dev):
+def dense(name, t, dtype, shape, index):
+    """A contiguous ``dtype`` tensor of ``shape`` on device ``index`` (-1: the CPU)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        fail(name, t, f"contiguous {dtype} {tuple(shape)}", index)
+
+
+def rows(name, t, dtype, shape, index):
     """A ``dtype`` tensor of ``shape`` whose rows (index 0) are contiguous and do not overlap; returns
     the row stride in elements."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev:
-        fail(name, t, f"{dtype} {tuple(shape)}", dev)
-    length = shape[1] if len(shape) == 2 else _row_len(shape)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        fail(name, t, f"{dtype} {tuple(shape)}", index)
+    length = shape[1] if len(shape) == 2 else shape[1] * shape[2]
     if t.is_contiguous():
         return length
     inner = 1
     for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
         if size > 1 and stride != inner:
-            fail(name, t, f"{dtype} {tuple(shape)} with contiguous rows", dev)
+            fail(name, t, f"{dtype} {tuple(shape)} with contiguous rows", index)
         inner *= size
     if shape[0] > 1 and t.stride(0) < length:
-        fail(name, t, f"{dtype} {tuple(shape)} with rows that do not overlap", dev)
+        fail(name, t, f"{dtype} {tuple(shape)} with rows that do not overlap", index)
     return max(t.stride(0), length)
 
 
-def _row_len(shape):
-    n = 1
-    for s in shape[1:]:
-        n *= s
-    return n
-
-
-def offsets(cu_seqlens, dev):
+def offsets(cu_seqlens, index):
     """The number of sequences of ``cu_seqlens`` (None: one)."""
     if cu_seqlens is None:
         return 1
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.device != dev or cu_seqlens.dim() != 1 \
+    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.get_device() != index or cu_seqlens.dim() != 1 \
             or not cu_seqlens.is_contiguous() or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens: expected a contiguous int32 vector of N+1 >= 2 offsets on the device")
     return cu_seqlens.shape[0] - 1
 
 
-def on_device(what, dev):
-    if dev.type != "cuda":
+def on_device(what, index):
+    if index < 0:
         raise ValueError(f"{what} needs device tensors")
 
 
 def ptr(t):
-    return t.data_ptr() if t is not None else None
+    return None if t is None else t.data_ptr()
 
 
-def scratch(workspace, nbytes, dev):
-    """The caller's workspace, or one of ``nbytes`` (None if none is needed); its pointer and size."""
+def like(x, shape, dtype=None):
+    """A new contiguous tensor of ``shape`` on x's device, of x's dtype by default."""
+    if dtype is None and x.shape == shape and x.is_contiguous():
+        return torch.empty_like(x)      # the cheapest of torch's allocating calls
+    return x.new_empty(shape, dtype=dtype or x.dtype)
+
+
+def scratch(workspace, nbytes, x):
+    """The caller's workspace, or one of ``nbytes`` on x's device (None if none is needed); its pointer and size."""
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    elif workspace.device != dev or not workspace.is_contiguous():
+        if not nbytes:
+            return None, None, 0
+        workspace = x.new_empty((nbytes,), dtype=torch.uint8)
+    elif workspace.get_device() != x.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace, ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 @contextlib.contextmanager
-def _elsewhere(dev, stream):
-    with torch.cuda.device(dev):
+def _elsewhere(index, stream):
+    with torch.cuda.device(index):
         if stream is None:
-            yield torch.cuda.current_stream(dev).cuda_stream
+            yield _current_stream(index)
         else:
             with torch.cuda.stream(stream):
                 yield stream.cuda_stream
@@ -92,6 +98,7 @@ def _elsewhere(dev, stream):
 
 class _Here:
     """The current device and its current stream."""
+    __slots__ = ("handle",)
 
     def __init__(self, handle):
         self.handle = handle
@@ -103,19 +110,25 @@ class _Here:
         return False
 
 
-def launch_on(dev, stream):
-    """Context of one call: ``dev`` is the current device, tensors allocated inside belong to the
+def launch_on(index, stream):
+    """Context of one call: device ``index`` is the current one, tensors allocated inside belong to the
     call's stream (torch's allocator hands their memory on in that stream's order), and the
-    value is that stream's handle. ``stream`` None: torch's current stream of ``dev``."""
-    if stream is None and torch.cuda.current_device() == dev.index:
-        return _Here(_current_stream(dev.index))
-    return _elsewhere(dev, stream)
+    value is that stream's handle. ``stream`` None: torch's current stream of the device."""
+    if stream is None and torch.cuda.current_device() == index:
+        return _Here(_current_stream(index))
+    return _elsewhere(index, stream)
 
 
-def checked(handle, call):
-    """``call`` with the device error word cleared before it and read after (both synchronise)."""
+def run(check, handle, call, *args):
+    """One call of the library; ``check``: with the device error word cleared before it and read after (both
+    synchronise)."""
+    if not check:
+        rc = call(*args)
+        if rc:
+            native.check(rc)
+        return
     native.device_errors(handle, clear=True)
-    call()
+    native.check(call(*args))
     bits = native.device_errors(handle, clear=True)
     if bits:
         raise native.KdaDeviceError(bits)

@@ -6,41 +6,43 @@ import math
 import torch
 
 from . import native
-from ._args import DTYPES, checked, dense, fail, launch_on, on_device, ptr, scratch
+from ._args import DTYPES, dense, fail, launch_on, like, on_device, ptr, run, scratch
 
 __all__ = ["attn_decode"]
 
 HEAD_DIMS = (64, 128, 256)
 
 
-def _strides(t):
-    """Strides but the last; those of dimensions of one entry do not matter."""
-    shape, stride = t.shape, t.stride()
-    return [stride[i] if shape[i] > 1 else 0 for i in range(len(shape) - 1)]
-
-
 def _by8(name, t, dev):
-    """Rows read 16 bytes at a time: the last dimension contiguous, other strides multiples of 8. Returns
-    those strides."""
-    strides = _strides(t)
-    off = 0
-    for s in strides:
-        off |= s
-    if off % 8 or t.stride(-1) != 1 or t.data_ptr() % 16 or t.device != dev:
+    """Rows read 16 bytes at a time: the last dimension contiguous, other strides multiples of 8 (those of
+    dimensions of one entry do not matter). Returns those strides."""
+    shape, last = t.shape, t.dim() - 1
+    if t.is_contiguous():
+        strides, step = [], shape[last]
+        for n in shape[last - 1:0:-1]:
+            strides.append(step)
+            step *= n
+        strides.append(step)
+        strides.reverse()
+        bad = False
+    else:
+        strides = [s if n > 1 else 0 for n, s in zip(shape[:last], t.stride())]
+        bad = t.stride(last) != 1 or any(s % 8 for s in strides)
+    if bad or t.data_ptr() % 16 or t.get_device() != dev:
         fail(name, t, "rows of contiguous elements, strides that are multiples of 8, a base aligned to 16 bytes", dev)
     return strides
 
 
 def _check(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse):
-    dev, dt, shape = q.device, q.dtype, q.shape
-    if dt not in (torch.bfloat16, torch.float16) or len(shape) != 3 or shape[0] < 1:
+    dev, dt, shape = q.get_device(), q.dtype, q.shape
+    if (dt is not torch.bfloat16 and dt is not torch.float16) or len(shape) != 3 or shape[0] < 1:
         raise ValueError(f"q: expected bf16 or fp16 [B, Hq, Dh], got {dt} {tuple(shape)}")
     B, hq, dh = shape
     if dh not in HEAD_DIMS:
         raise ValueError(f"q: head dimension {dh}; expected one of {HEAD_DIMS}")
     cache = k_cache.shape
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != dt or len(cache) != 4 or t.shape != cache or cache[3] != dh or min(cache) < 1:
+        if t.dtype is not dt or len(cache) != 4 or t.shape != cache or cache[3] != dh or min(cache) < 1:
             raise ValueError(f"{name}: expected {dt} [pages, page size, Hkv, {dh}], one shape for both, got {t.dtype} "
                              f"{tuple(t.shape)}")
     strides = _by8("q", q, dev) + _by8("k_cache", k_cache, dev) + _by8("v_cache", v_cache, dev)
@@ -48,7 +50,7 @@ def _check(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse):
     if hq % hkv:
         raise ValueError(f"q: {hq} heads are not a multiple of the cache's {hkv}")
     table = block_table.shape
-    if block_table.dtype != torch.int32 or len(table) != 2 or table[0] != B or table[1] < 1 or block_table.device != dev:
+    if block_table.dtype is not torch.int32 or len(table) != 2 or table[0] != B or table[1] < 1 or block_table.get_device() != dev:
         fail("block_table", block_table, f"int32 [{B}, pages of the longest]", dev)
     rows, inner = block_table.stride()
     if (table[1] > 1 and inner != 1) or (B > 1 and rows < table[1]):
@@ -58,7 +60,7 @@ def _check(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse):
     if scale is not None and not math.isfinite(scale):
         raise ValueError("scale: expected a finite number")
     if out is not None:
-        dense("out", out, dt, (B, hq, dh), dev)
+        dense("out", out, dt, shape, dev)
     if lse is not None:
         dense("lse", lse, torch.float32, (B, hq), dev)
     return B, hq, hkv, dh, pages, page, table[1], strides
@@ -87,18 +89,17 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, *, retur
     Returns out [B, Hq, Dh], or (out, lse). Tensors that the call allocates belong to its stream.
     """
     lib = native.load_library()
-    dev = q.device
+    dev = q.get_device()
     on_device("kda.attn_decode", dev)
     B, hq, hkv, dh, pages, page, width, strides = _check(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse)
     with launch_on(dev, stream) as st:
         if out is None:
-            out = torch.empty((B, hq, dh), dtype=q.dtype, device=dev)
+            out = like(q, q.shape)
         if lse is None and return_lse:
-            lse = torch.empty((B, hq), dtype=torch.float32, device=dev)
-        workspace, wp, wn = scratch(workspace, lib.kda_attn_workspace_bytes(B, hq, hkv, dh, width, page), dev)
+            lse = like(q, (B, hq), torch.float32)
+        workspace, wp, wn = scratch(workspace, lib.kda_attn_workspace_bytes(B, hq, hkv, dh, width, page), q)
         args = native.KdaAttnArgs(ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_table), ptr(seq_lens), ptr(out), ptr(lse),
                                   *strides, B, hq, hkv, dh, pages, page, width, DTYPES[q.dtype],
                                   1.0 / math.sqrt(dh) if scale is None else scale)
-        call = lambda: native.check(lib.kda_attn_decode(ctypes.byref(args), st, wp, wn))  # noqa: E731
-        checked(st, call) if check else call()
+        run(check, st, lib.kda_attn_decode, ctypes.byref(args), st, wp, wn)
     return (out, lse) if return_lse else out

@@ -4,7 +4,7 @@ import ctypes
 import torch
 
 from . import native
-from ._args import DTYPES, checked, dense, launch_on, offsets, on_device, ptr, rows, scratch
+from ._args import DTYPES, dense, launch_on, like, offsets, on_device, ptr, rows, run, scratch
 
 __all__ = ["ssm_fwd", "ssm_bwd", "ssm_decode"]
 
@@ -17,22 +17,23 @@ class _Sizes:
 def _check(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state):
     if u.dtype not in DTYPES or u.dim() != 2:
         raise ValueError(f"u: expected fp32, bf16 or fp16 [T, D], got {u.dtype} {tuple(u.shape)}")
-    dev, dt = u.device, u.dtype
+    dev, dt = u.get_device(), u.dtype
     s = _Sizes()
-    s.T, s.D = u.shape
+    s.T, s.D = td = tuple(u.shape)
     if A.dim() != 2 or not 1 <= A.shape[1] <= native.SSM_MAX_STATE:
         raise ValueError(f"A: expected fp32 [D, N] with N from 1 to {native.SSM_MAX_STATE}, got {tuple(A.shape)}")
     s.N = A.shape[1]
     if B.dim() != 3 or B.shape[1] < 1 or s.D % B.shape[1]:
         raise ValueError(f"B: expected [T, G, N] with G dividing the {s.D} channels, got {tuple(B.shape)}")
     s.G = B.shape[1]
-    strides = [rows("u", u, dt, (s.T, s.D), dev), rows("delta", delta, dt, (s.T, s.D), dev),
-               rows("B", B, dt, (s.T, s.G, s.N), dev), rows("C", C, dt, (s.T, s.G, s.N), dev), 0]
+    tgn = (s.T, s.G, s.N)
+    strides = [rows("u", u, dt, td, dev), rows("delta", delta, dt, td, dev), rows("B", B, dt, tgn, dev),
+               rows("C", C, dt, tgn, dev), 0]
     dense("A", A, torch.float32, (s.D, s.N), dev)
     if D is not None:
         dense("D", D, torch.float32, (s.D,), dev)
     if z is not None:
-        strides[4] = rows("z", z, dt, (s.T, s.D), dev)
+        strides[4] = rows("z", z, dt, td, dev)
     if delta_bias is not None:
         dense("delta_bias", delta_bias, torch.float32, (s.D,), dev)
     s.strides = strides
@@ -47,9 +48,9 @@ def check_ssm_fwd_args(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_se
     """Every check ssm_fwd makes before anything is launched; returns the sizes it found."""
     s = _check(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state)
     if out is not None:
-        dense("out", out, u.dtype, (s.T, s.D), u.device)
+        dense("out", out, u.dtype, (s.T, s.D), u.get_device())
     if final_state is not None:
-        dense("final_state", final_state, torch.float32, (s.S, s.D, s.N), u.device)
+        dense("final_state", final_state, torch.float32, (s.S, s.D, s.N), u.get_device())
     return s
 
 
@@ -78,20 +79,19 @@ def ssm_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_seqlens=None,
     allocates belong to its stream.
     """
     lib = native.load_library()
-    dev = u.device
+    dev = u.get_device()
     on_device("kda.ssm_fwd", dev)
     s = check_ssm_fwd_args(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, out, final_state)
     with launch_on(dev, stream) as st:
         if out is None:
-            out = torch.empty((s.T, s.D), dtype=u.dtype, device=dev)
+            out = like(u, (s.T, s.D))
         if not output_final_state:
             final_state = None
         elif final_state is None:
-            final_state = torch.empty((s.S, s.D, s.N), dtype=torch.float32, device=dev)
-        workspace, wp, wn = scratch(workspace, lib.kda_ssm_workspace_bytes(s.S, s.T, s.D, s.N, s.G), dev)
+            final_state = like(u, (s.S, s.D, s.N), torch.float32)
+        workspace, wp, wn = scratch(workspace, lib.kda_ssm_workspace_bytes(s.S, s.T, s.D, s.N, s.G), u)
         args = _args(s, u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, final_state, out, delta_softplus)
-        call = lambda: native.check(lib.kda_ssm_fwd(ctypes.byref(args), st, wp, wn))  # noqa: E731
-        checked(st, call) if check else call()
+        run(check, st, lib.kda_ssm_fwd, ctypes.byref(args), st, wp, wn)
     return out, final_state
 
 
@@ -105,9 +105,9 @@ def check_ssm_decode_args(u, delta, A, B, C, D=None, z=None, delta_bias=None, st
     s.S = s.T
     for name, t in (("state", state), ("state_out", state_out)):
         if isinstance(t, torch.Tensor):
-            dense(name, t, torch.float32, (s.S, s.D, s.N), u.device)
+            dense(name, t, torch.float32, (s.S, s.D, s.N), u.get_device())
     if out is not None:
-        dense("out", out, u.dtype, (s.T, s.D), u.device)
+        dense("out", out, u.dtype, (s.T, s.D), u.get_device())
     return s
 
 
@@ -117,16 +117,16 @@ def ssm_decode(u, delta, A, B, C, D=None, z=None, delta_bias=None, state=None, *
     [S, D, N] (None: zeros). state_out: "inplace" (update ``state``; a new tensor when state is None),
     None (not written), or a tensor. Returns (out [S, D], the updated state or None)."""
     lib = native.load_library()
-    dev = u.device
+    dev = u.get_device()
     on_device("kda.ssm_decode", dev)
     s = check_ssm_decode_args(u, delta, A, B, C, D, z, delta_bias, state, out, state_out)
     with launch_on(dev, stream) as st:
         if out is None:
-            out = torch.empty((s.T, s.D), dtype=u.dtype, device=dev)
+            out = like(u, (s.T, s.D))
         if isinstance(state_out, str):
-            state_out = state if state is not None else torch.empty((s.S, s.D, s.N), dtype=torch.float32, device=dev)
+            state_out = state if state is not None else like(u, (s.S, s.D, s.N), torch.float32)
         args = _args(s, u, delta, A, B, C, D, z, delta_bias, None, state, state_out, out, delta_softplus)
-        native.check(lib.kda_ssm_decode(ctypes.byref(args), st))
+        run(False, st, lib.kda_ssm_decode, ctypes.byref(args), st)
     return out, state_out
 
 
@@ -134,9 +134,9 @@ def check_ssm_bwd_args(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, c
                        d_final_state=None):
     """Every check ssm_bwd makes before anything is launched; returns the sizes it found and dy's row stride."""
     s = _check(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state)
-    stride = rows("dy", dy, u.dtype, (s.T, s.D), u.device)
+    stride = rows("dy", dy, u.dtype, (s.T, s.D), u.get_device())
     if d_final_state is not None:
-        dense("d_final_state", d_final_state, torch.float32, (s.S, s.D, s.N), u.device)
+        dense("d_final_state", d_final_state, torch.float32, (s.S, s.D, s.N), u.get_device())
     return s, stride
 
 
@@ -148,21 +148,20 @@ def ssm_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, cu_seqlens=N
     when need_d_initial_state is False); dz, dD and ddelta_bias are None without z, D and delta_bias. Needs
     nothing that the forward computed. The same results from run to run."""
     lib = native.load_library()
-    dev = u.device
+    dev = u.get_device()
     on_device("kda.ssm_bwd", dev)
     s, dy_stride = check_ssm_bwd_args(u, delta, A, B, C, dy, D, z, delta_bias, cu_seqlens, initial_state, d_final_state)
-    f32 = dict(dtype=torch.float32, device=dev)
+    f32 = torch.float32
     with launch_on(dev, stream) as st:
-        act = lambda *shape: torch.empty(shape, dtype=u.dtype, device=dev)  # noqa: E731
-        gr = dict(du=act(s.T, s.D), ddelta=act(s.T, s.D), dA=torch.empty((s.D, s.N), **f32), dB=act(s.T, s.G, s.N),
-                  dC=act(s.T, s.G, s.N), dD=torch.empty((s.D,), **f32) if D is not None else None,
-                  dz=act(s.T, s.D) if z is not None else None,
-                  ddelta_bias=torch.empty((s.D,), **f32) if delta_bias is not None else None,
-                  d_initial_state=torch.empty((s.S, s.D, s.N), **f32) if need_d_initial_state else None)
-        workspace, wp, wn = scratch(workspace, lib.kda_ssm_bwd_workspace_bytes(s.T, s.D, s.N, s.G), dev)
+        gr = dict(du=like(u, (s.T, s.D)), ddelta=like(u, (s.T, s.D)), dA=like(u, (s.D, s.N), f32), dB=like(u, (s.T, s.G, s.N)),
+                  dC=like(u, (s.T, s.G, s.N)), dD=like(u, (s.D,), f32) if D is not None else None,
+                  dz=like(u, (s.T, s.D)) if z is not None else None,
+                  ddelta_bias=like(u, (s.D,), f32) if delta_bias is not None else None,
+                  d_initial_state=like(u, (s.S, s.D, s.N), f32) if need_d_initial_state else None)
+        workspace, wp, wn = scratch(workspace, lib.kda_ssm_bwd_workspace_bytes(s.T, s.D, s.N, s.G), u)
         args = _args(s, u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, None, None, delta_softplus)
         grads = native.KdaSsmGrads(ptr(dy), ptr(d_final_state), ptr(gr["du"]), ptr(gr["ddelta"]), ptr(gr["dB"]), ptr(gr["dC"]),
                                    ptr(gr["dz"]), ptr(gr["dA"]), ptr(gr["dD"]), ptr(gr["ddelta_bias"]),
                                    ptr(gr["d_initial_state"]), dy_stride)
-        native.check(lib.kda_ssm_bwd(ctypes.byref(args), ctypes.byref(grads), st, wp, wn))
+        run(False, st, lib.kda_ssm_bwd, ctypes.byref(args), ctypes.byref(grads), st, wp, wn)
     return gr

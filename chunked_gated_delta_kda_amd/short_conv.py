@@ -5,7 +5,7 @@ import ctypes
 import torch
 
 from . import native
-from ._args import DTYPES, checked, dense, launch_on, offsets, on_device, ptr, rows, scratch
+from ._args import DTYPES, dense, launch_on, like, offsets, on_device, ptr, rows, run, scratch
 
 __all__ = ["conv_fwd", "conv_bwd", "conv_decode"]
 
@@ -18,7 +18,7 @@ def _check(x, weight, bias, cu_seqlens, initial_state, activation):
         raise ValueError('activation: "silu" or None')
     if x.dtype not in DTYPES or x.dim() != 2:
         raise ValueError(f"x: expected fp32, bf16 or fp16 [T, C], got {x.dtype} {tuple(x.shape)}")
-    dev = x.device
+    dev = x.get_device()
     T, C = x.shape
     if weight.dim() != 2 or not 2 <= weight.shape[1] <= native.CONV_MAX_WIDTH:
         raise ValueError(f"weight: expected fp32 [C, W] with W from 2 to {native.CONV_MAX_WIDTH}, got {tuple(weight.shape)}")
@@ -38,9 +38,9 @@ def check_conv_fwd_args(x, weight, bias=None, cu_seqlens=None, initial_state=Non
     """Every check conv_fwd makes before anything is launched; returns (T, C, W, N, row stride of x)."""
     T, C, W, N, stride = _check(x, weight, bias, cu_seqlens, initial_state, activation)
     if out is not None:
-        dense("out", out, x.dtype, (T, C), x.device)
+        dense("out", out, x.dtype, (T, C), x.get_device())
     if final_state is not None:
-        dense("final_state", final_state, x.dtype, (N, W - 1, C), x.device)
+        dense("final_state", final_state, x.dtype, (N, W - 1, C), x.get_device())
     return T, C, W, N, stride
 
 
@@ -60,20 +60,19 @@ def conv_fwd(x, weight, bias=None, cu_seqlens=None, initial_state=None, output_f
     allocates belong to its stream.
     """
     lib = native.load_library()
-    dev = x.device
+    dev = x.get_device()
     on_device("kda.conv_fwd", dev)
     T, C, W, N, stride = check_conv_fwd_args(x, weight, bias, cu_seqlens, initial_state, activation, out, final_state)
     with launch_on(dev, stream) as st:
         if out is None:
-            out = torch.empty((T, C), dtype=x.dtype, device=dev)
+            out = like(x, (T, C))
         if not output_final_state:
             final_state = None
         elif final_state is None:
-            final_state = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev)
+            final_state = like(x, (N, W - 1, C))
         args = native.KdaConvArgs(ptr(x), ptr(weight), ptr(bias), ptr(cu_seqlens), ptr(initial_state), ptr(final_state),
                                   ptr(out), stride, N, T, C, W, DTYPES[x.dtype], _ACTIVATIONS[activation])
-        call = lambda: native.check(lib.kda_conv_fwd(ctypes.byref(args), st))  # noqa: E731
-        checked(st, call) if check else call()
+        run(check, st, lib.kda_conv_fwd, ctypes.byref(args), st)
     return out, final_state
 
 
@@ -86,9 +85,9 @@ def check_conv_decode_args(x, weight, bias=None, state=None, activation="silu", 
         raise ValueError('state_out: "inplace", None or a tensor')
     for name, t in (("state", state), ("state_out", state_out)):
         if isinstance(t, torch.Tensor):
-            dense(name, t, x.dtype, (T, W - 1, C), x.device)
+            dense(name, t, x.dtype, (T, W - 1, C), x.get_device())
     if out is not None:
-        dense("out", out, x.dtype, (T, C), x.device)
+        dense("out", out, x.dtype, (T, C), x.get_device())
     return T, C, W, stride
 
 
@@ -98,17 +97,17 @@ def conv_decode(x, weight, bias=None, state=None, *, activation="silu", out=None
     ``state``; a new tensor when state is None), None (not written), or a tensor.
     Returns (out [N, C], the updated state or None)."""
     lib = native.load_library()
-    dev = x.device
+    dev = x.get_device()
     on_device("kda.conv_decode", dev)
     N, C, W, stride = check_conv_decode_args(x, weight, bias, state, activation, out, state_out)
     with launch_on(dev, stream) as st:
         if out is None:
-            out = torch.empty((N, C), dtype=x.dtype, device=dev)
+            out = like(x, (N, C))
         if isinstance(state_out, str):
-            state_out = state if state is not None else torch.empty((N, W - 1, C), dtype=x.dtype, device=dev)
+            state_out = state if state is not None else like(x, (N, W - 1, C))
         args = native.KdaConvArgs(ptr(x), ptr(weight), ptr(bias), None, ptr(state), ptr(state_out), ptr(out), stride, N, N,
                                   C, W, DTYPES[x.dtype], _ACTIVATIONS[activation])
-        native.check(lib.kda_conv_decode(ctypes.byref(args), st))
+        run(False, st, lib.kda_conv_decode, ctypes.byref(args), st)
     return out, state_out
 
 
@@ -116,9 +115,9 @@ def check_conv_bwd_args(x, weight, dy, bias=None, cu_seqlens=None, initial_state
                         activation="silu"):
     """Every check conv_bwd makes before anything is launched; returns (T, C, W, N, row strides of x and dy)."""
     T, C, W, N, stride = _check(x, weight, bias, cu_seqlens, initial_state, activation)
-    dy_stride = rows("dy", dy, x.dtype, (T, C), x.device)
+    dy_stride = rows("dy", dy, x.dtype, (T, C), x.get_device())
     if d_final_state is not None:
-        dense("d_final_state", d_final_state, torch.float32, (N, W - 1, C), x.device)
+        dense("d_final_state", d_final_state, torch.float32, (N, W - 1, C), x.get_device())
     return T, C, W, N, stride, dy_stride
 
 
@@ -129,19 +128,18 @@ def conv_bwd(x, weight, dy, bias=None, cu_seqlens=None, initial_state=None, d_fi
     dtype), dweight (fp32 [C, W]), dbias (fp32 [C], None without a bias) and d_initial_state (fp32
     [N, W-1, C], or None when need_d_initial_state is False). The same results from run to run."""
     lib = native.load_library()
-    dev = x.device
+    dev = x.get_device()
     on_device("kda.conv_bwd", dev)
     T, C, W, N, stride, dy_stride = check_conv_bwd_args(x, weight, dy, bias, cu_seqlens, initial_state, d_final_state,
                                                         activation)
-    f32 = dict(dtype=torch.float32, device=dev)
+    f32 = torch.float32
     with launch_on(dev, stream) as st:
-        gr = dict(dx=torch.empty((T, C), dtype=x.dtype, device=dev), dweight=torch.empty((C, W), **f32),
-                  dbias=torch.empty((C,), **f32) if bias is not None else None,
-                  d_initial_state=torch.empty((N, W - 1, C), **f32) if need_d_initial_state else None)
-        workspace, wp, wn = scratch(workspace, lib.kda_conv_bwd_workspace_bytes(T, C, W), dev)
+        gr = dict(dx=like(x, (T, C)), dweight=like(x, (C, W), f32), dbias=like(x, (C,), f32) if bias is not None else None,
+                  d_initial_state=like(x, (N, W - 1, C), f32) if need_d_initial_state else None)
+        workspace, wp, wn = scratch(workspace, lib.kda_conv_bwd_workspace_bytes(T, C, W), x)
         args = native.KdaConvArgs(ptr(x), ptr(weight), ptr(bias), ptr(cu_seqlens), ptr(initial_state), None, None, stride,
                                   N, T, C, W, DTYPES[x.dtype], _ACTIVATIONS[activation])
         grads = native.KdaConvGrads(ptr(dy), ptr(d_final_state), ptr(gr["dx"]), ptr(gr["dweight"]), ptr(gr["dbias"]),
                                     ptr(gr["d_initial_state"]), dy_stride)
-        native.check(lib.kda_conv_bwd(ctypes.byref(args), ctypes.byref(grads), st, wp, wn))
+        run(False, st, lib.kda_conv_bwd, ctypes.byref(args), ctypes.byref(grads), st, wp, wn)
     return gr
