@@ -40,15 +40,15 @@ template <int DT, int K, int M, bool OUT> struct Raw {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int64_t r = (int64_t)(t + k < stop ? t + k : stop - 1) * sizeof(E);   // past the end: the last row again
-            delta[k] = at<DT>(d0 + r * a.delta_stride, ch);
-            u[k] = at<DT>(u0 + r * a.u_stride, ch);
-            if (OUT && a.z) z[k] = at<DT>(z0 + r * a.z_stride, ch);
+            delta[k] = at<DT>(uniform(d0 + r * a.delta_stride), ch);
+            u[k] = at<DT>(uniform(u0 + r * a.u_stride), ch);
+            if (OUT && a.z) z[k] = at<DT>(uniform(z0 + r * a.z_stride), ch);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const int n = p.nat_state(m);
                 const uint32_t st = (uint32_t)(n < p.N ? n : p.N - 1) * sizeof(E);
-                B[k][m] = at<DT>(B0 + r * a.B_stride, st);
-                if (OUT) C[k][m] = at<DT>(C0 + r * a.C_stride, st);
+                B[k][m] = at<DT>(uniform(B0 + r * a.B_stride), st);
+                if (OUT) C[k][m] = at<DT>(uniform(C0 + r * a.C_stride), st);
             }
         }
     }
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_wide_kernel(const kda_ssm_args
         for (int k = 0; k < K; ++k) {
             float v = __builtin_fmaf(skip, u[k], y[k]);
             if (a.z) v *= z[k] * sigmoid_f(z[k]);
-            if (whole || k < count) *reinterpret_cast<E *>(out + (int64_t)k * a.channels * sizeof(E) + ch) = (E)v;
+            if (whole || k < count) put(uniform(out + (int64_t)k * a.channels * sizeof(E)), ch, (E)v);
         }
     };
     while (true) {
@@ -279,8 +279,14 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_wide_kernel(const kda_ssm_args
 //   3. a wave runs its tokens again from its input state, for y.
 // NB: 16-state blocks. The four blocks of a product are TP = 4/NB tokens by NB blocks of states; product
 // q holds tokens TP q + b / NB, states 16 (b % NB) + 4 g + j, channel i.
+#ifndef SW
+#define SW 12
+#endif
+#ifndef SQ
+#define SQ 2
+#endif
 template <int NB> struct Scan {
-    static constexpr int W = 12, KT = 8 / NB, TP = 4 / NB, Q = 2;   // waves, tokens of a wave, of a product, products
+    static constexpr int W = SW, Q = SQ, KT = 4 * Q / NB, TP = 4 / NB;   // waves, tokens of a wave, of a product, products
     static constexpr int NS = 16 * NB, PAIRS = 256 * NB, SROW = KT + 4, STEP = W * KT;
 };
 template <int NB> struct ScanLds {
@@ -520,7 +526,7 @@ __global__ __launch_bounds__(64 * Scan<NB>::W) void ssm_scan_kernel(const kda_ss
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const float v = __builtin_fmaf(skip, uc[q], y[q]) * gc[q];
-            if (TP * q + tl < left) *reinterpret_cast<E *>(out + (int64_t)(TP * q) * a.channels * es + oo) = (E)v;
+            if (TP * q + tl < left) put(uniform(out + (int64_t)(TP * q) * a.channels * es), oo, (E)v);
         }
         if (!more) break;
         cur = nxt, nxt = after;

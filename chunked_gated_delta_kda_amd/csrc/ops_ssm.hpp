@@ -28,10 +28,22 @@ namespace ssm {
 
 constexpr int WAVES = 4;      // independent waves of a block
 
-// One element of a row, from the row's uniform address and the lane's own offset in bytes.
+// One element of a row, from the row's address and the lane's own offset in bytes.
 template <int DT> __device__ __forceinline__ typename Elem<DT>::type at(const char *row, uint32_t bytes) {
     return *reinterpret_cast<const typename Elem<DT>::type *>(row + bytes);
 }
+// A row's address that all lanes share, held in scalar registers (and known to be global memory): an
+// access to it plus a lane's 32-bit offset then needs no address arithmetic of the lanes.
+#define KDA_GLOBAL __attribute__((address_space(1)))
+template <class P> __device__ __forceinline__ KDA_GLOBAL P *uniform(P *row) {
+    KDA_GLOBAL P *g = (KDA_GLOBAL P *)row;
+    asm("" : "+s"(g));
+    return g;
+}
+template <int DT> __device__ __forceinline__ typename Elem<DT>::type at(KDA_GLOBAL const char *row, uint32_t bytes) {
+    return *(KDA_GLOBAL const typename Elem<DT>::type *)(row + bytes);
+}
+template <class E> __device__ __forceinline__ void put(KDA_GLOBAL char *row, uint32_t bytes, E v) { *(KDA_GLOBAL E *)(row + bytes) = v; }
 
 template <int DT> __device__ __forceinline__ float load1(const void *p, int64_t off) {
     return (float)reinterpret_cast<const typename Elem<DT>::type *>(p)[off];

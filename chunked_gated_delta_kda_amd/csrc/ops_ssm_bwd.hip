@@ -65,16 +65,16 @@ template <int DT, int M> struct RawBwd {
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             const int64_t r = (int64_t)(t + k < stop ? t + k : stop - 1) * sizeof(E);
-            delta[k] = at<DT>(d0 + r * a.delta_stride, ch);
-            u[k] = at<DT>(u0 + r * a.u_stride, ch);
-            dy[k] = at<DT>(y0 + r * d.dy_stride, ch);
-            if (a.z) z[k] = at<DT>(z0 + r * a.z_stride, ch);
+            delta[k] = at<DT>(uniform(d0 + r * a.delta_stride), ch);
+            u[k] = at<DT>(uniform(u0 + r * a.u_stride), ch);
+            dy[k] = at<DT>(uniform(y0 + r * d.dy_stride), ch);
+            if (a.z) z[k] = at<DT>(uniform(z0 + r * a.z_stride), ch);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const int n = p.nat_state(m);
                 const uint32_t st = (uint32_t)(n < p.N ? n : p.N - 1) * sizeof(E);
-                B[k][m] = at<DT>(B0 + r * a.B_stride, st);
-                C[k][m] = at<DT>(C0 + r * a.C_stride, st);
+                B[k][m] = at<DT>(uniform(B0 + r * a.B_stride), st);
+                C[k][m] = at<DT>(uniform(C0 + r * a.C_stride), st);
             }
         }
     }
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_ar
 #pragma unroll
         for (int k = 0; k < KR; ++k) {
             const bool on = tb + k >= gs && tb + k < ge;
-            char *const row = on ? (char *)(rows + k * 2 * NP) : none;
+            KDA_GLOBAL char *const row = uniform(on ? (char *)(rows + k * 2 * NP) : none);
             float sc[CB], dyc[CB], B[M], r[CB];
             read_steps<CB>(S.s[k], p.i, sc);
             read_steps<CB>(S.dy[k], p.i, dyc);
@@ -404,14 +404,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_ar
                             dC[j] = __builtin_fmaf(dyc[b], hv, dC[j]);
                         }
                     }
-                    *reinterpret_cast<float *>(row + (NP + 16 * (nb + m * NB)) * 4 + srow) =
-                        row_sum4(dC[0], dC[1], dC[2], dC[3], odd, upper);
+                    put(row + (NP + 16 * (nb + m * NB)) * 4, srow, row_sum4(dC[0], dC[1], dC[2], dC[3], odd, upper));
                 }
             }
             if (a.z) {
                 const float y = __builtin_fmaf(skip, S.u[k][nat], to_natural<CB>(r));
-                char *const out = on ? (char *)d.dz + (int64_t)(tb + k) * a.channels * sizeof(E) : none;
-                *reinterpret_cast<E *>(out + ch) = (E)(S.dz[k][nat] * y);
+                put(uniform(on ? (char *)d.dz + (int64_t)(tb + k) * a.channels * sizeof(E) : none), ch, (E)(S.dz[k][nat] * y));
             }
         }
         // and back; what the next cell needs is fetched half way, when registers have come free
@@ -425,7 +423,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_ar
                     raw.template load<CB>(a, d, p, tb - KR, t1);
                 }
             }
-            char *const row = on ? (char *)(rows + k * 2 * NP) : none;
+            KDA_GLOBAL char *const row = uniform(on ? (char *)(rows + k * 2 * NP) : none);
             float sc[CB], xc[CB], C[M], r1[CB], r2[CB];
             read_steps<CB>(S.s[k], p.i, sc);
             read_steps<CB>(S.x[k], p.i, xc);
@@ -455,15 +453,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_ar
                             g[m][q] = dh * exp2_f(A2[m][q] * sc[b]);
                         }
                     }
-                    *reinterpret_cast<float *>(row + 16 * (nb + m * NB) * 4 + srow) = row_sum4(dB[0], dB[1], dB[2], dB[3], odd, upper);
+                    put(row + 16 * (nb + m * NB) * 4, srow, row_sum4(dB[0], dB[1], dB[2], dB[3], odd, upper));
                 }
             }
             const float into = to_natural<CB>(r1), dec = to_natural<CB>(r2) * LN2_F;
             const float u = S.u[k][nat], s = S.s[k][nat];
             const float ddelta = __builtin_fmaf(u, into, dec) * S.sig[k][nat];
             const int64_t o = (int64_t)(tb + k) * a.channels * sizeof(E);
-            *reinterpret_cast<E *>((on ? (char *)d.du + o : none) + ch) = (E)__builtin_fmaf(s, into, skip * dy);
-            *reinterpret_cast<E *>((on ? (char *)d.ddelta + o : none) + ch) = (E)ddelta;
+            put(uniform(on ? (char *)d.du + o : none), ch, (E)__builtin_fmaf(s, into, skip * dy));
+            put(uniform(on ? (char *)d.ddelta + o : none), ch, (E)ddelta);
             dD = __builtin_fmaf(dy, u, dD);
             dbias += on ? ddelta : 0.0f;
         }
