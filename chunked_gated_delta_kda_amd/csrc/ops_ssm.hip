@@ -127,47 +127,17 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_tile_kernel(const kda_ssm_args
     if (p.mine) sums[(int64_t)tile * a.channels + p.ch] = sum;
 }
 
-// The state every tile starts from: h <- e^{A S} h + E per (channel, state), tile after tile; loads
-// of AHEAD tiles are in flight together.
 template <int CB, int M>
-__global__ __launch_bounds__(256) void ssm_join_kernel(const kda_ssm_args a, float *ws, const float *sums,
-                                                       const int32_t *resets, int tiles, int blocks) {
-    constexpr int AHEAD = 8;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int unit = blockIdx.x * 4 + wave;                 // (block, register)
-    if (unit >= blocks * 16 * M) return;
-    const int block = unit / (16 * M), r = unit - block * (16 * M);
-    const Place<CB, M> p(a, block);
-    const int m = r / 16, b = (r % 16) / 4, j = r % 4;
-    const int c = p.copied(b), n = p.state(m, b, j);
-    const float A2 = n < p.N ? a.A[(int64_t)c * p.N + n] * LOG2E_F : 0.0f;
-    const int64_t step = (int64_t)blocks * 1024 * M;
-    float *at = tile_state<M>(ws, 0, blocks, block) + r * 64 + p.lane;
-    float h = 0.0f;
-    for (int k0 = 0; k0 < tiles; k0 += AHEAD) {
-        float E[AHEAD], S[AHEAD];
-        int reset[AHEAD];
-#pragma unroll
-        for (int q = 0; q < AHEAD; ++q) {
-            const int k = k0 + q < tiles ? k0 + q : tiles - 1;
-            E[q] = at[k * step];
-            S[q] = sums[(int64_t)k * a.channels + c];
-            reset[q] = resets[k];
-        }
-#pragma unroll
-        for (int q = 0; q < AHEAD; ++q) {
-            if (k0 + q < tiles) {
-                at[(k0 + q) * step] = h;
-                h = reset[q] ? E[q] : __builtin_fmaf(exp2_f(A2 * S[q]), h, E[q]);
-            }
-        }
-    }
+__global__ __launch_bounds__(256) void ssm_join_kernel(const kda_ssm_args a, float *ws, const float *sums, const int32_t *resets,
+                                                       int tiles, int blocks) {
+    __shared__ JoinLds lds;
+    join_tiles<CB, M>(a, lds, ws, sums, resets, 1, tiles, blocks, blockIdx.x / (16 * M), blockIdx.x % (16 * M), false);
 }
 
 // The scan for state sizes over 32 and for short sequences: a wave by itself, all states of its channels
 // in its registers, from the joined states of its tile.
 template <int DT, int CB, int M>
-__global__ __launch_bounds__(64 * WAVES) void ssm_wide_kernel(const kda_ssm_args a, const float *ws, int32_t *err, int L,
+__global__ __launch_bounds__(64 * WAVES, M == 1 ? 4 : 1) void ssm_wide_kernel(const kda_ssm_args a, const float *ws, int32_t *err, int L,
                                                               int tiles, int blocks) {
     using E = typename Elem<DT>::type;
     constexpr int K = K_SCAN;
@@ -269,7 +239,7 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_wide_kernel(const kda_ssm_args
 }
 
 // The scan in one launch, for state sizes up to 32 where the channels alone fill the card or the batch is
-// short (by_blocks): a block of W = 12 waves owns 16 channels and walks all tokens in steps of up to W KT of
+// short (by_blocks): a block of W = 8 waves owns 16 channels and walks all tokens in steps of up to W KT of
 // one sequence, each wave KT of them. The exponential of a (token, channel, state) is formed once and
 // one pass over the inputs is enough. Per step:
 //   1. a wave forms its tokens' decays and inputs, kept in registers, and runs them from a zero
@@ -279,14 +249,8 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_wide_kernel(const kda_ssm_args
 //   3. a wave runs its tokens again from its input state, for y.
 // NB: 16-state blocks. The four blocks of a product are TP = 4/NB tokens by NB blocks of states; product
 // q holds tokens TP q + b / NB, states 16 (b % NB) + 4 g + j, channel i.
-#ifndef SW
-#define SW 12
-#endif
-#ifndef SQ
-#define SQ 2
-#endif
 template <int NB> struct Scan {
-    static constexpr int W = SW, Q = SQ, KT = 4 * Q / NB, TP = 4 / NB;   // waves, tokens of a wave, of a product, products
+    static constexpr int W = 8, Q = 4, KT = 4 * Q / NB, TP = 4 / NB;   // waves, tokens of a wave, of a product, products
     static constexpr int NS = 16 * NB, PAIRS = 256 * NB, SROW = KT + 4, STEP = W * KT;
 };
 template <int NB> struct ScanLds {
@@ -627,14 +591,14 @@ bool by_blocks(int64_t T, int64_t S, int64_t D, int64_t N, int64_t G) {
 }
 
 template <int DT, int CB, int M>
-hipError_t join_tiles(const kda_ssm_args &a, float *ws, int32_t *err, int L, int64_t tiles, int64_t blocks, hipStream_t st) {
+hipError_t tile_states(const kda_ssm_args &a, float *ws, int32_t *err, int L, int64_t tiles, int64_t blocks, hipStream_t st) {
     const int64_t units = tiles * blocks;
     float *sums = ws + units * 1024 * M;
     int32_t *resets = (int32_t *)(sums + tiles * a.channels);
     ssm_tile_kernel<DT, CB, M><<<dim3((unsigned)ceil_div(units, WAVES)), 64 * WAVES, 0, st>>>(a, ws, sums, resets, err, L, (int)tiles,
                                                                                              (int)blocks);
     if (hipError_t e = hipGetLastError()) return e;
-    ssm_join_kernel<CB, M><<<dim3((unsigned)ceil_div(blocks * 16 * M, 4)), 256, 0, st>>>(a, ws, sums, resets, (int)tiles, (int)blocks);
+    ssm_join_kernel<CB, M><<<dim3((unsigned)(blocks * 16 * M)), 256, 0, st>>>(a, ws, sums, resets, (int)tiles, (int)blocks);
     return hipGetLastError();
 }
 
@@ -653,7 +617,7 @@ hipError_t fwd_wide(const kda_ssm_args &a, float *ws, int32_t *err, hipStream_t 
     const int L = tile_len(T, blocks);
     const int64_t tiles = T ? ceil_div(T, L) : 1;
     if (tiles > 1)
-        if (hipError_t e = join_tiles<DT, CB, M>(a, ws, err, L, tiles, blocks, st)) return e;
+        if (hipError_t e = tile_states<DT, CB, M>(a, ws, err, L, tiles, blocks, st)) return e;
     ssm_wide_kernel<DT, CB, M><<<dim3((unsigned)ceil_div(tiles * blocks, WAVES)), 64 * WAVES, 0, st>>>(a, ws, err, L, (int)tiles,
                                                                                                       (int)blocks);
     return hipGetLastError();

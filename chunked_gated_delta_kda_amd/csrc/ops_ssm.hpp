@@ -19,6 +19,8 @@
 // few KiB of LDS that only this wave touches.
 #pragma once
 
+#include <type_traits>
+
 #include "ops_common.hpp"
 #include "ops_launch.hpp"
 
@@ -171,6 +173,60 @@ template <int CB> __device__ __forceinline__ void read_steps(const float *row, i
 #pragma unroll
         for (int b = 0; b < CB; ++b) s[b] = row[CB * i + b];
     }
+}
+
+// The states that the tiles start from: the tiles' maps h -> e^{A S} h + E (E alone where `alone` says so) one
+// after another, from h = 0, for one register (r) of one block's lanes: what enters a tile takes its E's place.
+// back: from the last tile to the first. The four waves of the calling block take a quarter of the tiles each:
+// their quarters' maps first, then the states, so that the chain of loads is half as long as the tiles. Loads
+// of AHEAD tiles are in flight together.
+struct JoinLds {
+    float P[4][64], E[4][64];
+    int cut[4];
+};
+template <int CB, int M>
+__device__ __forceinline__ void join_tiles(const kda_ssm_args &a, JoinLds &lds, float *states, const float *sums, const int32_t *alone,
+                                           int alone_step, int tiles, int blocks, int block, int r, bool back) {
+    constexpr int AHEAD = 8;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place<CB, M> p(a, block);
+    const int c = p.copied((r % 16) / 4), n = p.state(r / 16, (r % 16) / 4, r % 4);
+    const float A2 = n < p.N ? a.A[(int64_t)c * p.N + n] * LOG2E_F : 0.0f;
+    const int64_t step = (int64_t)blocks * 1024 * M;
+    float *at = states + (int64_t)block * (1024 * M) + r * 64 + p.lane;
+    const int quarter = (tiles + 3) / 4, lo = w * quarter, hi = lo + quarter < tiles ? lo + quarter : tiles;
+    float P = 1.0f, h = 0.0f;
+    bool cut = false;
+    auto walk = [&](auto write) {
+        for (int k0 = lo; k0 < hi; k0 += AHEAD) {
+            float E[AHEAD], S[AHEAD];
+            int al[AHEAD];
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) {
+                const int f = k0 + q < hi ? k0 + q : hi - 1, k = back ? tiles - 1 - f : f;
+                E[q] = at[k * step];
+                S[q] = sums[(int64_t)k * a.channels + c];
+                al[q] = alone[k * alone_step];
+            }
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) {
+                if (k0 + q < hi) {
+                    const int k = back ? tiles - 1 - (k0 + q) : k0 + q;
+                    if (write) at[k * step] = h;
+                    const float d = exp2_f(A2 * S[q]);
+                    if (!write) P *= d, cut = cut || al[q];
+                    h = al[q] ? E[q] : __builtin_fmaf(d, h, E[q]);
+                }
+            }
+        }
+    };
+    walk(std::false_type{});
+    lds.P[w][p.lane] = P, lds.E[w][p.lane] = h;
+    if (p.lane == 0) lds.cut[w] = cut;
+    __syncthreads();
+    h = 0.0f;
+    for (int v = 0; v < w; ++v) h = lds.cut[v] ? lds.E[v][p.lane] : __builtin_fmaf(lds.P[v][p.lane], h, lds.E[v][p.lane]);
+    walk(std::true_type{});
 }
 
 // Host side: the form of a state size, and the tiles of a batch.

@@ -239,40 +239,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_tile_kernel(const kda_s
 // every tile's end from the tiles behind it, in G's place.
 template <int CB, int M>
 __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(const kda_ssm_args a, float *ws, const Layout lay, int tiles, int blocks) {
-    constexpr int AHEAD = 8;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int unit = blockIdx.x * 4 + wave;
-    if (unit >= blocks * 16 * M) return;
-    const int block = unit / (16 * M), r = unit - block * (16 * M);
-    const Place<CB, M> p(a, block);
-    const int m = r / 16, b = (r % 16) / 4, j = r % 4;
-    const int c = p.copied(b), n = p.state(m, b, j);
-    const float A2 = n < p.N ? a.A[(int64_t)c * p.N + n] * LOG2E_F : 0.0f;
+    __shared__ JoinLds lds;
     const bool back = blockIdx.y == 1;
-    const int64_t step = (int64_t)blocks * 1024 * M;
-    float *at = ws + (back ? lay.grad : lay.end_state) + (int64_t)block * (1024 * M) + r * 64 + p.lane;
-    const float *sums = ws + lay.first_sums;
-    const int32_t *flags = reinterpret_cast<const int32_t *>(ws + lay.flags) + (back ? 1 : 0);
-    float h = 0.0f;
-    for (int k0 = 0; k0 < tiles; k0 += AHEAD) {
-        float E[AHEAD], S[AHEAD];
-        int alone[AHEAD];
-#pragma unroll
-        for (int q = 0; q < AHEAD; ++q) {
-            const int f = k0 + q < tiles ? k0 + q : tiles - 1, k = back ? tiles - 1 - f : f;
-            E[q] = at[k * step];
-            S[q] = sums[(int64_t)k * a.channels + c];
-            alone[q] = flags[2 * k];
-        }
-#pragma unroll
-        for (int q = 0; q < AHEAD; ++q) {
-            if (k0 + q < tiles) {
-                const int k = back ? tiles - 1 - (k0 + q) : k0 + q;
-                at[k * step] = h;
-                h = alone[q] ? E[q] : __builtin_fmaf(exp2_f(A2 * S[q]), h, E[q]);
-            }
-        }
-    }
+    join_tiles<CB, M>(a, lds, ws + (back ? lay.grad : lay.end_state), ws + lay.first_sums,
+                      reinterpret_cast<const int32_t *>(ws + lay.flags) + (back ? 1 : 0), 2, tiles, blocks, blockIdx.x / (16 * M),
+                      blockIdx.x % (16 * M), back);
 }
 
 // Sums of four values over the 16 lanes of a row: in lane i that of v[i % 4].
@@ -552,7 +523,7 @@ hipError_t bwd_form(const kda_ssm_args &a, const kda_ssm_grads &d, float *ws, in
     if (T) {
         ssm_bwd_tile_kernel<DT, CB, M><<<grid, 64 * WAVES, 0, st>>>(a, d, ws, lay, err, L, (int)tiles, (int)blocks);
         if (hipError_t e = hipGetLastError()) return e;
-        ssm_bwd_join_kernel<CB, M><<<dim3((unsigned)ceil_div(blocks * 16 * M, 4), 2), 256, 0, st>>>(a, ws, lay, (int)tiles, (int)blocks);
+        ssm_bwd_join_kernel<CB, M><<<dim3((unsigned)(blocks * 16 * M), 2), 256, 0, st>>>(a, ws, lay, (int)tiles, (int)blocks);
         if (hipError_t e = hipGetLastError()) return e;
     }
     ssm_bwd_kernel<DT, CB, M><<<grid, 64 * WAVES, 0, st>>>(a, d, ws, lay, L, (int)tiles, (int)blocks);
