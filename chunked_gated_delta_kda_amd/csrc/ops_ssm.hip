@@ -101,7 +101,7 @@ __global__ __launch_bounds__(64 * WAVES) void ssm_tile_kernel(const kda_ssm_args
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const float d = (float)raw.delta[k] + bias;
-            float s = a.delta_softplus ? softplus_f(d) : d;
+            float s = step_of(d, a.delta_softplus);
             x[k] = s * (float)raw.u[k];
             const bool step = k < count;
             s = step ? s : 0.0f, x[k] = step ? x[k] : 0.0f;    // no step: e^0 h + 0 (B too: what is repeated may be infinite)
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(64 * WAVES, M == 1 ? 4 : 1) void ssm_wide_kernel(co
     float *steps = lds[wave], *rows = lds[wave] + K * 16 * CB;
     const uint32_t ch = (uint32_t)p.ch * sizeof(E);
     int t = t0;
-    Raw<DT, K, M, true> raw;
+    Raw<DT, K, M, true> raw{};
     raw.load(a, p, t, t1);
     // `count` tokens of one sequence
     auto stage = [&](int count, auto whole) {
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * WAVES, M == 1 ? 4 : 1) void ssm_wide_kernel(co
         for (int k = 0; k < K; ++k) {
             const bool on = whole || k < count;     // the next sequence's rows stay out of this state
             const float d = (float)raw.delta[k] + bias;
-            const float s = a.delta_softplus ? softplus_f(d) : d;
+            const float s = step_of(d, a.delta_softplus);
             u[k] = (float)raw.u[k];
             x[k] = on ? s * u[k] : 0.0f;
             z[k] = a.z ? (float)raw.z[k] : 0.0f;
@@ -217,8 +217,8 @@ __global__ __launch_bounds__(64 * WAVES, M == 1 ? 4 : 1) void ssm_wide_kernel(co
         char *out = (char *)a.out + (int64_t)from * a.channels * sizeof(E);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float v = __builtin_fmaf(skip, u[k], y[k]);
-            if (a.z) v *= z[k] * sigmoid_f(z[k]);
+            const float gated = z[k] * sigmoid_f(z[k]);
+            const float v = __builtin_fmaf(skip, u[k], y[k]) * (a.z ? gated : 1.0f);
             if (whole || k < count) put(uniform(out + (int64_t)k * a.channels * sizeof(E)), ch, (E)v);
         }
     };
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(64 * Scan<NB>::W) void ssm_scan_kernel(const kda_ss
     const char *const u0 = (const char *)a.u, *const d0 = (const char *)a.delta, *const z0 = (const char *)a.z;
     const char *const B0 = (const char *)a.B + (int64_t)group * N * es, *const C0 = (const char *)a.C + (int64_t)group * N * es;
     const bool has_z = a.z != nullptr;
-    E rdelta[Q], ru[Q], rz[Q], rB[Q], rC[Q];
+    E rdelta[Q], ru[Q], rz[Q] = {}, rB[Q], rC[Q];
     auto load = [&](const Step &s) {
         const int t = s.t + w * KT;
         if (t + KT <= T) {
@@ -377,11 +377,12 @@ __global__ __launch_bounds__(64 * Scan<NB>::W) void ssm_scan_kernel(const kda_ss
             const int k = TP * q + tl;
             const bool is = k < left;         // past the step's end: no step, nothing in (B too: what lies there may be infinite)
             const float d = (float)rdelta[q] + bias;
-            float s = a.delta_softplus ? softplus_f(d) : d;
+            float s = step_of(d, a.delta_softplus);
             s = is ? s : 0.0f;
             u[q] = is ? (float)ru[q] : 0.0f;
             x[q] = s * u[q];
-            gate[q] = has_z ? (float)rz[q] * sigmoid_f((float)rz[q]) : 1.0f;
+            const float gated = (float)rz[q] * sigmoid_f((float)rz[q]);
+            gate[q] = has_z ? gated : 1.0f;
             Bq[q] = is && state_in ? (float)rB[q] : 0.0f;
             lds.steps[w][i * SROW + k] = s;
             lds.C[w][turn][k * NS + nat_st] = state_in ? (float)rC[q] : 0.0f;

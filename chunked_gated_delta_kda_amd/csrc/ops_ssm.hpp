@@ -47,6 +47,13 @@ template <int DT> __device__ __forceinline__ typename Elem<DT>::type at(KDA_GLOB
 }
 template <class E> __device__ __forceinline__ void put(KDA_GLOBAL char *row, uint32_t bytes, E v) { *(KDA_GLOBAL E *)(row + bytes) = v; }
 
+// The step of delta + bias. Both forms are computed and one is taken: a branch here would keep the
+// compiler from interleaving the tokens of a stage.
+__device__ __forceinline__ float step_of(float d, bool softplus) {
+    const float s = softplus_f(d);
+    return softplus ? s : d;
+}
+
 template <int DT> __device__ __forceinline__ float load1(const void *p, int64_t off) {
     return (float)reinterpret_cast<const typename Elem<DT>::type *>(p)[off];
 }

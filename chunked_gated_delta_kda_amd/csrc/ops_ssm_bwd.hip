@@ -97,13 +97,10 @@ __device__ __forceinline__ void stage(StageBwd<CB, M> &S, const RawBwd<DT, M> &r
     for (int k = 0; k < KR_OF<M>; ++k) {
         const bool on = k >= lo && k < hi;
         const float d = (float)raw.delta[k] + bias, u = (float)raw.u[k], dy = (float)raw.dy[k];
-        float s = d, sig = 1.0f, g = dy, dz = 0.0f;
-        if (a.delta_softplus) s = softplus_f(d), sig = sigmoid_f(d);
-        if (a.z) {
-            const float z = (float)raw.z[k], sz = sigmoid_f(z);
-            g = dy * z * sz;
-            dz = dy * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
-        }
+        const float sd = sigmoid_f(d), sig = a.delta_softplus ? sd : 1.0f;
+        const float z = (float)raw.z[k], sz = sigmoid_f(z);
+        const float g = dy * (a.z ? z * sz : 1.0f), dz = dy * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f));
+        float s = step_of(d, a.delta_softplus);
         s = on ? s : 0.0f;
         steps += s;
         S.s[k][at] = s, S.x[k][at] = on ? s * u : 0.0f, S.dy[k][at] = on ? g : 0.0f;
@@ -168,7 +165,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_tile_kernel(const kda_s
 #pragma unroll
         for (int r = 0; r < 16 * M; ++r) grad[r * 64 + p.lane] = G[r / 16][r % 16];
     };
-    RawBwd<DT, M> raw;
+    RawBwd<DT, M> raw{};
     raw.template load<CB>(a, d, p, t0, t1);
     int gs = t0;                                    // the group's first token
     while (gs < t1) {
@@ -299,7 +296,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_ar
     StageBwd<CB, M> &S = stages[wave];
     const int nat = CB * p.i + p.g % CB;
     char *const none = (char *)(ws + lay.none);
-    RawBwd<DT, M> raw;
+    RawBwd<DT, M> raw{};
     f32x16 local[M];            // the stored state before the next cell, and the steps up to it
     float lsum[CB];
     auto fetch = [&](int tb) {
