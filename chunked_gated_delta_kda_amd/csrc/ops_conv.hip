@@ -451,14 +451,16 @@ Shape conv_shape(int64_t tiles, int C, int vec) {
 // the rows before them (and, backward, behind them) too often, long ones leave the card idle. Measured on MI355X
 // (us): forward, 8192 x 4096 bf16, 8 channels a thread, target 1024 | 2048 | 4096 | 8192 waves: 29.5 | 26.0 | 32.2 |
 // 33.0; gradients, 8 x 1024 x 2048 bf16, 2 channels a thread, target (of one channel a thread) 4096 | 8192 waves 32.2 |
-// 33.8, and with 4 channels a thread 37.6 | 33.6.
+// 33.8, and with 4 channels a thread 37.6 | 33.6. The forward's count is odd: tiles start at the same time, and with rows of a
+// power of two a power of two of them puts all tiles' rows on the same memory channels (forward, 31 | 32 | 33 rows, on
+// one card 32.5 | 36.0 | 26.6 us; the gradients do not mind: 64 | 65 rows 33.2 | 37.8).
 int conv_tile(int64_t T, int64_t C, int vec, int lo, int hi, int target) {
     const int64_t waves = ceil_div(ceil_div(C, vec), 64);
     int64_t L = T * waves / target;
     L = L < lo ? lo : L > hi ? hi : L;
     return (int)(L / 8 * 8);
 }
-int fwd_tile(int64_t T, int64_t C, int vec) { return conv_tile(T, C, vec, 8, 64, 2048); }
+int fwd_tile(int64_t T, int64_t C, int vec) { return conv_tile(T, C, vec, 8, 64, 2048) + 1; }
 int bwd_tile(int64_t T, int64_t C) { return conv_tile(T, C, 1, 32, 128, 4096); }
 
 template <int DT, int W, int VEC> hipError_t fwd_at(const kda_conv_args &a, int32_t *err, hipStream_t st) {
