@@ -29,13 +29,13 @@ int64_t rows_bytes(int64_t rows, int64_t stride, int64_t len, int64_t es) {
 
 bool dtype_ok(int dt) { return dt == KDA_DTYPE_F32 || dt == KDA_DTYPE_BF16 || dt == KDA_DTYPE_F16; }
 
-// A workspace: the caller's, or one allocated stream-ordered and freed on the stream after the
+// A workspace: the caller's (large enough, aligned to 16 bytes), or one allocated stream-ordered and freed on the stream after the
 // call's kernels.
 class Workspace {
 public:
     Workspace(void *given, size_t bytes, size_t need, hipStream_t st) : st_(st) {
         if (given) {
-            rc_ = bytes < need ? KDA_ERR_ALLOC : KDA_OK;
+            rc_ = bytes < need || (need && (uintptr_t)given % 16) ? KDA_ERR_ALLOC : KDA_OK;
             ptr_ = given;
         } else if (need) {
             if (hipMallocAsync(&ptr_, need, st) != hipSuccess) {
@@ -189,9 +189,12 @@ int kda_conv_bwd(const kda_conv_args *args, const kda_conv_grads *grads, void *s
                        span(a.weight, C * a.width * 4), span(a.initial_state, state * es), span(g.d_final_state, state * 4)};
     const Span out[] = {span(g.dx, T * C * es), span(g.dweight, C * a.width * 4), span(g.dbias, C * 4),
                         span(g.d_initial_state, state * 4)};
-    for (const Span &o : out)
+    for (int o = 0; o < 4; ++o) {
         for (const Span &i : in)
-            if (meet(o, i)) return KDA_ERR_ALIAS;
+            if (meet(out[o], i)) return KDA_ERR_ALIAS;
+        for (int q = 0; q < o; ++q)
+            if (meet(out[o], out[q])) return KDA_ERR_ALIAS;
+    }
     hipStream_t st = (hipStream_t)stream;
     Workspace ws(workspace, workspace_bytes, kda::ops::conv_bwd_workspace(T, C, a.width), st);
     if (ws.status() != KDA_OK) return ws.status();

@@ -295,7 +295,7 @@ int kda_bwd(const void *q, const void *k, const void *v, const float *g, const f
  * Operators beside the delta rule: what a hybrid decoder runs next to it. All of them take
  * a structure of arguments that the call reads and does not keep. Activations are fp32,
  * bf16 or fp16 (one dtype per call), parameters, states and their gradients fp32 unless
- * said otherwise; arithmetic is fp32. A row stride is counted in elements, is at least
+ * said otherwise; arithmetic is fp32. A workspace is aligned to 16 bytes. A row stride is counted in elements, is at least
  * the row's own length and need not be a multiple of anything; within a row elements are
  * contiguous. Base pointers are aligned to their element. Outputs must not overlap inputs
  * or each other, but where said; KDA_ERR_ALIAS reports an output over an input that the

@@ -143,10 +143,12 @@ def test_conv_bwd_abi_refusals(lib):
     assert bwd(dict(dy_stride=C - 1)) == 2
     assert bwd(width=9) == 3
     assert bwd(num_seqs=2) == 2
-    for g in (dict(dx=P), dict(dx=3 * big), dict(dweight=1 * big), dict(d_initial_state=3 * big)):
+    for g in (dict(dx=P), dict(dx=3 * big), dict(dweight=1 * big), dict(d_initial_state=3 * big), dict(dweight=4 * big),
+              dict(dbias=5 * big)):
         assert bwd(g) == 7, g
     need = lib.kda_conv_bwd_workspace_bytes(T, C, W)
     assert need >= (W + 1) * C * 4 and bwd(nbytes=need - 1) == 4
+    assert bwd(ws=P + 8, nbytes=need) == 4                                       # not aligned to 16 bytes
     assert lib.kda_conv_bwd_workspace_bytes(-1, C, W) == 0 and lib.kda_conv_bwd_workspace_bytes(T, C, 9) == 0
 
 
