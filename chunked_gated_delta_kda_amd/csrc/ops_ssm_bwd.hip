@@ -460,19 +460,19 @@ __global__ __launch_bounds__(256) void ssm_bwd_rows_kernel(const kda_ssm_args a,
     using E = typename Elem<DT>::type;
     const int N = a.state_size, G = a.groups;
     const int64_t line = (int64_t)a.total_tokens * 2 * NP;           // of one block
-    const int grp = blockIdx.y;
     // id: (token, which, state)
-    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < line; id += (int64_t)gridDim.x * 256) {
-        const int64_t t = id / (2 * NP);
-        const int r = (int)(id - t * 2 * NP), n = r < NP ? r : r - NP;
-        if (n >= N) continue;
-        const float *from = rows + (int64_t)grp * per_group * line + id;
-        float s = 0.0f;
+    for (int grp = blockIdx.y; grp < G; grp += gridDim.y)
+        for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < line; id += (int64_t)gridDim.x * 256) {
+            const int64_t t = id / (2 * NP);
+            const int r = (int)(id - t * 2 * NP), n = r < NP ? r : r - NP;
+            if (n >= N) continue;
+            const float *from = rows + (int64_t)grp * per_group * line + id;
+            float s = 0.0f;
 #pragma unroll 8
-        for (int b = 0; b < per_group; ++b) s += from[b * line];
-        E *to = reinterpret_cast<E *>(r < NP ? d.dB : d.dC);
-        to[(t * G + grp) * N + n] = (E)s;
-    }
+            for (int b = 0; b < per_group; ++b) s += from[b * line];
+            E *to = reinterpret_cast<E *>(r < NP ? d.dB : d.dC);
+            to[(t * G + grp) * N + n] = (E)s;
+        }
 }
 
 // dA (blockIdx.y 0 .. 16 M - 1: a register of every block's lanes), dD and dbias (the last): sums over tiles.
@@ -528,7 +528,7 @@ hipError_t bwd_form(const kda_ssm_args &a, const kda_ssm_grads &d, float *ws, in
     if (hipError_t e = hipGetLastError()) return e;
     if (T) {
         const int64_t line = T * 2 * (64 / CB * M);
-        ssm_bwd_rows_kernel<DT><<<dim3((unsigned)std::min<int64_t>(1 << 20, ceil_div(line, 256)), (unsigned)a.groups), 256, 0, st>>>(
+        ssm_bwd_rows_kernel<DT><<<dim3((unsigned)std::min<int64_t>(1 << 20, ceil_div(line, 256)), (unsigned)std::min(65535, a.groups)), 256, 0, st>>>(
             a, d, ws + lay.rows, (int)(blocks / a.groups), 64 / CB * M);
         if (hipError_t e = hipGetLastError()) return e;
     }

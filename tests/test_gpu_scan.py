@@ -74,6 +74,7 @@ CASES = [
     ([96, 192, 1, 0, 95, 400], 33, 16, "bf16", 1, True, True, 1, True, True),
     ([3] * 40, 50, 16, "fp32", 1, True, True, 1, True, True),
     ([2] * 30 + [50], 36, 25, "bf16", 3, True, True, 2, True, True),
+    ([90, 20], 24, 6, "fp32", 24, True, True, 1, True, True),
 ]
 
 
