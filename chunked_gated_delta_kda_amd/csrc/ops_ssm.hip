@@ -580,15 +580,18 @@ __global__ __launch_bounds__(256) void ssm_decode_kernel(const kda_ssm_args a) {
 }
 
 // ------------------------------------------------------------------------------ launches
-// Whether the scan by blocks takes a batch. Its blocks of 16 channels run one to a CU, ceil(blocks / 256)
-// rounds of 32 ns a token; the scan by waves costs 35 ns a token and 256 blocks' channels, spread over the card
-// at any count, and 12 us for its three launches and joined states. A step of a block is one sequence's:
-// sequences that are short on average go to the waves. Measured (us, blocks | waves): 8192 x 4096 x 16 275 | 290,
-// 65536 x 1024 x 16 2030 | 535, 256 x 256 x 16 9 | 17 (bf16, gate).
+// Whether the scan by blocks takes a batch. Its blocks of 16 channels run one to a CU, ceil(blocks / 256) rounds of
+// 32.5 ns a token (and 16 states); a step of it is one sequence's, so every sequence wastes half a step of 128 / NB
+// tokens. The scan by waves costs 30 ns a token and 256 blocks' channels, spread over the card at any count, and 40
+// us for its three launches and joined states. Measured on MI355X (us, blocks | waves; bf16, gate, tokens x channels x
+// states): 2048 x 4096 x 16 59 | 92, 4096 x 4096 x 16 113 | 149, 8192 x 4096 x 16 235 | 277, 16384 x 4096 x 16 534 | 490,
+// 2048 x 8192 x 16 111 | 149, 8192 x 4096 x 32 435 | 488, 2048 x 2048 x 16 52 | 67, 1024 x 1024 x 16 27.5 | 31.4, 1024 x 256
+// x 16 27.3 | 28.0, 512 x 256 x 16 15.5 | 26.2; 8192 tokens in 32 sequences x 4096 x 16 262 | 268, in 100 449 | 241.
 bool by_blocks(int64_t T, int64_t S, int64_t D, int64_t N, int64_t G) {
-    if (N > 32 || T < 64 * S) return false;
-    const double blocks = (double)(G * ceil_div(D / G, 16));
-    return std::ceil(blocks / 256.0) * (double)T * 0.032 <= blocks / 256.0 * (double)T * 0.035 + 12.0;
+    if (N > 32) return false;
+    const double NB = N > 16 ? 2.0 : 1.0, blocks = (double)(G * ceil_div(D / G, 16));
+    const double by_block = std::ceil(blocks / 256.0) * ((double)T + 64.0 / NB * (double)S) * 0.0325 * NB;
+    return by_block <= blocks / 256.0 * (double)T * 0.030 * NB + 40.0;
 }
 
 template <int DT, int CB, int M>
