@@ -67,18 +67,18 @@ __device__ __forceinline__ float rcp_f(float x) { return __builtin_amdgcn_rcpf(x
 // 1 / (1 + e^-x): 0 and 1 at the ends (e^-x overflows to infinity, whose reciprocal is 0).
 __device__ __forceinline__ float sigmoid_f(float x) { return rcp_f(1.0f + exp2_f(-x * LOG2E_F)); }
 
-// log(1 + e^x) = max(x, 0) + log1p(e^-|x|), with log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3:
-// the odd series to s^13 leaves s^15/15 <= 5e-9 relative. Unlike log(1 + e) it keeps its
-// relative precision where e is small (step sizes near 1e-3 come from there).
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|), with log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, and
+// atanh(s) / s = 1 + q p(q), q = s^2 <= 1/9: p is the polynomial of degree 3 whose largest relative error in the
+// result is smallest (found by linear programming): 5.5e-9 with these coefficients, as good as the odd series to s^13
+// and two operations shorter. Unlike log(1 + e) the form keeps its relative precision where e is small (step
+// sizes near 1e-3 come from there).
 __device__ __forceinline__ float softplus_f(float x) {
     const float e = exp2_f(-__builtin_fabsf(x) * LOG2E_F);
     const float s = e * rcp_f(2.0f + e);
     const float q = s * s;
-    float p = __builtin_fmaf(q, 1.0f / 13, 1.0f / 11);
-    p = __builtin_fmaf(p, q, 1.0f / 9);
-    p = __builtin_fmaf(p, q, 1.0f / 7);
-    p = __builtin_fmaf(p, q, 1.0f / 5);
-    p = __builtin_fmaf(p, q, 1.0f / 3);
+    float p = __builtin_fmaf(q, 0.14005993f, 0.14000903f);
+    p = __builtin_fmaf(p, q, 0.20010763f);
+    p = __builtin_fmaf(p, q, 0.33333209f);
     p = __builtin_fmaf(p, q, 1.0f);
     return __builtin_fmaf(2.0f * s, p, __builtin_fmaxf(x, 0.0f));
 }

@@ -81,30 +81,36 @@ template <int DT, int M> struct RawBwd {
 };
 
 // Staged tokens of a wave in LDS: per channel (natural lane l at CB i + g % CB) and per state.
-template <int CB, int M> struct StageBwd {
+template <int CB, int M> struct StageTile {
     static constexpr int CH = 16 * CB, NS = 64 / CB * M, KB = KR_OF<M>;
     float s[KB][CH], x[KB][CH], dy[KB][CH];       // step, step times input, dy'
-    float u[KB][CH], sig[KB][CH], dz[KB][CH];     // input, sigmoid(delta + bias), dy silu'(z)
     float B[KB][NS], C[KB][NS];
+};
+template <int CB, int M> struct StageBwd : StageTile<CB, M> {     // and what the gradients need on top
+    static constexpr int CH = 16 * CB, KB = KR_OF<M>;
+    float u[KB][CH], sig[KB][CH], dz[KB][CH];     // input, sigmoid(delta + bias), dy silu'(z)
 };
 
 // Tokens lo to hi - 1 of a cell are staged, the others masked.
-template <int DT, int CB, int M>
-__device__ __forceinline__ void stage(StageBwd<CB, M> &S, const RawBwd<DT, M> &raw, const kda_ssm_args &a, const Place<CB, M> &p,
+template <int DT, int CB, int M, class Stage>
+__device__ __forceinline__ void stage(Stage &S, const RawBwd<DT, M> &raw, const kda_ssm_args &a, const Place<CB, M> &p,
                                       float bias, int lo, int hi, float &steps) {
     const int at = CB * p.i + p.g % CB;
 #pragma unroll
     for (int k = 0; k < KR_OF<M>; ++k) {
         const bool on = k >= lo && k < hi;
         const float d = (float)raw.delta[k] + bias, u = (float)raw.u[k], dy = (float)raw.dy[k];
-        const float sd = sigmoid_f(d), sig = a.delta_softplus ? sd : 1.0f;
         const float z = (float)raw.z[k], sz = sigmoid_f(z);
-        const float g = dy * (a.z ? z * sz : 1.0f), dz = dy * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f));
+        const float g = dy * (a.z ? z * sz : 1.0f);
         float s = step_of(d, a.delta_softplus);
         s = on ? s : 0.0f;
         steps += s;
         S.s[k][at] = s, S.x[k][at] = on ? s * u : 0.0f, S.dy[k][at] = on ? g : 0.0f;
-        S.u[k][at] = on ? u : 0.0f, S.sig[k][at] = on ? sig : 0.0f, S.dz[k][at] = dz;
+        if constexpr (std::is_same_v<Stage, StageBwd<CB, M>>) {
+            const float sd = sigmoid_f(d), sig = a.delta_softplus ? sd : 1.0f;
+            S.u[k][at] = on ? u : 0.0f, S.sig[k][at] = on ? sig : 0.0f;
+            S.dz[k][at] = dy * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f));
+        }
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const bool is = on && p.nat_state(m) < p.N;
@@ -138,7 +144,7 @@ template <int DT, int CB, int M>
 __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_tile_kernel(const kda_ssm_args a, const kda_ssm_grads d, float *ws,
                                                                      const Layout lay, int32_t *err, int L, int tiles, int blocks) {
     constexpr int KR = KR_OF<M>;
-    __shared__ __align__(16) StageBwd<CB, M> stages[WAVES];
+    __shared__ __align__(16) StageTile<CB, M> stages[WAVES];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t unit = (int64_t)blockIdx.x * WAVES + wave;
     if (unit >= (int64_t)tiles * blocks) return;
@@ -159,7 +165,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_tile_kernel(const kda_s
     const float bias = a.delta_bias ? a.delta_bias[p.ch] : 0.0f;
     const int nat = CB * p.i + p.g % CB;
     float sum = 0.0f;
-    StageBwd<CB, M> &S = stages[wave];
+    StageTile<CB, M> &S = stages[wave];
     float *const grad = ws + lay.grad + unit * (1024 * M);
     auto store_grad = [&] {
 #pragma unroll
