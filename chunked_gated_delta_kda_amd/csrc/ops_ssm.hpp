@@ -45,6 +45,20 @@ template <class P> __device__ __forceinline__ KDA_GLOBAL P *uniform(P *row) {
 template <int DT> __device__ __forceinline__ typename Elem<DT>::type at(KDA_GLOBAL const char *row, uint32_t bytes) {
     return *(KDA_GLOBAL const typename Elem<DT>::type *)(row + bytes);
 }
+// K rows of an array from row t on, those past `last` (0 .. K - 1) row `last` again: one 64-bit product an array
+// and a few scalar operations a row. Strides of KDA_SSM_MAX_STRIDE = 2^27 elements keep 8 rows of fp32 under 2^32 bytes.
+struct RowsOf {
+    const char *first;
+    uint32_t step;
+    __device__ __forceinline__ RowsOf(const char *p, int64_t stride, int t, uint32_t es) : step((uint32_t)stride * es) {
+        first = p + (uint64_t)(uint32_t)t * step;
+    }
+    __device__ __forceinline__ KDA_GLOBAL const char *at(int k, int last) const {
+        return uniform(first + (uint32_t)(k < last ? k : last) * step);
+    }
+};
+static_assert(7ull * KDA_SSM_MAX_STRIDE * 4 < (1ull << 32), "eight rows within 32 bits");
+
 template <class E> __device__ __forceinline__ void put(KDA_GLOBAL char *row, uint32_t bytes, E v) { *(KDA_GLOBAL E *)(row + bytes) = v; }
 
 // The step of delta + bias. Both forms are computed and one is taken: a branch here would keep the

@@ -60,21 +60,24 @@ template <int DT, int M> struct RawBwd {
     template <int CB>
     __device__ __forceinline__ void load(const kda_ssm_args &a, const kda_ssm_grads &d, const Place<CB, M> &p, int t, int stop) {
         const uint32_t ch = (uint32_t)p.ch * sizeof(E);
-        const char *u0 = (const char *)a.u, *d0 = (const char *)a.delta, *z0 = (const char *)a.z, *y0 = (const char *)d.dy;
-        const char *B0 = (const char *)a.B + (int64_t)p.group * p.N * sizeof(E), *C0 = (const char *)a.C + (int64_t)p.group * p.N * sizeof(E);
+        const int64_t g0 = (int64_t)p.group * p.N * sizeof(E);
+        t = t < stop ? t : stop - 1;            // rows past the end: the last one again
+        const int last = stop - 1 - t;
+        const RowsOf dr((const char *)a.delta, a.delta_stride, t, sizeof(E)), ur((const char *)a.u, a.u_stride, t, sizeof(E));
+        const RowsOf yr((const char *)d.dy, d.dy_stride, t, sizeof(E)), zr((const char *)a.z, a.z_stride, t, sizeof(E));
+        const RowsOf Br((const char *)a.B + g0, a.B_stride, t, sizeof(E)), Cr((const char *)a.C + g0, a.C_stride, t, sizeof(E));
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-            const int64_t r = (int64_t)(t + k < stop ? t + k : stop - 1) * sizeof(E);
-            delta[k] = at<DT>(uniform(d0 + r * a.delta_stride), ch);
-            u[k] = at<DT>(uniform(u0 + r * a.u_stride), ch);
-            dy[k] = at<DT>(uniform(y0 + r * d.dy_stride), ch);
-            if (a.z) z[k] = at<DT>(uniform(z0 + r * a.z_stride), ch);
+            delta[k] = at<DT>(dr.at(k, last), ch);
+            u[k] = at<DT>(ur.at(k, last), ch);
+            dy[k] = at<DT>(yr.at(k, last), ch);
+            if (a.z) z[k] = at<DT>(zr.at(k, last), ch);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const int n = p.nat_state(m);
                 const uint32_t st = (uint32_t)(n < p.N ? n : p.N - 1) * sizeof(E);
-                B[k][m] = at<DT>(uniform(B0 + r * a.B_stride), st);
-                C[k][m] = at<DT>(uniform(C0 + r * a.C_stride), st);
+                B[k][m] = at<DT>(Br.at(k, last), st);
+                C[k][m] = at<DT>(Cr.at(k, last), st);
             }
         }
     }
