@@ -117,6 +117,8 @@ __device__ __forceinline__ void empty_final(const kda_conv_args &a, int n, int c
 // 4 | 8 rows): 26.0 | 27.3; more rows only cost registers (8 rows: 224, two waves a SIMD).
 constexpr int AHEAD = 4, BWD_AHEAD = 4;
 
+// Bound by memory: every row is read and written once. 8192 x 4096 bf16, rows of x 16 KiB apart: 134 MB in 26.6 us,
+// 5.0 TB/s, where a copy reaches 5.3.
 template <int DT, int W, int VEC>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(const kda_conv_args a, int32_t *err, int L) {
     const Offsets off{a.cu_seqlens, a.num_seqs, a.total_tokens};
@@ -194,7 +196,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const kda_conv_args a, in
 }
 
 // One row per sequence: the state's rows move up by one and the new row joins them. A thread
-// reads all it needs of its channels before it writes, so the state may be updated in place.
+// reads all it needs of its channels before it writes, so the state may be updated in place. 256 x 4096 bf16: 17 MB in
+// 5.4 us, most of it the latency of a launch and of one round of loads.
 template <int DT, int W, int VEC>
 __global__ __launch_bounds__(256) void conv_decode_kernel(const kda_conv_args a) {
     const int per = a.channels / VEC;
@@ -320,6 +323,9 @@ __device__ __forceinline__ void empty_grad(const kda_conv_args &a, const kda_con
     }
 }
 
+// Reads x and dy, writes dx; p_t is formed again. 8 x 1024 x 2048 bf16: 101 MB in 27.6 us, 3.7 TB/s; memory and vector
+// issue (about 40 operations an element) take about as long as each other. The taps' sums of a tile stay in
+// registers and go to the workspace.
 template <int DT, int W, int VEC>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(const kda_conv_args a, const kda_conv_grads g, float *part,
                                                        int32_t *err, int L) {
@@ -403,7 +409,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const kda_conv_args a, co
 }
 
 // dw[c][j] and db[c] from the tiles' sums: 16 channels' lanes by 16 groups of tiles a block, the
-// groups' sums joined in a fixed order.
+// groups' sums joined in a fixed order. 8 x 1024 x 2048: 4.0 us, latency.
 __global__ __launch_bounds__(256) void conv_dw_kernel(const float *part, int tiles, int C, int W, float *dw, float *db) {
     __shared__ float sum[16][17];
     const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
