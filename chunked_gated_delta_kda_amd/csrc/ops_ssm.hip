@@ -589,17 +589,20 @@ __global__ __launch_bounds__(256) void ssm_decode_kernel(const kda_ssm_args a) {
 
 // ------------------------------------------------------------------------------ launches
 // Whether the scan by blocks takes a batch. Its blocks of 16 channels run one to a CU, ceil(blocks / 256) rounds of
-// 32.5 ns a token (and 16 states); a step of it is one sequence's, so every sequence wastes half a step of 128 / NB
-// tokens. The scan by waves costs 30 ns a token and 256 blocks' channels, spread over the card at any count, and 40
-// us for its three launches and joined states. Measured on MI355X (us, blocks | waves; bf16, gate, tokens x channels x
-// states): 2048 x 4096 x 16 59 | 92, 4096 x 4096 x 16 113 | 149, 8192 x 4096 x 16 235 | 277, 16384 x 4096 x 16 534 | 490,
-// 2048 x 8192 x 16 111 | 149, 8192 x 4096 x 32 435 | 488, 2048 x 2048 x 16 52 | 67, 1024 x 1024 x 16 27.5 | 31.4, 1024 x 256
-// x 16 27.3 | 28.0, 512 x 256 x 16 15.5 | 26.2; 8192 tokens in 32 sequences x 4096 x 16 262 | 268, in 100 449 | 241.
+// 28 to 33 ns a token (inputs in the caches, or not); a step of it is one sequence's, so every sequence wastes half a
+// step of 128 tokens. The scan by waves costs 29 ns a token and 256 blocks' channels, spread over the card at any
+// count, and 40 us for its three launches and joined states. A second block of states costs 1.65 and 1.8 times that.
+// Measured on MI355X (us, blocks | waves; bf16, gate, tokens x channels x states, inputs in the caches where they
+// fit): 2048 x 4096 x 16 59 | 90, 4096 x 4096 x 16 113 | 144, 8192 x 4096 x 16 232 | 262 (not in the caches: 271 | 271),
+// 12288 x 4096 x 16 398 | 361, 16384 x 4096 x 16 528 | 470, 2048 x 8192 x 16 109 | 143, 4096 x 5120 x 16 217 | 170, 8192 x
+// 4096 x 32 432 | 464, 2048 x 2048 x 16 52 | 65, 4096 x 1024 x 16 101 | 70, 1024 x 1024 x 16 27 | 30, 1024 x 256 x 16 27 |
+// 27, 2048 x 256 x 16 51 | 31, 512 x 256 x 16 15.5 | 25; 8192 tokens in 32 sequences x 4096 x 16 265 | 255, in 100 439 | 232.
 bool by_blocks(int64_t T, int64_t S, int64_t D, int64_t N, int64_t G) {
     if (N > 32) return false;
-    const double NB = N > 16 ? 2.0 : 1.0, blocks = (double)(G * ceil_div(D / G, 16));
-    const double by_block = std::ceil(blocks / 256.0) * ((double)T + 64.0 / NB * (double)S) * 0.0325 * NB;
-    return by_block <= blocks / 256.0 * (double)T * 0.030 * NB + 40.0;
+    const bool two = N > 16;
+    const double blocks = (double)(G * ceil_div(D / G, 16));
+    const double by_block = std::ceil(blocks / 256.0) * ((double)T + (two ? 32.0 : 64.0) * (double)S) * 0.0325 * (two ? 1.65 : 1.0);
+    return by_block <= blocks / 256.0 * (double)T * 0.029 * (two ? 1.8 : 1.0) + 40.0;
 }
 
 template <int DT, int CB, int M>
