@@ -248,7 +248,7 @@ int kda_ssm_bwd(const kda_ssm_args *args, const kda_ssm_grads *grads, void *stre
     const kda_ssm_grads &g = *grads;
     if (const int rc = check_ssm(a, true)) return rc;
     if (!a.cu_seqlens && a.num_seqs != 1) return KDA_ERR_SHAPE;
-    if (g.dy_stride < a.channels) return KDA_ERR_SHAPE;
+    if (g.dy_stride < a.channels || g.dy_stride > KDA_SSM_MAX_STRIDE) return KDA_ERR_SHAPE;
     if (!g.dA || (a.total_tokens > 0 && (!g.dy || !g.du || !g.ddelta || !g.dB || !g.dC || (a.z && !g.dz)))) return KDA_ERR_NULL;
     const SsmSpans s(a);
     const int64_t es = (int64_t)dtype_bytes(a.dtype), T = a.total_tokens, D = a.channels, N = a.state_size;

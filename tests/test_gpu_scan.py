@@ -1,5 +1,5 @@
 """The selective state space scan on the GPU against a plain 64-bit form: prompts over packed
-batches, one token per sequence; every state-size form, odd sizes and strides, groups, lengths of
+batches, one token per sequence; every state-size form, odd sizes and strides, the largest strides, groups, lengths of
 zero and one, tiles that sequences start and end in, streams and graphs. Tolerances: one rounding
 to the output's type, plus the fp32 roundings that ops_oracle.scan counts."""
 import numpy as np
@@ -352,3 +352,34 @@ def test_gradients_of_malformed_offsets_stay_in_bounds():
             kda.device_errors()
             kda.ssm_bwd(**d, **g)
             assert kda.device_errors() == 2
+
+
+@pytest.mark.parametrize("N", [5, 16, 40], ids="states{}".format)
+def test_the_largest_strides(N):
+    """Rows 2^27 elements apart (20 of fp32 are 10 GiB): the same results as from rows one after another, by
+    blocks (up to 32 states) and by waves, forward, one token and backward."""
+    T, D, stride = 20, 24, 1 << 27
+    d = make([13, 7], D, N, "fp32", 77)
+    dy = torch.randn(T, D, generator=torch.Generator().manual_seed(78)).cuda()
+    near = dict(d, dy=dy)
+    for k in ("B", "C"):
+        near[k] = near[k].contiguous()
+    buf = torch.empty(T * stride, device="cuda")        # never filled: only the rows are touched
+    far, at = dict(near), 0
+    for k in ("u", "delta", "B", "C", "z", "dy"):
+        t = near[k]
+        inner = (t.stride(1),) if t.dim() == 2 else (t.stride(1), t.stride(2))
+        far[k] = buf.as_strided(t.shape, (stride,) + inner, at)
+        far[k].copy_(t)
+        at += 4096
+    for a, b in zip(all_calls(near), all_calls(far)):
+        assert torch.equal(a, b)
+
+
+def all_calls(d):
+    """The outputs of the three calls, in one list."""
+    import chunked_gated_delta_kda_amd as kda
+    fwd = {k: v for k, v in d.items() if k != "dy"}
+    step = {k: v for k, v in fwd.items() if k not in ("cu_seqlens", "initial_state")}
+    state = torch.ones(d["u"].shape[0], d["u"].shape[1], d["A"].shape[1], device="cuda")
+    return [*kda.ssm_fwd(**fwd), *kda.ssm_decode(**step, state=state), *kda.ssm_bwd(**d).values()]

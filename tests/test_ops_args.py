@@ -378,6 +378,7 @@ def test_ssm_bwd_abi_refusals(lib):
     for g in (dict(dy=None), dict(du=None), dict(ddelta=None), dict(dB=None), dict(dC=None), dict(dz=None), dict(dA=None)):
         assert bwd(g) == 1, g
     assert bwd(dict(dy_stride=Dn - 1)) == 2 and bwd(num_seqs=2) == 2 and bwd(state_size=257) == 2
+    assert bwd(dict(dy_stride=(1 << 27) + 1)) == 2      # rows past 32-bit offsets of the kernels' cells
     assert bwd(dtype=7) == 3
     for g in (dict(du=1 << 20), dict(dA=3 << 20), dict(d_initial_state=16 << 20), dict(dB=36 << 20, dC=36 << 20),
               dict(dz=32 << 20), dict(d_initial_state=33 << 20)):
