@@ -16,16 +16,13 @@ HEAD_DIMS = (64, 128, 256)
 def _by8(name, t, dev):
     """Rows read 16 bytes at a time: the last dimension contiguous, other strides multiples of 8 (those of
     dimensions of one entry do not matter). Returns those strides."""
-    shape, last = t.shape, t.dim() - 1
-    if t.is_contiguous():
-        strides, step = [], shape[last]
-        for n in shape[last - 1:0:-1]:
-            strides.append(step)
-            step *= n
-        strides.append(step)
-        strides.reverse()
+    shape = t.shape
+    if t.is_contiguous():       # (its strides of dimensions of one entry may be any: formed from the sizes)
+        inner = shape[-1]
+        strides = [shape[1] * inner, inner] if len(shape) == 3 else [shape[1] * shape[2] * inner, shape[2] * inner, inner]
         bad = False
     else:
+        last = len(shape) - 1
         strides = [s if n > 1 else 0 for n, s in zip(shape[:last], t.stride())]
         bad = t.stride(last) != 1 or any(s % 8 for s in strides)
     if bad or t.data_ptr() % 16 or t.get_device() != dev:
@@ -98,8 +95,8 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, *, retur
         if lse is None and return_lse:
             lse = like(q, (B, hq), torch.float32)
         workspace, wp, wn = scratch(workspace, lib.kda_attn_workspace_bytes(B, hq, hkv, dh, width, page), q)
-        args = native.KdaAttnArgs(ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_table), ptr(seq_lens), ptr(out), ptr(lse),
-                                  *strides, B, hq, hkv, dh, pages, page, width, DTYPES[q.dtype],
-                                  1.0 / math.sqrt(dh) if scale is None else scale)
+        args = native.KdaAttnArgs(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                  seq_lens.data_ptr(), out.data_ptr(), ptr(lse), *strides, B, hq, hkv, dh, pages, page,
+                                  width, DTYPES[q.dtype], 1.0 / math.sqrt(dh) if scale is None else scale)
         run(check, st, lib.kda_attn_decode, ctypes.byref(args), st, wp, wn)
     return (out, lse) if return_lse else out

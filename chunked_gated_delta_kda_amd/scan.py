@@ -15,17 +15,17 @@ class _Sizes:
 
 
 def _check(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state):
-    if u.dtype not in DTYPES or u.dim() != 2:
-        raise ValueError(f"u: expected fp32, bf16 or fp16 [T, D], got {u.dtype} {tuple(u.shape)}")
-    dev, dt = u.get_device(), u.dtype
+    dev, dt, td, dn, tgn = u.get_device(), u.dtype, tuple(u.shape), A.shape, B.shape
+    if dt not in DTYPES or len(td) != 2:
+        raise ValueError(f"u: expected fp32, bf16 or fp16 [T, D], got {dt} {td}")
     s = _Sizes()
-    s.T, s.D = td = tuple(u.shape)
-    if A.dim() != 2 or not 1 <= A.shape[1] <= native.SSM_MAX_STATE:
-        raise ValueError(f"A: expected fp32 [D, N] with N from 1 to {native.SSM_MAX_STATE}, got {tuple(A.shape)}")
-    s.N = A.shape[1]
-    if B.dim() != 3 or B.shape[1] < 1 or s.D % B.shape[1]:
-        raise ValueError(f"B: expected [T, G, N] with G dividing the {s.D} channels, got {tuple(B.shape)}")
-    s.G = B.shape[1]
+    s.T, s.D = td
+    if len(dn) != 2 or not 1 <= dn[1] <= native.SSM_MAX_STATE:
+        raise ValueError(f"A: expected fp32 [D, N] with N from 1 to {native.SSM_MAX_STATE}, got {tuple(dn)}")
+    s.N = dn[1]
+    if len(tgn) != 3 or tgn[1] < 1 or s.D % tgn[1]:
+        raise ValueError(f"B: expected [T, G, N] with G dividing the {s.D} channels, got {tuple(tgn)}")
+    s.G = tgn[1]
     tgn = (s.T, s.G, s.N)
     strides = [rows("u", u, dt, td, dev), rows("delta", delta, dt, td, dev), rows("B", B, dt, tgn, dev),
                rows("C", C, dt, tgn, dev), 0]
@@ -55,9 +55,9 @@ def check_ssm_fwd_args(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_se
 
 
 def _args(s, u, delta, A, B, C, D, z, delta_bias, cu_seqlens, initial_state, final_state, out, softplus):
-    return native.KdaSsmArgs(ptr(u), ptr(delta), ptr(A), ptr(B), ptr(C), ptr(D), ptr(z), ptr(delta_bias), ptr(cu_seqlens),
-                             ptr(initial_state), ptr(final_state), ptr(out), *s.strides, s.S, s.T, s.D, s.N, s.G,
-                             DTYPES[u.dtype], int(bool(softplus)))
+    return native.KdaSsmArgs(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), ptr(D), ptr(z),
+                             ptr(delta_bias), ptr(cu_seqlens), ptr(initial_state), ptr(final_state), ptr(out),
+                             *s.strides, s.S, s.T, s.D, s.N, s.G, DTYPES[u.dtype], int(bool(softplus)))
 
 
 def ssm_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_seqlens=None, initial_state=None,

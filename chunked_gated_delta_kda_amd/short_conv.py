@@ -70,8 +70,8 @@ def conv_fwd(x, weight, bias=None, cu_seqlens=None, initial_state=None, output_f
             final_state = None
         elif final_state is None:
             final_state = like(x, (N, W - 1, C))
-        args = native.KdaConvArgs(ptr(x), ptr(weight), ptr(bias), ptr(cu_seqlens), ptr(initial_state), ptr(final_state),
-                                  ptr(out), stride, N, T, C, W, DTYPES[x.dtype], _ACTIVATIONS[activation])
+        args = native.KdaConvArgs(x.data_ptr(), weight.data_ptr(), ptr(bias), ptr(cu_seqlens), ptr(initial_state),
+                                  ptr(final_state), out.data_ptr(), stride, N, T, C, W, DTYPES[x.dtype], _ACTIVATIONS[activation])
         run(check, st, lib.kda_conv_fwd, ctypes.byref(args), st)
     return out, final_state
 
@@ -105,8 +105,8 @@ def conv_decode(x, weight, bias=None, state=None, *, activation="silu", out=None
             out = like(x, (N, C))
         if isinstance(state_out, str):
             state_out = state if state is not None else like(x, (N, W - 1, C))
-        args = native.KdaConvArgs(ptr(x), ptr(weight), ptr(bias), None, ptr(state), ptr(state_out), ptr(out), stride, N, N,
-                                  C, W, DTYPES[x.dtype], _ACTIVATIONS[activation])
+        args = native.KdaConvArgs(x.data_ptr(), weight.data_ptr(), ptr(bias), None, ptr(state), ptr(state_out), out.data_ptr(),
+                                  stride, N, N, C, W, DTYPES[x.dtype], _ACTIVATIONS[activation])
         run(False, st, lib.kda_conv_decode, ctypes.byref(args), st)
     return out, state_out
 
