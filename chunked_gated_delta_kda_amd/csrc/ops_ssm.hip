@@ -671,13 +671,14 @@ template <int DT> hipError_t decode_dt(const kda_ssm_args &a, hipStream_t st) {
 
 }  // namespace
 
-// Tokens of a tile: as many tiles as give the card about 4096 waves (four to a SIMD), of 16 tokens or more; and where
+// Tokens of a tile: as many tiles as give the card about 4096 waves (four to a SIMD), of 8 tokens or more; and where
 // the channels are few, sqrt(0.12 T): a wave takes 0.25 us a token in each of its two kernels, the join 0.06 us a tile.
 // Measured on MI355X (us, with 0 | 0.06 | 0.12 | 0.25 T under the root; bf16): 23739 x 9 x 16 106 | 68 | 68 | 75, 65536 x 64 x 16
-// 259 | 106 | 107 | 117, 32768 x 128 x 16 157 | 98 | 79 | 89, 8192 x 64 x 16 48 | 45 | 45 | 51, 65536 x 48 x 64 181 | 163 | 178 | 171.
+// 259 | 106 | 107 | 117, 32768 x 128 x 16 157 | 98 | 79 | 89, 8192 x 64 x 16 48 | 45 | 45 | 51, 65536 x 48 x 64 181 | 163 | 178 | 171. At
+// least 16 | 8 tokens: 128 x 64 x 64 26 | 21, 500 x 128 x 128 36 | 32, 300 x 1000 x 128 in 3 sequences 64 | 67.
 int tile_len(int64_t T, int64_t blocks) {
     int64_t L = std::max<int64_t>(T * blocks / 4096, (int64_t)std::sqrt(0.12 * (double)T));
-    L = L < 16 ? 16 : L > T ? T : L;
+    L = L < 8 ? 8 : L > T ? T : L;
     return (int)((L + 7) / 8 * 8);
 }
 

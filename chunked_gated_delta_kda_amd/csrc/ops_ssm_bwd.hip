@@ -519,13 +519,14 @@ __global__ __launch_bounds__(256) void ssm_bwd_params_kernel(const kda_ssm_args 
     }
 }
 
-// Tokens of a tile: as many tiles as give the card 2048 waves (two to a SIMD), of 16 tokens or more. 8 x 1024 x 2048 x
+// Tokens of a tile: as many tiles as give the card 2048 waves (two to a SIMD), of 4 tokens or more. 8 x 1024 x 2048 x
 // 16 with 2048 | 4096 waves: 401 | 426 us. Few channels: sqrt(0.06 T), a wave's time for a token against the join's for a tile (as
 // in the forward); with 0 | 0.03 | 0.06 | 0.12 T under the root 65536 x 64 x 16 326 | 303 | 251 | 267, 32768 x 128 x 16 217 | 218 |
-// 219 | 194, 16384 x 48 x 64 199 | 199 | 180 | 199, 4096 x 40 x 16 75 | 75 | 75 | 81.
+// 219 | 194, 16384 x 48 x 64 199 | 199 | 180 | 199, 4096 x 40 x 16 75 | 75 | 75 | 81. At least 16 | 8 | 4 tokens: 60 x 1876 x 74 168 |
+// 125 | 124, 24 x 4096 x 16 55 | 44 | 40, 500 x 128 x 64 58 | 49 | 50.
 int bwd_tile_len(int64_t T, int64_t blocks) {
     int64_t L = std::max<int64_t>(T * blocks / 2048, (int64_t)std::sqrt(0.06 * (double)T));
-    L = L < 16 ? 16 : L > T ? T : L;
+    L = L < 4 ? 4 : L > T ? T : L;
     return (int)((L + 3) / 4 * 4);
 }
 
