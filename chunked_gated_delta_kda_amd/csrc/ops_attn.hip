@@ -12,7 +12,7 @@
 //  * O^T = V^T P^T. P leaves S^T in the very lanes its operand wants (the 32 tokens of the
 //    contraction are relabelled: slot 8 g + i is token 4 g + i for i < 4, 16 + 4 g + i - 4 else), split
 //    into a rounded part and the rest, two products, so that P does not lose what the output
-//    keeps. V's operand holds 8 tokens of one element: a lane loads DV neighbouring elements
+//    keeps: 2^-16 of a probability in bf16; 2^-22 in fp16, or 2^-40 of the wave's largest one. V's operand holds 8 tokens of one element: a lane loads DV neighbouring elements
 //    of 8 tokens (whole rows of the cache per instruction) and pairs the tokens' halves up with
 //    byte permutes. Neither K nor V passes through LDS.
 //  * The result has a head's elements in its own lanes, so rescaling needs no exchange.
@@ -35,11 +35,16 @@ constexpr float NEG_INF = -__builtin_inff();
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+// UP: what probabilities (0 to 1) are multiplied by before they are split. fp16 ends at 2^-24 below, and with a
+// largest score 10 above the rest (one token that draws the attention) the many small probabilities beside it would
+// lose their digits there, at 17 above it themselves; times 2^15 they fill fp16's range up to its top. The
+// factor, a power of two, leaves with the wave's results.
 template <int DT> struct Ops;
 template <> struct Ops<KDA_DTYPE_BF16> {
     typedef __bf16 x8 __attribute__((ext_vector_type(8)));
     typedef __bf16 x2 __attribute__((ext_vector_type(2)));
     using E = __bf16;
+    static constexpr float UP = 1.0f;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
     }
@@ -48,6 +53,7 @@ template <> struct Ops<KDA_DTYPE_F16> {
     typedef _Float16 x8 __attribute__((ext_vector_type(8)));
     typedef _Float16 x2 __attribute__((ext_vector_type(2)));
     using E = _Float16;
+    static constexpr float UP = 32768.0f;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
     }
@@ -291,7 +297,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             uint32_t x, y;
-            split_pair<DT>(p[2 * s], p[2 * s + 1], x, y);
+            split_pair<DT>(p[2 * s] * O::UP, p[2 * s + 1] * O::UP, x, y);
             hi[s] = x, lo[s] = y;
         }
         if (seen != 0xffffffffu) {          // rows that are not there may hold anything: 0 x NaN
@@ -330,7 +336,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
     const float ref = M == NEG_INF ? 0.0f : M;
 #pragma unroll
     for (int v = 0; v < WAVES; ++v) L += stat[v][i][1] * exp2_f(stat[v][i][0] - ref);
-    const float f = exp2_f(m - ref);
+    const float f = exp2_f(m - ref) * (1.0f / O::UP);
     // O^T: element DV (4 g + j) + d of head i
 #pragma unroll
     for (int j = 0; j < 4; ++j)
