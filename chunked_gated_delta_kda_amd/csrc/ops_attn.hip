@@ -20,6 +20,8 @@
 // lengths (on the device: the host does not know them), so that skewed batches spread evenly and a
 // captured launch stays right when lengths change. Chunks' partial results go to the workspace;
 // attn_join_kernel joins them in their order. A sequence of one chunk is written at once.
+#include <type_traits>
+
 #include "ops_common.hpp"
 #include "ops_launch.hpp"
 
@@ -45,6 +47,7 @@ template <> struct Ops<KDA_DTYPE_BF16> {
     typedef __bf16 x2 __attribute__((ext_vector_type(2)));
     using E = __bf16;
     static constexpr float UP = 1.0f;
+    static constexpr uint32_t EXPONENT = 0x7f80;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
     }
@@ -54,19 +57,34 @@ template <> struct Ops<KDA_DTYPE_F16> {
     typedef _Float16 x2 __attribute__((ext_vector_type(2)));
     using E = _Float16;
     static constexpr float UP = 32768.0f;
+    static constexpr uint32_t EXPONENT = 0x7c00;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
     }
 };
 
-// Two probabilities to a rounded pair and the pair of what rounding left.
-template <int DT> __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
+// Two probabilities to a rounded pair and the pair of what rounding left. RAISED: a rounded part is at least
+// the type's smallest normal number where the probability is not zero (what is left may then be negative).
+template <int DT, bool RAISED> __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
     using x2 = typename Ops<DT>::x2;
     using E = typename Ops<DT>::E;
-    const x2 h = {(E)a, (E)b};
+    x2 h = {(E)a, (E)b};
+    if constexpr (RAISED && DT == KDA_DTYPE_F16) {      // in bf16 they share fp32's range
+        constexpr float LEAST = 0x1p-14f;
+        h = {(E)(a > 0.0f ? __builtin_fmaxf(a, LEAST) : a), (E)(b > 0.0f ? __builtin_fmaxf(b, LEAST) : b)};
+    }
     const x2 l = {(E)(a - (float)h[0]), (E)(b - (float)h[1])};
     hi = __builtin_bit_cast(uint32_t, h);
     lo = __builtin_bit_cast(uint32_t, l);
+}
+
+// Pairs of values with infinities and NaN put to zero: their exponent is all ones.
+template <int DT> __device__ __forceinline__ u32x4 finite_of(u32x4 x) {
+    constexpr uint32_t LO = Ops<DT>::EXPONENT, HI = LO << 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] &= ((x[i] & LO) == LO ? 0u : 0xffffu) | ((x[i] & HI) == HI ? 0u : 0xffff0000u);
+    return x;
 }
 
 // maximum and sum over a lane's column (its four 16-lane rows)
@@ -191,9 +209,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
     }
     const float scale = a.scale * LOG2E_F;
     f32x4 acc[DV];
-#pragma unroll
-    for (int d = 0; d < DV; ++d) acc[d] = f32x4{0, 0, 0, 0};
-    float m = NEG_INF, l = 0.0f;
+    float m, l;
     const int32_t *table = a.block_table + (int64_t)seq * a.table_stride;
     const E *kc = (const E *)a.k_cache + (int64_t)kvh * a.k_head_stride;
     const E *vc = (const E *)a.v_cache + (int64_t)kvh * a.v_head_stride;
@@ -248,82 +264,100 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
             }
         }
     };
-    int t0 = begin + wave * TILE, turn = 0, ahead = 0;
-    uint32_t seen = 0;
-    if (t0 < end) {
-        seen = place(t0, page_of(t0), 0);
-        load_k(0);
-        load_v(0);
-        if (t0 + ROUND < end) ahead = page_of(t0 + ROUND);
-    }
-    for (; t0 < end; t0 += ROUND, turn ^= 1) {
-        const bool more = t0 + ROUND < end;
-        uint32_t then = 0;
-        if (more) {
-            then = place(t0 + ROUND, ahead, turn ^ 1);
-            if (t0 + 2 * ROUND < end) ahead = page_of(t0 + 2 * ROUND);
+    // One pass over the wave's tokens. An infinite value times a rest that is zero or negative would make NaN of
+    // an infinite result. Nothing is spent on that in the first pass; where it ends with a NaN, a second one
+    // keeps values that are not finite out of the product with the rest (that with the rounded part gives
+    // what they give), and lets no rounded part be zero that stands for a positive probability.
+    auto walk = [&](auto careful) {
+        constexpr bool CAREFUL = decltype(careful)::value;
+#pragma unroll
+        for (int d = 0; d < DV; ++d) acc[d] = f32x4{0, 0, 0, 0};
+        m = NEG_INF, l = 0.0f;
+        int t0 = begin + wave * TILE, turn = 0, ahead = 0;
+        uint32_t seen = 0;
+        if (t0 < end) {
+            seen = place(t0, page_of(t0), 0);
+            load_k(0);
+            load_v(0);
+            if (t0 + ROUND < end) ahead = page_of(t0 + ROUND);
         }
-        f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        for (; t0 < end; t0 += ROUND, turn ^= 1) {
+            const bool more = t0 + ROUND < end;
+            uint32_t then = 0;
+            if (more) {
+                then = place(t0 + ROUND, ahead, turn ^ 1);
+                if (t0 + 2 * ROUND < end) ahead = page_of(t0 + 2 * ROUND);
+            }
+            f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-        for (int k = 0; k < KD; ++k)
+            for (int k = 0; k < KD; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) st[h] = O::mma(kr[h][k], q[k], st[h]);
-        if (more) load_k(turn ^ 1);
-        // this lane's tokens: 4 g + j and 16 + 4 g + j
-        float sc[8], top = NEG_INF;
-        const uint32_t mine = (seen >> (4 * g)) & 0xf000f;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const bool on = (mine >> ((s < 4 ? 0 : 12) + s)) & 1;
-            sc[s] = on ? st[s >> 2][s & 3] * scale : NEG_INF;
-            top = __builtin_fmaxf(top, sc[s]);
-        }
-        const float mn = __builtin_fmaxf(m, column_max(top));
-        if (__any(mn > m)) {
-            const float f = mn > m ? exp2_f(m - mn) : 1.0f;      // m may be -inf: 0
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < DV; ++d) acc[d] *= f;
-            m = mn;
-        }
-        const float ref = m == NEG_INF ? 0.0f : m;
-        float p[8];
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            p[s] = exp2_f(sc[s] - ref);
-            l += p[s];
-        }
-        u32x4 hi, lo;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            uint32_t x, y;
-            split_pair<DT>(p[2 * s] * O::UP, p[2 * s + 1] * O::UP, x, y);
-            hi[s] = x, lo[s] = y;
-        }
-        if (seen != 0xffffffffu) {          // rows that are not there may hold anything: 0 x NaN
+                for (int h = 0; h < 2; ++h) st[h] = O::mma(kr[h][k], q[k], st[h]);
+            if (more) load_k(turn ^ 1);
+            // this lane's tokens: 4 g + j and 16 + 4 g + j
+            float sc[8], top = NEG_INF;
+            const uint32_t mine = (seen >> (4 * g)) & 0xf000f;
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
                 const bool on = (mine >> ((s < 4 ? 0 : 12) + s)) & 1;
-#pragma unroll
-                for (int e = 0; e < DV / 2; ++e) vr[s][e] = on ? vr[s][e] : 0u;
+                sc[s] = on ? st[s >> 2][s & 3] * scale : NEG_INF;
+                top = __builtin_fmaxf(top, sc[s]);
             }
-        }
+            const float mn = __builtin_fmaxf(m, column_max(top));
+            if (__any(mn > m)) {
+                const float f = mn > m ? exp2_f(m - mn) : 1.0f;      // m may be -inf: 0
+                l *= f;
 #pragma unroll
-        for (int e = 0; e < DV / 2; ++e) {
-            u32x4 even, odd;
+                for (int d = 0; d < DV; ++d) acc[d] *= f;
+                m = mn;
+            }
+            const float ref = m == NEG_INF ? 0.0f : m;
+            float p[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                p[s] = exp2_f(sc[s] - ref);
+                l += p[s];
+            }
+            u32x4 hi, lo;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                even[s] = __builtin_amdgcn_perm(vr[2 * s + 1][e], vr[2 * s][e], 0x05040100);
-                odd[s] = __builtin_amdgcn_perm(vr[2 * s + 1][e], vr[2 * s][e], 0x07060302);
+                uint32_t x, y;
+                split_pair<DT, CAREFUL>(p[2 * s] * O::UP, p[2 * s + 1] * O::UP, x, y);
+                hi[s] = x, lo[s] = y;
             }
-            acc[2 * e] = O::mma(even, hi, acc[2 * e]);
-            acc[2 * e + 1] = O::mma(odd, hi, acc[2 * e + 1]);
-            acc[2 * e] = O::mma(even, lo, acc[2 * e]);
-            acc[2 * e + 1] = O::mma(odd, lo, acc[2 * e + 1]);
+            if (seen != 0xffffffffu) {          // rows that are not there may hold anything: 0 x NaN
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const bool on = (mine >> ((s < 4 ? 0 : 12) + s)) & 1;
+#pragma unroll
+                    for (int e = 0; e < DV / 2; ++e) vr[s][e] = on ? vr[s][e] : 0u;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < DV / 2; ++e) {
+                u32x4 even, odd;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    even[s] = __builtin_amdgcn_perm(vr[2 * s + 1][e], vr[2 * s][e], 0x05040100);
+                    odd[s] = __builtin_amdgcn_perm(vr[2 * s + 1][e], vr[2 * s][e], 0x07060302);
+                }
+                acc[2 * e] = O::mma(even, hi, acc[2 * e]);
+                acc[2 * e + 1] = O::mma(odd, hi, acc[2 * e + 1]);
+                if constexpr (CAREFUL) even = finite_of<DT>(even), odd = finite_of<DT>(odd);
+                acc[2 * e] = O::mma(even, lo, acc[2 * e]);
+                acc[2 * e + 1] = O::mma(odd, lo, acc[2 * e + 1]);
+            }
+            if (more) load_v(turn ^ 1);
+            seen = then;
         }
-        if (more) load_v(turn ^ 1);
-        seen = then;
-    }
+    };
+    walk(std::false_type{});
+    bool nan = false;
+#pragma unroll
+    for (int d = 0; d < DV; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) nan |= acc[d][j] != acc[d][j];
+    if (__any(nan)) walk(std::true_type{});
     if (err && __any(bad) && lane == 0) atomicOr(err, KDA_DEVERR_PAGES);
     l = column_sum(l);
 

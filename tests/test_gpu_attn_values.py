@@ -68,3 +68,43 @@ def test_small_probabilities_beside_a_large_one(kind, gap):
     ro, oe, rl, le = oracle(d, lens, kind)
     oo.check("out", np64(out), ro, oe / oo.U, kind, 1)
     oo.check("lse", np64(lse), rl, le / oo.U, "fp32", 1)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_values_that_are_not_finite(kind, dh):
+    """An infinite value of a cached token makes its element infinite in every head that reads it, whatever the
+    token's probability; infinities of both signs, or a NaN, make it NaN. Other elements keep theirs."""
+    import chunked_gated_delta_kda_amd as kda
+
+    lens, hkv, group, page = [40, 3000, 300, 129], 2, 3, 16
+    d = make(lens, hkv * group, hkv, dh, page, kind, 21)
+    k, v = d["k_cache"], d["v_cache"]
+    at = place(d, 2, 17)                # beside a token with all but e^-30 of the attention
+    k[at[0], at[1]] = 0
+    k[at[0], at[1], :, 0] = 40
+    d["q"][2] = 0
+    d["q"][2, :, 0] = 1
+    for t in range(lens[2]):
+        if t != 17:
+            p = place(d, 2, t)
+            k[p[0], p[1], :, 0] = 10
+    inf, nan = float("inf"), float("nan")
+    want = {}                           # (sequence, cache head, element): what the output holds
+    for seq, head, element, values in ((0, 0, 3, {7: inf}), (0, 1, 0, {39: -inf}), (1, 0, 5, {0: inf, 2999: inf}),
+                                       (1, 0, dh - 1, {1500: -inf}), (1, 1, 8, {100: inf, 2000: -inf}), (1, 1, 9, {64: nan}),
+                                       (2, 0, 1, {200: inf}), (2, 1, 2, {299: -inf}), (3, 0, 33, {128: inf})):
+        for token, x in values.items():
+            p = place(d, seq, token)
+            v[p[0], p[1], head, element] = x
+        want[seq, head, element] = sum(values.values())
+    out, lse = kda.attn_decode(**d, scale=1.0, return_lse=True, check=True)
+    got = np64(out)
+    plain = dict(d, v_cache=torch.nan_to_num(v, nan=0.0, posinf=0.0, neginf=0.0))
+    ro, oe, rl, le = oracle(plain, lens, kind)
+    for (seq, head, element), x in want.items():
+        rows = got[seq, head * group:(head + 1) * group, element]
+        assert (np.isnan(rows) if np.isnan(x) else rows == x).all(), (seq, head, element, x, rows)
+        got[seq, head * group:(head + 1) * group, element] = ro[seq, head * group:(head + 1) * group, element]
+    oo.check("out", got, ro, oe / oo.U, kind, 1)
+    oo.check("lse", np64(lse), rl, le / oo.U, "fp32", 1)
