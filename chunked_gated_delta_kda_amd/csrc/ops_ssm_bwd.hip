@@ -255,13 +255,15 @@ __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(const kda_ssm_args a,
                       blockIdx.x % (16 * M), back);
 }
 
-// Sums of four values over the 16 lanes of a row: in lane i that of v[i % 4].
+// Sums of four values over the 16 lanes of a row: in lane i that of v[i % 4]. Four lanes have the same sum, and all
+// of them store it: it has to be the same to the last bit, so the quads' sums are added as (0 + 2) + (1 + 3) in each
+// (halves first; quarters first would add other pairs in lanes 4 apart).
 __device__ __forceinline__ float row_sum4(float v0, float v1, float v2, float v3, bool odd, bool upper) {
     const float a = (odd ? v1 : v0) + dpp_f<0xb1>(odd ? v0 : v1);       // quad_perm [1,0,3,2]
     const float b = (odd ? v3 : v2) + dpp_f<0xb1>(odd ? v2 : v3);
     float c = (upper ? b : a) + dpp_f<0x4e>(upper ? a : b);             // quad_perm [2,3,0,1]
-    c += dpp_f<0x124>(c);                                               // row_ror:4
     c += dpp_f<0x128>(c);                                               // row_ror:8
+    c += dpp_f<0x124>(c);                                               // row_ror:4
     return c;
 }
 
