@@ -542,6 +542,10 @@ hipError_t bwd_form(const kda_ssm_args &a, const kda_ssm_grads &d, float *ws, in
     if (T) {
         ssm_bwd_tile_kernel<DT, CB, M><<<grid, 64 * WAVES, 0, st>>>(a, d, ws, lay, err, L, (int)tiles, (int)blocks);
         if (hipError_t e = hipGetLastError()) return e;
+    }
+    // One tile has no neighbours to join; more than one there are for less than 2048 blocks only, so that the
+    // threads of a launch stay under 2^32 whatever the number of groups.
+    if (tiles > 1) {
         ssm_bwd_join_kernel<CB, M><<<dim3((unsigned)(blocks * 16 * M), 2), 256, 0, st>>>(a, ws, lay, (int)tiles, (int)blocks);
         if (hipError_t e = hipGetLastError()) return e;
     }

@@ -24,3 +24,32 @@ def test_lanes_that_store_one_sum_agree():
     got = kda.ssm_bwd(one(1, 16), one(1, 16), torch.zeros(16, 16, device="cuda"), one(1, 1, 16), one(1, 1, 16), dy,
                       delta_softplus=False)
     assert (got["dB"] == 2).all() and (got["dC"] == 2).all()
+
+
+def test_gradients_of_as_many_groups_as_fill_a_launch():
+    """2^18 groups of one channel with 129 states, one token: everything has a closed form. A rounding or two an
+    operation: exponents up to 1 (8), products (4), sums over states (a rounding a term)."""
+    import chunked_gated_delta_kda_amd as kda
+
+    D, N = 1 << 18, 129
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    s = 0.1 + 0.9 * torch.rand(1, D, generator=g, device="cuda")
+    u, dy, h0 = r(1, D), r(1, D), r(1, D, N)
+    A, B, C = -torch.rand(D, N, generator=g, device="cuda"), r(1, D, N), r(1, D, N)
+    got = kda.ssm_bwd(u, s, A, B, C, dy, initial_state=h0, delta_softplus=False)
+    s, u, dy, h0, A, B, C = (t.double() for t in (s[0], u[0], dy[0], h0[0], A, B[0], C[0]))
+    a = torch.exp(s[:, None] * A)
+    x, dh = (s * u)[:, None], C * dy[:, None]
+    h, hs = a * h0 + x * B, a * h0.abs() + (x * B).abs()
+    into, size = (dh * B).sum(1), (dh * B).abs().sum(1)
+    decay = dh * a * h0
+    U = 2.0 ** -24
+    for name, want, err in (("dB", dh * x, 4 * (dh * x).abs()), ("dC", h * dy[:, None], 14 * hs * dy[:, None].abs()),
+                            ("dA", decay * s[:, None], 16 * (decay * s[:, None]).abs()),
+                            ("d_initial_state", dh * a, 12 * (dh * a).abs()),
+                            ("du", s * into, (N + 8) * s * size),
+                            ("ddelta", (decay * A).sum(1) + u * into,
+                             (N + 20) * ((decay * A).abs().sum(1) + u.abs() * size))):
+        off = (got[name].double().reshape(want.shape) - want).abs() - U * err - 2.0 ** -126
+        assert (off <= 0).all(), (name, off.max().item())
