@@ -279,11 +279,12 @@ struct BwdWalk {
                 v *= sg * __builtin_fmaf(p, 1.0f - sg, 1.0f);
             }
             e[W - 1][i] = v;
-            const float own = mine ? v : 0.0f;
-            db[i] += own;
+            if (mine) {         // of the next tile's rows nothing: 0 times an infinite row would be NaN
+                db[i] += v;
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) dw[j][i] = __builtin_fmaf(own, hist[j][i], dw[j][i]);
-            dw[W - 1][i] = __builtin_fmaf(own, x[i], dw[W - 1][i]);
+                for (int j = 0; j < W - 1; ++j) dw[j][i] = __builtin_fmaf(v, hist[j][i], dw[j][i]);
+                dw[W - 1][i] = __builtin_fmaf(v, x[i], dw[W - 1][i]);
+            }
 #pragma unroll
             for (int j = 0; j + 1 < W - 1; ++j) hist[j][i] = hist[j + 1][i];
             hist[W - 2][i] = x[i];
