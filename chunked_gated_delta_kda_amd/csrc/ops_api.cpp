@@ -79,6 +79,26 @@ int check_conv(const kda_conv_args &a, bool grads) {
     return KDA_OK;
 }
 
+// the convolution's inputs, the initial state last
+struct ConvSpans {
+    Span in[5];
+    int64_t state;      // elements
+    explicit ConvSpans(const kda_conv_args &a) {
+        const int64_t es = (int64_t)dtype_bytes(a.dtype), C = a.channels;
+        state = (int64_t)a.num_seqs * (a.width - 1) * C;
+        in[0] = span(a.x, rows_bytes(a.total_tokens, a.x_stride, C, es));
+        in[1] = span(a.weight, C * a.width * 4);
+        in[2] = span(a.bias, C * 4);
+        in[3] = span(a.cu_seqlens, ((int64_t)a.num_seqs + 1) * 4);
+        in[4] = span(a.initial_state, state * es);
+    }
+    bool over(Span out, int count = 5) const {
+        for (int i = 0; i < count; ++i)
+            if (meet(in[i], out)) return true;
+        return false;
+    }
+};
+
 // ---------------------------------------------------------------- selective scan
 bool ssm_sizes_ok(int64_t T, int64_t D, int64_t N, int64_t G) {
     return T >= 0 && T <= 1 << 27 && D >= 1 && D <= 1 << 20 && N >= 1 && N <= KDA_SSM_MAX_STATE && G >= 1 && G <= D && D % G == 0;
@@ -99,9 +119,9 @@ int check_ssm(const kda_ssm_args &a, bool grads) {
     return KDA_OK;
 }
 
-// the inputs of a scan over `rows` rows
+// a scan's inputs, the initial state last
 struct SsmSpans {
-    Span in[9];
+    Span in[10];
     int64_t state;
     explicit SsmSpans(const kda_ssm_args &a) {
         const int64_t es = (int64_t)dtype_bytes(a.dtype), T = a.total_tokens, D = a.channels, N = a.state_size;
@@ -114,9 +134,10 @@ struct SsmSpans {
         in[5] = span(a.A, D * N * 4);
         in[6] = span(a.D, D * 4);
         in[7] = span(a.delta_bias, D * 4);
-        in[8] = span(a.initial_state, state);
+        in[8] = span(a.cu_seqlens, ((int64_t)a.num_seqs + 1) * 4);
+        in[9] = span(a.initial_state, state);
     }
-    bool over(Span out, int count = 9) const {
+    bool over(Span out, int count = 10) const {
         for (int i = 0; i < count; ++i)
             if (meet(in[i], out)) return true;
         return false;
@@ -143,12 +164,10 @@ int kda_conv_fwd(const kda_conv_args *args, void *stream) {
     const kda_conv_args &a = *args;
     if (const int rc = check_conv(a, false)) return rc;
     if (!a.cu_seqlens && a.num_seqs != 1) return KDA_ERR_SHAPE;
+    const ConvSpans s(a);
     const int64_t es = (int64_t)dtype_bytes(a.dtype);
-    const Span x = span(a.x, rows_bytes(a.total_tokens, a.x_stride, a.channels, es));
-    const Span out = span(a.out, (int64_t)a.total_tokens * a.channels * es);
-    const int64_t state = (int64_t)a.num_seqs * (a.width - 1) * a.channels * es;
-    const Span si = span(a.initial_state, state), sf = span(a.final_state, state);
-    if (meet(x, out) || meet(si, sf) || meet(x, sf) || meet(si, out) || meet(out, sf)) return KDA_ERR_ALIAS;
+    const Span out = span(a.out, (int64_t)a.total_tokens * a.channels * es), fin = span(a.final_state, s.state * es);
+    if (s.over(out) || s.over(fin) || meet(out, fin)) return KDA_ERR_ALIAS;
     return launched(kda::ops::launch_conv_fwd(a, kda::device_error_word(), (hipStream_t)stream));
 }
 
@@ -157,13 +176,11 @@ int kda_conv_decode(const kda_conv_args *args, void *stream) {
     const kda_conv_args &a = *args;
     if (const int rc = check_conv(a, false)) return rc;
     if (a.cu_seqlens || a.total_tokens != a.num_seqs) return KDA_ERR_SHAPE;
+    const ConvSpans s(a);
     const int64_t es = (int64_t)dtype_bytes(a.dtype);
-    const Span x = span(a.x, rows_bytes(a.total_tokens, a.x_stride, a.channels, es));
-    const Span out = span(a.out, (int64_t)a.total_tokens * a.channels * es);
-    const int64_t state = (int64_t)a.num_seqs * (a.width - 1) * a.channels * es;
-    const Span si = span(a.initial_state, state), sf = span(a.final_state, state);
-    if (meet(x, out) || (a.initial_state != a.final_state && meet(si, sf)) || meet(x, sf) || meet(si, out) || meet(out, sf))
-        return KDA_ERR_ALIAS;
+    const Span out = span(a.out, (int64_t)a.total_tokens * a.channels * es), fin = span(a.final_state, s.state * es);
+    const bool in_place = a.initial_state == a.final_state;
+    if (s.over(out) || s.over(fin, in_place ? 4 : 5) || meet(out, fin)) return KDA_ERR_ALIAS;
     return launched(kda::ops::launch_conv_decode(a, (hipStream_t)stream));
 }
 
@@ -183,15 +200,13 @@ int kda_conv_bwd(const kda_conv_args *args, const kda_conv_grads *grads, void *s
     if (!a.cu_seqlens && a.num_seqs != 1) return KDA_ERR_SHAPE;
     if (g.dy_stride < a.channels) return KDA_ERR_SHAPE;
     if (!g.dweight || (a.total_tokens > 0 && (!g.dy || !g.dx))) return KDA_ERR_NULL;
+    const ConvSpans s(a);
     const int64_t es = (int64_t)dtype_bytes(a.dtype), C = a.channels, T = a.total_tokens;
-    const int64_t state = (int64_t)a.num_seqs * (a.width - 1) * C;
-    const Span in[] = {span(a.x, rows_bytes(T, a.x_stride, C, es)), span(g.dy, rows_bytes(T, g.dy_stride, C, es)),
-                       span(a.weight, C * a.width * 4), span(a.initial_state, state * es), span(g.d_final_state, state * 4)};
+    const Span dy = span(g.dy, rows_bytes(T, g.dy_stride, C, es)), dfin = span(g.d_final_state, s.state * 4);
     const Span out[] = {span(g.dx, T * C * es), span(g.dweight, C * a.width * 4), span(g.dbias, C * 4),
-                        span(g.d_initial_state, state * 4)};
+                        span(g.d_initial_state, s.state * 4)};
     for (int o = 0; o < 4; ++o) {
-        for (const Span &i : in)
-            if (meet(out[o], i)) return KDA_ERR_ALIAS;
+        if (s.over(out[o]) || meet(dy, out[o]) || meet(dfin, out[o])) return KDA_ERR_ALIAS;
         for (int q = 0; q < o; ++q)
             if (meet(out[o], out[q])) return KDA_ERR_ALIAS;
     }
@@ -231,7 +246,7 @@ int kda_ssm_decode(const kda_ssm_args *args, void *stream) {
     const Span out = span(a.out, (int64_t)a.total_tokens * a.channels * (int64_t)dtype_bytes(a.dtype));
     const Span fin = span(a.final_state, s.state);
     const bool in_place = a.initial_state == a.final_state;
-    if (s.over(out) || s.over(fin, in_place ? 8 : 9) || meet(out, fin)) return KDA_ERR_ALIAS;
+    if (s.over(out) || s.over(fin, in_place ? 9 : 10) || meet(out, fin)) return KDA_ERR_ALIAS;
     return launched(kda::ops::launch_ssm_decode(a, (hipStream_t)stream));
 }
 

@@ -387,3 +387,33 @@ def test_ssm_bwd_abi_refusals(lib):
     assert need > 0 and bwd(nbytes=need - 1) == 4
     assert bwd(dict(dz=None), z=None, nbytes=need - 1) == 4       # no gate, no gradient of one
     assert lib.kda_ssm_bwd_workspace_bytes(T, Dn, Ns, 5) == 0
+
+
+# ---------------------------------------------------------------- outputs over parameters and offsets
+@pytest.mark.parametrize("name,at,size", [("weight", 100 << 20, C * W * 4), ("bias", 101 << 20, C * 4), ("cu_seqlens", 102 << 20, 8)])
+def test_conv_abi_refuses_outputs_over_parameters(lib, name, at, size):
+    def grads(**over):
+        g = dict(dy=110 << 20, d_final_state=None, dx=111 << 20, dweight=112 << 20, dbias=113 << 20, d_initial_state=None, dy_stride=C)
+        g.update(over)
+        return lib.kda_conv_bwd(ctypes.byref(conv_args(**{name: at})), ctypes.byref(native.KdaConvGrads(**g)), None, None, 0)
+
+    for end in (at, at + size - 2):                                              # the first and the last of it
+        assert lib.kda_conv_fwd(ctypes.byref(conv_args(**{name: at}, out=end)), None) == 7
+        assert lib.kda_conv_fwd(ctypes.byref(conv_args(**{name: at}, final_state=end)), None) == 7
+        if name != "cu_seqlens":
+            for kw in (dict(out=end), dict(final_state=end)):
+                assert lib.kda_conv_decode(ctypes.byref(conv_args(**{name: at}, num_seqs=T, **kw)), None) == 7
+        for out in ("dx", "dweight", "dbias", "d_initial_state"):
+            assert grads(**{out: end}) == 7, out
+
+
+def test_ssm_abi_refuses_outputs_over_offsets(lib):
+    at = 100 << 20
+    for end in (at, at + 4):
+        for kw in (dict(out=end), dict(final_state=end)):
+            assert lib.kda_ssm_fwd(ctypes.byref(ssm_args(cu_seqlens=at, **kw)), None, None, 0) == 7, kw
+        names = ("dy", "d_final_state", "du", "ddelta", "dB", "dC", "dz", "dA", "dD", "ddelta_bias", "d_initial_state")
+        for out in names[2:]:
+            g = {n: (32 + i) << 20 for i, n in enumerate(names)}
+            g.update({out: end, "dy_stride": Dn})
+            assert lib.kda_ssm_bwd(ctypes.byref(ssm_args(cu_seqlens=at)), ctypes.byref(native.KdaSsmGrads(**g)), None, None, 0) == 7, out
