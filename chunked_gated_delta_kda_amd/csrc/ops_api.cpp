@@ -104,7 +104,9 @@ bool ssm_sizes_ok(int64_t T, int64_t D, int64_t N, int64_t G) {
     return T >= 0 && T <= 1 << 27 && D >= 1 && D <= 1 << 20 && N >= 1 && N <= KDA_SSM_MAX_STATE && G >= 1 && G <= D && D % G == 0;
 }
 
-int check_ssm(const kda_ssm_args &a, bool grads) {
+// far: rows may lie further apart than KDA_SSM_MAX_STRIDE (the token kernel forms 64-bit offsets, those that walk the
+// time axis 32-bit ones between a few rows)
+int check_ssm(const kda_ssm_args &a, bool grads, bool far = false) {
     if (!dtype_ok(a.dtype) || (a.delta_softplus != 0 && a.delta_softplus != 1)) return KDA_ERR_UNSUPPORTED;
     if (!ssm_sizes_ok(a.total_tokens, a.channels, a.state_size, a.groups) || a.num_seqs < 1 ||
         (int64_t)a.num_seqs * a.channels > (int64_t)1 << 31)
@@ -114,7 +116,7 @@ int check_ssm(const kda_ssm_args &a, bool grads) {
         (a.z && a.z_stride < a.channels))
         return KDA_ERR_SHAPE;
     for (const int64_t s : {a.u_stride, a.delta_stride, a.B_stride, a.C_stride, a.z ? a.z_stride : 0})
-        if (s > KDA_SSM_MAX_STRIDE) return KDA_ERR_SHAPE;
+        if (!far && s > KDA_SSM_MAX_STRIDE) return KDA_ERR_SHAPE;
     if (!a.A || (a.total_tokens > 0 && (!a.u || !a.delta || !a.B || !a.C || (!grads && !a.out)))) return KDA_ERR_NULL;
     return KDA_OK;
 }
@@ -240,7 +242,7 @@ int kda_ssm_fwd(const kda_ssm_args *args, void *stream, void *workspace, size_t 
 int kda_ssm_decode(const kda_ssm_args *args, void *stream) {
     if (!args) return KDA_ERR_NULL;
     const kda_ssm_args &a = *args;
-    if (const int rc = check_ssm(a, false)) return rc;
+    if (const int rc = check_ssm(a, false, true)) return rc;
     if (a.cu_seqlens || a.total_tokens != a.num_seqs) return KDA_ERR_SHAPE;
     const SsmSpans s(a);
     const Span out = span(a.out, (int64_t)a.total_tokens * a.channels * (int64_t)dtype_bytes(a.dtype));

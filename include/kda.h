@@ -362,7 +362,8 @@ size_t kda_conv_bwd_workspace_bytes(int32_t total_tokens, int32_t channels, int3
 int kda_conv_bwd(const kda_conv_args *args, const kda_conv_grads *grads, void *stream, void *workspace,
                  size_t workspace_bytes);
 
-/* Largest state size and row stride (elements) of the scan. */
+/* Largest state size of the scan, and largest row stride (elements) of kda_ssm_fwd and
+ * kda_ssm_bwd (kda_ssm_decode takes any). */
 #define KDA_SSM_MAX_STATE 256
 #define KDA_SSM_MAX_STRIDE (1 << 27)
 

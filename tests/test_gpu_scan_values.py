@@ -53,3 +53,22 @@ def test_gradients_of_as_many_groups_as_fill_a_launch():
                              (N + 20) * ((decay * A).abs().sum(1) + u.abs() * size))):
         off = (got[name].double().reshape(want.shape) - want).abs() - U * err - 2.0 ** -126
         assert (off <= 0).all(), (name, off.max().item())
+
+
+def test_tokens_of_rows_further_apart_than_the_scan_takes():
+    """One token of two sequences whose rows lie 2^27 + 8 elements apart: as from rows side by side."""
+    import chunked_gated_delta_kda_amd as kda
+
+    g = torch.Generator(device="cuda").manual_seed(6)
+    D, N, stride = 40, 16, (1 << 27) + 8
+    buf = torch.empty(stride + 4096, dtype=torch.bfloat16, device="cuda")
+    near, far = {}, {}
+    for i, (name, shape) in enumerate(dict(u=(2, D), delta=(2, D), z=(2, D), B=(2, 1, N), C=(2, 1, N)).items()):
+        near[name] = torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+        far[name] = buf.as_strided(shape, (stride,) + near[name].stride()[1:], 256 * i)
+        far[name].copy_(near[name])
+    A, state = -torch.rand(D, N, generator=g, device="cuda"), torch.randn(2, D, N, generator=g, device="cuda")
+    want, got = state.clone(), state.clone()
+    y, _ = kda.ssm_decode(A=A, state=want, **near)
+    x, _ = kda.ssm_decode(A=A, state=got, **far)
+    assert torch.equal(x, y) and torch.equal(got, want)

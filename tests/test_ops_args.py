@@ -417,3 +417,13 @@ def test_ssm_abi_refuses_outputs_over_offsets(lib):
             g = {n: (32 + i) << 20 for i, n in enumerate(names)}
             g.update({out: end, "dy_stride": Dn})
             assert lib.kda_ssm_bwd(ctypes.byref(ssm_args(cu_seqlens=at)), ctypes.byref(native.KdaSsmGrads(**g)), None, None, 0) == 7, out
+
+
+def test_only_the_scan_over_time_limits_strides(lib):
+    far = (1 << 27) + 8
+    spread = {n: (i + 1) << 45 for i, n in enumerate(("u", "delta", "B", "C", "z", "out"))}
+    for name in ("u", "delta", "B", "C", "z"):
+        kw = {f"{name}_stride": far, **spread}
+        assert lib.kda_ssm_fwd(ctypes.byref(ssm_args(**kw)), None, None, 0) == 2, name
+        kw["out"] = kw["u"]             # refused, but for the overlap: the stride has passed
+        assert lib.kda_ssm_decode(ctypes.byref(ssm_args(num_seqs=T, **kw)), None) == 7, name
