@@ -74,7 +74,7 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, *, retur
     """Attention of one new token of each of B sequences over its cached tokens, on the current
     HIP device: out[h] = sum_t softmax_t(scale q[h].k_t) v_t.
 
-    q: bf16 or fp16 [B, Hq, Dh], Dh 64, 128 or 256; k_cache, v_cache: [pages, page size, Hkv, Dh] of
+    q: bf16 or fp16 [B, Hq, Dh], B up to 65536, Dh 64, 128 or 256; k_cache, v_cache: [pages, page size, Hkv, Dh] of
     q's dtype, Hkv dividing Hq (query head h reads cache head h // (Hq // Hkv)), any strides that
     are multiples of 8 elements (a transposed layout or a slice of a joint cache is read in
     place); block_table: int32 [B, W], the pages of each sequence in order (entries past its

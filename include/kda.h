@@ -474,7 +474,9 @@ typedef struct kda_attn_args {
  * the library allocates it stream-ordered on `stream`. The launches depend on the sizes in
  * args alone: a captured call stays right when lengths, pages and table entries change. The
  * same results from run to run. Limits: table_width * page_size <= 2^30, q_heads <= 65535,
- * (num_seqs + 1) * kv_heads * ceil(q_heads / kv_heads / 16) <= 2^22.
+ * num_seqs <= 65536, (num_seqs + 1) * kv_heads * ceil(q_heads / kv_heads / 16) <= 2^22. Every
+ * workgroup reads all lengths, so that the time of many short sequences grows with the square of
+ * their number (16 tokens each, one cache head: 16384 sequences 4.7 ms, where 24 us of cache are read).
  */
 size_t kda_attn_workspace_bytes(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                 int32_t table_width, int32_t page_size);

@@ -427,3 +427,17 @@ def test_only_the_scan_over_time_limits_strides(lib):
         assert lib.kda_ssm_fwd(ctypes.byref(ssm_args(**kw)), None, None, 0) == 2, name
         kw["out"] = kw["u"]             # refused, but for the overlap: the stride has passed
         assert lib.kda_ssm_decode(ctypes.byref(ssm_args(num_seqs=T, **kw)), None) == 7, name
+
+
+def test_attn_number_of_sequences(lib):
+    size = lambda n: lib.kda_attn_workspace_bytes(n, 1, 1, 64, 64, 16)  # noqa: E731
+    assert size(1 << 16) > 0 and size((1 << 16) + 1) == 0
+    mb = 1 << 20
+    a = dict(q=mb << 10, k_cache=mb << 20, v_cache=mb << 21, block_table=mb << 11, seq_lens=mb << 12, out=mb << 13, lse=None,
+             q_stride=64, q_head_stride=64, k_page_stride=1024, k_token_stride=64, k_head_stride=64, v_page_stride=1024,
+             v_token_stride=64, v_head_stride=64, table_stride=64, num_seqs=1 << 16, q_heads=1, kv_heads=1, head_dim=64,
+             num_pages=10, page_size=16, table_width=64, dtype=1, scale=0.1)
+    call = lambda: lib.kda_attn_decode(ctypes.byref(native.KdaAttnArgs(**a)), None, P, 0)  # noqa: E731
+    assert call() == 4                      # the workspace is too small: the number has passed
+    a["num_seqs"] += 1
+    assert call() == 2
