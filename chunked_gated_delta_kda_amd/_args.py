@@ -116,6 +116,8 @@ def launch_on(index, stream):
     value is that stream's handle. ``stream`` None: torch's current stream of the device."""
     if stream is None and torch.cuda.current_device() == index:
         return _Here(_current_stream(index))
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream: expected one of {_place(index)}, where the inputs are, got one of {stream.device}")
     return _elsewhere(index, stream)
 
 

@@ -441,3 +441,13 @@ def test_attn_number_of_sequences(lib):
     assert call() == 4                      # the workspace is too small: the number has passed
     a["num_seqs"] += 1
     assert call() == 2
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Its kernels would run beside what torch's allocator orders on the inputs' device."""
+    from types import SimpleNamespace
+
+    from chunked_gated_delta_kda_amd._args import launch_on
+    with pytest.raises(ValueError, match="stream:"):
+        with launch_on(0, SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)):
+            pass
