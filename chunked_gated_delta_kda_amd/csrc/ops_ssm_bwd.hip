@@ -492,11 +492,13 @@ __global__ __launch_bounds__(256) void ssm_bwd_rows_kernel(const kda_ssm_args a,
         }
 }
 
-// dA (blockIdx.y 0 .. 16 M - 1: a register of every block's lanes), dD and dbias (the last): sums over tiles.
+// dA (blockIdx.y 0 .. 16 M - 1: a register of every block's lanes), dD and dbias (the last): sums over tiles. Without
+// tiles (no tokens) the offsets are checked here.
 template <int CB, int M>
 __global__ __launch_bounds__(256) void ssm_bwd_params_kernel(const kda_ssm_args a, const kda_ssm_grads d, const float *ws,
-                                                             const Layout lay, int tiles, int blocks) {
+                                                             const Layout lay, int32_t *err, int tiles, int blocks) {
     const int r = blockIdx.y;
+    if (tiles == 0 && r == 0 && blockIdx.x == 0) check_offsets(Offsets{a.cu_seqlens, a.num_seqs, a.total_tokens}, err, threadIdx.x, 256);
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (r < 16 * M) {
         const int block = (int)(id >> 6);
@@ -558,8 +560,8 @@ hipError_t bwd_form(const kda_ssm_args &a, const kda_ssm_grads &d, float *ws, in
         if (hipError_t e = hipGetLastError()) return e;
     }
     const int64_t wide = std::max<int64_t>(blocks * 64, 2 * (int64_t)a.channels);
-    ssm_bwd_params_kernel<CB, M><<<dim3((unsigned)ceil_div(wide, 256), 16 * M + 1), 256, 0, st>>>(a, d, ws, lay, T ? (int)tiles : 0,
-                                                                                                  (int)blocks);
+    ssm_bwd_params_kernel<CB, M><<<dim3((unsigned)ceil_div(wide, 256), 16 * M + 1), 256, 0, st>>>(a, d, ws, lay, err,
+                                                                                                  T ? (int)tiles : 0, (int)blocks);
     return hipGetLastError();
 }
 

@@ -72,3 +72,22 @@ def test_tokens_of_rows_further_apart_than_the_scan_takes():
     y, _ = kda.ssm_decode(A=A, state=want, **near)
     x, _ = kda.ssm_decode(A=A, state=got, **far)
     assert torch.equal(x, y) and torch.equal(got, want)
+
+
+def test_malformed_offsets_without_tokens_raise_the_error_bit():
+    import chunked_gated_delta_kda_amd as kda
+
+    row, rows = torch.zeros(0, 8, device="cuda"), torch.zeros(0, 1, 16, device="cuda")
+    A, last = -torch.ones(8, 16, device="cuda"), torch.randn(2, 8, 16, device="cuda")
+    for cu, bits in (([0, 0, 0], 0), ([0, 3, 0], 2), ([0, 0, 4], 2), ([1, 0, 0], 2)):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        kda.device_errors()
+        got = kda.ssm_bwd(row, row, A, rows, rows, row, cu_seqlens=cu, d_final_state=last)
+        assert kda.device_errors() == bits, cu
+        assert torch.equal(got["d_initial_state"], last) and not got["dA"].any()
+        kda.ssm_fwd(row, row, A, rows, rows, cu_seqlens=cu)
+        assert kda.device_errors() == bits, cu
+        kda.conv_fwd(row, A[:, :4].contiguous(), cu_seqlens=cu)
+        assert kda.device_errors() == bits, cu
+        kda.conv_bwd(row, A[:, :4].contiguous(), row, cu_seqlens=cu)
+        assert kda.device_errors() == bits, cu
