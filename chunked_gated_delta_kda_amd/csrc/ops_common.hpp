@@ -96,16 +96,9 @@ __device__ __forceinline__ float swap16_add(float a, float b) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Sum over the 16 lanes of a row, in every lane.
+// What another lane of the row holds, by a DPP control word.
 template <int CTRL> __device__ __forceinline__ float dpp_f(float x) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float row_sum(float x) {
-    x += dpp_f<0x128>(x);   // row_ror:8
-    x += dpp_f<0x124>(x);   // row_ror:4
-    x += dpp_f<0x122>(x);   // row_ror:2
-    x += dpp_f<0x121>(x);   // row_ror:1
-    return x;
 }
 
 // Barrier of a block over its LDS traffic alone: unlike __syncthreads it does not wait for global
