@@ -33,6 +33,8 @@ def oracle(d, lens, kind, scale=1.0):
     if kind == "fp16":
         group, page = d["q"].shape[1] // v.shape[2], v.shape[1]
         for b, n in enumerate(lens):
+            if n == 0:
+                continue
             t = np.arange(n)
             size = np.abs(v[table[b, t // page], t % page]).sum(0).repeat(group, 0)
             k = np.nan_to_num(np64(d["k_cache"]))[table[b, t // page], t % page].repeat(group, 1)
