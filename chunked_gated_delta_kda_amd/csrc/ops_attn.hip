@@ -4,8 +4,9 @@
 //   out[h] = sum_t softmax_t(scale q[h].k_t) v_t over the len cached tokens of the sequence, in
 //   one pass with the running maximum and sum; lse[h] = log sum_t e^{scale q[h].k_t}
 //
-// Bound by the bytes of the cache, each read once. A wave takes 32 tokens of one key-value head at
-// a time, for up to 16 query heads that share it:
+// Bound by the bytes of the cache, each read once for every 16 query heads that share a cache head (8 x 4096
+// tokens of 128 bf16: 64 heads over 1 take 22.0 us, as long as over 4). A wave takes 32 tokens of one
+// key-value head at a time, for up to 16 query heads that share it:
 //  * S^T = K Q^T (v_mfma_f32_16x16x32: rows tokens, columns heads). A lane holds the scores of one
 //    head for 8 tokens, so maxima and sums are lane-local but for two exchanges between the
 //    wave's four 16-lane rows.
@@ -172,8 +173,9 @@ struct Rows {
     int64_t k[TILE], v[TILE];
 };
 
-// 1 x 65536 tokens, 32 heads over 8, bf16: 268 MB in 45 to 54 us, 5.0 to 6.0 TB/s; 64 skewed sequences, 32 heads over 4, fp16: 364
-// MB in 80 us, 4.5 TB/s.
+// 1 x 65536 tokens, 32 heads over 8, bf16: 268 MB in 44 to 54 us, 5.0 to 6.1 TB/s; 64 skewed sequences, 32 heads over 4, fp16: 364
+// MB in 80 us, 4.5 TB/s; 256 x 1024 tokens, 32 heads over 8, bf16: 1.07 GB in 210 us, 5.1 TB/s. Every wave finds its chunk
+// from all lengths, which shows from about a thousand sequences on: 1024 x 16 tokens, 32 heads over 8, 195 us for 67 MB.
 template <int DT, int DH>
 __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_args a, float *acc_out, float *ml_out,
                                                                 int32_t *err, int spread, int min_chunk, int tiles_h) {
@@ -403,8 +405,10 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const kda_attn_a
     }
 }
 
-// Blocks that all tokens are spread over. Measured on MI355X (us, 512 | 768 | 1024 | 1536): 1 x 65536 tokens, 32 heads over 8,
-// 58.6 | 62.5 | 62.4 | 66; 64 skewed sequences fp16, 32 heads over 4, 93.0 | 90.0 | 87.8 | 87.
+// Blocks that all tokens are spread over: 768 run at once at head dimension 128, three to each of 256 CUs (166 registers allow
+// three waves a SIMD). Measured on MI355X (us, 512 | 768 | 1024 | 1536): 1 x 65536 tokens, 32 heads over 8, 58.9 | 61.3 |
+// 61.8 | 65.8; 64 skewed sequences fp16, 32 heads over 4, 92.5 | 90.2 | 87.6 | 88.7: fewer blocks suit one long sequence (fewer
+// chunks to join), more of them skewed ones, and what lies between loses 4% and 3% to the best of each.
 constexpr int SPREAD = 768, MAX_PARTS = SPREAD + 1;
 
 // Joins the chunks of one (sequence, head), in their order, where there are several: threads take four

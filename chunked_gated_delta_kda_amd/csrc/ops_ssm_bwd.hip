@@ -145,7 +145,8 @@ __device__ __forceinline__ void add_state(f32x16 (&x)[M], const f32x16 (&f)[M], 
 }
 
 // 8 x 1024 x 2048 x 16 bf16 with a gate: 111 us, 64% of the busy cycles issue vector instructions; 268 MB of states go out.
-// Two waves a SIMD: with registers for four it spills (710 us for all kernels against 400), for three nothing changes.
+// Two waves a SIMD: with registers for four it spills (710 us for all kernels against 400), for three nothing changes. At
+// two only the form of more than 128 states spills (about 300 registers).
 template <int DT, int CB, int M>
 __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_tile_kernel(const kda_ssm_args a, const kda_ssm_grads d, float *ws,
                                                                      const Layout lay, int32_t *err, int L, int tiles, int blocks) {
@@ -268,7 +269,9 @@ __device__ __forceinline__ float row_sum4(float v0, float v1, float v2, float v3
 }
 
 // 8 x 1024 x 2048 x 16 bf16 with a gate: 264 us, 76% of the busy cycles issue vector instructions (379 a token of a
-// wave), two waves a SIMD at 256 registers.
+// wave), two waves a SIMD at 256 registers, 21 to 23 of them spilled (88 to 96 bytes a lane). States of 17 to 64 do not
+// spill; of 65 to 128 they spill 113 registers, of more 530 to 560, and there the time is the spills': all kernels of 8 x
+// 1024 x 2048 with 16 | 32 | 64 | 128 | 256 states take 0.39 | 0.73 | 1.6 | 5.6 | 54 ms.
 template <int DT, int CB, int M>
 __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_args a, const kda_ssm_grads d, float *ws,
                                                                 const Layout lay, int L, int tiles, int blocks) {
@@ -469,8 +472,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const kda_ssm_ar
     }
 }
 
-// dB and dC of every (token, group, state): the sums over the group's channel blocks. 8192 tokens, 32 blocks: 67 MB in
-// 7.6 us.
+// dB and dC of every (token, group, state): the sums over the group's channel blocks. 8192 tokens, 32 blocks: 34 MB in
+// 7.5 us.
 template <int DT>
 __global__ __launch_bounds__(256) void ssm_bwd_rows_kernel(const kda_ssm_args a, const kda_ssm_grads d, const float *rows, int per_group,
                                                            int NP) {

@@ -73,7 +73,8 @@ def ssm_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, cu_seqlens=None,
     dividing D), rows contiguous, any row stride (slices of a projection are read in place); A:
     fp32 [D, N]; D, delta_bias: fp32 [D] or None; z: None for no gate; cu_seqlens: int32 [S+1] on the
     device or None (one sequence); initial_state: fp32 [S, D, N] or None (zeros); delta_softplus
-    False: the steps are delta + delta_bias as they are; out, final_state: caller buffers or None.
+    False: the steps are delta + delta_bias as they are; out, final_state: caller buffers or None. s_t A
+    is meant to be negative or zero: where states grow past fp32's range within some hundred tokens, zeros become NaN.
     final_state must not overlap initial_state (ssm_decode updates in place). check: as in fwd.
     Returns (out [T, D] of u's dtype, final_state fp32 [S, D, N] or None). Tensors that the call
     allocates belong to its stream.
@@ -146,7 +147,8 @@ def ssm_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, cu_seqlens=N
     d_final_state = dL/d(final_state) (fp32 [S, D, N]), returns a dict of du, ddelta, dz ([T, D]), dB, dC
     ([T, G, N]) of u's dtype, and fp32 dA ([D, N]), dD, ddelta_bias ([D]) and d_initial_state ([S, D, N], or None
     when need_d_initial_state is False); dz, dD and ddelta_bias are None without z, D and delta_bias. Needs
-    nothing that the forward computed. The same results from run to run."""
+    nothing that the forward computed. The same results from run to run. The workspace holds a state per channel for
+    every 4 tokens (2 from state sizes over 64, 1 over 128): 4.8 GiB for 65536 tokens of 4096 channels and 16 states."""
     lib = native.load_library()
     dev = u.get_device()
     on_device("kda.ssm_bwd", dev)

@@ -400,7 +400,10 @@ typedef struct kda_ssm_args {
  * scanned in tiles whose states are joined in the workspace: kda_ssm_workspace_bytes() bytes
  * of device memory, or NULL: then the library allocates it stream-ordered on `stream`. The
  * same results from run to run. Limits: total_tokens <= 2^27, channels <= 2^20,
- * num_seqs * channels <= 2^31. final_state must not overlap initial_state.
+ * num_seqs * channels <= 2^31. final_state must not overlap initial_state. The recurrence is
+ * meant to decay (s_t A <= 0): factors of up to some hundred tokens are multiplied together, and
+ * where they grow past fp32's range a state of zero becomes NaN. From an infinite input on, its
+ * channel is infinite or NaN.
  */
 size_t kda_ssm_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t channels, int32_t state_size,
                                int32_t groups);
@@ -432,7 +435,10 @@ typedef struct kda_ssm_grads {
  * the forward computed. Sums run in a fixed order: the same results from run to run. workspace:
  * kda_ssm_bwd_workspace_bytes() bytes of device memory, or NULL: then the library allocates it
  * stream-ordered on `stream`; it holds, above all, a state per channel for every 4 tokens (2 from
- * state sizes over 64, 1 over 128).
+ * state sizes over 64, 1 over 128) and has no cap: 65536 tokens of 4096 channels
+ * take 4.8 GiB with 16 states, 24 with 64 and 81 with 128. Where that is not to be had the call
+ * returns KDA_ERR_ALLOC: a caller then splits the batch between sequences, or a sequence at a
+ * token whose state it has (d_initial_state of what follows is d_final_state of what precedes).
  */
 size_t kda_ssm_bwd_workspace_bytes(int32_t total_tokens, int32_t channels, int32_t state_size, int32_t groups);
 int kda_ssm_bwd(const kda_ssm_args *args, const kda_ssm_grads *grads, void *stream, void *workspace,
@@ -470,10 +476,11 @@ typedef struct kda_attn_args {
  * tokens gives zeros and lse = -infinity. Rows of q and of the caches are read 16 bytes at a
  * time: their base pointers are aligned to 16 bytes and their strides are multiples of 8
  * elements, else KDA_ERR_UNSUPPORTED. What a page holds past a sequence's length is not used,
- * whatever it is. workspace: kda_attn_workspace_bytes() bytes of device memory, or NULL: then
- * the library allocates it stream-ordered on `stream`. The launches depend on the sizes in
- * args alone: a captured call stays right when lengths, pages and table entries change. The
- * same results from run to run. Limits: table_width * page_size <= 2^30, q_heads <= 65535,
+ * whatever it is; an infinite value or a NaN in use makes its element of the output so, and no
+ * other. workspace: kda_attn_workspace_bytes() bytes of device memory, or NULL: then the library
+ * allocates it stream-ordered on `stream`. The launches depend on the sizes in args alone: a
+ * captured call stays right when lengths, pages and table entries change. The same results
+ * from run to run. Limits: table_width * page_size <= 2^30, q_heads <= 65535,
  * num_seqs <= 65536, (num_seqs + 1) * kv_heads * ceil(q_heads / kv_heads / 16) <= 2^22. Every
  * workgroup reads all lengths, so that the time of many short sequences grows with the square of
  * their number (16 tokens each, one cache head: 16384 sequences 4.7 ms, where 24 us of cache are read).
