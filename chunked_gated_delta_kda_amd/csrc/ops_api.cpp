@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "kda.h"
 #include "kda_launch.hpp"
@@ -159,6 +160,92 @@ int check_attn_sizes(int64_t B, int64_t hq, int64_t hkv, int64_t dh, int64_t wid
 
 bool by16(const void *p) { return (uintptr_t)p % 16 == 0; }
 
+// the bytes that a paged cache lies in: rows of `row` elements of `es` bytes
+Span cache_span(const void *p, int64_t pages, int64_t page_size, int64_t heads, int64_t page, int64_t token, int64_t head, int64_t row,
+                int64_t es) {
+    return span(p, ((pages - 1) * page + (page_size - 1) * token + (heads - 1) * head + row) * es);
+}
+
+// what both token attentions check of their arguments; strides of the caches are multiples of `unit`
+int check_attn(const kda_attn_args &a, int64_t unit) {
+    if (a.dtype != KDA_DTYPE_BF16 && a.dtype != KDA_DTYPE_F16) return KDA_ERR_UNSUPPORTED;
+    if (!std::isfinite(a.scale)) return KDA_ERR_UNSUPPORTED;
+    if (const int rc = check_attn_sizes(a.num_seqs, a.q_heads, a.kv_heads, a.head_dim, a.table_width, a.page_size)) return rc;
+    if (a.num_pages < 1 || a.table_stride < 0 || (a.num_seqs > 1 && a.table_stride < a.table_width)) return KDA_ERR_SHAPE;
+    const int64_t strides[] = {a.q_stride, a.q_head_stride, a.k_page_stride, a.k_token_stride,
+                               a.k_head_stride, a.v_page_stride, a.v_token_stride, a.v_head_stride};
+    for (const int64_t s : strides)
+        if (s < 0) return KDA_ERR_SHAPE;
+    for (int i = 0; i < 8; ++i)
+        if (strides[i] % (i < 2 ? 8 : unit)) return KDA_ERR_UNSUPPORTED;
+    if (!a.q || !a.k_cache || !a.v_cache || !a.block_table || !a.seq_lens || !a.out) return KDA_ERR_NULL;
+    if (!by16(a.q) || !by16(a.k_cache) || !by16(a.v_cache)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// whether an output of a token attention lies over an input or the other output
+bool attn_over(const kda_attn_args &a, const Span *caches, int count) {
+    const int64_t es = 2, B = a.num_seqs;
+    const Span in[] = {span(a.q, ((B - 1) * a.q_stride + (a.q_heads - 1) * a.q_head_stride + a.head_dim) * es),
+                       span(a.block_table, ((B - 1) * a.table_stride + a.table_width) * 4), span(a.seq_lens, B * 4)};
+    const Span out = span(a.out, B * a.q_heads * a.head_dim * es), lse = span(a.lse, B * a.q_heads * 4);
+    if (meet(out, lse)) return true;
+    for (const Span &i : in)
+        if (meet(i, out) || meet(i, lse)) return true;
+    for (int i = 0; i < count; ++i)
+        if (meet(caches[i], out) || meet(caches[i], lse)) return true;
+    return false;
+}
+
+size_t attn_need(const kda_attn_args &a) {
+    return kda::ops::attn_workspace(a.num_seqs, a.q_heads, a.kv_heads, a.head_dim, a.table_width, a.page_size);
+}
+
+// ---------------------------------------------------------------- paged cache
+struct Scales {     // of a cache, or its codes
+    const uint8_t *p;
+    int64_t page, token, head;
+};
+
+int check_cache_sizes(int64_t seqs, int64_t tokens, int64_t heads, int64_t dh, int64_t pages, int64_t page, int64_t width, int64_t table_stride) {
+    if (dh != 64 && dh != 128 && dh != 256) return KDA_ERR_UNSUPPORTED;
+    if (seqs < 1 || tokens < 0 || tokens > 1 << 27 || heads < 1 || heads > 65535 || pages < 1 || page < 1 || width < 1 ||
+        width > (1 << 30) / page || table_stride < 0 || (seqs > 1 && table_stride < width))
+        return KDA_ERR_SHAPE;
+    return KDA_OK;
+}
+
+// rows read and written 16 bytes at a time
+int check_rows(const Scales &c, int64_t unit) {
+    if (c.page < 0 || c.token < 0 || c.head < 0) return KDA_ERR_SHAPE;
+    if (c.page % unit || c.token % unit || c.head % unit || !by16(c.p)) return KDA_ERR_UNSUPPORTED;
+    return c.p ? KDA_OK : KDA_ERR_NULL;
+}
+
+// scales: rows of `sb` bytes, read at once
+int check_scales(const Scales &s, int64_t sb) {
+    if (s.page < 0 || s.token < 0 || s.head < 0) return KDA_ERR_SHAPE;
+    if (s.page % sb || s.token % sb || s.head % sb || (uintptr_t)s.p % sb) return KDA_ERR_UNSUPPORTED;
+    return s.p ? KDA_OK : KDA_ERR_NULL;
+}
+
+// whether no two rows of a cache that is written share a byte: each stride steps over what the smaller ones span
+bool apart(const Scales &c, int64_t pages, int64_t page_size, int64_t heads, int64_t row) {
+    struct Dim {
+        int64_t size, stride;
+    } d[] = {{pages, c.page}, {page_size, c.token}, {heads, c.head}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (d[j].stride > d[j + 1].stride) std::swap(d[j], d[j + 1]);
+    int64_t spanned = row;
+    for (const Dim &x : d) {
+        if (x.size == 1) continue;
+        if (x.stride < spanned) return false;
+        spanned += (x.size - 1) * x.stride;
+    }
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -296,35 +383,127 @@ size_t kda_attn_workspace_bytes(int32_t num_seqs, int32_t q_heads, int32_t kv_he
 int kda_attn_decode(const kda_attn_args *args, void *stream, void *workspace, size_t workspace_bytes) {
     if (!args) return KDA_ERR_NULL;
     const kda_attn_args &a = *args;
-    if (a.dtype != KDA_DTYPE_BF16 && a.dtype != KDA_DTYPE_F16) return KDA_ERR_UNSUPPORTED;
-    if (!std::isfinite(a.scale)) return KDA_ERR_UNSUPPORTED;
-    if (const int rc = check_attn_sizes(a.num_seqs, a.q_heads, a.kv_heads, a.head_dim, a.table_width, a.page_size)) return rc;
-    if (a.num_pages < 1 || a.table_stride < 0 || (a.num_seqs > 1 && a.table_stride < a.table_width)) return KDA_ERR_SHAPE;
-    const int64_t strides[] = {a.q_stride, a.q_head_stride, a.k_page_stride, a.k_token_stride,
-                               a.k_head_stride, a.v_page_stride, a.v_token_stride, a.v_head_stride};
-    for (const int64_t s : strides)
-        if (s < 0) return KDA_ERR_SHAPE;
-    for (const int64_t s : strides)
-        if (s % 8) return KDA_ERR_UNSUPPORTED;
-    if (!a.q || !a.k_cache || !a.v_cache || !a.block_table || !a.seq_lens || !a.out) return KDA_ERR_NULL;
-    if (!by16(a.q) || !by16(a.k_cache) || !by16(a.v_cache)) return KDA_ERR_UNSUPPORTED;
-    const int64_t es = 2, B = a.num_seqs;
+    if (const int rc = check_attn(a, 8)) return rc;
     auto cache = [&](const void *p, int64_t page, int64_t token, int64_t head) {
-        return span(p, ((a.num_pages - 1) * page + (a.page_size - 1) * token + (a.kv_heads - 1) * head + a.head_dim) * es);
+        return cache_span(p, a.num_pages, a.page_size, a.kv_heads, page, token, head, a.head_dim, 2);
     };
-    const Span in[] = {span(a.q, ((B - 1) * a.q_stride + (a.q_heads - 1) * a.q_head_stride + a.head_dim) * es),
-                       cache(a.k_cache, a.k_page_stride, a.k_token_stride, a.k_head_stride),
-                       cache(a.v_cache, a.v_page_stride, a.v_token_stride, a.v_head_stride),
-                       span(a.block_table, ((B - 1) * a.table_stride + a.table_width) * 4), span(a.seq_lens, B * 4)};
-    const Span out = span(a.out, B * a.q_heads * a.head_dim * es), lse = span(a.lse, B * a.q_heads * 4);
-    if (meet(out, lse)) return KDA_ERR_ALIAS;
-    for (const Span &i : in)
-        if (meet(i, out) || meet(i, lse)) return KDA_ERR_ALIAS;
+    const Span in[] = {cache(a.k_cache, a.k_page_stride, a.k_token_stride, a.k_head_stride),
+                       cache(a.v_cache, a.v_page_stride, a.v_token_stride, a.v_head_stride)};
+    if (attn_over(a, in, 2)) return KDA_ERR_ALIAS;
     hipStream_t st = (hipStream_t)stream;
-    Workspace ws(workspace, workspace_bytes,
-                 kda::ops::attn_workspace(B, a.q_heads, a.kv_heads, a.head_dim, a.table_width, a.page_size), st);
+    Workspace ws(workspace, workspace_bytes, attn_need(a), st);
     if (ws.status() != KDA_OK) return ws.status();
     return ws.finish(launched(kda::ops::launch_attn_decode(a, (float *)ws.ptr(), kda::device_error_word(), st)));
+}
+
+int kda_attn_decode_fp4(const kda_attn_fp4_args *args, void *stream, void *workspace, size_t workspace_bytes) {
+    if (!args) return KDA_ERR_NULL;
+    const kda_attn_fp4_args &f = *args;
+    const kda_attn_args &a = f.attn;
+    if (const int rc = check_attn(a, 16)) return rc;
+    const int64_t sb = a.head_dim / KDA_FP4_GROUP;
+    const Scales sc[] = {{f.k_scale, f.k_scale_page_stride, f.k_scale_token_stride, f.k_scale_head_stride},
+                         {f.v_scale, f.v_scale_page_stride, f.v_scale_token_stride, f.v_scale_head_stride}};
+    for (const Scales &s : sc)
+        if (const int rc = check_scales(s, sb)) return rc;
+    auto cache = [&](const void *p, int64_t page, int64_t token, int64_t head, int64_t row) {
+        return cache_span(p, a.num_pages, a.page_size, a.kv_heads, page, token, head, row, 1);
+    };
+    const Span in[] = {cache(a.k_cache, a.k_page_stride, a.k_token_stride, a.k_head_stride, a.head_dim / 2),
+                       cache(a.v_cache, a.v_page_stride, a.v_token_stride, a.v_head_stride, a.head_dim / 2),
+                       cache(sc[0].p, sc[0].page, sc[0].token, sc[0].head, sb), cache(sc[1].p, sc[1].page, sc[1].token, sc[1].head, sb)};
+    if (attn_over(a, in, 4)) return KDA_ERR_ALIAS;
+    hipStream_t st = (hipStream_t)stream;
+    Workspace ws(workspace, workspace_bytes, attn_need(a), st);
+    if (ws.status() != KDA_OK) return ws.status();
+    return ws.finish(launched(kda::ops::launch_attn_decode_fp4(f, (float *)ws.ptr(), kda::device_error_word(), st)));
+}
+
+int kda_kv_append(const kda_kv_args *args, void *stream) {
+    if (!args) return KDA_ERR_NULL;
+    const kda_kv_args &a = *args;
+    if (a.dtype != KDA_DTYPE_BF16 && a.dtype != KDA_DTYPE_F16) return KDA_ERR_UNSUPPORTED;
+    if (a.interleaved != 0 && a.interleaved != 1) return KDA_ERR_UNSUPPORTED;
+    if (const int rc = check_cache_sizes(a.num_seqs, a.total_tokens, a.kv_heads, a.head_dim, a.num_pages, a.page_size, a.table_width,
+                                         a.table_stride)) return rc;
+    if (a.rope && (a.rot_dim % 16 || a.rot_dim < 16 || a.rot_dim > a.head_dim)) return KDA_ERR_UNSUPPORTED;
+    if (a.q_heads < 0 || a.q_heads > 65535 || (a.q && a.q_heads < 1) || (!a.q && a.q_heads) || (a.rope && a.max_positions < 1) ||
+        (!a.cu_seqlens && a.total_tokens != a.num_seqs))
+        return KDA_ERR_SHAPE;
+    const bool four = a.k_scale || a.v_scale;
+    const int64_t sb = a.head_dim / KDA_FP4_GROUP, row = four ? a.head_dim / 2 : a.head_dim, unit = four ? 16 : 8;
+    const int64_t in_strides[] = {a.k_stride, a.k_head_stride, a.v_stride, a.v_head_stride, a.q ? a.q_stride : 0, a.q ? a.q_head_stride : 0};
+    for (const int64_t s : in_strides)
+        if (s < 0) return KDA_ERR_SHAPE;
+    for (const int64_t s : in_strides)
+        if (s % 8) return KDA_ERR_UNSUPPORTED;
+    const Scales caches[] = {{(const uint8_t *)a.k_cache, a.k_page_stride, a.k_token_stride, a.k_cache_head_stride},
+                             {(const uint8_t *)a.v_cache, a.v_page_stride, a.v_token_stride, a.v_cache_head_stride}};
+    const Scales sc[] = {{a.k_scale, a.k_scale_page_stride, a.k_scale_token_stride, a.k_scale_head_stride},
+                         {a.v_scale, a.v_scale_page_stride, a.v_scale_token_stride, a.v_scale_head_stride}};
+    for (const Scales &c : caches)
+        if (const int rc = check_rows(c, unit)) return rc;
+    if (four)
+        for (const Scales &s : sc)
+            if (const int rc = check_scales(s, sb)) return rc;
+    if (!a.block_table || !a.seq_lens || (a.total_tokens > 0 && (!a.k || !a.v || (a.q && !a.q_out)))) return KDA_ERR_NULL;
+    if (!by16(a.k) || !by16(a.v) || !by16(a.q) || !by16(a.q_out)) return KDA_ERR_UNSUPPORTED;
+    for (int i = 0; i < 2; ++i)
+        if (!apart(caches[i], a.num_pages, a.page_size, a.kv_heads, row) || (four && !apart(sc[i], a.num_pages, a.page_size, a.kv_heads, sb)))
+            return KDA_ERR_SHAPE;
+    const int64_t T = a.total_tokens, es = 2;
+    auto rows3 = [&](const void *p, int64_t stride, int64_t head, int64_t heads) {
+        return span(T > 0 ? p : nullptr, ((T - 1) * stride + (heads - 1) * head + a.head_dim) * es);
+    };
+    const Span in[] = {rows3(a.k, a.k_stride, a.k_head_stride, a.kv_heads), rows3(a.v, a.v_stride, a.v_head_stride, a.kv_heads),
+                       rows3(a.q, a.q_stride, a.q_head_stride, a.q_heads), span(a.rope, (int64_t)a.max_positions * a.rot_dim * 4),
+                       span(a.cu_seqlens, ((int64_t)a.num_seqs + 1) * 4),
+                       span(a.block_table, (((int64_t)a.num_seqs - 1) * a.table_stride + a.table_width) * 4), span(a.seq_lens, (int64_t)a.num_seqs * 4)};
+    // (caches that are slices of one tensor interleave: their spans may meet)
+    const Span out[] = {span(a.q_out, T * a.q_heads * a.head_dim * es),
+                        cache_span(caches[0].p, a.num_pages, a.page_size, a.kv_heads, caches[0].page, caches[0].token, caches[0].head, row, four ? 1 : 2),
+                        cache_span(caches[1].p, a.num_pages, a.page_size, a.kv_heads, caches[1].page, caches[1].token, caches[1].head, row, four ? 1 : 2),
+                        cache_span(sc[0].p, a.num_pages, a.page_size, a.kv_heads, sc[0].page, sc[0].token, sc[0].head, sb, 1),
+                        cache_span(sc[1].p, a.num_pages, a.page_size, a.kv_heads, sc[1].page, sc[1].token, sc[1].head, sb, 1)};
+    for (const Span &o : out)
+        for (const Span &i : in)
+            if (meet(i, o)) return KDA_ERR_ALIAS;
+    for (int i = 1; i < 5; ++i)
+        if (meet(out[0], out[i])) return KDA_ERR_ALIAS;
+    if (a.k_cache == a.v_cache || (four && a.k_scale == a.v_scale)) return KDA_ERR_ALIAS;
+    return launched(kda::ops::launch_kv_append(a, kda::device_error_word(), (hipStream_t)stream));
+}
+
+int kda_kv_read_fp4(const kda_kv_read_args *args, void *stream) {
+    if (!args) return KDA_ERR_NULL;
+    const kda_kv_read_args &a = *args;
+    if (a.dtype != KDA_DTYPE_BF16 && a.dtype != KDA_DTYPE_F16) return KDA_ERR_UNSUPPORTED;
+    if (const int rc = check_cache_sizes(a.num_seqs, a.total_tokens, a.kv_heads, a.head_dim, a.num_pages, a.page_size, a.table_width,
+                                         a.table_stride)) return rc;
+    const Scales caches[] = {{(const uint8_t *)a.k_cache, a.k_page_stride, a.k_token_stride, a.k_head_stride},
+                             {(const uint8_t *)a.v_cache, a.v_page_stride, a.v_token_stride, a.v_head_stride}};
+    const Scales sc[] = {{a.k_scale, a.k_scale_page_stride, a.k_scale_token_stride, a.k_scale_head_stride},
+                         {a.v_scale, a.v_scale_page_stride, a.v_scale_token_stride, a.v_scale_head_stride}};
+    const int64_t sb = a.head_dim / KDA_FP4_GROUP;
+    for (const Scales &c : caches)
+        if (const int rc = check_rows(c, 16)) return rc;
+    for (const Scales &s : sc)
+        if (const int rc = check_scales(s, sb)) return rc;
+    if (!a.block_table || !a.cu_seqlens || (a.total_tokens > 0 && (!a.k || !a.v))) return KDA_ERR_NULL;
+    if (!by16(a.k) || !by16(a.v)) return KDA_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)a.total_tokens * a.kv_heads * a.head_dim * 2;
+    const Span out[] = {span(a.k, rows), span(a.v, rows)};
+    const Span in[] = {span(a.block_table, (((int64_t)a.num_seqs - 1) * a.table_stride + a.table_width) * 4),
+                       span(a.cu_seqlens, ((int64_t)a.num_seqs + 1) * 4),
+                       cache_span(caches[0].p, a.num_pages, a.page_size, a.kv_heads, caches[0].page, caches[0].token, caches[0].head, a.head_dim / 2, 1),
+                       cache_span(caches[1].p, a.num_pages, a.page_size, a.kv_heads, caches[1].page, caches[1].token, caches[1].head, a.head_dim / 2, 1),
+                       cache_span(sc[0].p, a.num_pages, a.page_size, a.kv_heads, sc[0].page, sc[0].token, sc[0].head, sb, 1),
+                       cache_span(sc[1].p, a.num_pages, a.page_size, a.kv_heads, sc[1].page, sc[1].token, sc[1].head, sb, 1)};
+    if (meet(out[0], out[1])) return KDA_ERR_ALIAS;
+    for (const Span &o : out)
+        for (const Span &i : in)
+            if (meet(i, o)) return KDA_ERR_ALIAS;
+    return launched(kda::ops::launch_kv_read_fp4(a, kda::device_error_word(), (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,300 @@
+// ops_kv.hip -- new keys and values into a paged cache, with the position rotation on the way (kv_append), into a
+// cache of the activations' type or one of 4 bits, and the read-back of the latter (kv_read_fp4).
+//
+//   pair (x, y) at position p:  (x c - y s, y c + x s),  c, s = the row p of the table of cosines and sines
+//   4 bits: e = floor(log2 max|x|) - 2 over 32 elements, one more where max|x| > 1.75 2^{e + 2} (then the largest
+//   value lies over 3.5 and up to 7 steps of 2^e, and is off by at most the half step that values between 4 and 6 are);
+//   codes = x 2^-e rounded to e2m1, to even halfway, at most 6
+//
+// Bound by memory: each row is read and written once. A thread has 8 neighbouring elements of one head (16 bytes) and
+// goes from head to head of its token with the same 8 cosines and sines in registers; the elements that they are
+// paired with come through the cache, which the neighbouring lanes fill.
+#include <type_traits>
+
+#include "ops_common.hpp"
+#include "ops_launch.hpp"
+
+namespace kda {
+namespace ops {
+namespace kv {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int THREADS = 256;
+
+// Packed new rows: offsets clamped to [0, T]; rows before the first sequence or behind the last one belong to none.
+struct Batch {
+    const int32_t *cu;      // NULL: row n is sequence n
+    int N, T;
+    __device__ __forceinline__ int at(int i) const {
+        const int c = cu[i];
+        return c < 0 ? 0 : c > T ? T : c;
+    }
+    // the sequence of row t and the rows left from t on (t included); 0 left: none
+    __device__ __forceinline__ void find(int t, int &seq, int &left, int &past) const {
+        if (!cu) {
+            seq = t, left = 1, past = 0;
+            return;
+        }
+        int lo = 0, hi = N;      // at(lo) <= t < at(hi), where offsets are in order
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (at(mid) <= t) lo = mid;
+            else hi = mid;
+        }
+        seq = lo;
+        past = t - at(lo);
+        left = past < 0 ? 0 : at(lo + 1) - t;
+        if (left < 0) left = 0;
+    }
+};
+
+// Raises KDA_DEVERR_CU_SEQLENS unless 0 = c_0 <= ... <= c_N <= T (rows behind c_N are padding).
+__device__ __forceinline__ void check_batch(const Batch &b, int32_t *err) {
+    if (!b.cu || !err) return;
+    bool bad = false;
+    for (int i = threadIdx.x; i <= b.N; i += THREADS) {
+        const int c = b.cu[i];
+        bad |= i == 0 ? c != 0 : c < b.cu[i - 1];
+        bad |= c > b.T;
+    }
+    if (bad) atomicOr(err, KDA_DEVERR_CU_SEQLENS);
+}
+
+template <int DT> __device__ __forceinline__ void load8(const void *p, int64_t at, float (&x)[8]) {
+    using E = typename Elem<DT>::type;
+    typedef E E8 __attribute__((ext_vector_type(8)));
+    const E8 r = *reinterpret_cast<const E8 *>((const E *)p + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)r[i];
+}
+template <int DT> __device__ __forceinline__ void store8(void *p, int64_t at, const float (&x)[8]) {
+    using E = typename Elem<DT>::type;
+    typedef E E8 __attribute__((ext_vector_type(8)));
+    E8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (E)x[i];
+    *reinterpret_cast<E8 *>((E *)p + at) = r;
+}
+
+// How 8 elements of a head are rotated.
+struct Turn {
+    enum Kind { NONE, FIRST, SECOND, PAIRS } kind;      // FIRST, SECOND: of pairs (i, i + rot / 2)
+    int other;          // where the elements lie that they are paired with
+    float c[8], s[8];   // PAIRS: four of each
+};
+
+__device__ __forceinline__ Turn turn_of(const kda_kv_args &a, int pos, int e) {
+    Turn r;
+    const int d = 8 * e, half = a.rot_dim / 2;
+    r.other = d;
+    if (!a.rope || d >= a.rot_dim) {
+        r.kind = Turn::NONE;
+        return r;
+    }
+    const float *row = a.rope + (int64_t)pos * a.rot_dim;
+    if (a.interleaved) {
+        r.kind = Turn::PAIRS;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.c[i] = row[d / 2 + i], r.s[i] = row[half + d / 2 + i];
+        return r;
+    }
+    r.kind = d < half ? Turn::FIRST : Turn::SECOND;
+    const int at = d < half ? d : d - half;
+    r.other = d < half ? d + half : d - half;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.c[i] = row[at + i], r.s[i] = row[half + at + i];
+    return r;
+}
+
+// x c -+ y s. F double: rounded once from 64 bits (the products of a 16-bit and a 32-bit number are exact there), so that
+// which side of a border of the 4-bit codes a value falls on does not hang on the order of roundings.
+template <class F> __device__ __forceinline__ float turned(float x, float c, float y, float s) {
+    if constexpr (sizeof(F) == 8) return (float)__builtin_fma((F)x, (F)c, (F)y * (F)s);
+    else return __builtin_fmaf(x, c, y * s);
+}
+
+template <int DT, class F> __device__ __forceinline__ void rotated(const Turn &r, const void *p, int64_t row, int d, float (&x)[8]) {
+    load8<DT>(p, row + d, x);
+    if (r.kind == Turn::PAIRS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = turned<F>(u, r.c[i], -v, r.s[i]);
+            x[2 * i + 1] = turned<F>(v, r.c[i], u, r.s[i]);
+        }
+    } else if (r.kind != Turn::NONE) {
+        float y[8];
+        load8<DT>(p, row + r.other, y);
+        const float sign = r.kind == Turn::FIRST ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = turned<F>(x[i], r.c[i], sign * y[i], r.s[i]);
+    }
+}
+
+// What DPP hands on within four neighbouring lanes: the maximum over their 32 elements.
+__device__ __forceinline__ uint32_t group_max(uint32_t x) {
+    uint32_t y = __builtin_amdgcn_update_dpp(0, x, 0xb1, 0xf, 0xf, true);      // lanes 1 0 3 2
+    x = x > y ? x : y;
+    y = __builtin_amdgcn_update_dpp(0, x, 0x4e, 0xf, 0xf, true);               // lanes 2 3 0 1
+    return x > y ? x : y;
+}
+
+// 8 values of this lane (32 of the four lanes it belongs to) to codes; returns the biased exponent of the scale.
+// Infinities and NaN: 255, the scale that stands for NaN. MOST keeps 6 2^e in the type that reads it back.
+template <int DT> __device__ __forceinline__ uint32_t to_fp4(const float (&x)[8], uint32_t &code) {
+    constexpr uint32_t MOST = DT == KDA_DTYPE_BF16 ? 252 : 140;
+    uint32_t top = 0;      // magnitudes compare as their bits do; those of infinities and NaN lie above all others
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
+        top = top > b ? top : b;
+    }
+    top = group_max(top);
+    uint32_t e = (top + 0x1fffffu) >> 23;       // 0x600000 of the mantissa is 1.75
+    e = e < 3 ? 1 : e - 2;
+    e = e > MOST ? MOST : e;
+    e = top >= 0x7f800000u ? 255 : e;
+    const float s = __uint_as_float(e << 23);
+    code = 0;
+    code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, x[0], x[1], s, 0);
+    code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, x[2], x[3], s, 1);
+    code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, x[4], x[5], s, 2);
+    code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, x[6], x[7], s, 3);
+    return e;
+}
+
+// A block takes one new token; its threads 8 elements of a head each, head after head: queries, keys, values.
+template <int DT, int DH, bool FOUR>
+__global__ __launch_bounds__(THREADS) void kv_append_kernel(const kda_kv_args a, int32_t *err) {
+    constexpr int LANES = DH / 8, HEADS = THREADS / LANES;      // of a head; heads at a time
+    const Batch batch = {a.cu_seqlens, a.num_seqs, a.total_tokens};
+    if (blockIdx.x == 0) check_batch(batch, err);
+    const int t = blockIdx.x;
+    int seq, left, past;
+    batch.find(t, seq, left, past);
+    if (!left) return;
+    const int len = a.seq_lens[seq];
+    if (len == 0) return;       // an empty slot
+    const int64_t pos = (int64_t)len - left;
+    int page = -1;
+    const bool inside = len > 0 && pos >= 0 && pos < (int64_t)a.table_width * a.page_size && (!a.rope || pos < a.max_positions);
+    if (inside) page = a.block_table[(int64_t)seq * a.table_stride + pos / a.page_size];
+    if (page < 0 || page >= a.num_pages) {
+        if (err && threadIdx.x == 0) atomicOr(err, KDA_DEVERR_PAGES);
+        return;
+    }
+    const int at = (int)(pos % a.page_size);
+    const int e = threadIdx.x % LANES, d = 8 * e;
+    const Turn turn = turn_of(a, (int)pos, e);
+    const Turn none = {Turn::NONE, d, {}, {}};
+    const int slots = a.q_heads + 2 * a.kv_heads;
+    for (int h = threadIdx.x / LANES; h < slots; h += HEADS) {
+        float x[8];
+        if (h < a.q_heads) {
+            rotated<DT, float>(turn, a.q, (int64_t)t * a.q_stride + (int64_t)h * a.q_head_stride, d, x);
+            store8<DT>(a.q_out, ((int64_t)t * a.q_heads + h) * DH + d, x);
+            continue;
+        }
+        const bool key = h < a.q_heads + a.kv_heads;
+        const int c = h - a.q_heads - (key ? 0 : a.kv_heads);
+        if (key) rotated<DT, std::conditional_t<FOUR, double, float>>(turn, a.k, (int64_t)t * a.k_stride + (int64_t)c * a.k_head_stride, d, x);
+        else rotated<DT, float>(none, a.v, (int64_t)t * a.v_stride + (int64_t)c * a.v_head_stride, d, x);
+        void *cache = key ? a.k_cache : a.v_cache;
+        const int64_t row = key ? page * a.k_page_stride + at * a.k_token_stride + c * a.k_cache_head_stride
+                                : page * a.v_page_stride + at * a.v_token_stride + c * a.v_cache_head_stride;
+        if constexpr (!FOUR) store8<DT>(cache, row + d, x);
+        else {
+            uint32_t code;
+            const uint32_t s = to_fp4<DT>(x, code);
+            *reinterpret_cast<uint32_t *>((uint8_t *)cache + row + d / 2) = code;
+            uint8_t *scale = key ? a.k_scale + page * a.k_scale_page_stride + at * a.k_scale_token_stride + c * a.k_scale_head_stride
+                                 : a.v_scale + page * a.v_scale_page_stride + at * a.v_scale_token_stride + c * a.v_scale_head_stride;
+            if (e % 4 == 0) scale[e / 4] = (uint8_t)s;
+        }
+    }
+}
+
+// A block takes TOKENS rows of the packed result.
+constexpr int TOKENS = 4;
+template <int DT, int DH>
+__global__ __launch_bounds__(THREADS) void kv_read_fp4_kernel(const kda_kv_read_args a, int32_t *err) {
+    constexpr int LANES = DH / 8, HEADS = THREADS / LANES;
+    using E = typename Elem<DT>::type;
+    const Batch batch = {a.cu_seqlens, a.num_seqs, a.total_tokens};
+    if (blockIdx.x == 0) check_batch(batch, err);
+    const int e = threadIdx.x % LANES;
+    for (int t = blockIdx.x * TOKENS; t < a.total_tokens && t < (blockIdx.x + 1) * TOKENS; ++t) {
+        int seq, left, past;
+        batch.find(t, seq, left, past);
+        if (!left) continue;
+        int page = -1;
+        if (past < (int64_t)a.table_width * a.page_size) page = a.block_table[(int64_t)seq * a.table_stride + past / a.page_size];
+        const bool there = page >= 0 && page < a.num_pages;
+        if (!there && err && threadIdx.x == 0) atomicOr(err, KDA_DEVERR_PAGES);
+        const int at = past % a.page_size;
+        for (int h = threadIdx.x / LANES; h < 2 * a.kv_heads; h += HEADS) {
+            const bool key = h < a.kv_heads;
+            const int c = key ? h : h - a.kv_heads;
+            u32x4 r = {0, 0, 0, 0};
+            if (there) {
+                const uint8_t *cache = key ? (const uint8_t *)a.k_cache + page * a.k_page_stride + at * a.k_token_stride + c * a.k_head_stride
+                                           : (const uint8_t *)a.v_cache + page * a.v_page_stride + at * a.v_token_stride + c * a.v_head_stride;
+                const uint8_t *scale = key ? a.k_scale + page * a.k_scale_page_stride + at * a.k_scale_token_stride + c * a.k_scale_head_stride
+                                           : a.v_scale + page * a.v_scale_page_stride + at * a.v_scale_token_stride + c * a.v_scale_head_stride;
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(cache + 4 * e);
+                const float s = __uint_as_float((uint32_t)scale[e / 4] << 23);
+                if constexpr (DT == KDA_DTYPE_BF16)
+                    r = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+                else
+                    r = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3))};
+            }
+            E *to = (E *)(key ? a.k : a.v) + ((int64_t)t * a.kv_heads + c) * DH + 8 * e;
+            *reinterpret_cast<u32x4 *>(to) = r;
+        }
+    }
+}
+
+template <int DT, int DH> hipError_t append(const kda_kv_args &a, int32_t *err, hipStream_t st) {
+    const dim3 grid((unsigned)a.total_tokens);
+    if (a.k_scale) kv_append_kernel<DT, DH, true><<<grid, THREADS, 0, st>>>(a, err);
+    else kv_append_kernel<DT, DH, false><<<grid, THREADS, 0, st>>>(a, err);
+    return hipGetLastError();
+}
+template <int DT> hipError_t append_dt(const kda_kv_args &a, int32_t *err, hipStream_t st) {
+    if (a.head_dim == 64) return append<DT, 64>(a, err, st);
+    if (a.head_dim == 128) return append<DT, 128>(a, err, st);
+    return append<DT, 256>(a, err, st);
+}
+template <int DT, int DH> hipError_t read(const kda_kv_read_args &a, int32_t *err, hipStream_t st) {
+    kv_read_fp4_kernel<DT, DH><<<dim3((unsigned)ceil_div(a.total_tokens, TOKENS)), THREADS, 0, st>>>(a, err);
+    return hipGetLastError();
+}
+template <int DT> hipError_t read_dt(const kda_kv_read_args &a, int32_t *err, hipStream_t st) {
+    if (a.head_dim == 64) return read<DT, 64>(a, err, st);
+    if (a.head_dim == 128) return read<DT, 128>(a, err, st);
+    return read<DT, 256>(a, err, st);
+}
+
+}  // namespace
+}  // namespace kv
+
+hipError_t launch_kv_append(const kda_kv_args &a, int32_t *err, hipStream_t st) {
+    if (a.total_tokens == 0) return hipSuccess;
+    return a.dtype == KDA_DTYPE_BF16 ? kv::append_dt<KDA_DTYPE_BF16>(a, err, st) : kv::append_dt<KDA_DTYPE_F16>(a, err, st);
+}
+
+hipError_t launch_kv_read_fp4(const kda_kv_read_args &a, int32_t *err, hipStream_t st) {
+    if (a.total_tokens == 0) return hipSuccess;
+    return a.dtype == KDA_DTYPE_BF16 ? kv::read_dt<KDA_DTYPE_BF16>(a, err, st) : kv::read_dt<KDA_DTYPE_F16>(a, err, st);
+}
+
+}  // namespace ops
+}  // namespace kda

@@ -29,6 +29,12 @@ hipError_t launch_ssm_bwd(const kda_ssm_args &a, const kda_ssm_grads &g, float *
 // paged token attention (ops_attn.hip)
 size_t attn_workspace(int64_t B, int64_t hq, int64_t hkv, int64_t dh, int64_t width, int64_t page);
 hipError_t launch_attn_decode(const kda_attn_args &a, float *ws, int32_t *err, hipStream_t st);
+// the same over a cache of 4 bits (ops_attn_fp4.hip)
+hipError_t launch_attn_decode_fp4(const kda_attn_fp4_args &f, float *ws, int32_t *err, hipStream_t st);
+
+// writer of the paged cache, read-back of the 4-bit one (ops_kv.hip)
+hipError_t launch_kv_append(const kda_kv_args &a, int32_t *err, hipStream_t st);
+hipError_t launch_kv_read_fp4(const kda_kv_read_args &a, int32_t *err, hipStream_t st);
 
 }  // namespace ops
 }  // namespace kda

@@ -23,6 +23,7 @@ EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_noalloc", "kda_workspace_bytes", "k
            "kda_ssm_fwd", "kda_ssm_workspace_bytes", "kda_ssm_decode",
            "kda_ssm_bwd", "kda_ssm_bwd_workspace_bytes",
            "kda_attn_decode", "kda_attn_workspace_bytes",
+           "kda_attn_decode_fp4", "kda_kv_append", "kda_kv_read_fp4",
            "kda_device_errors", "kda_status_string", "kda_version")
 #: KDA_DEVERR_* bits of the device error word
 DEVERR = {1: "fused hand-off wait gave up (outputs invalid)", 2: "malformed cu_seqlens (sanitised)",
@@ -47,9 +48,10 @@ class KdaLaunchInfo(ctypes.Structure):
                 ("chunk_len", ctypes.c_int32)]
 
 
-ACT_DTYPES = {"f32": 0, "bf16": 1, "f16": 2}   # KDA_DTYPE_* of the activations of kda_conv_*, kda_ssm_*, kda_attn_*
+ACT_DTYPES = {"f32": 0, "bf16": 1, "f16": 2}   # KDA_DTYPE_* of the activations of kda_conv_*, kda_ssm_*, kda_attn_*, kda_kv_*
 CONV_MAX_WIDTH = 8   # KDA_CONV_MAX_WIDTH
 SSM_MAX_STATE = 256   # KDA_SSM_MAX_STATE
+FP4_GROUP = 32   # KDA_FP4_GROUP
 
 
 class KdaConvArgs(ctypes.Structure):
@@ -86,6 +88,34 @@ class KdaAttnArgs(ctypes.Structure):
                                                "table_stride")] +
                 [(n, ctypes.c_int32) for n in ("num_seqs", "q_heads", "kv_heads", "head_dim", "num_pages", "page_size",
                                                "table_width", "dtype")] + [("scale", ctypes.c_float)])
+
+
+_CACHE_STRIDES = [(f"{x}_scale_{n}_stride", ctypes.c_int64) for x in "kv" for n in ("page", "token", "head")]
+
+
+class KdaAttnFp4Args(ctypes.Structure):
+    _fields_ = [("attn", KdaAttnArgs), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)] + _CACHE_STRIDES
+
+
+class KdaKvArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "q", "q_out", "rope", "cu_seqlens", "block_table", "seq_lens",
+                                                "k_cache", "v_cache", "k_scale", "v_scale")] +
+                [(n, ctypes.c_int64) for n in ("k_stride", "k_head_stride", "v_stride", "v_head_stride", "q_stride",
+                                               "q_head_stride", "k_page_stride", "k_token_stride", "k_cache_head_stride",
+                                               "v_page_stride", "v_token_stride", "v_cache_head_stride")] + _CACHE_STRIDES +
+                [("table_stride", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "q_heads", "kv_heads", "head_dim", "rot_dim",
+                                               "max_positions", "num_pages", "page_size", "table_width", "dtype",
+                                               "interleaved")])
+
+
+class KdaKvReadArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "k_scale", "v_scale", "block_table", "cu_seqlens", "k",
+                                                "v")] +
+                [(f"{x}_{n}_stride", ctypes.c_int64) for x in "kv" for n in ("page", "token", "head")] + _CACHE_STRIDES +
+                [("table_stride", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "kv_heads", "head_dim", "num_pages", "page_size",
+                                               "table_width", "dtype")])
 
 
 class KdaError(RuntimeError):
@@ -156,6 +186,12 @@ def load_library(path=LIB_PATH):
     lib.kda_attn_decode.restype = ctypes.c_int
     lib.kda_attn_workspace_bytes.argtypes = [i32] * 6
     lib.kda_attn_workspace_bytes.restype = ctypes.c_size_t
+    lib.kda_attn_decode_fp4.argtypes = [ctypes.POINTER(KdaAttnFp4Args), vp, vp, ctypes.c_size_t]
+    lib.kda_attn_decode_fp4.restype = ctypes.c_int
+    lib.kda_kv_append.argtypes = [ctypes.POINTER(KdaKvArgs), vp]
+    lib.kda_kv_append.restype = ctypes.c_int
+    lib.kda_kv_read_fp4.argtypes = [ctypes.POINTER(KdaKvReadArgs), vp]
+    lib.kda_kv_read_fp4.restype = ctypes.c_int
     lib.kda_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]
     lib.kda_device_errors.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]

@@ -80,7 +80,7 @@ typedef enum kda_variant {
 /* Element types of kda_options.g_dtype / state_dtype (and of kda_decode_ex). */
 #define KDA_DTYPE_F32 0
 #define KDA_DTYPE_BF16 1
-#define KDA_DTYPE_F16 2   /* activations of the operators below only (kda_conv_*, kda_ssm_*, kda_attn_*) */
+#define KDA_DTYPE_F16 2   /* activations of the operators below only (kda_conv_*, kda_ssm_*, kda_attn_*, kda_kv_*) */
 
 typedef struct kda_options {
     int32_t variant;        /* kda_variant                                              */
@@ -488,6 +488,101 @@ typedef struct kda_attn_args {
 size_t kda_attn_workspace_bytes(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                 int32_t table_width, int32_t page_size);
 int kda_attn_decode(const kda_attn_args *args, void *stream, void *workspace, size_t workspace_bytes);
+
+/* ------------------------------------------------------------------------------------
+ * A cache of 4 bits an element. A row of head_dim elements is head_dim / 2 bytes of e2m1 codes, element 2 j in the
+ * low half of byte j (sign, two bits of exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives),
+ * and head_dim / 32 bytes of scales, one for every KDA_FP4_GROUP elements: s stands for 2^(s - 127), 255 for
+ * NaN. Codes are [num_pages, page_size, kv_heads, head_dim / 2], scales [num_pages, page_size, kv_heads, head_dim / 32],
+ * rows contiguous, any other strides (in bytes): those of codes multiples of 16 on a base aligned to 16, those of
+ * scales multiples of head_dim / 32 on a base aligned to that. Rows of one head that lie next to each other in a page
+ * ([num_pages, kv_heads, page_size, ..]) suit the memory best.
+ */
+#define KDA_FP4_GROUP 32
+
+typedef struct kda_attn_fp4_args {
+    kda_attn_args attn;       /* k_cache and v_cache are codes, their strides bytes           */
+    const uint8_t *k_scale, *v_scale;
+    int64_t k_scale_page_stride, k_scale_token_stride, k_scale_head_stride;
+    int64_t v_scale_page_stride, v_scale_token_stride, v_scale_head_stride;
+} kda_attn_fp4_args;
+
+/*
+ * kda_attn_decode_fp4 -- kda_attn_decode over a cache of 4 bits, in the arithmetic of a cache of q's type that holds the
+ * values that the codes stand for (each of them is exact in bf16 and, between 2^-24 and 65504, in fp16: larger ones are
+ * infinite there). Values that are not finite make their elements of the output infinite or NaN. Workspace, limits, errors and
+ * the rest as kda_attn_decode; the workspace is of kda_attn_workspace_bytes() bytes.
+ */
+int kda_attn_decode_fp4(const kda_attn_fp4_args *args, void *stream, void *workspace, size_t workspace_bytes);
+
+typedef struct kda_kv_args {
+    const void *k, *v;        /* [total_tokens, kv_heads, head_dim]: the new rows              */
+    const void *q;            /* [total_tokens, q_heads, head_dim] or NULL (q_heads 0)         */
+    void *q_out;              /* the same, contiguous: q rotated; required with q              */
+    const float *rope;        /* fp32 [max_positions, rot_dim], contiguous: of each position   */
+                              /* rot_dim / 2 cosines and as many sines; NULL: no rotation      */
+    const int32_t *cu_seqlens; /* int32 [num_seqs+1]: the new rows of each sequence; rows      */
+                              /* behind the last offset are padding. NULL: one row each        */
+                              /* (total_tokens = num_seqs)                                     */
+    const int32_t *block_table; /* as kda_attn_args                                            */
+    const int32_t *seq_lens;  /* int32 [num_seqs]: cached tokens, the new ones included        */
+    void *k_cache, *v_cache;  /* as kda_attn_args, or codes where scales are given             */
+    uint8_t *k_scale, *v_scale; /* both, or both NULL: the caches hold dtype                   */
+    int64_t k_stride, k_head_stride, v_stride, v_head_stride, q_stride, q_head_stride;
+    int64_t k_page_stride, k_token_stride, k_cache_head_stride; /* elements; bytes for codes    */
+    int64_t v_page_stride, v_token_stride, v_cache_head_stride;
+    int64_t k_scale_page_stride, k_scale_token_stride, k_scale_head_stride;
+    int64_t v_scale_page_stride, v_scale_token_stride, v_scale_head_stride;
+    int64_t table_stride;
+    int32_t num_seqs, total_tokens;
+    int32_t q_heads, kv_heads;
+    int32_t head_dim;         /* 64, 128 or 256                                                */
+    int32_t rot_dim;          /* with rope: a multiple of 16 up to head_dim; the rest of a     */
+                              /* head is left as it is. Without: not read                      */
+    int32_t max_positions;    /* rows of rope                                                  */
+    int32_t num_pages, page_size, table_width;
+    int32_t dtype;            /* KDA_DTYPE_BF16 or KDA_DTYPE_F16                               */
+    int32_t interleaved;      /* 0: element i turns with i + rot_dim / 2; 1: 2 i with 2 i + 1  */
+} kda_kv_args;
+
+/*
+ * kda_kv_append -- the new rows of each sequence go into its last places in the paged cache that kda_attn_decode or
+ * kda_attn_decode_fp4 reads: the j-th of the n new rows of a sequence with seq_lens = L cached tokens lies at position
+ * p = L - n + j. Keys (and q) are rotated on the way: with c and s the cosine and sine of rope's row p for the i-th pair,
+ * (x, y) becomes (x c - y s, y c + x s), in fp32, rounded once; keys that go into 4 bits are rotated in 64 bits and
+ * rounded to fp32 before that. 4 bits: the scale of 32 elements is 2^(floor(log2 max) - 2), twice that where max is over 1.75
+ * times its power of two, within 2^-126 and the power of two that keeps 6 times the scale in dtype; codes are
+ * rounded to nearest, halfway cases to the even code, at most 6; a group with an infinity or a NaN is stored as NaN. A sequence with
+ * seq_lens 0 is an empty slot: its rows are passed over. Rows that would lie before position 0 (n > L), past the
+ * sequence's row of the table, past the table of rotations or on a page outside the cache are left out
+ * (KDA_DEVERR_PAGES). Rows that are left out or padding leave q_out as it was. Two sequences whose table rows name one
+ * page must not append to the same place of it. Rows of q, k, v and of a cache of dtype are read and written 16 bytes at a
+ * time: bases aligned to 16 bytes, strides multiples of 8 elements, else KDA_ERR_UNSUPPORTED; rows of the caches must not
+ * overlap (KDA_ERR_SHAPE). Captured calls stay right when lengths, pages, offsets and table entries change. Limits:
+ * total_tokens <= 2^27, table_width * page_size <= 2^30, heads <= 65535.
+ */
+int kda_kv_append(const kda_kv_args *args, void *stream);
+
+typedef struct kda_kv_read_args {
+    const void *k_cache, *v_cache; /* codes and scales as in kda_kv_args                       */
+    const uint8_t *k_scale, *v_scale;
+    const int32_t *block_table;
+    const int32_t *cu_seqlens; /* int32 [num_seqs+1]: how many tokens of each sequence          */
+    void *k, *v;              /* [total_tokens, kv_heads, head_dim] of dtype, contiguous       */
+    int64_t k_page_stride, k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride; /* bytes */
+    int64_t k_scale_page_stride, k_scale_token_stride, k_scale_head_stride;
+    int64_t v_scale_page_stride, v_scale_token_stride, v_scale_head_stride;
+    int64_t table_stride;
+    int32_t num_seqs, total_tokens, kv_heads, head_dim, num_pages, page_size, table_width, dtype;
+} kda_kv_read_args;
+
+/*
+ * kda_kv_read_fp4 -- the first tokens of each sequence of a 4-bit cache as packed rows of dtype: sequence n's first
+ * c_{n+1} - c_n cached tokens are rows c_n.. of k and v (rows behind c_N are left as they were). Exact in bf16; fp16 as
+ * kda_attn_decode_fp4. Tokens past the table's row or on a page outside the cache are zeros (KDA_DEVERR_PAGES). Limits as
+ * kda_kv_append.
+ */
+int kda_kv_read_fp4(const kda_kv_read_args *args, void *stream);
 
 /*
  * kda_device_errors -- the device error word of the current device: the OR of the
