@@ -427,7 +427,7 @@ int kda_kv_append(const kda_kv_args *args, void *stream) {
     if (const int rc = check_cache_sizes(a.num_seqs, a.total_tokens, a.kv_heads, a.head_dim, a.num_pages, a.page_size, a.table_width,
                                          a.table_stride)) return rc;
     if (a.rope && (a.rot_dim % 16 || a.rot_dim < 16 || a.rot_dim > a.head_dim)) return KDA_ERR_UNSUPPORTED;
-    if (a.q_heads < 0 || a.q_heads > 65535 || (a.q && a.q_heads < 1) || (!a.q && a.q_heads) || (a.rope && a.max_positions < 1) ||
+    if (a.q_heads < 0 || a.q_heads > 65535 || (a.q && a.q_heads < 1) || (!a.q && a.q_heads && a.total_tokens > 0) || (a.rope && a.max_positions < 1) ||
         (!a.cu_seqlens && a.total_tokens != a.num_seqs))
         return KDA_ERR_SHAPE;
     const bool four = a.k_scale || a.v_scale;

@@ -172,6 +172,7 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(const kda_kv_args a,
     const Batch batch = {a.cu_seqlens, a.num_seqs, a.total_tokens};
     if (blockIdx.x == 0) check_batch(batch, err);
     const int t = blockIdx.x;
+    if (t >= a.total_tokens) return;
     int seq, left, past;
     batch.find(t, seq, left, past);
     if (!left) return;
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(THREADS) void kv_read_fp4_kernel(const kda_kv_read_
 }
 
 template <int DT, int DH> hipError_t append(const kda_kv_args &a, int32_t *err, hipStream_t st) {
-    const dim3 grid((unsigned)a.total_tokens);
+    const dim3 grid(a.total_tokens > 0 ? (unsigned)a.total_tokens : 1);      // without rows: the check of the offsets
     if (a.k_scale) kv_append_kernel<DT, DH, true><<<grid, THREADS, 0, st>>>(a, err);
     else kv_append_kernel<DT, DH, false><<<grid, THREADS, 0, st>>>(a, err);
     return hipGetLastError();
@@ -274,7 +275,8 @@ template <int DT> hipError_t append_dt(const kda_kv_args &a, int32_t *err, hipSt
     return append<DT, 256>(a, err, st);
 }
 template <int DT, int DH> hipError_t read(const kda_kv_read_args &a, int32_t *err, hipStream_t st) {
-    kv_read_fp4_kernel<DT, DH><<<dim3((unsigned)ceil_div(a.total_tokens, TOKENS)), THREADS, 0, st>>>(a, err);
+    const int64_t blocks = ceil_div(a.total_tokens, TOKENS);
+    kv_read_fp4_kernel<DT, DH><<<dim3(blocks > 0 ? (unsigned)blocks : 1), THREADS, 0, st>>>(a, err);
     return hipGetLastError();
 }
 template <int DT> hipError_t read_dt(const kda_kv_read_args &a, int32_t *err, hipStream_t st) {
@@ -287,12 +289,10 @@ template <int DT> hipError_t read_dt(const kda_kv_read_args &a, int32_t *err, hi
 }  // namespace kv
 
 hipError_t launch_kv_append(const kda_kv_args &a, int32_t *err, hipStream_t st) {
-    if (a.total_tokens == 0) return hipSuccess;
     return a.dtype == KDA_DTYPE_BF16 ? kv::append_dt<KDA_DTYPE_BF16>(a, err, st) : kv::append_dt<KDA_DTYPE_F16>(a, err, st);
 }
 
 hipError_t launch_kv_read_fp4(const kda_kv_read_args &a, int32_t *err, hipStream_t st) {
-    if (a.total_tokens == 0) return hipSuccess;
     return a.dtype == KDA_DTYPE_BF16 ? kv::read_dt<KDA_DTYPE_BF16>(a, err, st) : kv::read_dt<KDA_DTYPE_F16>(a, err, st);
 }
 

@@ -153,7 +153,21 @@ def test_padding_rows_and_no_rows():
     check_append(d, lens, new + [], False, "bf16", check=True)
     d = make([9, 4], [0, 0], 4, 2, 128, 128, 16, "bf16", True, 3)
     before = d["k_cache"].clone()
-    assert append(d).shape == (0, 4, 128) and torch.equal(before, d["k_cache"])
+    assert append(d, check=True).shape == (0, 4, 128) and torch.equal(before, d["k_cache"])
+
+
+def test_malformed_offsets_without_rows_raise():
+    import chunked_gated_delta_kda_amd as kda
+    from chunked_gated_delta_kda_amd import native
+
+    d = make([9, 4], [0, 0], 4, 2, 128, 128, 16, "bf16", True, 3)
+    d["cu_seqlens"] = torch.tensor([0, 5, 5], dtype=torch.int32, device="cuda")
+    with pytest.raises(native.KdaDeviceError) as err:
+        append(d, check=True)
+    assert err.value.bits == 2
+    with pytest.raises(native.KdaDeviceError) as err:
+        kda.kv_read_fp4(d["k_cache"], d["v_cache"], d["k_scale"], d["v_scale"], d["block_table"], d["cu_seqlens"], 0, check=True)
+    assert err.value.bits == 2
 
 
 def test_without_queries():
