@@ -1,6 +1,7 @@
 """MI355X-native Kimi Delta Attention (KDA) forward, and the operators a hybrid decoder runs
 beside it: the short causal convolution (``conv_fwd``, ``conv_bwd``, ``conv_decode``), the
-selective state space scan (``ssm_fwd``, ``ssm_bwd``, ``ssm_decode``) and the attention of one new token over a
+selective state space scan (``ssm_fwd``, ``ssm_bwd``, ``ssm_decode``), the linear attention with a decay for each head
+(``lin_fwd``, ``lin_bwd``, ``lin_decode``), and the attention of one new token over a
 paged key-value cache (``attn_decode``), over one of 4 bits (``attn_decode_fp4``), and the writer of both (``kv_append``).
 
 ``fwd`` marshals torch tensors into the C ABI of libkda.so (include/kda.h).
@@ -15,13 +16,14 @@ from . import native
 
 __all__ = ["fwd", "fwd_noalloc", "bwd", "decode", "workspace_bytes", "select_variant", "device_errors", "version", "native",
            "conv_fwd", "conv_bwd", "conv_decode", "ssm_fwd", "ssm_bwd", "ssm_decode",
-           "attn_decode", "attn_decode_fp4", "kv_append", "kv_cache_fp4", "kv_read_fp4"]
+           "attn_decode", "attn_decode_fp4", "kv_append", "kv_cache_fp4", "kv_read_fp4",
+           "lin_fwd", "lin_bwd", "lin_decode"]
 
 #: the operators beside the delta rule, by the module that is imported on first use (it needs torch)
 _OPERATORS = {"conv_fwd": "short_conv", "conv_bwd": "short_conv", "conv_decode": "short_conv",
               "ssm_fwd": "scan", "ssm_bwd": "scan", "ssm_decode": "scan", "attn_decode": "paged_attention",
               "attn_decode_fp4": "paged_attention", "kv_append": "paged_cache", "kv_cache_fp4": "paged_cache",
-              "kv_read_fp4": "paged_cache"}
+              "kv_read_fp4": "paged_cache", "lin_fwd": "linear", "lin_bwd": "linear", "lin_decode": "linear"}
 
 
 def __getattr__(name):

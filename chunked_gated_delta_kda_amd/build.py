@@ -21,7 +21,7 @@ ARCH = "gfx950"
 
 SOURCES = ["kda_api.cpp", "kda_split.hip", "kda_h32.hip", "kda_fused.hip", "kda_recurrent.hip", "kda_bwd.hip",
            "ops_api.cpp", "ops_conv.hip", "ops_ssm.hip", "ops_ssm_bwd.hip", "ops_attn.hip",
-           "ops_attn_fp4.hip", "ops_kv.hip"]
+           "ops_attn_fp4.hip", "ops_kv.hip", "ops_lin.hip", "ops_lin_bwd.hip", "ops_lin_bwd_f16.hip"]
 
 COMMON = ["--offload-arch=" + ARCH, "-O3", "-fPIC", "-std=c++17", "-Wall", "-Werror",
           "-Wno-unused-command-line-argument",

@@ -246,6 +246,52 @@ bool apart(const Scales &c, int64_t pages, int64_t page_size, int64_t heads, int
     return true;
 }
 
+// ---------------------------------------------------------------- linear attention
+bool lin_dim(int64_t d) { return d == 64 || d == 128; }
+
+bool lin_sizes_ok(int64_t S, int64_t T, int64_t H) {
+    return S >= 1 && T >= 0 && T <= 1 << 27 && H >= 1 && H <= 65535 && S * H <= 1 << 27;
+}
+
+int check_lin(const kda_lin_args &a, bool grads) {
+    if ((a.dtype != KDA_DTYPE_BF16 && a.dtype != KDA_DTYPE_F16) || !lin_dim(a.key_dim) || !lin_dim(a.value_dim) ||
+        (a.g_per_head != 0 && a.g_per_head != 1) || !std::isfinite(a.scale))
+        return KDA_ERR_UNSUPPORTED;
+    if (!lin_sizes_ok(a.num_seqs, a.total_tokens, a.heads)) return KDA_ERR_SHAPE;
+    const int64_t strides[] = {a.q_stride, a.q_head_stride, a.k_stride, a.k_head_stride, a.v_stride, a.v_head_stride};
+    for (const int64_t s : strides)
+        if (s < 0) return KDA_ERR_SHAPE;
+    for (const int64_t s : strides)
+        if (s % 8) return KDA_ERR_UNSUPPORTED;
+    if (a.total_tokens > 0 && (!a.q || !a.k || !a.v || !a.g || (!grads && !a.out))) return KDA_ERR_NULL;
+    if (!by16(a.q) || !by16(a.k) || !by16(a.v) || !by16(a.initial_state) || !by16(a.final_state) || !by16(a.out)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// its inputs, the initial state last
+struct LinSpans {
+    Span in[6];
+    int64_t state;      // bytes
+    static Span rows3(const void *p, int64_t T, int64_t stride, int64_t H, int64_t head, int64_t D) {
+        return span(T > 0 ? p : nullptr, ((T - 1) * stride + (H - 1) * head + D) * 2);
+    }
+    explicit LinSpans(const kda_lin_args &a) {
+        const int64_t T = a.total_tokens, H = a.heads;
+        state = (int64_t)a.num_seqs * H * a.key_dim * a.value_dim * 4;
+        in[0] = rows3(a.q, T, a.q_stride, H, a.q_head_stride, a.key_dim);
+        in[1] = rows3(a.k, T, a.k_stride, H, a.k_head_stride, a.key_dim);
+        in[2] = rows3(a.v, T, a.v_stride, H, a.v_head_stride, a.value_dim);
+        in[3] = span(a.g, (a.g_per_head ? H : T * H) * 4);
+        in[4] = span(a.cu_seqlens, ((int64_t)a.num_seqs + 1) * 4);
+        in[5] = span(a.initial_state, state);
+    }
+    bool over(Span out, int count = 6) const {
+        for (int i = 0; i < count; ++i)
+            if (meet(in[i], out)) return true;
+        return false;
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -504,6 +550,73 @@ int kda_kv_read_fp4(const kda_kv_read_args *args, void *stream) {
         for (const Span &i : in)
             if (meet(i, o)) return KDA_ERR_ALIAS;
     return launched(kda::ops::launch_kv_read_fp4(a, kda::device_error_word(), (hipStream_t)stream));
+}
+
+size_t kda_lin_workspace_bytes(int32_t total_tokens, int32_t heads, int32_t key_dim, int32_t value_dim) {
+    if (!lin_sizes_ok(1, total_tokens, heads) || !lin_dim(key_dim) || !lin_dim(value_dim)) return 0;
+    return kda::ops::lin_workspace(total_tokens, heads, key_dim, value_dim);
+}
+
+int kda_lin_fwd(const kda_lin_args *args, void *stream, void *workspace, size_t workspace_bytes) {
+    if (!args) return KDA_ERR_NULL;
+    const kda_lin_args &a = *args;
+    if (const int rc = check_lin(a, false)) return rc;
+    if (!a.cu_seqlens && a.num_seqs != 1) return KDA_ERR_SHAPE;
+    const LinSpans s(a);
+    const Span out = span(a.out, (int64_t)a.total_tokens * a.heads * a.value_dim * 2), fin = span(a.final_state, s.state);
+    if (s.over(out) || s.over(fin) || meet(out, fin)) return KDA_ERR_ALIAS;
+    hipStream_t st = (hipStream_t)stream;
+    Workspace ws(workspace, workspace_bytes, kda::ops::lin_workspace(a.total_tokens, a.heads, a.key_dim, a.value_dim), st);
+    if (ws.status() != KDA_OK) return ws.status();
+    return ws.finish(launched(kda::ops::launch_lin_fwd(a, (float *)ws.ptr(), kda::device_error_word(), st)));
+}
+
+int kda_lin_decode(const kda_lin_args *args, void *stream) {
+    if (!args) return KDA_ERR_NULL;
+    const kda_lin_args &a = *args;
+    if (const int rc = check_lin(a, false)) return rc;
+    if (a.cu_seqlens || a.total_tokens != a.num_seqs) return KDA_ERR_SHAPE;
+    const LinSpans s(a);
+    const Span out = span(a.out, (int64_t)a.total_tokens * a.heads * a.value_dim * 2), fin = span(a.final_state, s.state);
+    const bool in_place = a.initial_state == a.final_state;
+    if (s.over(out) || s.over(fin, in_place ? 5 : 6) || meet(out, fin)) return KDA_ERR_ALIAS;
+    return launched(kda::ops::launch_lin_decode(a, (hipStream_t)stream));
+}
+
+size_t kda_lin_bwd_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t heads, int32_t key_dim, int32_t value_dim,
+                                   int32_t g_per_head, int32_t need_d_initial_state) {
+    if (!lin_sizes_ok(num_seqs, total_tokens, heads) || !lin_dim(key_dim) || !lin_dim(value_dim)) return 0;
+    return kda::ops::lin_bwd_workspace(total_tokens, heads, num_seqs, key_dim, value_dim, g_per_head != 0, need_d_initial_state == 0);
+}
+
+int kda_lin_bwd(const kda_lin_args *args, const kda_lin_grads *grads, void *stream, void *workspace, size_t workspace_bytes) {
+    if (!args || !grads) return KDA_ERR_NULL;
+    kda_lin_args a = *args;
+    a.out = nullptr, a.final_state = nullptr;
+    const kda_lin_grads &g = *grads;
+    if (const int rc = check_lin(a, true)) return rc;
+    if (!a.cu_seqlens && a.num_seqs != 1) return KDA_ERR_SHAPE;
+    if (g.d_out_stride < 0 || g.d_out_head_stride < 0) return KDA_ERR_SHAPE;
+    if (g.d_out_stride % 8 || g.d_out_head_stride % 8 || !by16(g.d_out) || !by16(g.d_final_state) || !by16(g.dq) || !by16(g.dk) ||
+        !by16(g.dv) || !by16(g.d_initial_state))
+        return KDA_ERR_UNSUPPORTED;
+    const int64_t T = a.total_tokens, H = a.heads;
+    if ((a.g_per_head && !g.dg) || (T > 0 && (!g.d_out || !g.dq || !g.dk || !g.dv || !g.dg))) return KDA_ERR_NULL;
+    const LinSpans s(a);
+    const Span dout = LinSpans::rows3(g.d_out, T, g.d_out_stride, H, g.d_out_head_stride, a.value_dim), dfin = span(g.d_final_state, s.state);
+    const Span out[] = {span(g.dq, T * H * a.key_dim * 2), span(g.dk, T * H * a.key_dim * 2), span(g.dv, T * H * a.value_dim * 2),
+                        span(g.dg, (a.g_per_head ? H : T * H) * 4), span(g.d_initial_state, s.state)};
+    constexpr int outs = sizeof(out) / sizeof(out[0]);
+    for (int i = 0; i < outs; ++i) {
+        if (s.over(out[i]) || meet(dout, out[i]) || meet(dfin, out[i])) return KDA_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return KDA_ERR_ALIAS;
+    }
+    hipStream_t st = (hipStream_t)stream;
+    Workspace ws(workspace, workspace_bytes,
+                 kda::ops::lin_bwd_workspace(T, H, a.num_seqs, a.key_dim, a.value_dim, a.g_per_head != 0, a.initial_state && !g.d_initial_state), st);
+    if (ws.status() != KDA_OK) return ws.status();
+    return ws.finish(launched(kda::ops::launch_lin_bwd(a, g, (float *)ws.ptr(), kda::device_error_word(), st)));
 }
 
 }  // extern "C"

@@ -36,5 +36,14 @@ hipError_t launch_attn_decode_fp4(const kda_attn_fp4_args &f, float *ws, int32_t
 hipError_t launch_kv_append(const kda_kv_args &a, int32_t *err, hipStream_t st);
 hipError_t launch_kv_read_fp4(const kda_kv_read_args &a, int32_t *err, hipStream_t st);
 
+// linear attention with a decay for each head (ops_lin.hip)
+size_t lin_workspace(int64_t T, int64_t H, int64_t KD, int64_t VD);
+hipError_t launch_lin_fwd(const kda_lin_args &a, float *ws, int32_t *err, hipStream_t st);
+hipError_t launch_lin_decode(const kda_lin_args &a, hipStream_t st);
+// its gradients (ops_lin_bwd.hip, ops_lin_bwd_f16.hip)
+size_t lin_bwd_workspace(int64_t T, int64_t H, int64_t S, int64_t KD, int64_t VD, bool per_head, bool own_d_init);
+hipError_t launch_lin_bwd(const kda_lin_args &a, const kda_lin_grads &g, float *ws, int32_t *err, hipStream_t st);
+hipError_t launch_lin_bwd_f16(const kda_lin_args &a, const kda_lin_grads &g, float *ws, int32_t *err, hipStream_t st);
+
 }  // namespace ops
 }  // namespace kda

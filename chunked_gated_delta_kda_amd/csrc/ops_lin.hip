@@ -1,0 +1,135 @@
+// ops_lin.hip -- linear attention with a decay for each head: prompts (a pass for what segments of the time axis add to
+// their states, a join, the walk over the chunks; ops_lin.hpp) and single tokens.
+#include "ops_lin.hpp"
+
+namespace kda {
+namespace ops {
+namespace lin {
+namespace {
+
+template <int DT, int KD, int VD>
+__global__ __launch_bounds__(THREADS, 2) void lin_state_kernel(const Batch b, const Own a) {
+    __shared__ Tile<PLANES<DT>, KD> k;
+    __shared__ Tile<PLANES<DT>, VD> v;
+    __shared__ Clock clock;
+    own_state<DT, KD, VD, false>(b, a, k, v, clock);
+}
+
+template <int SIZE> __global__ __launch_bounds__(THREADS) void lin_join_kernel(const Batch b, float *state, const float *factor) {
+    join<SIZE>(b, state, factor, false);
+}
+
+template <int DT, int KD, int VD>
+__global__ __launch_bounds__(THREADS, PLANES<DT> == 1 ? 2 : 1) void lin_walk_kernel(const Batch b, const Walk a, int32_t *err) {
+    __shared__ WalkLds<DT, KD, VD, 2> lds;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS);
+    walk<DT, KD, VD, false, false>(b, a, lds);
+}
+
+// One token of each sequence: S <- e^g S + k v^T, out = scale S^T q. The state is read and written once; a block takes one
+// head of one sequence, a thread 4 value columns of every GROUPS-th row.
+template <int DT, int KD, int VD>
+__global__ __launch_bounds__(THREADS) void lin_decode_kernel(const kda_lin_args a) {
+    using E = typename Elem<DT>::type;
+    constexpr int COLS = VD / 4, GROUPS = THREADS / COLS, ROWS = KD / GROUPS;
+    __shared__ float q[KD], k[KD];
+    __shared__ f32x4 part[GROUPS][COLS];
+    const int n = blockIdx.x, h = blockIdx.y, x = threadIdx.x % COLS, grp = threadIdx.x / COLS;
+    const int64_t at = ((int64_t)n * a.heads + h) * (KD * VD);
+    f32x4 S[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        S[r] = f32x4{0, 0, 0, 0};
+        if (a.initial_state) S[r] = *reinterpret_cast<const f32x4 *>(a.initial_state + at + (r * GROUPS + grp) * VD + 4 * x);
+    }
+    if (threadIdx.x < KD) q[threadIdx.x] = (float)((const E *)a.q)[n * a.q_stride + h * a.q_head_stride + threadIdx.x] * a.scale;
+    else if (threadIdx.x < 2 * KD) k[threadIdx.x - KD] = (float)((const E *)a.k)[n * a.k_stride + h * a.k_head_stride + threadIdx.x - KD];
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    const E4 ve = *reinterpret_cast<const E4 *>((const E *)a.v + n * a.v_stride + h * a.v_head_stride + 4 * x);
+    f32x4 v, o = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)ve[e];
+    const float decay = exp2_f((float)log2_decay(a.g[a.g_per_head ? h : (int64_t)n * a.heads + h]));
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int row = r * GROUPS + grp;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            S[r][e] = __builtin_fmaf(decay, S[r][e], k[row] * v[e]);
+            o[e] = __builtin_fmaf(q[row], S[r][e], o[e]);
+        }
+        if (a.final_state) *reinterpret_cast<f32x4 *>(a.final_state + at + row * VD + 4 * x) = S[r];
+    }
+    part[grp][x] = o;
+    __syncthreads();
+    if (threadIdx.x < COLS) {
+#pragma unroll
+        for (int p = 1; p < GROUPS; ++p) o += part[p][x];
+        E4 e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = (E)o[i];
+        *reinterpret_cast<E4 *>((E *)a.out + ((int64_t)n * a.heads + h) * VD + 4 * x) = e;
+    }
+}
+
+struct Plan {
+    int seg, segs;
+};
+Plan plan(int64_t T, int64_t H) {
+    Plan p;
+    p.seg = segment(T, H, 512, C);
+    p.segs = (int)ceil_div(T > 0 ? T : 1, p.seg);
+    return p;
+}
+
+template <int DT, int KD, int VD> hipError_t forward(const kda_lin_args &a, float *ws, int32_t *err, hipStream_t st) {
+    const Plan p = plan(a.total_tokens, a.heads);
+    const Batch b = {a.cu_seqlens, a.g, a.g_per_head ? 0 : a.heads, a.num_seqs, a.total_tokens, a.heads, p.seg, p.segs};
+    const Role q = {a.q, a.q_stride, a.q_head_stride}, k = {a.k, a.k_stride, a.k_head_stride}, v = {a.v, a.v_stride, a.v_head_stride};
+    const dim3 grid((unsigned)p.segs, (unsigned)a.heads);
+    if (p.segs > 1) {
+        float *factor = ws + (size_t)p.segs * a.heads * (KD * VD);
+        const Own own = {k, v, a.initial_state, ws, factor, 1.0f};
+        lin_state_kernel<DT, KD, VD><<<grid, THREADS, 0, st>>>(b, own);
+        if (hipError_t e = hipGetLastError()) return e;
+        lin_join_kernel<KD * VD><<<dim3(KD * VD / THREADS, (unsigned)a.heads), THREADS, 0, st>>>(b, ws, factor);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    const Walk w = {q, k, v, a.out, ws, a.initial_state, a.final_state, VD, 1, a.scale, a.scale, 1.0f, {nullptr, 0, 0}, nullptr};
+    lin_walk_kernel<DT, KD, VD><<<grid, THREADS, 0, st>>>(b, w, err);
+    return hipGetLastError();
+}
+
+template <int DT, int KD, int VD> hipError_t decode(const kda_lin_args &a, hipStream_t st) {
+    lin_decode_kernel<DT, KD, VD><<<dim3((unsigned)a.num_seqs, (unsigned)a.heads), THREADS, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <int DT> hipError_t forward_dt(const kda_lin_args &a, float *ws, int32_t *err, hipStream_t st) {
+    if (a.key_dim == 64) return a.value_dim == 64 ? forward<DT, 64, 64>(a, ws, err, st) : forward<DT, 64, 128>(a, ws, err, st);
+    return a.value_dim == 64 ? forward<DT, 128, 64>(a, ws, err, st) : forward<DT, 128, 128>(a, ws, err, st);
+}
+template <int DT> hipError_t decode_dt(const kda_lin_args &a, hipStream_t st) {
+    if (a.key_dim == 64) return a.value_dim == 64 ? decode<DT, 64, 64>(a, st) : decode<DT, 64, 128>(a, st);
+    return a.value_dim == 64 ? decode<DT, 128, 64>(a, st) : decode<DT, 128, 128>(a, st);
+}
+
+}  // namespace
+}  // namespace lin
+
+size_t lin_workspace(int64_t T, int64_t H, int64_t KD, int64_t VD) {
+    const lin::Plan p = lin::plan(T, H);
+    return p.segs > 1 ? (size_t)p.segs * H * (KD * VD + 1) * sizeof(float) : 0;
+}
+
+hipError_t launch_lin_fwd(const kda_lin_args &a, float *ws, int32_t *err, hipStream_t st) {
+    return a.dtype == KDA_DTYPE_BF16 ? lin::forward_dt<KDA_DTYPE_BF16>(a, ws, err, st) : lin::forward_dt<KDA_DTYPE_F16>(a, ws, err, st);
+}
+
+hipError_t launch_lin_decode(const kda_lin_args &a, hipStream_t st) {
+    return a.dtype == KDA_DTYPE_BF16 ? lin::decode_dt<KDA_DTYPE_BF16>(a, st) : lin::decode_dt<KDA_DTYPE_F16>(a, st);
+}
+
+}  // namespace ops
+}  // namespace kda

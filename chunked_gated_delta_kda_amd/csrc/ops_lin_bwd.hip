@@ -1,0 +1,305 @@
+// ops_lin_bwd.hip -- gradients of the linear attention with a decay for each head (ops_lin.hpp).
+//
+// With X the state that enters a chunk and Y the gradient of the one that leaves it, three walks give dq (forwards on X),
+// dv and dk (backwards on Y), and on the way u_i = q_i . (part of dq_i from X), w_j = k_j . (part of dk_j from Y).
+// A decay's gradient is what passes it, from tokens before t to tokens from t on:
+//
+//   dg_t = sum_{j < t <= i} W_ij + F - sum_{i < t} u_i + sum_{j < t} w_j,   W_ij = scale e^{G_i - G_j} (q_i . k_j) (do_i . v_j)
+//
+// in the chunk, F = <X, Y before the chunk> what passes the chunk's first border; the next chunk's F is this one's less its u plus its w.
+// So nothing is subtracted over more than a segment, and pairs of a token with itself (large where decays are
+// short) never enter.
+#include "ops_lin.hpp"
+
+namespace kda {
+namespace ops {
+namespace lin {
+namespace {
+
+// What both directions add to their states, by blockIdx.z.
+template <int DT, int KD, int VD>
+__global__ __launch_bounds__(THREADS, 2) void lin_bwd_state_kernel(const Batch b, const Own x, const Own y) {
+    __shared__ Tile<PLANES<DT>, KD> k;
+    __shared__ Tile<PLANES<DT>, VD> v;
+    __shared__ Clock clock;
+    if (blockIdx.z == 0) own_state<DT, KD, VD, false>(b, x, k, v, clock);
+    else own_state<DT, KD, VD, true>(b, y, k, v, clock);
+}
+
+template <int SIZE>
+__global__ __launch_bounds__(THREADS) void lin_bwd_join_kernel(const Batch b, float *x, const float *xf, float *y, const float *yf) {
+    if (blockIdx.z == 0) join<SIZE>(b, x, xf, false);
+    else join<SIZE>(b, y, yf, true);
+}
+
+template <int DT, int KD, int VD>
+__global__ __launch_bounds__(THREADS, PLANES<DT> == 1 ? 2 : 1) void lin_dq_kernel(const Batch b, const Walk a, int32_t *err) {
+    __shared__ WalkLds<DT, KD, VD, 2> lds;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS);
+    walk<DT, KD, VD, false, true>(b, a, lds);
+}
+template <int DT, int KD, int VD>
+__global__ __launch_bounds__(THREADS, PLANES<DT> == 1 ? 2 : 1) void lin_dv_kernel(const Batch b, const Walk a) {
+    __shared__ WalkLds<DT, KD, VD, 2> lds;
+    walk<DT, KD, VD, true, false>(b, a, lds);
+}
+template <int DT, int KD, int VD>
+__global__ __launch_bounds__(THREADS, PLANES<DT> == 1 ? 2 : 1) void lin_dk_kernel(const Batch b, const Walk a) {
+    __shared__ WalkLds<DT, KD, VD, 2> lds;
+    walk<DT, KD, VD, true, true>(b, a, lds);
+}
+
+// ---------------------------------------------------------------- gradients of the decays
+struct Decays {
+    Role q, k, v, d_out;
+    const float *x, *y;         // joined states and gradients
+    const float *init, *d_init; // of sequences, or both NULL
+    const float *u, *w;         // [T, H]
+    float *dg;                  // [T, H], or partial sums [segs, H]
+    float scale;
+    int per_head;
+};
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+// sum over the 16 lanes of a row
+__device__ __forceinline__ float row_sum(float x) {
+    x += dpp_f<0xb1>(x);        // lanes 1 0 3 2
+    x += dpp_f<0x4e>(x);        // lanes 2 3 0 1
+    x += dpp_f<0x141>(x);       // the other four of eight, mirrored
+    x += dpp_f<0x140>(x);       // the other eight, mirrored
+    return x;
+}
+
+// operand: 8 elements of a row, as bf16 parts
+template <int DT> __device__ __forceinline__ void global_operand(const Role &s, int h, int t, bool there, int at, u32x4 (&to)[PLANES<DT>]) {
+    u32x4 r = {0, 0, 0, 0};
+    if (there) r = *reinterpret_cast<const u32x4 *>((const uint16_t *)s.p + (int64_t)t * s.row + (int64_t)h * s.head + at);
+    if constexpr (DT == KDA_DTYPE_BF16) to[0] = r;
+    else {
+        typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+        const f16x8 e = __builtin_bit_cast(f16x8, r);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
+        split<2>(v, to);
+    }
+}
+
+// A block takes a segment of one head, a wave every fourth chunk of it.
+template <int DT, int KD, int VD>
+__global__ __launch_bounds__(THREADS) void lin_decay_kernel(const Batch b, const Decays a) {
+    constexpr int NP = PLANES<DT>, SIZE = KD * VD;
+    __shared__ Clock clocks[4];
+    __shared__ float rows[4][C], cols[4][C], part[4];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int seg = blockIdx.x, h = blockIdx.y;
+    const Offsets o = b.offsets();
+    const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
+    Chunks<false> chunks(o, s0, s1);
+    Clock &clock = clocks[wave];
+    float all = 0.0f, F = 0.0f;
+    int n = 0, part0 = 0;
+#pragma unroll 1
+    for (Chunk c = chunks.next(); c.len; c = chunks.next(), ++n) {
+        if (c.enter) {      // what passes the part's first border: the block together
+            const float *x = nullptr, *y = nullptr;
+            part0 = c.first;
+            if (!c.open) x = a.x + ((int64_t)(seg - 1) * b.H + h) * SIZE, y = a.y + ((int64_t)seg * b.H + h) * SIZE;
+            else if (a.init) x = a.init + ((int64_t)c.seq * b.H + h) * SIZE, y = a.d_init + ((int64_t)c.seq * b.H + h) * SIZE;
+            float sum = 0.0f;
+            if (x) {
+                for (int e = 4 * threadIdx.x; e < SIZE; e += 4 * THREADS) {
+                    const f32x4 p = *reinterpret_cast<const f32x4 *>(x + e), q = *reinterpret_cast<const f32x4 *>(y + e);
+                    sum += (p[0] * q[0] + p[1] * q[1]) + (p[2] * q[2] + p[3] * q[3]);
+                }
+            }
+            sum = wave_sum(sum);
+            __syncthreads();
+            if (lane == 0) part[wave] = sum;
+            __syncthreads();
+            F = (part[0] + part[1]) + (part[2] + part[3]);
+        }
+        if ((n & 3) != wave) continue;
+        const bool there = lane < c.len;
+        const int64_t at = (int64_t)(c.first + lane) * b.H + h;
+        tick<false>(clock, there ? log2_decay(b.decay(c.first + lane, h)) : 0.0, 1.0f, 1.0f);
+        // u and w of the part's chunks before this one
+        float over = 0.0f;
+        for (int t = part0 + lane; t < c.first; t += 64) over += a.w[(int64_t)t * b.H + h] - a.u[(int64_t)t * b.H + h];
+        over = wave_sum(over) + F;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        // W: rows tokens j, columns tokens i > j
+        float colsum[4][4];     // over i, of token 16 jt + 4 g + r
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) colsum[jt][r] = 0.0f;
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it) {
+            float rowsum = 0.0f;
+            const int ti = 16 * it + i;
+            const float wi = clock.whole[ti], ri = clock.rest[ti];
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) {
+                if (jt > it) continue;
+                const int tj = 16 * jt + i;
+                f32x4 qk = {0, 0, 0, 0}, dv = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < KD / 32; ++s) {
+                    u32x4 x[NP], y[NP];
+                    global_operand<DT>(a.k, h, c.first + tj, tj < c.len, 32 * s + 8 * g, x);
+                    global_operand<DT>(a.q, h, c.first + ti, ti < c.len, 32 * s + 8 * g, y);
+                    pairs<NP, NP, 4>([&](int m, int k) { qk = mma(x[m], y[k], qk); });
+                }
+#pragma unroll
+                for (int s = 0; s < VD / 32; ++s) {
+                    u32x4 x[NP], y[NP];
+                    global_operand<DT>(a.v, h, c.first + tj, tj < c.len, 32 * s + 8 * g, x);
+                    global_operand<DT>(a.d_out, h, c.first + ti, ti < c.len, 32 * s + 8 * g, y);
+                    pairs<NP, NP, 4>([&](int m, int k) { dv = mma(x[m], y[k], dv); });
+                }
+                const f32x4 wj = *reinterpret_cast<const f32x4 *>(&clock.whole[16 * jt + 4 * g]);
+                const f32x4 rj = *reinterpret_cast<const f32x4 *>(&clock.rest[16 * jt + 4 * g]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float x = qk[r] * dv[r] * exp2_f((wi - wj[r]) + (ri - rj[r])) * a.scale;
+                    const float e = 16 * jt + 4 * g + r < ti ? x : 0.0f;
+                    rowsum += e;
+                    colsum[jt][r] += e;
+                }
+            }
+            rowsum = swap16_add(rowsum, rowsum);
+            rowsum = swap32_add(rowsum, rowsum);
+            if (g == 0) rows[wave][ti] = rowsum;
+        }
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float x = row_sum(colsum[jt][r]);
+                if (i == 0) cols[wave][16 * jt + 4 * g + r] = x;
+            }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        // lane t: sums from t on of the rows less the columns, sums before t of w - u
+        const float mine = rows[wave][lane] - cols[wave][lane];
+        const float flow = there ? a.w[at] - a.u[at] : 0.0f;
+        float from = mine, upto = flow;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const float x = __shfl_down(from, d), y = __shfl_up(upto, d);
+            if (lane + d < 64) from += x;
+            if (lane >= d) upto += y;
+        }
+        const float before = __shfl_up(upto, 1);
+        const float dg = from + (lane ? before : 0.0f) + over;
+        if (!a.per_head) {
+            if (there) a.dg[at] = dg;
+        } else all += there ? dg : 0.0f;
+    }
+    if (a.per_head) {
+        all = wave_sum(all);
+        __syncthreads();
+        if (lane == 0) part[wave] = all;
+        __syncthreads();
+        if (threadIdx.x == 0) a.dg[(int64_t)seg * b.H + h] = (part[0] + part[1]) + (part[2] + part[3]);
+    }
+}
+
+// dg [H] from the segments' sums, in their order: a wave a head.
+__global__ __launch_bounds__(64) void lin_decay_sum_kernel(const float *part, float *dg, int segs, int H) {
+    const int h = blockIdx.x;
+    float x = 0.0f;
+    for (int s = threadIdx.x; s < segs; s += 64) x += part[(int64_t)s * H + h];
+    x = wave_sum(x);
+    if (threadIdx.x == 0) dg[h] = x;
+}
+
+// ---------------------------------------------------------------- host
+struct Plan {
+    int seg, segs;
+    size_t state, factor, token, d_init, sums;     // elements of the parts of the workspace
+};
+Plan plan(int64_t T, int64_t H, int64_t S, int64_t size, bool per_head, bool own_d_init) {
+    Plan p;
+    p.seg = segment(T, H, 512, C);
+    p.segs = (int)ceil_div(T > 0 ? T : 1, p.seg);
+    p.state = p.segs > 1 ? (size_t)p.segs * H * size : 0;
+    p.factor = p.segs > 1 ? (size_t)p.segs * H : 0;
+    p.token = (size_t)T * H;
+    p.d_init = own_d_init ? (size_t)S * H * size : 0;
+    p.sums = per_head ? (size_t)p.segs * H : 0;
+    return p;
+}
+inline size_t elements(const Plan &p) { return 2 * p.state + p.d_init + 2 * p.factor + 2 * p.token + p.sums; }
+
+template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, const kda_lin_grads &r, float *ws, int32_t *err, hipStream_t st) {
+    const bool own_d_init = a.initial_state && !r.d_initial_state;
+    const Plan p = plan(a.total_tokens, a.heads, a.num_seqs, KD * VD, a.g_per_head, own_d_init);
+    const Batch b = {a.cu_seqlens, a.g, a.g_per_head ? 0 : a.heads, a.num_seqs, a.total_tokens, a.heads, p.seg, p.segs};
+    const Role q = {a.q, a.q_stride, a.q_head_stride}, k = {a.k, a.k_stride, a.k_head_stride}, v = {a.v, a.v_stride, a.v_head_stride};
+    const Role d = {r.d_out, r.d_out_stride, r.d_out_head_stride}, none = {nullptr, 0, 0};
+    // 16-byte pieces first
+    float *x = ws, *y = x + p.state, *di = y + p.state, *xf = di + p.d_init, *yf = xf + p.factor, *u = yf + p.factor, *w = u + p.token,
+          *sums = w + p.token;
+    float *d_init = own_d_init ? di : r.d_initial_state;
+    const dim3 grid((unsigned)p.segs, (unsigned)a.heads);
+    hipError_t e;
+    if (p.segs > 1) {
+        const Own ox = {k, v, a.initial_state, x, xf, 1.0f}, oy = {q, d, r.d_final_state, y, yf, a.scale};
+        lin_bwd_state_kernel<DT, KD, VD><<<dim3(grid.x, grid.y, 2), THREADS, 0, st>>>(b, ox, oy);
+        if ((e = hipGetLastError())) return e;
+        lin_bwd_join_kernel<KD * VD><<<dim3(KD * VD / THREADS, grid.y, 2), THREADS, 0, st>>>(b, x, xf, y, yf);
+        if ((e = hipGetLastError())) return e;
+    }
+    // dq on X^T, dk on Y^T: their states' rows are value elements
+    const Walk wq = {d, v, k, r.dq, x, a.initial_state, nullptr, 1, VD, a.scale, a.scale, 1.0f, q, u};
+    const Walk wv = {k, q, d, r.dv, y, r.d_final_state, d_init, VD, 1, a.scale, 1.0f, a.scale, none, nullptr};
+    const Walk wk = {v, d, q, r.dk, y, r.d_final_state, nullptr, 1, VD, a.scale, 1.0f, a.scale, k, w};
+    lin_dq_kernel<DT, VD, KD><<<grid, THREADS, 0, st>>>(b, wq, err);
+    if ((e = hipGetLastError())) return e;
+    lin_dv_kernel<DT, KD, VD><<<grid, THREADS, 0, st>>>(b, wv);
+    if ((e = hipGetLastError())) return e;
+    lin_dk_kernel<DT, VD, KD><<<grid, THREADS, 0, st>>>(b, wk);
+    if ((e = hipGetLastError())) return e;
+    const Decays dec = {q, k, v, d, x, y, a.initial_state, d_init, u, w, a.g_per_head ? sums : r.dg, a.scale, a.g_per_head};
+    lin_decay_kernel<DT, KD, VD><<<grid, THREADS, 0, st>>>(b, dec);
+    if ((e = hipGetLastError())) return e;
+    if (a.g_per_head) {
+        lin_decay_sum_kernel<<<dim3(grid.y), 64, 0, st>>>(sums, r.dg, p.segs, a.heads);
+        if ((e = hipGetLastError())) return e;
+    }
+    return hipSuccess;
+}
+
+template <int DT> hipError_t backward_dt(const kda_lin_args &a, const kda_lin_grads &g, float *ws, int32_t *err, hipStream_t st) {
+    if (a.key_dim == 64) return a.value_dim == 64 ? backward<DT, 64, 64>(a, g, ws, err, st) : backward<DT, 64, 128>(a, g, ws, err, st);
+    return a.value_dim == 64 ? backward<DT, 128, 64>(a, g, ws, err, st) : backward<DT, 128, 128>(a, g, ws, err, st);
+}
+
+}  // namespace
+}  // namespace lin
+
+#ifndef KDA_LIN_BWD_F16
+size_t lin_bwd_workspace(int64_t T, int64_t H, int64_t S, int64_t KD, int64_t VD, bool per_head, bool own_d_init) {
+    return lin::elements(lin::plan(T, H, S, KD * VD, per_head, own_d_init)) * sizeof(float);
+}
+
+hipError_t launch_lin_bwd(const kda_lin_args &a, const kda_lin_grads &g, float *ws, int32_t *err, hipStream_t st) {
+    return a.dtype == KDA_DTYPE_BF16 ? lin::backward_dt<KDA_DTYPE_BF16>(a, g, ws, err, st) : launch_lin_bwd_f16(a, g, ws, err, st);
+}
+#else
+hipError_t launch_lin_bwd_f16(const kda_lin_args &a, const kda_lin_grads &g, float *ws, int32_t *err, hipStream_t st) {
+    return lin::backward_dt<KDA_DTYPE_F16>(a, g, ws, err, st);
+}
+#endif
+
+}  // namespace ops
+}  // namespace kda

@@ -24,6 +24,7 @@ EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_noalloc", "kda_workspace_bytes", "k
            "kda_ssm_bwd", "kda_ssm_bwd_workspace_bytes",
            "kda_attn_decode", "kda_attn_workspace_bytes",
            "kda_attn_decode_fp4", "kda_kv_append", "kda_kv_read_fp4",
+           "kda_lin_fwd", "kda_lin_workspace_bytes", "kda_lin_decode", "kda_lin_bwd", "kda_lin_bwd_workspace_bytes",
            "kda_device_errors", "kda_status_string", "kda_version")
 #: KDA_DEVERR_* bits of the device error word
 DEVERR = {1: "fused hand-off wait gave up (outputs invalid)", 2: "malformed cu_seqlens (sanitised)",
@@ -48,7 +49,7 @@ class KdaLaunchInfo(ctypes.Structure):
                 ("chunk_len", ctypes.c_int32)]
 
 
-ACT_DTYPES = {"f32": 0, "bf16": 1, "f16": 2}   # KDA_DTYPE_* of the activations of kda_conv_*, kda_ssm_*, kda_attn_*, kda_kv_*
+ACT_DTYPES = {"f32": 0, "bf16": 1, "f16": 2}   # KDA_DTYPE_* of the activations of kda_conv_*, kda_ssm_*, kda_attn_*, kda_kv_*, kda_lin_*
 CONV_MAX_WIDTH = 8   # KDA_CONV_MAX_WIDTH
 SSM_MAX_STATE = 256   # KDA_SSM_MAX_STATE
 FP4_GROUP = 32   # KDA_FP4_GROUP
@@ -116,6 +117,19 @@ class KdaKvReadArgs(ctypes.Structure):
                 [("table_stride", ctypes.c_int64)] +
                 [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "kv_heads", "head_dim", "num_pages", "page_size",
                                                "table_width", "dtype")])
+
+
+class KdaLinArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "cu_seqlens", "initial_state", "final_state", "out")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "q_head_stride", "k_stride", "k_head_stride", "v_stride",
+                                               "v_head_stride")] +
+                [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "heads", "key_dim", "value_dim", "dtype",
+                                               "g_per_head")] + [("scale", ctypes.c_float)])
+
+
+class KdaLinGrads(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("d_out", "d_final_state", "dq", "dk", "dv", "dg", "d_initial_state")] +
+                [("d_out_stride", ctypes.c_int64), ("d_out_head_stride", ctypes.c_int64)])
 
 
 class KdaError(RuntimeError):
@@ -192,6 +206,16 @@ def load_library(path=LIB_PATH):
     lib.kda_kv_append.restype = ctypes.c_int
     lib.kda_kv_read_fp4.argtypes = [ctypes.POINTER(KdaKvReadArgs), vp]
     lib.kda_kv_read_fp4.restype = ctypes.c_int
+    lib.kda_lin_fwd.argtypes = [ctypes.POINTER(KdaLinArgs), vp, vp, ctypes.c_size_t]
+    lib.kda_lin_fwd.restype = ctypes.c_int
+    lib.kda_lin_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.kda_lin_workspace_bytes.restype = ctypes.c_size_t
+    lib.kda_lin_decode.argtypes = [ctypes.POINTER(KdaLinArgs), vp]
+    lib.kda_lin_decode.restype = ctypes.c_int
+    lib.kda_lin_bwd.argtypes = [ctypes.POINTER(KdaLinArgs), ctypes.POINTER(KdaLinGrads), vp, vp, ctypes.c_size_t]
+    lib.kda_lin_bwd.restype = ctypes.c_int
+    lib.kda_lin_bwd_workspace_bytes.argtypes = [i32] * 7
+    lib.kda_lin_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]
     lib.kda_device_errors.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]

@@ -80,7 +80,7 @@ typedef enum kda_variant {
 /* Element types of kda_options.g_dtype / state_dtype (and of kda_decode_ex). */
 #define KDA_DTYPE_F32 0
 #define KDA_DTYPE_BF16 1
-#define KDA_DTYPE_F16 2   /* activations of the operators below only (kda_conv_*, kda_ssm_*, kda_attn_*, kda_kv_*) */
+#define KDA_DTYPE_F16 2   /* activations of the operators below only (kda_conv_*, kda_ssm_*, kda_attn_*, kda_kv_*, kda_lin_*) */
 
 typedef struct kda_options {
     int32_t variant;        /* kda_variant                                              */
@@ -583,6 +583,71 @@ typedef struct kda_kv_read_args {
  * kda_kv_append.
  */
 int kda_kv_read_fp4(const kda_kv_read_args *args, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Linear attention with a decay for each head: KDA's recurrence without the delta rule's correction, with one decay
+ * for all channels of a head.
+ */
+typedef struct kda_lin_args {
+    const void *q, *k;        /* [total_tokens, heads, key_dim]                               */
+    const void *v;            /* [total_tokens, heads, value_dim]                             */
+    const float *g;           /* natural-log decays: fp32 [total_tokens, heads], or [heads]    */
+                              /* where g_per_head                                             */
+    const int32_t *cu_seqlens; /* int32 [num_seqs+1] or NULL (one sequence), as kda_fwd        */
+    const float *initial_state; /* fp32 [num_seqs, heads, key_dim, value_dim] or NULL (zeros)  */
+    float *final_state;       /* the same, or NULL (not written)                              */
+    void *out;                /* [total_tokens, heads, value_dim], contiguous                 */
+    int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;
+    int32_t num_seqs, total_tokens, heads;
+    int32_t key_dim, value_dim; /* 64 or 128 each                                              */
+    int32_t dtype;            /* KDA_DTYPE_BF16 or KDA_DTYPE_F16: q, k, v and out              */
+    int32_t g_per_head;       /* 0 or 1                                                       */
+    float scale;              /* finite                                                       */
+} kda_lin_args;
+
+/*
+ * kda_lin_fwd -- per sequence and head, tokens t in order:
+ *
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   out_t = scale S_t^T q_t
+ *
+ * with S from initial_state and final_state the last S. g_t is meant to be 0 or less; -infinity (anything under -2839)
+ * forgets all that was before. Chunks of 64 tokens go through matrix instructions; states and the gradients of g
+ * are as exact as fp32 sums are, the outputs lose about 2^-16 beside their rounding to dtype. An input that is not
+ * finite makes its head of its sequence infinite or NaN, from up to 63 tokens before it on; no other head or sequence. Rows are read 16
+ * bytes at a time: bases aligned to 16 bytes, strides multiples of 8 elements, else KDA_ERR_UNSUPPORTED; states are
+ * aligned to 16 bytes too. Segments of the time axis run side by side, their states joined in the workspace:
+ * kda_lin_workspace_bytes() bytes of device memory, or NULL: then the library allocates it stream-ordered on `stream`. The
+ * same results from run to run. Limits: total_tokens <= 2^27, heads <= 65535, num_seqs * heads <= 2^27. final_state must not
+ * overlap initial_state.
+ */
+size_t kda_lin_workspace_bytes(int32_t total_tokens, int32_t heads, int32_t key_dim, int32_t value_dim);
+int kda_lin_fwd(const kda_lin_args *args, void *stream, void *workspace, size_t workspace_bytes);
+
+/*
+ * kda_lin_decode -- one token per sequence (total_tokens = num_seqs, cu_seqlens NULL; g [num_seqs, heads] or [heads]), in
+ * fp32. final_state may be the same pointer as initial_state (updated in place). No workspace.
+ */
+int kda_lin_decode(const kda_lin_args *args, void *stream);
+
+typedef struct kda_lin_grads {
+    const void *d_out;        /* [total_tokens, heads, value_dim] of args' dtype               */
+    const float *d_final_state; /* fp32 [num_seqs, heads, key_dim, value_dim] or NULL (zeros)  */
+    void *dq, *dk, *dv;       /* as q, k, v, contiguous                                       */
+    float *dg;                /* fp32, of g's shape                                           */
+    float *d_initial_state;   /* fp32 [num_seqs, heads, key_dim, value_dim] or NULL (not written) */
+    int64_t d_out_stride, d_out_head_stride;
+} kda_lin_grads;
+
+/*
+ * kda_lin_bwd -- gradients of kda_lin_fwd with respect to every input, from d_out and d_final_state (args->out and
+ * args->final_state are ignored). Needs nothing that the forward computed. Sums run in a fixed order: the same results from run to
+ * run. workspace: kda_lin_bwd_workspace_bytes() bytes of device memory, or NULL: then the library allocates it
+ * stream-ordered on `stream`. Where initial_state is given and d_initial_state is not, the workspace holds it
+ * (need_d_initial_state 0; 1 where initial_state is NULL).
+ */
+size_t kda_lin_bwd_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t heads, int32_t key_dim, int32_t value_dim,
+                                   int32_t g_per_head, int32_t need_d_initial_state);
+int kda_lin_bwd(const kda_lin_args *args, const kda_lin_grads *grads, void *stream, void *workspace, size_t workspace_bytes);
 
 /*
  * kda_device_errors -- the device error word of the current device: the OR of the
