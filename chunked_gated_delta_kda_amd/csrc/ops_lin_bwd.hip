@@ -4,11 +4,13 @@
 // dv and dk (backwards on Y), and on the way u_i = q_i . (part of dq_i from X), w_j = k_j . (part of dk_j from Y).
 // A decay's gradient is what passes it, from tokens before t to tokens from t on:
 //
-//   dg_t = sum_{j < t <= i} W_ij + F - sum_{i < t} u_i + sum_{j < t} w_j,   W_ij = scale e^{G_i - G_j} (q_i . k_j) (do_i . v_j)
+//   dg_t = sum_{j < t <= i} W_ij + sum_{i >= t} u_i + sum_{j < t} w_j + c,   W_ij = scale e^{G_i - G_j} (q_i . k_j) (do_i . v_j)
 //
-// in the chunk, F = <X, Y before the chunk> what passes the chunk's first border; the next chunk's F is this one's less its u plus its w.
-// So nothing is subtracted over more than a segment, and pairs of a token with itself (large where decays are
-// short) never enter.
+// over the chunk, with c what passes all of it: F, what passes its first border (<X, Y> there, formed at a segment's
+// border or a sequence's), less the chunk's u; c plus the chunk's w pass the next border. That is the only subtraction, over
+// the chunks of a segment: pairs of a token with itself, which outweigh all else where decays are short, never enter,
+// and where a chunk leaves less than 2^-24 of a state and c is under 2^-16 of its u's sizes, c is what rounding left of that difference
+// and put to 0, so that nothing outlives a reset.
 #include "ops_lin.hpp"
 
 namespace kda {
@@ -65,15 +67,6 @@ __device__ __forceinline__ float wave_sum(float x) {
     for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
     return x;
 }
-// sum over the 16 lanes of a row
-__device__ __forceinline__ float row_sum(float x) {
-    x += dpp_f<0xb1>(x);        // lanes 1 0 3 2
-    x += dpp_f<0x4e>(x);        // lanes 2 3 0 1
-    x += dpp_f<0x141>(x);       // the other four of eight, mirrored
-    x += dpp_f<0x140>(x);       // the other eight, mirrored
-    return x;
-}
-
 // operand: 8 elements of a row, as bf16 parts
 template <int DT> __device__ __forceinline__ void global_operand(const Role &s, int h, int t, bool there, int at, u32x4 (&to)[PLANES<DT>]) {
     u32x4 r = {0, 0, 0, 0};
@@ -89,12 +82,21 @@ template <int DT> __device__ __forceinline__ void global_operand(const Role &s, 
     }
 }
 
-// A block takes a segment of one head, a wave every fourth chunk of it.
+// sums over a row's lanes from each lane on: four steps to the right
+__device__ __forceinline__ float row_suffix(float x) {
+    x += dpp_f<0x101>(x);       // the lane one to the right (0 past the row's end), then two, four, eight
+    x += dpp_f<0x102>(x);
+    x += dpp_f<0x104>(x);
+    x += dpp_f<0x108>(x);
+    return x;
+}
+
+// A block takes a segment of one head, four chunks at a time, a wave each.
 template <int DT, int KD, int VD>
 __global__ __launch_bounds__(THREADS) void lin_decay_kernel(const Batch b, const Decays a) {
     constexpr int NP = PLANES<DT>, SIZE = KD * VD;
     __shared__ Clock clocks[4];
-    __shared__ float rows[4][C], cols[4][C], part[4];
+    __shared__ float part[4], border[4], sums[4][4];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
     const int seg = blockIdx.x, h = blockIdx.y;
     const Offsets o = b.offsets();
@@ -102,12 +104,20 @@ __global__ __launch_bounds__(THREADS) void lin_decay_kernel(const Batch b, const
     Chunks<false> chunks(o, s0, s1);
     Clock &clock = clocks[wave];
     float all = 0.0f, F = 0.0f;
-    int n = 0, part0 = 0;
 #pragma unroll 1
-    for (Chunk c = chunks.next(); c.len; c = chunks.next(), ++n) {
-        if (c.enter) {      // what passes the part's first border: the block together
+    for (;;) {
+        Chunk own = {0, 0, 0, false, false, false, false};
+        int enters = 0, count = 0;
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+            const Chunk c = chunks.next();
+            if (!c.len) break;
+            ++count;
+            if (n == wave) own = c;
+            if (!c.enter) continue;
+            // what passes the first border of a part: the block together
+            enters |= 1 << n;
             const float *x = nullptr, *y = nullptr;
-            part0 = c.first;
             if (!c.open) x = a.x + ((int64_t)(seg - 1) * b.H + h) * SIZE, y = a.y + ((int64_t)seg * b.H + h) * SIZE;
             else if (a.init) x = a.init + ((int64_t)c.seq * b.H + h) * SIZE, y = a.d_init + ((int64_t)c.seq * b.H + h) * SIZE;
             float sum = 0.0f;
@@ -121,28 +131,38 @@ __global__ __launch_bounds__(THREADS) void lin_decay_kernel(const Batch b, const
             __syncthreads();
             if (lane == 0) part[wave] = sum;
             __syncthreads();
-            F = (part[0] + part[1]) + (part[2] + part[3]);
+            if (threadIdx.x == 0) border[n] = (part[0] + part[1]) + (part[2] + part[3]);
         }
-        if ((n & 3) != wave) continue;
-        const bool there = lane < c.len;
-        const int64_t at = (int64_t)(c.first + lane) * b.H + h;
-        tick<false>(clock, there ? log2_decay(b.decay(c.first + lane, h)) : 0.0, 1.0f, 1.0f);
-        // u and w of the part's chunks before this one
-        float over = 0.0f;
-        for (int t = part0 + lane; t < c.first; t += 64) over += a.w[(int64_t)t * b.H + h] - a.u[(int64_t)t * b.H + h];
-        over = wave_sum(over) + F;
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        // W: rows tokens j, columns tokens i > j
-        float colsum[4][4];     // over i, of token 16 jt + 4 g + r
+        if (!count) break;
+        const bool there = lane < own.len;
+        const int64_t at = (int64_t)(own.first + lane) * b.H + h;
+        const float u = there ? a.u[at] : 0.0f, w = there ? a.w[at] : 0.0f;
+        tick<false>(clock, there ? log2_decay(b.decay(own.first + lane, h)) : 0.0, 1.0f, 1.0f);
+        {
+            const float su = wave_sum(u), sw = wave_sum(w), size = wave_sum(__builtin_fabsf(u));
+            if (lane == 0) sums[wave][0] = su, sums[wave][1] = sw, sums[wave][2] = clock.total, sums[wave][3] = size;
+        }
+        __syncthreads();
+        float mine = 0.0f;      // what passes all of the wave's chunk
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if (n >= count) break;
+            if (enters >> n & 1) F = border[n];
+            float c = F - sums[n][0];
+            if (sums[n][2] < 0x1p-24f && __builtin_fabsf(c) < 0x1p-16f * sums[n][3]) c = 0.0f;
+            if (n == wave) mine = c;
+            F = c + sums[n][1];
+        }
+        // W: rows tokens j, columns tokens i > j. Summed over i from each token on, then over the j before it: nothing is subtracted.
+        float inside[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // of token 16 it + i
+        float later[4][4];                              // over the tiles of i behind
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) colsum[jt][r] = 0.0f;
-#pragma unroll 1
-        for (int it = 0; it < 4; ++it) {
-            float rowsum = 0.0f;
+            for (int r = 0; r < 4; ++r) later[jt][r] = 0.0f;
+#pragma unroll
+        for (int it = 3; it >= 0; --it) {
+            if (16 * it >= own.len) continue;
             const int ti = 16 * it + i;
             const float wi = clock.whole[ti], ri = clock.rest[ti];
 #pragma unroll
@@ -153,45 +173,38 @@ __global__ __launch_bounds__(THREADS) void lin_decay_kernel(const Batch b, const
 #pragma unroll
                 for (int s = 0; s < KD / 32; ++s) {
                     u32x4 x[NP], y[NP];
-                    global_operand<DT>(a.k, h, c.first + tj, tj < c.len, 32 * s + 8 * g, x);
-                    global_operand<DT>(a.q, h, c.first + ti, ti < c.len, 32 * s + 8 * g, y);
+                    global_operand<DT>(a.k, h, own.first + tj, tj < own.len, 32 * s + 8 * g, x);
+                    global_operand<DT>(a.q, h, own.first + ti, ti < own.len, 32 * s + 8 * g, y);
                     pairs<NP, NP, 4>([&](int m, int k) { qk = mma(x[m], y[k], qk); });
                 }
 #pragma unroll
                 for (int s = 0; s < VD / 32; ++s) {
                     u32x4 x[NP], y[NP];
-                    global_operand<DT>(a.v, h, c.first + tj, tj < c.len, 32 * s + 8 * g, x);
-                    global_operand<DT>(a.d_out, h, c.first + ti, ti < c.len, 32 * s + 8 * g, y);
+                    global_operand<DT>(a.v, h, own.first + tj, tj < own.len, 32 * s + 8 * g, x);
+                    global_operand<DT>(a.d_out, h, own.first + ti, ti < own.len, 32 * s + 8 * g, y);
                     pairs<NP, NP, 4>([&](int m, int k) { dv = mma(x[m], y[k], dv); });
                 }
                 const f32x4 wj = *reinterpret_cast<const f32x4 *>(&clock.whole[16 * jt + 4 * g]);
                 const f32x4 rj = *reinterpret_cast<const f32x4 *>(&clock.rest[16 * jt + 4 * g]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
+                    const int j = 16 * jt + 4 * g + r;
                     const float x = qk[r] * dv[r] * exp2_f((wi - wj[r]) + (ri - rj[r])) * a.scale;
-                    const float e = 16 * jt + 4 * g + r < ti ? x : 0.0f;
-                    rowsum += e;
-                    colsum[jt][r] += e;
+                    const float from = row_suffix(j < ti ? x : 0.0f) + later[jt][r];
+                    inside[it] += j < ti ? from : 0.0f;
+                    later[jt][r] = __shfl(from, lane & 48);     // of the tile's first token
                 }
             }
-            rowsum = swap16_add(rowsum, rowsum);
-            rowsum = swap32_add(rowsum, rowsum);
-            if (g == 0) rows[wave][ti] = rowsum;
         }
+        // lane t: the tokens' own sums, u from t on, w before t
+        float dg = 0.0f;
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float x = row_sum(colsum[jt][r]);
-                if (i == 0) cols[wave][16 * jt + 4 * g + r] = x;
-            }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        // lane t: sums from t on of the rows less the columns, sums before t of w - u
-        const float mine = rows[wave][lane] - cols[wave][lane];
-        const float flow = there ? a.w[at] - a.u[at] : 0.0f;
-        float from = mine, upto = flow;
+        for (int it = 0; it < 4; ++it) {
+            float x = swap16_add(inside[it], inside[it]);
+            x = swap32_add(x, x);
+            if (g == it) dg = x;
+        }
+        float from = u, upto = w;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
             const float x = __shfl_down(from, d), y = __shfl_up(upto, d);
@@ -199,10 +212,12 @@ __global__ __launch_bounds__(THREADS) void lin_decay_kernel(const Batch b, const
             if (lane >= d) upto += y;
         }
         const float before = __shfl_up(upto, 1);
-        const float dg = from + (lane ? before : 0.0f) + over;
-        if (!a.per_head) {
-            if (there) a.dg[at] = dg;
-        } else all += there ? dg : 0.0f;
+        dg += from + (lane ? before : 0.0f) + mine;
+        if (there) {
+            if (a.per_head) all += dg;
+            else a.dg[at] = dg;
+        }
+        __syncthreads();        // border and sums are read
     }
     if (a.per_head) {
         all = wave_sum(all);
