@@ -253,7 +253,8 @@ bool lin_sizes_ok(int64_t S, int64_t T, int64_t H) {
     return S >= 1 && T >= 0 && T <= 1 << 27 && H >= 1 && H <= 65535 && S * H <= 1 << 27;
 }
 
-int check_lin(const kda_lin_args &a, bool grads) {
+// far: rows may lie further apart than KDA_LIN_MAX_STRIDE (a token alone)
+int check_lin(const kda_lin_args &a, bool grads, bool far = false) {
     if ((a.dtype != KDA_DTYPE_BF16 && a.dtype != KDA_DTYPE_F16) || !lin_dim(a.key_dim) || !lin_dim(a.value_dim) ||
         (a.g_per_head != 0 && a.g_per_head != 1) || !std::isfinite(a.scale))
         return KDA_ERR_UNSUPPORTED;
@@ -263,6 +264,8 @@ int check_lin(const kda_lin_args &a, bool grads) {
         if (s < 0) return KDA_ERR_SHAPE;
     for (const int64_t s : strides)
         if (s % 8) return KDA_ERR_UNSUPPORTED;
+    for (const int64_t s : {a.q_stride, a.k_stride, a.v_stride})
+        if (!far && s > KDA_LIN_MAX_STRIDE) return KDA_ERR_SHAPE;
     if (a.total_tokens > 0 && (!a.q || !a.k || !a.v || !a.g || (!grads && !a.out))) return KDA_ERR_NULL;
     if (!by16(a.q) || !by16(a.k) || !by16(a.v) || !by16(a.initial_state) || !by16(a.final_state) || !by16(a.out)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
@@ -574,7 +577,7 @@ int kda_lin_fwd(const kda_lin_args *args, void *stream, void *workspace, size_t 
 int kda_lin_decode(const kda_lin_args *args, void *stream) {
     if (!args) return KDA_ERR_NULL;
     const kda_lin_args &a = *args;
-    if (const int rc = check_lin(a, false)) return rc;
+    if (const int rc = check_lin(a, false, true)) return rc;
     if (a.cu_seqlens || a.total_tokens != a.num_seqs) return KDA_ERR_SHAPE;
     const LinSpans s(a);
     const Span out = span(a.out, (int64_t)a.total_tokens * a.heads * a.value_dim * 2), fin = span(a.final_state, s.state);
@@ -596,7 +599,7 @@ int kda_lin_bwd(const kda_lin_args *args, const kda_lin_grads *grads, void *stre
     const kda_lin_grads &g = *grads;
     if (const int rc = check_lin(a, true)) return rc;
     if (!a.cu_seqlens && a.num_seqs != 1) return KDA_ERR_SHAPE;
-    if (g.d_out_stride < 0 || g.d_out_head_stride < 0) return KDA_ERR_SHAPE;
+    if (g.d_out_stride < 0 || g.d_out_head_stride < 0 || g.d_out_stride > KDA_LIN_MAX_STRIDE) return KDA_ERR_SHAPE;
     if (g.d_out_stride % 8 || g.d_out_head_stride % 8 || !by16(g.d_out) || !by16(g.d_final_state) || !by16(g.dq) || !by16(g.dk) ||
         !by16(g.dv) || !by16(g.d_initial_state))
         return KDA_ERR_UNSUPPORTED;

@@ -8,30 +8,29 @@ namespace lin {
 namespace {
 
 template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS, 2) void lin_state_kernel(const Batch b, const Own a) {
-    __shared__ Tile<PLANES<DT>, KD> k;
-    __shared__ Tile<PLANES<DT>, VD> v;
-    __shared__ Clock clock;
-    own_state<DT, KD, VD, false>(b, a, k, v, clock);
+__global__ __launch_bounds__(THREADS<VD>, WAVES<VD> / 2) void lin_state_kernel(const Batch b, const Own a) {
+    __shared__ OwnLds<DT, KD, VD> lds;
+    own_state<DT, KD, VD, false>(b, a, lds);
 }
 
-template <int SIZE> __global__ __launch_bounds__(THREADS) void lin_join_kernel(const Batch b, float *state, const float *factor) {
+template <int SIZE> __global__ __launch_bounds__(JOIN_THREADS) void lin_join_kernel(const Batch b, float *state, const float *factor) {
     join<SIZE>(b, state, factor, false);
 }
 
 template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS, PLANES<DT> == 1 ? 2 : 1) void lin_walk_kernel(const Batch b, const Walk a, int32_t *err) {
-    __shared__ WalkLds<DT, KD, VD, 2> lds;
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS);
+__global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_walk_kernel(const Batch b, const Walk a, int32_t *err) {
+    __shared__ WalkLds<DT, KD, VD> lds;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS<VD>);
     walk<DT, KD, VD, false, false>(b, a, lds);
 }
 
 // One token of each sequence: S <- e^g S + k v^T, out = scale S^T q. The state is read and written once; a block takes one
 // head of one sequence, a thread 4 value columns of every GROUPS-th row.
+constexpr int DECODE_THREADS = 256;
 template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS) void lin_decode_kernel(const kda_lin_args a) {
+__global__ __launch_bounds__(DECODE_THREADS) void lin_decode_kernel(const kda_lin_args a) {
     using E = typename Elem<DT>::type;
-    constexpr int COLS = VD / 4, GROUPS = THREADS / COLS, ROWS = KD / GROUPS;
+    constexpr int COLS = VD / 4, GROUPS = DECODE_THREADS / COLS, ROWS = KD / GROUPS;
     __shared__ float q[KD], k[KD];
     __shared__ f32x4 part[GROUPS][COLS];
     const int n = blockIdx.x, h = blockIdx.y, x = threadIdx.x % COLS, grp = threadIdx.x / COLS;
@@ -91,18 +90,18 @@ template <int DT, int KD, int VD> hipError_t forward(const kda_lin_args &a, floa
     if (p.segs > 1) {
         float *factor = ws + (size_t)p.segs * a.heads * (KD * VD);
         const Own own = {k, v, a.initial_state, ws, factor, 1.0f};
-        lin_state_kernel<DT, KD, VD><<<grid, THREADS, 0, st>>>(b, own);
+        lin_state_kernel<DT, KD, VD><<<grid, THREADS<VD>, 0, st>>>(b, own);
         if (hipError_t e = hipGetLastError()) return e;
-        lin_join_kernel<KD * VD><<<dim3(KD * VD / THREADS, (unsigned)a.heads), THREADS, 0, st>>>(b, ws, factor);
+        lin_join_kernel<KD * VD><<<dim3(KD * VD / JOIN_THREADS, (unsigned)a.heads), JOIN_THREADS, 0, st>>>(b, ws, factor);
         if (hipError_t e = hipGetLastError()) return e;
     }
     const Walk w = {q, k, v, a.out, ws, a.initial_state, a.final_state, VD, 1, a.scale, a.scale, 1.0f, {nullptr, 0, 0}, nullptr};
-    lin_walk_kernel<DT, KD, VD><<<grid, THREADS, 0, st>>>(b, w, err);
+    lin_walk_kernel<DT, KD, VD><<<grid, THREADS<VD>, 0, st>>>(b, w, err);
     return hipGetLastError();
 }
 
 template <int DT, int KD, int VD> hipError_t decode(const kda_lin_args &a, hipStream_t st) {
-    lin_decode_kernel<DT, KD, VD><<<dim3((unsigned)a.num_seqs, (unsigned)a.heads), THREADS, 0, st>>>(a);
+    lin_decode_kernel<DT, KD, VD><<<dim3((unsigned)a.num_seqs, (unsigned)a.heads), DECODE_THREADS, 0, st>>>(a);
     return hipGetLastError();
 }
 

@@ -28,8 +28,11 @@ namespace lin {
 namespace {
 
 constexpr int C = 64;              // tokens of a chunk
-constexpr int THREADS = 256;       // four waves, each a quarter of the value columns
 constexpr int PAD = 8;             // elements behind a row in LDS: rows 4 banks apart
+
+// A block has a wave for every 16 value columns, which holds those columns of the state.
+template <int VD> constexpr int WAVES = VD / 16;
+template <int VD> constexpr int THREADS = 64 * WAVES<VD>;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -82,23 +85,24 @@ struct Role {
     int64_t row, head;       // strides, elements
 };
 
-// Rows of a chunk on their way from memory to LDS: a thread D / 32 pieces of 8 elements.
-template <int DT, int D> struct Stage {
-    static constexpr int N = D / 32;
+// Rows of a chunk on their way from memory to LDS, 8 elements of a row a time. NT: threads of the block. Offsets from
+// a chunk's first row fit 32 bits (strides are at most KDA_LIN_MAX_STRIDE).
+template <int DT, int D, int NT> struct Stage {
+    static constexpr int N = C * D / 8 / NT, ROWS = NT / (D / 8);     // rows of a piece
     u32x4 r[N];
     __device__ __forceinline__ void load(const Role &s, int h, int first, int len) {
-        const uint16_t *p = (const uint16_t *)s.p + (int64_t)first * s.row + (int64_t)h * s.head;
+        const char *p = (const char *)s.p + 2 * ((int64_t)first * s.row + (int64_t)h * s.head);
+        const uint32_t row = threadIdx.x / (D / 8), at = 2 * (row * (uint32_t)s.row + 8 * (threadIdx.x % (D / 8)));
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int x = threadIdx.x + THREADS * n, row = x / (D / 8), col = 8 * (x % (D / 8));
             r[n] = u32x4{0, 0, 0, 0};
-            if (row < len) r[n] = *reinterpret_cast<const u32x4 *>(p + (int64_t)row * s.row + col);
+            if ((int)row + ROWS * n < len) r[n] = *reinterpret_cast<const u32x4 *>(p + 2 * ROWS * n * s.row + at);
         }
     }
     __device__ __forceinline__ void store(Tile<PLANES<DT>, D> &t) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int x = threadIdx.x + THREADS * n, row = x / (D / 8), col = 8 * (x % (D / 8));
+            const int row = threadIdx.x / (D / 8) + ROWS * n, col = 8 * (threadIdx.x % (D / 8));
             if constexpr (DT == KDA_DTYPE_BF16) *reinterpret_cast<u32x4 *>(&t.x[0][row][col]) = r[n];
             else {
                 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -152,15 +156,29 @@ __device__ __forceinline__ double log2_decay(float g) {
     return x < -4096.0 ? -4096.0 : x;
 }
 
-// by one wave, lane t for token t: g of the token, 0 past the chunk's end
+// what lane - D of the 16-lane row holds, 0 before the row
+template <int D> __device__ __forceinline__ double row_shr(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)b, 0x110 + D, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(b >> 32), 0x110 + D, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_of(double x, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// by one wave, lane t for token t: x, log2 of the token's decay, 0 past the chunk's end. Returns the chunk's sum.
 template <bool REV> __device__ __forceinline__ double tick(Clock &c, double x, float in_scale, float up_scale) {
     const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const double y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
-    const double total = __shfl(x, 63);
+    x += row_shr<1>(x);
+    x += row_shr<2>(x);
+    x += row_shr<4>(x);
+    x += row_shr<8>(x);
+    const double a = lane_of(x, 15), b = a + lane_of(x, 31), d = b + lane_of(x, 47);
+    x += lane < 16 ? 0.0 : lane < 32 ? a : lane < 48 ? b : d;
+    const double total = lane_of(x, 63);
     const double whole = __builtin_rint(x);
     const float from = exp2_f((float)x), to = exp2_f((float)(total - x));
     c.whole[lane] = (float)whole;
@@ -226,73 +244,61 @@ template <bool REV> struct Chunks {
 };
 
 // S <- total S + sum_j k_j (up_j v_j)^T over a chunk, for the wave's columns. v's operands as the second product wants them.
-template <int NP, int KD, int VT>
-__device__ __forceinline__ void update(f32x4 (&S)[KD / 16][VT], const Tile<NP, KD> &k, const u32x4 (&v)[NP][VT][2], const Clock &clock) {
+template <int NP, int KD>
+__device__ __forceinline__ void update(f32x4 (&S)[KD / 16], const Tile<NP, KD> &k, const u32x4 (&v)[NP][2], const Clock &clock) {
     const int g = (threadIdx.x & 63) >> 4;
     const float total = clock.total;
 #pragma unroll
-    for (int kt = 0; kt < KD / 16; ++kt)
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) S[kt][vt] *= total;
+    for (int kt = 0; kt < KD / 16; ++kt) S[kt] *= total;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const f32x4 a = *reinterpret_cast<const f32x4 *>(&clock.up[32 * s + 4 * g]);
         const f32x4 b = *reinterpret_cast<const f32x4 *>(&clock.up[32 * s + 16 + 4 * g]);
-        u32x4 w[VT][3];
+        float x[8];
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-            float x[8];
+        for (int i = 0; i < 8; ++i) {
+            float e = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float e = 0.0f;
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    const uint32_t word = v[p][vt][s][i / 2];
-                    e += __uint_as_float(i & 1 ? word & 0xffff0000u : word << 16);
-                }
-                x[i] = e * (i < 4 ? a[i & 3] : b[i & 3]);
+            for (int p = 0; p < NP; ++p) {
+                const uint32_t word = v[p][s][i / 2];
+                const float f = __uint_as_float(i & 1 ? word & 0xffff0000u : word << 16);
+                e = p ? e + f : f;
             }
-            split<3>(x, w[vt]);
+            x[i] = e * (i < 4 ? a[i & 3] : b[i & 3]);
         }
+        u32x4 w[3];
+        split<3>(x, w);
 #pragma unroll
         for (int kt = 0; kt < KD / 16; ++kt) {
             u32x4 row[NP];
 #pragma unroll
             for (int p = 0; p < NP; ++p) row[p] = column_operand(k, p, kt, s);
-#pragma unroll
-            for (int vt = 0; vt < VT; ++vt) pairs<NP, 3, 3>([&](int p, int t) { S[kt][vt] = mma(row[p], w[vt][t], S[kt][vt]); });
+            pairs<NP, 3, 3>([&](int p, int n) { S[kt] = mma(row[p], w[n], S[kt]); });
         }
     }
 }
 
-template <int NP, int VD, int VT>
-__device__ __forceinline__ void value_operands(const Tile<NP, VD> &v, int wave, u32x4 (&to)[NP][VT][2]) {
+template <int NP, int VD> __device__ __forceinline__ void value_operands(const Tile<NP, VD> &v, int wave, u32x4 (&to)[NP][2]) {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) to[p][vt][s] = column_operand(v, p, wave * VT + vt, s);
+        for (int s = 0; s < 2; ++s) to[p][s] = column_operand(v, p, wave, s);
 }
 
 // A state [KD][VD] between memory (element (a, b) at a sk + b sv) and the wave's columns. p NULL: zeros.
-template <int KD, int VT> __device__ __forceinline__ void load_state(f32x4 (&S)[KD / 16][VT], const float *p, int sk, int sv, int wave) {
-    const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+template <int KD> __device__ __forceinline__ void load_state(f32x4 (&S)[KD / 16], const float *p, int sk, int sv, int wave) {
+    const uint32_t at = 4 * ((threadIdx.x & 63) >> 4) * sk + (16 * wave + (threadIdx.x & 15)) * sv;
 #pragma unroll
     for (int kt = 0; kt < KD / 16; ++kt)
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[kt][vt][r] = p ? p[(16 * kt + 4 * g + r) * sk + (16 * (wave * VT + vt) + i) * sv] : 0.0f;
+        for (int r = 0; r < 4; ++r) S[kt][r] = p ? (p + (16 * kt + r) * sk)[at] : 0.0f;
 }
-template <int KD, int VT> __device__ __forceinline__ void store_state(const f32x4 (&S)[KD / 16][VT], float *p, int sk, int sv, int wave) {
-    const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+template <int KD> __device__ __forceinline__ void store_state(const f32x4 (&S)[KD / 16], float *p, int sk, int sv, int wave) {
+    const uint32_t at = 4 * ((threadIdx.x & 63) >> 4) * sk + (16 * wave + (threadIdx.x & 15)) * sv;
 #pragma unroll
     for (int kt = 0; kt < KD / 16; ++kt)
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) p[(16 * kt + 4 * g + r) * sk + (16 * (wave * VT + vt) + i) * sv] = S[kt][vt][r];
+        for (int r = 0; r < 4; ++r) (p + (16 * kt + r) * sk)[at] = S[kt][r];
 }
 
 // The batch and its segments.
@@ -317,10 +323,15 @@ struct Own {
     float up;
 };
 
-template <int DT, int KD, int VD, bool REV>
-__device__ __forceinline__ void own_state(const Batch &b, const Own &a, Tile<PLANES<DT>, KD> &kt, Tile<PLANES<DT>, VD> &vt, Clock &clock) {
-    constexpr int NP = PLANES<DT>, VT = VD / 64;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), seg = blockIdx.x, h = blockIdx.y;
+template <int DT, int KD, int VD> struct OwnLds {
+    Tile<PLANES<DT>, KD> k;
+    Tile<PLANES<DT>, VD> v;
+    Clock clock[2];
+};
+
+template <int DT, int KD, int VD, bool REV> __device__ __forceinline__ void own_state(const Batch &b, const Own &a, OwnLds<DT, KD, VD> &L) {
+    constexpr int NP = PLANES<DT>, NT = THREADS<VD>;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, seg = blockIdx.x, h = blockIdx.y;
     const Offsets o = b.offsets();
     const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
     float *factor = a.factor + (int64_t)seg * b.H + h;
@@ -334,42 +345,41 @@ __device__ __forceinline__ void own_state(const Batch &b, const Own &a, Tile<PLA
         if (threadIdx.x == 0) *factor = -1.0f;
         return;
     }
-    f32x4 S[KD / 16][VT];
-    load_state<KD, VT>(S, open && a.init ? a.init + ((int64_t)seq * b.H + h) * (KD * VD) : nullptr, VD, 1, wave);
-    double sum = 0.0;
-    Stage<DT, KD> sk;
-    Stage<DT, VD> sv;
+    f32x4 S[KD / 16];
+    load_state<KD>(S, open && a.init ? a.init + ((int64_t)seq * b.H + h) * (KD * VD) : nullptr, VD, 1, wave);
+    double sum = 0.0, g = 0.0;
+    Stage<DT, KD, NT> sk;
+    Stage<DT, VD, NT> sv;
     const int count = (p1 - p0 + C - 1) / C;
-    auto first_of = [&](int n) { return p0 + C * (REV ? count - 1 - n : n); };
-    auto len_of = [&](int first) { return p1 - first < C ? p1 - first : C; };
-    double g = 0.0;
     auto load = [&](int n) {
-        const int first = first_of(n), len = len_of(first), lane = threadIdx.x & 63;
+        const int first = p0 + C * (REV ? count - 1 - n : n), len = p1 - first < C ? p1 - first : C;
+        if (wave == 0) g = lane < len ? log2_decay(b.decay(first + lane, h)) : 0.0;
         sk.load(a.k, h, first, len);
         sv.load(a.v, h, first, len);
-        g = wave == 0 && lane < len ? log2_decay(b.decay(first + lane, h)) : 0.0;
     };
     load(0);
+    if (wave == 0) sum += tick<REV>(L.clock[0], g, 1.0f, a.up);
 #pragma unroll 1
     for (int n = 0; n < count; ++n) {
         lds_barrier();
-        sk.store(kt);
-        sv.store(vt);
-        if (wave == 0) sum += tick<REV>(clock, g, 1.0f, a.up);
+        sk.store(L.k);
+        sv.store(L.v);
         lds_barrier();
         if (n + 1 < count) load(n + 1);
-        u32x4 v[NP][VT][2];
-        value_operands<NP, VD, VT>(vt, wave, v);
-        update<NP, KD, VT>(S, kt, v, clock);
+        u32x4 v[NP][2];
+        value_operands(L.v, wave, v);
+        update<NP, KD>(S, L.k, v, L.clock[n & 1]);
+        if (wave == 0 && n + 1 < count) sum += tick<REV>(L.clock[(n + 1) & 1], g, 1.0f, a.up);
     }
-    store_state<KD, VT>(S, a.state + ((int64_t)seg * b.H + h) * (KD * VD), VD, 1, wave);
+    store_state<KD>(S, a.state + ((int64_t)seg * b.H + h) * (KD * VD), VD, 1, wave);
     if (threadIdx.x == 0) *factor = open ? -1.0f : exp2_f((float)sum);
 }
 
 // ---------------------------------------------------------------- join
 // state[s] <- what leaves segment s (backwards: what it hands to the one before), in the order of the segments.
+constexpr int JOIN_THREADS = 256;
 template <int SIZE> __device__ __forceinline__ void join(const Batch &b, float *state, const float *factor, bool rev) {
-    const int h = blockIdx.y, x = blockIdx.x * THREADS + threadIdx.x;
+    const int h = blockIdx.y, x = blockIdx.x * JOIN_THREADS + threadIdx.x;
     float c = 0.0f;
     const int64_t step = (int64_t)b.H * SIZE;
     float *p = state + (int64_t)h * SIZE + x;
@@ -405,18 +415,19 @@ struct Walk {
     float *dot;             // DOT: [T, H]
 };
 
-template <int DT, int KD, int VD, int PARTS> struct WalkLds {
+// The pairs' weights go in as two parts.
+constexpr int PARTS = 2;
+template <int DT, int KD, int VD> struct WalkLds {
     Tile<PLANES<DT>, KD> q, k;
     Tile<PLANES<DT>, VD> v;
     u32x4 pair[4][2][PARTS][64];      // operands of the pairs' weights: 16 columns (tokens i), 32 tokens j, part, lane
-    Clock clock;
-    float dots[4][C];
+    Clock clock[2];
+    float dots[WAVES<VD>][C];
 };
 
-// IN: parts of the state in its product with q. The pairs' weights go in as two parts.
 template <int DT, int KD, int VD, bool REV, bool DOT>
-__device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, KD, VD, 2> &L) {
-    constexpr int NP = PLANES<DT>, VT = VD / 64, IN = DOT ? 3 : 2, PARTS = 2;
+__device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, KD, VD> &L) {
+    constexpr int NP = PLANES<DT>, NT = THREADS<VD>, NW = WAVES<VD>, IN = DOT ? 3 : 2;      // IN: parts of the state in its product with q
     using E = typename Elem<DT>::type;
     typedef E E4 __attribute__((ext_vector_type(4)));
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -425,14 +436,14 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
     const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
     constexpr int SIZE = KD * VD;
     // empty sequences, spread over the segments: what enters them leaves them
-    if (a.fin) {
+    if (a.fin && b.cu) {
         for (int n0 = seg * 64; n0 < b.N; n0 += b.segs * 64) {
             const int n = n0 + lane;
             uint64_t none = __ballot(n < b.N && o.at(n) >= o.at(n + 1));
             while (none) {
                 const int at = n0 + __builtin_ctzll(none);
                 none &= none - 1;
-                for (int x = threadIdx.x; x < SIZE; x += THREADS) {
+                for (int x = threadIdx.x; x < SIZE; x += NT) {
                     const int64_t to = ((int64_t)at * b.H + h) * SIZE + x;
                     a.fin[to] = a.init ? a.init[to] : 0.0f;
                 }
@@ -440,119 +451,114 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
         }
     }
     Chunks<REV> chunks(o, s0, s1);
-    Stage<DT, KD> sq, sk;
-    Stage<DT, VD> sv;
+    Stage<DT, KD, NT> sq, sk;
+    Stage<DT, VD, NT> sv;
     double decay = 0.0;
     auto load = [&](const Chunk &c) {
+        if (wave == 0) decay = lane < c.len ? log2_decay(b.decay(c.first + lane, h)) : 0.0;
         sq.load(a.q, h, c.first, c.len);
         sk.load(a.k, h, c.first, c.len);
         sv.load(a.v, h, c.first, c.len);
-        decay = wave == 0 && lane < c.len ? log2_decay(b.decay(c.first + lane, h)) : 0.0;
     };
-    auto put_dots = [&](const Chunk &c) {
-        if (threadIdx.x < c.len)
-            a.dot[(int64_t)(c.first + threadIdx.x) * b.H + h] =
-                (L.dots[0][threadIdx.x] + L.dots[1][threadIdx.x]) + (L.dots[2][threadIdx.x] + L.dots[3][threadIdx.x]);
+    auto put_dots = [&](int first, int len) {
+        if ((int)threadIdx.x < len) {
+            float sum = L.dots[0][threadIdx.x];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) sum += L.dots[w][threadIdx.x];
+            a.dot[(int64_t)(first + threadIdx.x) * b.H + h] = sum;
+        }
     };
-    f32x4 S[KD / 16][VT];
-    Chunk c = chunks.next(), before = {0, 0, 0, false, false, false, false};
-    if (c.len) load(c);
+    f32x4 S[KD / 16];
+    Chunk c = chunks.next();
+    int before_first = 0, before_len = 0, turn = 0;
+    if (c.len) {
+        load(c);
+        if (wave == 0) tick<REV>(L.clock[0], decay, a.in_scale, a.up_scale);
+    }
 #pragma unroll 1
     while (c.len) {
         const Chunk then = chunks.next();
+        const Clock &clock = L.clock[turn];
         lds_barrier();
-        if constexpr (DOT) put_dots(before);
+        if constexpr (DOT) put_dots(before_first, before_len);
         sq.store(L.q);
         sk.store(L.k);
         sv.store(L.v);
-        if (wave == 0) tick<REV>(L.clock, decay, a.in_scale, a.up_scale);
         lds_barrier();
         if (then.len) load(then);
         if (c.enter) {
             const float *from = c.open ? (a.init ? a.init + ((int64_t)c.seq * b.H + h) * SIZE : nullptr)
                                        : a.carry + ((int64_t)(REV ? seg + 1 : seg - 1) * b.H + h) * SIZE;
-            load_state<KD, VT>(S, from, a.sk, a.sv, wave);
+            load_state<KD>(S, from, a.sk, a.sv, wave);
         }
-        // weights of the pairs: wave w for its 16 tokens i, rows tokens j
-        {
-            float p[4][4];
-            const float wi = L.clock.whole[16 * wave + i], ri = L.clock.rest[16 * wave + i];
+        // weights of the pairs: columns 16 tokens i, rows 32 tokens j, an operand a wave (two of four waves' each)
+#pragma unroll 1
+        for (int f = wave; f < 8; f += NW) {
+            const int it = f >> 1, s = f & 1;
+            if (REV ? 2 * s + 1 < it : 2 * s > it) continue;      // no pairs there
+            f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-            for (int jt = 0; jt < 4; ++jt) {
+            for (int n = 0; n < KD / 32; ++n) {
+                u32x4 qq[NP];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[jt][r] = 0.0f;
-                if (REV ? jt >= wave : jt <= wave) {
-                    f32x4 st = {0, 0, 0, 0};
+                for (int p = 0; p < NP; ++p) qq[p] = row_operand(L.q, p, it, n);
 #pragma unroll
-                    for (int s = 0; s < KD / 32; ++s) {
-                        u32x4 kk[NP], qq[NP];
+                for (int t = 0; t < 2; ++t) {
+                    u32x4 kk[NP];
 #pragma unroll
-                        for (int n = 0; n < NP; ++n) kk[n] = row_operand(L.k, n, jt, s), qq[n] = row_operand(L.q, n, wave, s);
-                        pairs<NP, NP, 4>([&](int x, int y) { st = mma(kk[x], qq[y], st); });
-                    }
-                    const f32x4 wj = *reinterpret_cast<const f32x4 *>(&L.clock.whole[16 * jt + 4 * g]);
-                    const f32x4 rj = *reinterpret_cast<const f32x4 *>(&L.clock.rest[16 * jt + 4 * g]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int j = 16 * jt + 4 * g + r, ii = 16 * wave + i;
-                        const float x = REV ? (wj[r] - wi) + (rj[r] - ri) : (wi - wj[r]) + (ri - rj[r]);
-                        p[jt][r] = (REV ? j >= ii : j <= ii) ? st[r] * exp2_f(x) * a.pair_scale : 0.0f;
-                    }
+                    for (int p = 0; p < NP; ++p) kk[p] = row_operand(L.k, p, 2 * s + t, n);
+                    pairs<NP, NP, 4>([&](int x, int y) { st[t] = mma(kk[x], qq[y], st[t]); });
                 }
             }
+            const int ti = 16 * it + i;
+            const float wi = clock.whole[ti], ri = clock.rest[ti];
+            float x[8];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (REV ? 2 * s + 1 < wave : 2 * s > wave) continue;      // no pairs there
-                float x[8];
+            for (int t = 0; t < 2; ++t) {
+                const int j0 = 32 * s + 16 * t + 4 * g;
+                const f32x4 wj = *reinterpret_cast<const f32x4 *>(&clock.whole[j0]);
+                const f32x4 rj = *reinterpret_cast<const f32x4 *>(&clock.rest[j0]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = p[2 * s][r], x[4 + r] = p[2 * s + 1][r];
-                u32x4 part[PARTS];
-                split<PARTS>(x, part);
-#pragma unroll
-                for (int n = 0; n < PARTS; ++n) L.pair[wave][s][n][lane] = part[n];
+                for (int r = 0; r < 4; ++r) {
+                    const float y = REV ? (wj[r] - wi) + (rj[r] - ri) : (wi - wj[r]) + (ri - rj[r]);
+                    x[4 * t + r] = (REV ? j0 + r >= ti : j0 + r <= ti) ? st[t][r] * exp2_f(y) * a.pair_scale : 0.0f;
+                }
             }
+            u32x4 part[PARTS];
+            split<PARTS>(x, part);
+#pragma unroll
+            for (int n = 0; n < PARTS; ++n) L.pair[it][s][n][lane] = part[n];
         }
         lds_barrier();
         // from the state that enters: columns are tokens, rows value elements of the wave
-        f32x4 acc[VT][4];
+        f32x4 acc[4];
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-            for (int it = 0; it < 4; ++it) acc[vt][it] = f32x4{0, 0, 0, 0};
+        for (int it = 0; it < 4; ++it) acc[it] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < KD / 32; ++s) {
-            u32x4 part[VT][IN];
+            float x[8];
 #pragma unroll
-            for (int vt = 0; vt < VT; ++vt) {
-                float x[8];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = S[2 * s][vt][r], x[4 + r] = S[2 * s + 1][vt][r];
-                split<IN>(x, part[vt]);
-            }
+            for (int r = 0; r < 4; ++r) x[r] = S[2 * s][r], x[4 + r] = S[2 * s + 1][r];
+            u32x4 part[IN];
+            split<IN>(x, part);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 u32x4 qq[NP];
 #pragma unroll
-                for (int n = 0; n < NP; ++n) qq[n] = row_operand(L.q, n, it, s);
-#pragma unroll
-                for (int vt = 0; vt < VT; ++vt) pairs<IN, NP, IN>([&](int x, int y) { acc[vt][it] = mma(part[vt][x], qq[y], acc[vt][it]); });
+                for (int p = 0; p < NP; ++p) qq[p] = row_operand(L.q, p, it, s);
+                pairs<IN, NP, IN>([&](int x, int y) { acc[it] = mma(part[x], qq[y], acc[it]); });
             }
         }
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-            const float w = L.clock.in[16 * it + i];
-#pragma unroll
-            for (int vt = 0; vt < VT; ++vt) acc[vt][it] *= w;
+            acc[it] *= clock.in[16 * it + i];
             if constexpr (DOT) {
                 float sum = 0.0f;
                 if (16 * it + i < c.len) {
-                    const E *row = (const E *)a.e.p + (int64_t)(c.first + 16 * it + i) * a.e.row + (int64_t)h * a.e.head;
+                    const char *e = (const char *)a.e.p + 2 * ((int64_t)c.first * a.e.row + (int64_t)h * a.e.head);
+                    const E4 x = *reinterpret_cast<const E4 *>(e + 2 * ((16 * it + i) * (uint32_t)a.e.row + 16 * wave + 4 * g));
 #pragma unroll
-                    for (int vt = 0; vt < VT; ++vt) {
-                        const E4 e = *reinterpret_cast<const E4 *>(row + 16 * (wave * VT + vt) + 4 * g);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(acc[vt][it][r], (float)e[r], sum);
-                    }
+                    for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(acc[it][r], (float)x[r], sum);
                 }
                 sum = swap16_add(sum, sum);
                 sum = swap32_add(sum, sum);
@@ -560,8 +566,8 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
             }
         }
         // from the chunk's own tokens
-        u32x4 v[NP][VT][2];
-        value_operands<NP, VD, VT>(L.v, wave, v);
+        u32x4 v[NP][2];
+        value_operands(L.v, wave, v);
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -570,31 +576,34 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
                 u32x4 part[PARTS];
 #pragma unroll
                 for (int n = 0; n < PARTS; ++n) part[n] = L.pair[it][s][n][lane];
-#pragma unroll
-                for (int vt = 0; vt < VT; ++vt) pairs<NP, PARTS, 2>([&](int x, int y) { acc[vt][it] = mma(v[x][vt][s], part[y], acc[vt][it]); });
+                pairs<NP, PARTS, 2>([&](int x, int y) { acc[it] = mma(v[x][s], part[y], acc[it]); });
             }
+        {
+            char *out = (char *)a.out + 2 * (((int64_t)c.first * b.H + h) * VD);
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            if (16 * it + i >= c.len) continue;
-            E *row = (E *)a.out + ((int64_t)(c.first + 16 * it + i) * b.H + h) * VD;
-#pragma unroll
-            for (int vt = 0; vt < VT; ++vt) {
+            for (int it = 0; it < 4; ++it) {
+                if (16 * it + i >= c.len) continue;
                 E4 e;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) e[r] = (E)acc[vt][it][r];
-                *reinterpret_cast<E4 *>(row + 16 * (wave * VT + vt) + 4 * g) = e;
+                for (int r = 0; r < 4; ++r) e[r] = (E)acc[it][r];
+                *reinterpret_cast<E4 *>(out + 2 * ((16 * it + i) * (uint32_t)(b.H * VD) + 16 * wave + 4 * g)) = e;
             }
         }
-        if (!c.leave || (c.close && a.fin)) update<NP, KD, VT>(S, L.k, v, L.clock);
-        if (c.leave && c.close && a.fin) store_state<KD, VT>(S, a.fin + ((int64_t)c.seq * b.H + h) * SIZE, a.sk, a.sv, wave);
-        before = c;
+        if (!c.leave || (c.close && a.fin)) update<NP, KD>(S, L.k, v, clock);
+        if (c.leave && c.close && a.fin) store_state<KD>(S, a.fin + ((int64_t)c.seq * b.H + h) * SIZE, a.sk, a.sv, wave);
+        if (wave == 0 && then.len) tick<REV>(L.clock[turn ^ 1], decay, a.in_scale, a.up_scale);
+        before_first = c.first, before_len = c.len;
+        turn ^= 1;
         c = then;
     }
     if constexpr (DOT) {
         lds_barrier();
-        put_dots(before);
+        put_dots(before_first, before_len);
     }
 }
+
+// The second argument of launch bounds, waves a SIMD: two blocks on a CU where LDS holds them.
+template <int DT, int VD> constexpr int WAVES_A_SIMD = (PLANES<DT> == 1 ? 2 : 1) * WAVES<VD> / 4;
 
 // Tokens of a segment: short enough for `blocks` blocks (segments x heads) where the batch has the chunks for it.
 inline int segment(int64_t T, int64_t H, int64_t blocks, int64_t least) {

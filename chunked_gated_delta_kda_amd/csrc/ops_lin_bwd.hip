@@ -20,34 +20,32 @@ namespace {
 
 // What both directions add to their states, by blockIdx.z.
 template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS, 2) void lin_bwd_state_kernel(const Batch b, const Own x, const Own y) {
-    __shared__ Tile<PLANES<DT>, KD> k;
-    __shared__ Tile<PLANES<DT>, VD> v;
-    __shared__ Clock clock;
-    if (blockIdx.z == 0) own_state<DT, KD, VD, false>(b, x, k, v, clock);
-    else own_state<DT, KD, VD, true>(b, y, k, v, clock);
+__global__ __launch_bounds__(THREADS<VD>, WAVES<VD> / 2) void lin_bwd_state_kernel(const Batch b, const Own x, const Own y) {
+    __shared__ OwnLds<DT, KD, VD> lds;
+    if (blockIdx.z == 0) own_state<DT, KD, VD, false>(b, x, lds);
+    else own_state<DT, KD, VD, true>(b, y, lds);
 }
 
 template <int SIZE>
-__global__ __launch_bounds__(THREADS) void lin_bwd_join_kernel(const Batch b, float *x, const float *xf, float *y, const float *yf) {
+__global__ __launch_bounds__(JOIN_THREADS) void lin_bwd_join_kernel(const Batch b, float *x, const float *xf, float *y, const float *yf) {
     if (blockIdx.z == 0) join<SIZE>(b, x, xf, false);
     else join<SIZE>(b, y, yf, true);
 }
 
 template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS, PLANES<DT> == 1 ? 2 : 1) void lin_dq_kernel(const Batch b, const Walk a, int32_t *err) {
-    __shared__ WalkLds<DT, KD, VD, 2> lds;
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS);
+__global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_dq_kernel(const Batch b, const Walk a, int32_t *err) {
+    __shared__ WalkLds<DT, KD, VD> lds;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS<VD>);
     walk<DT, KD, VD, false, true>(b, a, lds);
 }
 template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS, PLANES<DT> == 1 ? 2 : 1) void lin_dv_kernel(const Batch b, const Walk a) {
-    __shared__ WalkLds<DT, KD, VD, 2> lds;
+__global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_dv_kernel(const Batch b, const Walk a) {
+    __shared__ WalkLds<DT, KD, VD> lds;
     walk<DT, KD, VD, true, false>(b, a, lds);
 }
 template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS, PLANES<DT> == 1 ? 2 : 1) void lin_dk_kernel(const Batch b, const Walk a) {
-    __shared__ WalkLds<DT, KD, VD, 2> lds;
+__global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_dk_kernel(const Batch b, const Walk a) {
+    __shared__ WalkLds<DT, KD, VD> lds;
     walk<DT, KD, VD, true, true>(b, a, lds);
 }
 
@@ -91,9 +89,11 @@ __device__ __forceinline__ float row_suffix(float x) {
     return x;
 }
 
+constexpr int DECAY_THREADS = 256;
+
 // A block takes a segment of one head, four chunks at a time, a wave each.
 template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS) void lin_decay_kernel(const Batch b, const Decays a) {
+__global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b, const Decays a) {
     constexpr int NP = PLANES<DT>, SIZE = KD * VD;
     __shared__ Clock clocks[4];
     __shared__ float part[4], border[4], sums[4][4];
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(THREADS) void lin_decay_kernel(const Batch b, const
             else if (a.init) x = a.init + ((int64_t)c.seq * b.H + h) * SIZE, y = a.d_init + ((int64_t)c.seq * b.H + h) * SIZE;
             float sum = 0.0f;
             if (x) {
-                for (int e = 4 * threadIdx.x; e < SIZE; e += 4 * THREADS) {
+                for (int e = 4 * threadIdx.x; e < SIZE; e += 4 * DECAY_THREADS) {
                     const f32x4 p = *reinterpret_cast<const f32x4 *>(x + e), q = *reinterpret_cast<const f32x4 *>(y + e);
                     sum += (p[0] * q[0] + p[1] * q[1]) + (p[2] * q[2] + p[3] * q[3]);
                 }
@@ -269,23 +269,23 @@ template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, con
     hipError_t e;
     if (p.segs > 1) {
         const Own ox = {k, v, a.initial_state, x, xf, 1.0f}, oy = {q, d, r.d_final_state, y, yf, a.scale};
-        lin_bwd_state_kernel<DT, KD, VD><<<dim3(grid.x, grid.y, 2), THREADS, 0, st>>>(b, ox, oy);
+        lin_bwd_state_kernel<DT, KD, VD><<<dim3(grid.x, grid.y, 2), THREADS<VD>, 0, st>>>(b, ox, oy);
         if ((e = hipGetLastError())) return e;
-        lin_bwd_join_kernel<KD * VD><<<dim3(KD * VD / THREADS, grid.y, 2), THREADS, 0, st>>>(b, x, xf, y, yf);
+        lin_bwd_join_kernel<KD * VD><<<dim3(KD * VD / JOIN_THREADS, grid.y, 2), JOIN_THREADS, 0, st>>>(b, x, xf, y, yf);
         if ((e = hipGetLastError())) return e;
     }
     // dq on X^T, dk on Y^T: their states' rows are value elements
     const Walk wq = {d, v, k, r.dq, x, a.initial_state, nullptr, 1, VD, a.scale, a.scale, 1.0f, q, u};
     const Walk wv = {k, q, d, r.dv, y, r.d_final_state, d_init, VD, 1, a.scale, 1.0f, a.scale, none, nullptr};
     const Walk wk = {v, d, q, r.dk, y, r.d_final_state, nullptr, 1, VD, a.scale, 1.0f, a.scale, k, w};
-    lin_dq_kernel<DT, VD, KD><<<grid, THREADS, 0, st>>>(b, wq, err);
+    lin_dq_kernel<DT, VD, KD><<<grid, THREADS<KD>, 0, st>>>(b, wq, err);
     if ((e = hipGetLastError())) return e;
-    lin_dv_kernel<DT, KD, VD><<<grid, THREADS, 0, st>>>(b, wv);
+    lin_dv_kernel<DT, KD, VD><<<grid, THREADS<VD>, 0, st>>>(b, wv);
     if ((e = hipGetLastError())) return e;
-    lin_dk_kernel<DT, VD, KD><<<grid, THREADS, 0, st>>>(b, wk);
+    lin_dk_kernel<DT, VD, KD><<<grid, THREADS<KD>, 0, st>>>(b, wk);
     if ((e = hipGetLastError())) return e;
     const Decays dec = {q, k, v, d, x, y, a.initial_state, d_init, u, w, a.g_per_head ? sums : r.dg, a.scale, a.g_per_head};
-    lin_decay_kernel<DT, KD, VD><<<grid, THREADS, 0, st>>>(b, dec);
+    lin_decay_kernel<DT, KD, VD><<<grid, DECAY_THREADS, 0, st>>>(b, dec);
     if ((e = hipGetLastError())) return e;
     if (a.g_per_head) {
         lin_decay_sum_kernel<<<dim3(grid.y), 64, 0, st>>>(sums, r.dg, p.segs, a.heads);

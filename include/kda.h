@@ -588,6 +588,9 @@ int kda_kv_read_fp4(const kda_kv_read_args *args, void *stream);
  * Linear attention with a decay for each head: KDA's recurrence without the delta rule's correction, with one decay
  * for all channels of a head.
  */
+/* Largest stride between tokens' rows (elements) of kda_lin_fwd and kda_lin_bwd. */
+#define KDA_LIN_MAX_STRIDE (1 << 24)
+
 typedef struct kda_lin_args {
     const void *q, *k;        /* [total_tokens, heads, key_dim]                               */
     const void *v;            /* [total_tokens, heads, value_dim]                             */
