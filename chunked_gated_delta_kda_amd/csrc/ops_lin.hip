@@ -95,7 +95,7 @@ template <int DT, int KD, int VD> hipError_t forward(const kda_lin_args &a, floa
         lin_join_kernel<KD * VD><<<dim3(KD * VD / JOIN_THREADS, (unsigned)a.heads), JOIN_THREADS, 0, st>>>(b, ws, factor);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    const Walk w = {q, k, v, a.out, ws, a.initial_state, a.final_state, VD, 1, a.scale, a.scale, 1.0f, {nullptr, 0, 0}, nullptr};
+    const Walk w = {q, k, v, a.out, ws, a.initial_state, a.final_state, a.scale, a.scale, 1.0f, {nullptr, 0, 0}, nullptr};
     lin_walk_kernel<DT, KD, VD><<<grid, THREADS<VD>, 0, st>>>(b, w, err);
     return hipGetLastError();
 }

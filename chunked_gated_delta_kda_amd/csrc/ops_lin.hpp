@@ -28,8 +28,6 @@ namespace lin {
 namespace {
 
 constexpr int C = 64;              // tokens of a chunk
-constexpr int PAD = 8;             // elements behind a row in LDS: rows 4 banks apart
-
 // A block has a wave for every 16 value columns, which holds those columns of the state.
 template <int VD> constexpr int WAVES = VD / 16;
 template <int VD> constexpr int THREADS = 64 * WAVES<VD>;
@@ -45,6 +43,9 @@ template <int DT> constexpr int PLANES = DT == KDA_DTYPE_BF16 ? 1 : 2;
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
+
+// Nothing is moved over this place: without such places reads are taken so far ahead that their registers spill.
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
 // 8 fp32 numbers as N bf16 numbers each: each the rounding of what those before it leave.
 template <int N> __device__ __forceinline__ void split(const float (&x)[8], u32x4 (&to)[N]) {
@@ -74,9 +75,30 @@ template <int A, int B, int MOST, class F> __device__ __forceinline__ void pairs
             if (a + b < MOST) f(a, b);
 }
 
-// One chunk of rows in LDS.
+// Memory through buffer descriptors: a base that is the same for the block, 32-bit offsets, and reads past `bytes` that give
+// zeros, writes that are dropped, so that short chunks need no branches.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr uint32_t OUTSIDE = 0xffffffffu;
+__device__ __forceinline__ const char *same(const void *p) {     // told to be the same in all lanes: kept in scalar registers
+    const uint64_t x = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+    return (const char *)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ Buffer buffer(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)same(p), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
+}
+__device__ __forceinline__ u32x4 read16(Buffer b, uint32_t at, uint32_t more = 0) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, __builtin_amdgcn_readfirstlane((int)more), 0));
+}
+
+// One chunk of rows in LDS, 16 bytes between them: LDS serves 256 bytes at once, and neither one 16-byte unit of 16 rows
+// (row_operand) nor halves of every fourth unit of 8 rows (key_operand) meet in a bank.
 template <int NP, int D> struct Tile {
-    uint16_t x[NP][C][D + PAD];
+    static constexpr int ROW = D + 8;
+    uint16_t x[NP][C * ROW];
+    __device__ __forceinline__ void put(int plane, int row, int unit, u32x4 e) {
+        *reinterpret_cast<u32x4 *>(&x[plane][row * ROW + 8 * unit]) = e;
+    }
 };
 
 // An input in one of the three roles: rows [T, H, D], contiguous elements.
@@ -84,26 +106,34 @@ struct Role {
     const void *p;
     int64_t row, head;       // strides, elements
 };
+// One head of it.
+struct Rows {
+    const char *p;
+    uint32_t row;            // bytes
+    __device__ __forceinline__ Rows(const Role &r, int h) : p(same((const char *)r.p + 2 * h * r.head)), row(2 * (uint32_t)r.row) {}
+    // from row `first` on, the last of `len` rows of D elements included
+    __device__ __forceinline__ Buffer from(int first, int len, int D) const {
+        return buffer(p + (uint64_t)(uint32_t)first * row, len ? (len - 1) * row + 2 * D : 0);
+    }
+};
 
 // Rows of a chunk on their way from memory to LDS, 8 elements of a row a time. NT: threads of the block. Offsets from
 // a chunk's first row fit 32 bits (strides are at most KDA_LIN_MAX_STRIDE).
 template <int DT, int D, int NT> struct Stage {
     static constexpr int N = C * D / 8 / NT, ROWS = NT / (D / 8);     // rows of a piece
     u32x4 r[N];
-    __device__ __forceinline__ void load(const Role &s, int h, int first, int len) {
-        const char *p = (const char *)s.p + 2 * ((int64_t)first * s.row + (int64_t)h * s.head);
-        const uint32_t row = threadIdx.x / (D / 8), at = 2 * (row * (uint32_t)s.row + 8 * (threadIdx.x % (D / 8)));
+    __device__ __forceinline__ void load(const Rows &s, int first, int len) {
+        const Buffer b = s.from(first, len, D);
+        const uint32_t row = threadIdx.x / (D / 8), at = row * s.row + 16 * (threadIdx.x % (D / 8));
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            r[n] = u32x4{0, 0, 0, 0};
-            if ((int)row + ROWS * n < len) r[n] = *reinterpret_cast<const u32x4 *>(p + 2 * ROWS * n * s.row + at);
-        }
+        for (int n = 0; n < N; ++n)      // (rows that lie over each other, strides of 0, are cut off as well)
+            r[n] = read16(b, (int)row + ROWS * n < len ? at : OUTSIDE, ROWS * n * s.row);
     }
     __device__ __forceinline__ void store(Tile<PLANES<DT>, D> &t) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int row = threadIdx.x / (D / 8) + ROWS * n, col = 8 * (threadIdx.x % (D / 8));
-            if constexpr (DT == KDA_DTYPE_BF16) *reinterpret_cast<u32x4 *>(&t.x[0][row][col]) = r[n];
+            const int row = threadIdx.x / (D / 8) + ROWS * n, q = threadIdx.x % (D / 8);
+            if constexpr (DT == KDA_DTYPE_BF16) t.put(0, row, q, r[n]);
             else {
                 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
                 const f16x8 e = __builtin_bit_cast(f16x8, r[n]);
@@ -112,33 +142,56 @@ template <int DT, int D, int NT> struct Stage {
                 for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
                 u32x4 part[2];
                 split<2>(v, part);
-                *reinterpret_cast<u32x4 *>(&t.x[0][row][col]) = part[0];
-                *reinterpret_cast<u32x4 *>(&t.x[1][row][col]) = part[1];
+                t.put(0, row, q, part[0]);
+                t.put(1, row, q, part[1]);
             }
         }
     }
 };
 
-// Operands of v_mfma_f32_16x16x32: a lane (i = lane & 15, g = lane >> 4) holds 8 numbers of row (or column) i. Their places in
-// the contraction are relabelled alike in both operands: slot 8 g + s is place 4 g + s for s < 4, 16 + 4 g + s - 4 else,
-// where a result (rows 4 g + r of column i) of two 16-row tiles leaves its numbers, so that results are operands as
-// they are.
-// of row 16 t + i, elements 32 s ..
+// Operands of v_mfma_f32_16x16x32: a lane (i = lane & 15, g = lane >> 4) holds 8 numbers of row (or column) i, places 8 g .. of the
+// contraction, which may be labelled at will as long as both operands agree. A result holds rows 4 g + r of column i; two
+// results of 16 rows each are an operand as they are, if their rows are labelled so:
+//  * tokens of two tiles of pairs: slot 8 g + s is token 4 g + s for s < 4, 16 + 4 g + s - 4 else (value_operand reads
+//    values in that order);
+//  * key elements of two tiles of a state: lane group g's rows 4 g .. + 3 of tiles 2 s and 2 s + 1 are the halves of unit
+//    s + K / 32 g of a key row (the first half in tile 2 s where g is even, in the other where it is odd: state_operand),
+//    which row_operand reads at once.
+template <int KD> __device__ __forceinline__ int key_element(int t, int g) { return 8 * ((t >> 1) + KD / 32 * g) + 4 * ((g ^ t) & 1); }
+
+// of row 16 t + i, units s + D / 32 g
 template <int NP, int D> __device__ __forceinline__ u32x4 row_operand(const Tile<NP, D> &m, int plane, int t, int s) {
     const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    const uint16_t *p = &m.x[plane][16 * t + i][32 * s + 4 * g];
-    const u32x2 a = *reinterpret_cast<const u32x2 *>(p), b = *reinterpret_cast<const u32x2 *>(p + 16);
-    return u32x4{a[0], a[1], b[0], b[1]};
+    return *reinterpret_cast<const u32x4 *>(&m.x[plane][(16 * t + i) * m.ROW + 8 * (s + D / 32 * g)]);
 }
-// of element 16 t + i, rows 32 s ..: a transposing read hands the 16 lanes of a row of 16 columns a column of 4 rows each
-template <int NP, int D> __device__ __forceinline__ u32x4 column_operand(const Tile<NP, D> &m, int plane, int t, int s) {
+
+// A transposing read hands the 16 lanes of a row of 16 columns (each lane's address: 4 columns of row lane / 4) a column of 4
+// rows each; two of them make an operand of rows 32 s .. of the tile.
+template <int NP, int D> __device__ __forceinline__ u32x4 turned(const uint16_t *p) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    const uint16_t *p = &m.x[plane][32 * s + 4 * g + (i >> 2)][16 * t + 4 * (i & 3)];
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * (D + PAD)));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * Tile<NP, D>::ROW));
     const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
     return u32x4{x[0], x[1], y[0], y[1]};
+}
+// of the key element that tile t has in row i, rows 32 s ..
+template <int NP, int D> __device__ __forceinline__ u32x4 key_operand(const Tile<NP, D> &m, int plane, int t, int s) {
+    const int i = threadIdx.x & 15, row = 4 * ((threadIdx.x & 63) >> 4) + (i >> 2);
+    return turned<NP, D>(&m.x[plane][(32 * s + row) * m.ROW + key_element<D>(t, i & 3)]);
+}
+// of value element 16 t + i, rows 32 s ..
+template <int NP, int D> __device__ __forceinline__ u32x4 value_operand(const Tile<NP, D> &m, int plane, int t, int s) {
+    const int i = threadIdx.x & 15, row = 4 * ((threadIdx.x & 63) >> 4) + (i >> 2);
+    return turned<NP, D>(&m.x[plane][(32 * s + row) * m.ROW + 16 * t + 4 * (i & 3)]);
+}
+// of the wave's column i of the state, key elements as row_operand(s) has them; before it is split
+template <int KD> __device__ __forceinline__ void state_operand(const f32x4 (&S)[KD / 16], int s, float (&x)[8]) {
+    const bool odd = threadIdx.x & 16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        x[r] = odd ? S[2 * s + 1][r] : S[2 * s][r];
+        x[4 + r] = odd ? S[2 * s][r] : S[2 * s + 1][r];
+    }
 }
 
 // What a chunk's tokens are multiplied by. Sums of decays are formed in 64 bits; G_i is kept as a whole number and
@@ -169,9 +222,11 @@ __device__ __forceinline__ double lane_of(double x, int lane) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// by one wave, lane t for token t: x, log2 of the token's decay, 0 past the chunk's end. Returns the chunk's sum.
-template <bool REV> __device__ __forceinline__ double tick(Clock &c, double x, float in_scale, float up_scale) {
+// by one wave, lane t for token t: its log decay, 0 past the chunk's end. Returns the sum of the chunk's, base 2. (The caller
+// loads g a chunk ahead: what it does with it before it calls would wait for the load.)
+template <bool REV> __device__ __forceinline__ double tick(Clock &c, float g, float in_scale, float up_scale) {
     const int lane = threadIdx.x & 63;
+    double x = log2_decay(g);
     x += row_shr<1>(x);
     x += row_shr<2>(x);
     x += row_shr<4>(x);
@@ -200,9 +255,9 @@ struct Chunk {
 
 template <bool REV> struct Chunks {
     Offsets o;
-    int s0, s1, at, seq, p0, p1;     // the part [p0, p1); at: the next chunk's first token (REV: the end of the rest)
+    int s0, s1, at, seq, begin, end, p0, p1;     // the sequence; the part [p0, p1); at: the next chunk's first token (REV: the end of the rest)
     bool fresh;
-    __device__ __forceinline__ Chunks(const Offsets &off, int a, int b) : o(off), s0(a), s1(b), at(REV ? b : a), seq(-1), p0(0), p1(0), fresh(true) {}
+    __device__ __forceinline__ Chunks(const Offsets &off, int a, int b) : o(off), s0(a), s1(b), at(REV ? b : a), seq(-1), begin(0), end(0), p0(0), p1(0), fresh(true) {}
     // the sequence of token t, next to the last one where that is so
     __device__ __forceinline__ int find(int t) const {
         if (seq >= 0) {
@@ -216,10 +271,11 @@ template <bool REV> struct Chunks {
         if (REV ? at <= s0 : at >= s1) return c;
         if (fresh) {
             const int t = REV ? at - 1 : at;
-            seq = find(t);
-            const int b = o.at(seq), e = o.at(seq + 1);
-            p0 = REV ? (b < s0 ? s0 : b > t ? t : b) : t;            // (clamped where offsets are out of order)
-            p1 = REV ? t + 1 : (e > s1 ? s1 : e <= t ? t + 1 : e);
+            seq = __builtin_amdgcn_readfirstlane(find(t));
+            begin = __builtin_amdgcn_readfirstlane(o.at(seq)), end = __builtin_amdgcn_readfirstlane(o.at(seq + 1));
+            const int b = begin, e = end;
+            p0 = __builtin_amdgcn_readfirstlane(REV ? (b < s0 ? s0 : b > t ? t : b) : t);            // (clamped where offsets are out of order)
+            p1 = __builtin_amdgcn_readfirstlane(REV ? t + 1 : (e > s1 ? s1 : e <= t ? t + 1 : e));
         }
         c.seq = seq;
         c.enter = fresh;
@@ -234,8 +290,11 @@ template <bool REV> struct Chunks {
             at += c.len;
             c.leave = at >= p1;
         }
+        // (scalars: told to be the same in all lanes)
+        at = __builtin_amdgcn_readfirstlane(at);
+        c.first = __builtin_amdgcn_readfirstlane(c.first), c.len = __builtin_amdgcn_readfirstlane(c.len);
         // (only the part at the segment's edge continues what lies beyond, whatever the offsets say)
-        const bool begins = o.at(seq) >= p0 || p0 != s0, ends = o.at(seq + 1) <= p1 || p1 != s1;
+        const bool begins = begin >= p0 || p0 != s0, ends = end <= p1 || p1 != s1;
         c.open = REV ? ends : begins;
         c.close = REV ? begins : ends;
         fresh = c.leave;
@@ -272,8 +331,9 @@ __device__ __forceinline__ void update(f32x4 (&S)[KD / 16], const Tile<NP, KD> &
         for (int kt = 0; kt < KD / 16; ++kt) {
             u32x4 row[NP];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) row[p] = column_operand(k, p, kt, s);
+            for (int p = 0; p < NP; ++p) row[p] = key_operand(k, p, kt, s);
             pairs<NP, 3, 3>([&](int p, int n) { S[kt] = mma(row[p], w[n], S[kt]); });
+            if (kt % 4 == 3) hold();
         }
     }
 }
@@ -282,23 +342,33 @@ template <int NP, int VD> __device__ __forceinline__ void value_operands(const T
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) to[p][s] = column_operand(v, p, wave, s);
+        for (int s = 0; s < 2; ++s) to[p][s] = value_operand(v, p, wave, s);
 }
 
-// A state [KD][VD] between memory (element (a, b) at a sk + b sv) and the wave's columns. p NULL: zeros.
-template <int KD> __device__ __forceinline__ void load_state(f32x4 (&S)[KD / 16], const float *p, int sk, int sv, int wave) {
-    const uint32_t at = 4 * ((threadIdx.x & 63) >> 4) * sk + (16 * wave + (threadIdx.x & 15)) * sv;
+// A state of KD x VD between memory and the wave's columns. TURNED: memory holds it as [VD][KD]. p NULL: zeros.
+template <int KD, int VD, bool TURNED> __device__ __forceinline__ void load_state(f32x4 (&S)[KD / 16], const float *p, int wave) {
+    const uint32_t i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    const Buffer b = buffer(p, p ? 4 * KD * VD : 0);
 #pragma unroll
-    for (int kt = 0; kt < KD / 16; ++kt)
+    for (int kt = 0; kt < KD / 16; ++kt) {
+        const uint32_t k = key_element<KD>(kt & 1, g);
+        if constexpr (TURNED) S[kt] = __builtin_bit_cast(f32x4, read16(b, 4 * ((16 * wave + i) * KD + k), 32 * (kt >> 1)));
+        else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[kt][r] = p ? (p + (16 * kt + r) * sk)[at] : 0.0f;
+            for (int r = 0; r < 4; ++r)
+                S[kt][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, 4 * (k * VD + 16 * wave + i), 4 * VD * (8 * (kt >> 1) + r), 0));
+        }
+    }
 }
-template <int KD> __device__ __forceinline__ void store_state(const f32x4 (&S)[KD / 16], float *p, int sk, int sv, int wave) {
-    const uint32_t at = 4 * ((threadIdx.x & 63) >> 4) * sk + (16 * wave + (threadIdx.x & 15)) * sv;
+template <int KD, int VD> __device__ __forceinline__ void store_state(const f32x4 (&S)[KD / 16], float *p, int wave) {
+    const uint32_t i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    const Buffer b = buffer(p, 4 * KD * VD);
 #pragma unroll
     for (int kt = 0; kt < KD / 16; ++kt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) (p + (16 * kt + r) * sk)[at] = S[kt][r];
+        for (int r = 0; r < 4; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[kt][r]), b, 4 * (key_element<KD>(kt & 1, g) * VD + 16 * wave + i),
+                                                  4 * VD * (8 * (kt >> 1) + r), 0);
 }
 
 // The batch and its segments.
@@ -308,7 +378,12 @@ struct Batch {
     int64_t g_row;          // 0 where they are [H]
     int N, T, H, seg, segs; // seg: tokens of a segment (a multiple of C); segs of them
     __device__ __forceinline__ Offsets offsets() const { return Offsets{cu, N, T}; }
-    __device__ __forceinline__ float decay(int t, int h) const { return g[(int64_t)t * g_row + h]; }
+    // lane t's, of token first + t; 0 from len on
+    __device__ __forceinline__ float decay(int first, int len, int h) const {
+        const uint32_t lane = threadIdx.x & 63, row = 4 * (uint32_t)g_row;
+        const Buffer b = buffer(g + (uint64_t)(uint32_t)first * (uint32_t)g_row + h, len ? (len - 1) * row + 4 : 0);
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (int)((int)lane < len ? lane * row : OUTSIDE), 0, 0));
+    }
 };
 
 // ---------------------------------------------------------------- segments' own states
@@ -331,14 +406,15 @@ template <int DT, int KD, int VD> struct OwnLds {
 
 template <int DT, int KD, int VD, bool REV> __device__ __forceinline__ void own_state(const Batch &b, const Own &a, OwnLds<DT, KD, VD> &L) {
     constexpr int NP = PLANES<DT>, NT = THREADS<VD>;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, seg = blockIdx.x, h = blockIdx.y;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), seg = blockIdx.x, h = blockIdx.y;
     const Offsets o = b.offsets();
     const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
     float *factor = a.factor + (int64_t)seg * b.H + h;
     // the part that goes on past the segment
     int p0 = s0, p1 = s1;
     bool open, on;
-    const int edge = REV ? s0 : s1 - 1, seq = o.find(edge), sb = o.at(seq), se = o.at(seq + 1);
+    const int edge = REV ? s0 : s1 - 1, seq = __builtin_amdgcn_readfirstlane(o.find(edge));
+    const int sb = __builtin_amdgcn_readfirstlane(o.at(seq)), se = __builtin_amdgcn_readfirstlane(o.at(seq + 1));
     if constexpr (REV) on = sb < s0, open = se <= s1, p1 = se < s1 ? (se <= s0 ? s0 + 1 : se) : s1;
     else on = se > s1, open = sb >= s0, p0 = sb > s0 ? (sb >= s1 ? s1 - 1 : sb) : s0;
     if (!on) {
@@ -346,16 +422,18 @@ template <int DT, int KD, int VD, bool REV> __device__ __forceinline__ void own_
         return;
     }
     f32x4 S[KD / 16];
-    load_state<KD>(S, open && a.init ? a.init + ((int64_t)seq * b.H + h) * (KD * VD) : nullptr, VD, 1, wave);
-    double sum = 0.0, g = 0.0;
+    load_state<KD, VD, false>(S, open && a.init ? a.init + ((int64_t)seq * b.H + h) * (KD * VD) : nullptr, wave);
+    double sum = 0.0;
+    float g = 0.0f;
     Stage<DT, KD, NT> sk;
     Stage<DT, VD, NT> sv;
+    const Rows rk(a.k, h), rv(a.v, h);
     const int count = (p1 - p0 + C - 1) / C;
     auto load = [&](int n) {
         const int first = p0 + C * (REV ? count - 1 - n : n), len = p1 - first < C ? p1 - first : C;
-        if (wave == 0) g = lane < len ? log2_decay(b.decay(first + lane, h)) : 0.0;
-        sk.load(a.k, h, first, len);
-        sv.load(a.v, h, first, len);
+        if (wave == 0) g = b.decay(first, len, h);
+        sk.load(rk, first, len);
+        sv.load(rv, first, len);
     };
     load(0);
     if (wave == 0) sum += tick<REV>(L.clock[0], g, 1.0f, a.up);
@@ -371,7 +449,7 @@ template <int DT, int KD, int VD, bool REV> __device__ __forceinline__ void own_
         update<NP, KD>(S, L.k, v, L.clock[n & 1]);
         if (wave == 0 && n + 1 < count) sum += tick<REV>(L.clock[(n + 1) & 1], g, 1.0f, a.up);
     }
-    store_state<KD>(S, a.state + ((int64_t)seg * b.H + h) * (KD * VD), VD, 1, wave);
+    store_state<KD, VD>(S, a.state + ((int64_t)seg * b.H + h) * (KD * VD), wave);
     if (threadIdx.x == 0) *factor = open ? -1.0f : exp2_f((float)sum);
 }
 
@@ -408,10 +486,9 @@ struct Walk {
     void *out;              // [T, H, VD], contiguous
     const float *carry;     // joined states [segs, H, KD, VD]
     const float *init;      // [N, H, KD, VD] or NULL: what enters a sequence
-    float *fin;             // what leaves it, or NULL
-    int sk, sv;             // strides of a state's elements in carry, init and fin
+    float *fin;             // what leaves it, or NULL (not with DOT, whose states lie turned in memory)
     float pair_scale, in_scale, up_scale;
-    Role e;                 // DOT: rows that the part of the result from the state that enters is multiplied with
+    Role e;                 // DOT: rows that the part of the result from the state that enters is multiplied with; states are [VD][KD]
     float *dot;             // DOT: [T, H]
 };
 
@@ -450,33 +527,38 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
             }
         }
     }
+    const Rows rq(a.q, h), rk(a.k, h), rv(a.v, h), re(a.e, h);
+    float *const dots = DOT ? a.dot + h : nullptr;
     Chunks<REV> chunks(o, s0, s1);
     Stage<DT, KD, NT> sq, sk;
     Stage<DT, VD, NT> sv;
-    double decay = 0.0;
+    float decay = 0.0f;
     auto load = [&](const Chunk &c) {
-        if (wave == 0) decay = lane < c.len ? log2_decay(b.decay(c.first + lane, h)) : 0.0;
-        sq.load(a.q, h, c.first, c.len);
-        sk.load(a.k, h, c.first, c.len);
-        sv.load(a.v, h, c.first, c.len);
+        if (wave == 0) decay = b.decay(c.first, c.len, h);
+        sq.load(rq, c.first, c.len);
+        sk.load(rk, c.first, c.len);
+        sv.load(rv, c.first, c.len);
     };
     auto put_dots = [&](int first, int len) {
         if ((int)threadIdx.x < len) {
             float sum = L.dots[0][threadIdx.x];
 #pragma unroll
             for (int w = 1; w < NW; ++w) sum += L.dots[w][threadIdx.x];
-            a.dot[(int64_t)(first + threadIdx.x) * b.H + h] = sum;
+            (dots + (uint64_t)(uint32_t)first * (uint32_t)b.H)[threadIdx.x * (uint32_t)b.H] = sum;
         }
     };
-    f32x4 S[KD / 16];
     Chunk c = chunks.next();
     int before_first = 0, before_len = 0, turn = 0;
-    if (c.len) {
-        load(c);
-        if (wave == 0) tick<REV>(L.clock[0], decay, a.in_scale, a.up_scale);
-    }
+    load(c);
+    if (wave == 0) tick<REV>(L.clock[0], decay, a.in_scale, a.up_scale);
 #pragma unroll 1
-    while (c.len) {
+    while (c.len) {      // a part
+        f32x4 S[KD / 16];
+        load_state<KD, VD, DOT>(S, c.open ? (a.init ? a.init + ((int64_t)c.seq * b.H + h) * SIZE : nullptr)
+                                          : a.carry + ((int64_t)(REV ? seg + 1 : seg - 1) * b.H + h) * SIZE, wave);
+        bool leave;
+#pragma unroll 1
+        do {
         const Chunk then = chunks.next();
         const Clock &clock = L.clock[turn];
         lds_barrier();
@@ -485,12 +567,7 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
         sk.store(L.k);
         sv.store(L.v);
         lds_barrier();
-        if (then.len) load(then);
-        if (c.enter) {
-            const float *from = c.open ? (a.init ? a.init + ((int64_t)c.seq * b.H + h) * SIZE : nullptr)
-                                       : a.carry + ((int64_t)(REV ? seg + 1 : seg - 1) * b.H + h) * SIZE;
-            load_state<KD>(S, from, a.sk, a.sv, wave);
-        }
+        load(then);
         // weights of the pairs: columns 16 tokens i, rows 32 tokens j, an operand a wave (two of four waves' each)
 #pragma unroll 1
         for (int f = wave; f < 8; f += NW) {
@@ -537,8 +614,7 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
 #pragma unroll
         for (int s = 0; s < KD / 32; ++s) {
             float x[8];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = S[2 * s][r], x[4 + r] = S[2 * s + 1][r];
+            state_operand<KD>(S, s, x);
             u32x4 part[IN];
             split<IN>(x, part);
 #pragma unroll
@@ -548,23 +624,24 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
                 for (int p = 0; p < NP; ++p) qq[p] = row_operand(L.q, p, it, s);
                 pairs<IN, NP, IN>([&](int x, int y) { acc[it] = mma(part[x], qq[y], acc[it]); });
             }
+            hold();
         }
+        Buffer e = buffer(nullptr, 0);
+        if constexpr (DOT) e = re.from(c.first, c.len, VD);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
             acc[it] *= clock.in[16 * it + i];
             if constexpr (DOT) {
                 float sum = 0.0f;
-                if (16 * it + i < c.len) {
-                    const char *e = (const char *)a.e.p + 2 * ((int64_t)c.first * a.e.row + (int64_t)h * a.e.head);
-                    const E4 x = *reinterpret_cast<const E4 *>(e + 2 * ((16 * it + i) * (uint32_t)a.e.row + 16 * wave + 4 * g));
+                const E4 x = __builtin_bit_cast(E4, __builtin_amdgcn_raw_buffer_load_b64(e, (16 * it + i) * re.row + 2 * (16 * wave + 4 * g), 0, 0));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(acc[it][r], (float)x[r], sum);
-                }
+                for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(acc[it][r], (float)x[r], sum);
                 sum = swap16_add(sum, sum);
                 sum = swap32_add(sum, sum);
                 if (g == 0) L.dots[wave][16 * it + i] = sum;
             }
         }
+        hold();
         // from the chunk's own tokens
         u32x4 v[NP][2];
         value_operands(L.v, wave, v);
@@ -578,23 +655,25 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
                 for (int n = 0; n < PARTS; ++n) part[n] = L.pair[it][s][n][lane];
                 pairs<NP, PARTS, 2>([&](int x, int y) { acc[it] = mma(v[x][s], part[y], acc[it]); });
             }
-        {
-            char *out = (char *)a.out + 2 * (((int64_t)c.first * b.H + h) * VD);
+        const uint32_t out_row = 2 * (uint32_t)(b.H * VD);
+        const Buffer out = buffer((char *)a.out + ((int64_t)c.first * b.H + h) * (2 * VD), (c.len - 1) * out_row + 2 * VD);
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                if (16 * it + i >= c.len) continue;
-                E4 e;
+        for (int it = 0; it < 4; ++it) {
+            E4 x;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) e[r] = (E)acc[it][r];
-                *reinterpret_cast<E4 *>(out + 2 * ((16 * it + i) * (uint32_t)(b.H * VD) + 16 * wave + 4 * g)) = e;
-            }
+            for (int r = 0; r < 4; ++r) x[r] = (E)acc[it][r];
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), out, (16 * it + i) * out_row + 2 * (16 * wave + 4 * g), 0, 0);
         }
-        if (!c.leave || (c.close && a.fin)) update<NP, KD>(S, L.k, v, clock);
-        if (c.leave && c.close && a.fin) store_state<KD>(S, a.fin + ((int64_t)c.seq * b.H + h) * SIZE, a.sk, a.sv, wave);
-        if (wave == 0 && then.len) tick<REV>(L.clock[turn ^ 1], decay, a.in_scale, a.up_scale);
+        hold();
+        leave = c.leave;
+        if (!leave || (c.close && a.fin)) update<NP, KD>(S, L.k, v, clock);
+        if constexpr (!DOT)
+            if (leave && c.close && a.fin) store_state<KD, VD>(S, a.fin + ((int64_t)c.seq * b.H + h) * SIZE, wave);
+        if (wave == 0) tick<REV>(L.clock[turn ^ 1], decay, a.in_scale, a.up_scale);
         before_first = c.first, before_len = c.len;
         turn ^= 1;
         c = then;
+        } while (!leave);
     }
     if constexpr (DOT) {
         lds_barrier();

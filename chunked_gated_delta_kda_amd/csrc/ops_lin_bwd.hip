@@ -137,7 +137,7 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
         const bool there = lane < own.len;
         const int64_t at = (int64_t)(own.first + lane) * b.H + h;
         const float u = there ? a.u[at] : 0.0f, w = there ? a.w[at] : 0.0f;
-        tick<false>(clock, there ? log2_decay(b.decay(own.first + lane, h)) : 0.0, 1.0f, 1.0f);
+        tick<false>(clock, b.decay(own.first, own.len, h), 1.0f, 1.0f);
         {
             const float su = wave_sum(u), sw = wave_sum(w), size = wave_sum(__builtin_fabsf(u));
             if (lane == 0) sums[wave][0] = su, sums[wave][1] = sw, sums[wave][2] = clock.total, sums[wave][3] = size;
@@ -275,9 +275,9 @@ template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, con
         if ((e = hipGetLastError())) return e;
     }
     // dq on X^T, dk on Y^T: their states' rows are value elements
-    const Walk wq = {d, v, k, r.dq, x, a.initial_state, nullptr, 1, VD, a.scale, a.scale, 1.0f, q, u};
-    const Walk wv = {k, q, d, r.dv, y, r.d_final_state, d_init, VD, 1, a.scale, 1.0f, a.scale, none, nullptr};
-    const Walk wk = {v, d, q, r.dk, y, r.d_final_state, nullptr, 1, VD, a.scale, 1.0f, a.scale, k, w};
+    const Walk wq = {d, v, k, r.dq, x, a.initial_state, nullptr, a.scale, a.scale, 1.0f, q, u};
+    const Walk wv = {k, q, d, r.dv, y, r.d_final_state, d_init, a.scale, 1.0f, a.scale, none, nullptr};
+    const Walk wk = {v, d, q, r.dk, y, r.d_final_state, nullptr, a.scale, 1.0f, a.scale, k, w};
     lin_dq_kernel<DT, VD, KD><<<grid, THREADS<KD>, 0, st>>>(b, wq, err);
     if ((e = hipGetLastError())) return e;
     lin_dv_kernel<DT, KD, VD><<<grid, THREADS<VD>, 0, st>>>(b, wv);
