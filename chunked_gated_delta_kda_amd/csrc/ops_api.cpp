@@ -445,11 +445,20 @@ int kda_attn_decode(const kda_attn_args *args, void *stream, void *workspace, si
     return ws.finish(launched(kda::ops::launch_attn_decode(a, (float *)ws.ptr(), kda::device_error_word(), st)));
 }
 
+size_t kda_attn_fp4_workspace_bytes(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width,
+                                    int32_t page_size) {
+    if (check_attn_sizes(num_seqs, q_heads, kv_heads, head_dim, table_width, page_size) != KDA_OK) return 0;
+    return kda::ops::attn_fp4_workspace(num_seqs, q_heads, kv_heads, head_dim, table_width, page_size);
+}
+
 int kda_attn_decode_fp4(const kda_attn_fp4_args *args, void *stream, void *workspace, size_t workspace_bytes) {
     if (!args) return KDA_ERR_NULL;
     const kda_attn_fp4_args &f = *args;
     const kda_attn_args &a = f.attn;
     if (const int rc = check_attn(a, 16)) return rc;
+    for (const int64_t s : {a.k_page_stride, a.k_token_stride, a.v_page_stride, a.v_token_stride, f.k_scale_page_stride,
+                            f.k_scale_token_stride, f.v_scale_page_stride, f.v_scale_token_stride})
+        if (s > UINT32_MAX) return KDA_ERR_SHAPE;
     const int64_t sb = a.head_dim / KDA_FP4_GROUP;
     const Scales sc[] = {{f.k_scale, f.k_scale_page_stride, f.k_scale_token_stride, f.k_scale_head_stride},
                          {f.v_scale, f.v_scale_page_stride, f.v_scale_token_stride, f.v_scale_head_stride}};
@@ -463,7 +472,8 @@ int kda_attn_decode_fp4(const kda_attn_fp4_args *args, void *stream, void *works
                        cache(sc[0].p, sc[0].page, sc[0].token, sc[0].head, sb), cache(sc[1].p, sc[1].page, sc[1].token, sc[1].head, sb)};
     if (attn_over(a, in, 4)) return KDA_ERR_ALIAS;
     hipStream_t st = (hipStream_t)stream;
-    Workspace ws(workspace, workspace_bytes, attn_need(a), st);
+    Workspace ws(workspace, workspace_bytes,
+                 kda::ops::attn_fp4_workspace(a.num_seqs, a.q_heads, a.kv_heads, a.head_dim, a.table_width, a.page_size), st);
     if (ws.status() != KDA_OK) return ws.status();
     return ws.finish(launched(kda::ops::launch_attn_decode_fp4(f, (float *)ws.ptr(), kda::device_error_word(), st)));
 }
@@ -496,7 +506,7 @@ int kda_kv_append(const kda_kv_args *args, void *stream) {
         for (const Scales &s : sc)
             if (const int rc = check_scales(s, sb)) return rc;
     if (!a.block_table || !a.seq_lens || (a.total_tokens > 0 && (!a.k || !a.v || (a.q && !a.q_out)))) return KDA_ERR_NULL;
-    if (!by16(a.k) || !by16(a.v) || !by16(a.q) || !by16(a.q_out)) return KDA_ERR_UNSUPPORTED;
+    if (!by16(a.k) || !by16(a.v) || !by16(a.q) || !by16(a.q_out) || !by16(a.rope)) return KDA_ERR_UNSUPPORTED;
     for (int i = 0; i < 2; ++i)
         if (!apart(caches[i], a.num_pages, a.page_size, a.kv_heads, row) || (four && !apart(sc[i], a.num_pages, a.page_size, a.kv_heads, sb)))
             return KDA_ERR_SHAPE;

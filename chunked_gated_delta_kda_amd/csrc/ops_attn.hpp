@@ -151,7 +151,7 @@ __device__ __forceinline__ bool find_work(const kda_attn_args &a, int slot, int 
 // three waves a SIMD). Measured on MI355X (us, 512 | 768 | 1024 | 1536): 1 x 65536 tokens, 32 heads over 8, 58.9 | 61.3 |
 // 61.8 | 65.8; 64 skewed sequences fp16, 32 heads over 4, 92.5 | 90.2 | 87.6 | 88.7: fewer blocks suit one long sequence (fewer
 // chunks to join), more of them skewed ones, and what lies between loses 4% and 3% to the best of each.
-constexpr int SPREAD = 768, MAX_PARTS = SPREAD + 1;
+constexpr int SPREAD = 768, MAX_SPREAD = 1024, MAX_PARTS = MAX_SPREAD + 1;
 
 // Joins the chunks of one (sequence, head), in their order, where there are several: threads take four
 // elements each, groups of threads every GROUPS-th chunk. 1 x 65536 tokens, 32 heads: 97 chunks in 6.8 us, two rounds
@@ -218,13 +218,16 @@ struct Plan {
     int spread, slots, min_chunk, tiles_h;
     bool join;
 };
-Plan plan(int64_t B, int64_t hq, int64_t hkv, int64_t width, int64_t page) {
+// run: blocks that run at once where that is more than SPREAD, or 0. Chunks of rests come on top of those that tokens are spread over, one
+// a sequence, so that they are taken off, but for three quarters of `run` that are always there.
+inline Plan plan(int64_t B, int64_t hq, int64_t hkv, int64_t width, int64_t page, int64_t run = 0) {
     Plan p;
     p.tiles_h = (int)ceil_div(hq / hkv, 16);
     const int64_t per = hkv * p.tiles_h;
     p.min_chunk = 2 * ROUND;
     const int64_t most = width * page;
-    const int64_t spread = ceil_div(SPREAD, per);
+    int64_t spread = ceil_div(SPREAD, per);
+    if (run / per - B > spread) spread = run / per - B;
     p.spread = (int)spread;
     p.join = most > p.min_chunk;
     // sum of ceil(len / chunk) <= spread + B, and no sequence has more than its table allows

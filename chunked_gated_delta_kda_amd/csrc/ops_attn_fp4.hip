@@ -31,11 +31,6 @@ template <int DT, int J> __device__ __forceinline__ uint32_t pair_of(uint32_t w,
     else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, J));
 }
 
-// Bytes of 32 tokens' rows (from the caches' bases).
-struct Places {
-    int64_t k[TILE], v[TILE];
-};
-
 template <int BYTES> struct Word;
 template <> struct Word<2> { using type = uint16_t; };
 template <> struct Word<4> { using type = uint32_t; };
@@ -45,18 +40,32 @@ template <> struct Word<8> { typedef uint32_t type __attribute__((ext_vector_typ
 __device__ __forceinline__ uint32_t at_exponent(uint32_t w, uint32_t b) { return __builtin_amdgcn_alignbit(w, w, 8 * b + 9); }
 
 template <int DT, int DH>
-__global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_attn_fp4_args f, float *acc_out, float *ml_out,
+__global__ __launch_bounds__(64 * WAVES, (DH == 256 ? 2 : 4)) void attn_fp4_chunk_kernel(const kda_attn_fp4_args f, float *acc_out, float *ml_out,
                                                                     int32_t *err, int spread, int min_chunk, int tiles_h) {
     using O = Ops<DT>;
     using E = typename O::E;
     constexpr int KW = DH / 32;      // words of codes in a lane's part of a key, each a step of 32 of the score's contraction
     constexpr int DV = DH / 16;      // elements of a lane in O^T's operand rows
     constexpr int VW = DV / 8 ? DV / 8 : 1;
+    constexpr int ROW = DH / 2;      // bytes of a row
+    constexpr int NV = TILE * ROW / 1024;      // 16-byte loads of a lane for a tile of values
     constexpr int SB = DH / 32;      // bytes of a row's scales
     constexpr int SW = SB / 4 ? SB / 4 : 1;
-    __shared__ Places places[WAVES][2];
-    __shared__ __attribute__((aligned(16))) uint32_t scales[WAVES][2][SW][TILE];
-    __shared__ float join[WAVES][16 * (DH + 4)];
+    // What a wave keeps while it walks its tokens, and q; at the end, the waves' results.
+    struct Own {
+        u32x4 values[TILE * ROW / 16];          // the tile of values
+        uint32_t scales[2][SW][TILE];           // of its keys and values
+        int64_t places[2][2 * TILE];            // of 32 keys' rows and 32 values', bytes from the caches' bases
+    };
+    struct Walking {
+        u32x4 q[KW][64];
+        Own own[WAVES];
+    };
+    union Lds {
+        Walking walking;
+        float join[WAVES][16 * (DH + 4)];
+    };
+    __shared__ Lds lds;
     __shared__ float stat[WAVES][16][2];
     const kda_attn_args &a = f.attn;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -74,42 +83,58 @@ __global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_at
     const int group = a.q_heads / a.kv_heads;
     const int heads = group - ht * 16 < 16 ? group - ht * 16 : 16;      // of this block
     const int head0 = kvh * group + ht * 16;
-    u32x4 q[KW];
-#pragma unroll
-    for (int k = 0; k < KW; ++k) {
-        q[k] = u32x4{0, 0, 0, 0};
+    // q's operands, kept in LDS: the registers are worth more. A negative scale turns q's signs over, so that the largest
+    // product is that of the largest score.
+    for (int k = wave; k < KW; k += WAVES) {
+        u32x4 q = {0, 0, 0, 0};
         if (i < heads)
-            q[k] = *reinterpret_cast<const u32x4 *>((const E *)a.q + seq * a.q_stride + (int64_t)(head0 + i) * a.q_head_stride +
-                                                    DH / 4 * g + 8 * k);
+            q = *reinterpret_cast<const u32x4 *>((const E *)a.q + seq * a.q_stride + (int64_t)(head0 + i) * a.q_head_stride +
+                                                 DH / 4 * g + 8 * k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] ^= a.scale < 0.0f ? 0x80008000u : 0u;
+        lds.walking.q[k][lane] = q;
     }
-    const float scale = a.scale * LOG2E_F;
+    __syncthreads();
+    const float scale = __builtin_fabsf(a.scale) * LOG2E_F;
     f32x4 acc[DV];
     const int32_t *table = a.block_table + (int64_t)seq * a.table_stride;
     const uint8_t *kc = (const uint8_t *)a.k_cache + (int64_t)kvh * a.k_head_stride;
     const uint8_t *vc = (const uint8_t *)a.v_cache + (int64_t)kvh * a.v_head_stride;
-    // this lane's side of the scales: the lower half of the wave keys, the upper one values
-    const uint8_t *sc_base = lane < 32 ? f.k_scale + (int64_t)kvh * f.k_scale_head_stride : f.v_scale + (int64_t)kvh * f.v_scale_head_stride;
-    const int64_t sc_page = lane < 32 ? f.k_scale_page_stride : f.v_scale_page_stride;
-    const int64_t sc_token = lane < 32 ? f.k_scale_token_stride : f.v_scale_token_stride;
-    Places *const R = places[wave];
-    auto &S = scales[wave];
+    // this lane's side: the lower half of the wave keys, the upper one values
+    const bool keys = lane < 32;
+    const uint8_t *sc_base = keys ? f.k_scale + (int64_t)kvh * f.k_scale_head_stride : f.v_scale + (int64_t)kvh * f.v_scale_head_stride;
+    const uint32_t to_page = (uint32_t)(keys ? a.k_page_stride : a.v_page_stride);
+    const uint32_t to_token = (uint32_t)(keys ? a.k_token_stride : a.v_token_stride);
+    const uint32_t sc_page = (uint32_t)(keys ? f.k_scale_page_stride : f.v_scale_page_stride);
+    const uint32_t sc_token = (uint32_t)(keys ? f.k_scale_token_stride : f.v_scale_token_stride);
+    auto &R = lds.walking.own[wave].places;
+    auto &S = lds.walking.own[wave].scales;
+    uint8_t *const tile = reinterpret_cast<uint8_t *>(lds.walking.own[wave].values);
     bool bad = false;
 
-    uint32_t kr[2][KW], vr[8][VW], sr[SW];
-    auto page_of = [&](int t0) {
-        const int t = t0 + (lane & 31), tc = t < end ? t : end - 1;
-        return table[tc / a.page_size];
+    uint32_t kr[2][KW], sr[SW];
+    u32x4 vq[NV];
+    // Every lane one token of a tile (the upper half of the wave repeats the lower): its page's place in the table and its own in
+    // the page, moved on by a round a time without a division.
+    struct Spot {
+        int page, at;
     };
-    // Every lane one token (the upper half of the wave repeats the lower): its page, checked, its row and its scales.
-    // Rows that are not there stand for finite numbers (scales of 1), which probabilities of 0 take away.
-    auto place = [&](int t0, int page, int turn) {
-        const int t = t0 + (lane & 31), tc = t < end ? t : end - 1;
-        const int at = tc - tc / a.page_size * a.page_size;
-        bool there = t < end;
+    const int whole_pages = ROUND / a.page_size, rest_of_round = ROUND - whole_pages * a.page_size;
+    auto next_of = [&](Spot s) {
+        s.page += whole_pages, s.at += rest_of_round;
+        if (s.at >= a.page_size) s.at -= a.page_size, ++s.page;
+        return s;
+    };
+    const int most = (end - 1) / a.page_size;       // the last page in use: those behind it are not read
+    auto page_of = [&](Spot s) { return table[s.page < most ? s.page : most]; };
+    // Its page, checked, its row and its scales. Rows that are not there stand for finite numbers (scales of 1), which
+    // probabilities of 0 take away.
+    auto place = [&](int t0, Spot s, int page, int turn) {
+        bool there = t0 + (lane & 31) < end;
         if (page < 0 || page >= a.num_pages) bad = true, there = false, page = 0;
-        if (lane < 32) R[turn].k[lane] = (int64_t)page * a.k_page_stride + (int64_t)at * a.k_token_stride;
-        else R[turn].v[lane - 32] = (int64_t)page * a.v_page_stride + (int64_t)at * a.v_token_stride;
-        const auto x = *reinterpret_cast<const typename Word<SB>::type *>(sc_base + (int64_t)page * sc_page + (int64_t)at * sc_token);
+        R[turn][lane] = (int64_t)((uint64_t)(uint32_t)page * to_page + (uint64_t)(uint32_t)s.at * to_token);
+        const uint8_t *from = sc_base + ((uint64_t)(uint32_t)page * sc_page + (uint64_t)(uint32_t)s.at * sc_token);
+        const auto x = *reinterpret_cast<const typename Word<SB>::type *>(from);
         if constexpr (SB == 8) sr[0] = there ? x[0] : 0x7f7f7f7fu, sr[1] = there ? x[1] : 0x7f7f7f7fu;
         else sr[0] = there ? x : 0x7f7f7f7fu;
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -120,7 +145,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_at
     auto load_k = [&](int turn) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint8_t *row = kc + R[turn].k[16 * h + i] + DH / 8 * g;
+            const uint8_t *row = kc + (R[turn][16 * h + i] + DH / 8 * g);
             if constexpr (KW == 2) {
                 const uint2 x = *reinterpret_cast<const uint2 *>(row);
                 kr[h][0] = x.x, kr[h][1] = x.y;
@@ -134,37 +159,44 @@ __global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_at
             }
         }
     };
+    // Values are loaded as whole lines (16 bytes a lane, 1 KiB at a time: loads of 4 bytes a lane for 4 tokens each wait in L1 for lines
+    // that the load before them asked for) and handed over through LDS, rows in the order in which lanes want them: row
+    // 4 s + g is token 4 g + s for s < 4, 16 + 4 g + s - 4 else.
     auto load_v = [&](int turn) {
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const int tok = (s < 4 ? 0 : 12) + 4 * g + s;
-            const uint8_t *row = vc + R[turn].v[tok] + DV / 2 * i;
-            const auto x = *reinterpret_cast<const typename Word<DV / 2>::type *>(row);
-            if constexpr (DV == 16) vr[s][0] = x[0], vr[s][1] = x[1];
-            else vr[s][0] = x;
+        for (int n = 0; n < NV; ++n) {
+            const int x = 16 * (64 * n + lane), row = x / ROW, s = row >> 2, tok = 4 * (row & 3) + (s < 4 ? 0 : 12) + s;
+            vq[n] = *reinterpret_cast<const u32x4 *>(vc + (R[turn][TILE + tok] + x % ROW));
         }
     };
 
 #pragma unroll
     for (int d = 0; d < DV; ++d) acc[d] = f32x4{0, 0, 0, 0};
-    float m = NEG_INF, l = 0.0f;
+    float m = NEG_INF, l = 0.0f;        // the largest product of q and k, before the scale
     int t0 = begin + wave * TILE, turn = 0, ahead = 0;
     uint32_t seen = 0;
+    Spot spot;
+    spot.page = (t0 + (lane & 31)) / a.page_size, spot.at = t0 + (lane & 31) - spot.page * a.page_size;
     if (t0 < end) {
-        seen = place(t0, page_of(t0), 0);
+        seen = place(t0, spot, page_of(spot), 0);
         load_k(0);
         load_v(0);
-        if (t0 + ROUND < end) ahead = page_of(t0 + ROUND);
+        spot = next_of(spot);
+        if (t0 + ROUND < end) ahead = page_of(spot);
     }
     for (; t0 < end; t0 += ROUND, turn ^= 1) {
         const bool more = t0 + ROUND < end;
         // this tile's scales, to the lanes that need them
 #pragma unroll
         for (int c = 0; c < SW; ++c) S[lane >> 5][c][lane & 31] = sr[c];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) *reinterpret_cast<u32x4 *>(tile + 16 * (64 * n + lane)) = vq[n];
         uint32_t then = 0;
         if (more) {
-            then = place(t0 + ROUND, ahead, turn ^ 1);
-            if (t0 + 2 * ROUND < end) ahead = page_of(t0 + 2 * ROUND);
+            then = place(t0 + ROUND, spot, ahead, turn ^ 1);
+            load_v(turn ^ 1);
+            spot = next_of(spot);
+            if (t0 + 2 * ROUND < end) ahead = page_of(spot);
         } else {
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
@@ -183,34 +215,40 @@ __global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_at
             for (int k = 0; k < KW; ++k) {
                 const uint32_t x = kr[h][k], s = ks[DH == 256 ? k / 4 : 0];
                 const u32x4 row = {pair_of<DT, 0>(x, s), pair_of<DT, 1>(x, s), pair_of<DT, 2>(x, s), pair_of<DT, 3>(x, s)};
-                st[h] = O::mma(row, q[k], st[h]);
+                st[h] = O::mma(row, lds.walking.q[k][lane], st[h]);
             }
         }
         if (more) load_k(turn ^ 1);
         // this lane's tokens: 4 g + j and 16 + 4 g + j
-        float sc[8], top = NEG_INF;
+        const bool all = seen == 0xffffffffu;
         const uint32_t mine = (seen >> (4 * g)) & 0xf000f;
+        if (!all) {
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const bool on = (mine >> ((s < 4 ? 0 : 12) + s)) & 1;
-            sc[s] = on ? st[s >> 2][s & 3] * scale : NEG_INF;
-            top = __builtin_fmaxf(top, sc[s]);
+            for (int s = 0; s < 8; ++s)
+                if (!((mine >> ((s < 4 ? 0 : 12) + s)) & 1)) st[s >> 2][s & 3] = NEG_INF;
         }
+        float top = NEG_INF;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) top = __builtin_fmaxf(top, st[s >> 2][s & 3]);
         const float mn = __builtin_fmaxf(m, column_max(top));
         if (__any(mn > m)) {
-            const float r = mn > m ? exp2_f(m - mn) : 1.0f;      // m may be -inf: 0
+            const float r = m == NEG_INF ? 0.0f : mn > m ? exp2_f((m - mn) * scale) : 1.0f;
             l *= r;
 #pragma unroll
             for (int d = 0; d < DV; ++d) acc[d] *= r;
             m = mn;
         }
-        const float ref = m == NEG_INF ? 0.0f : m;
+        const float ref = m == NEG_INF ? 0.0f : -m * scale;
         float p[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            p[s] = exp2_f(sc[s] - ref);
-            l += p[s];
+        for (int s = 0; s < 8; ++s) p[s] = exp2_f(__builtin_fmaf(st[s >> 2][s & 3], scale, ref));
+        if (!all) {         // (-infinity times a scale of 0 is NaN)
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (!((mine >> ((s < 4 ? 0 : 12) + s)) & 1)) p[s] = 0.0f;
         }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) l += p[s];
         u32x4 hi, lo;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -226,6 +264,13 @@ __global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_at
             const u32x4 y = *reinterpret_cast<const u32x4 *>(&S[1][grp >> 2][16 + 4 * g]);
 #pragma unroll
             for (int s = 0; s < 4; ++s) vs[s] = at_exponent(x[s], grp & 3), vs[4 + s] = at_exponent(y[s], grp & 3);
+        }
+        uint32_t vr[8][VW];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const auto x = *reinterpret_cast<const typename Word<DV / 2>::type *>(tile + (4 * s + g) * ROW + DV / 2 * i);
+            if constexpr (DV == 16) vr[s][0] = x[0], vr[s][1] = x[1];
+            else vr[s][0] = x;
         }
         auto product = [&](auto word, auto pr, int e) {      // elements 2 e and 2 e + 1
             uint32_t x[8];
@@ -255,11 +300,11 @@ __global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_at
             product(integral_constant<int, 1>{}, integral_constant<int, 2>{}, 6);
             product(integral_constant<int, 1>{}, integral_constant<int, 3>{}, 7);
         }
-        if (more) load_v(turn ^ 1);
         seen = then;
     }
     if (err && __any(bad) && lane == 0) atomicOr(err, KDA_DEVERR_PAGES);
     l = column_sum(l);
+    m = m == NEG_INF ? NEG_INF : m * scale;      // as a score, base 2
 
     // the waves' results, against the block's largest maximum
     if (g == 0) stat[wave][i][0] = m, stat[wave][i][1] = l;
@@ -275,14 +320,14 @@ __global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_at
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int d = 0; d < DV; ++d) join[wave][i * (DH + 4) + DV * (4 * g + j) + d] = acc[d][j] * r;
+        for (int d = 0; d < DV; ++d) lds.join[wave][i * (DH + 4) + DV * (4 * g + j) + d] = acc[d][j] * r;
     __syncthreads();
     const bool whole = w.whole;
     for (int x = threadIdx.x; x < heads * DH; x += 64 * WAVES) {
         const int h = x / DH, d = x - h * DH;
         float o = 0.0f;
 #pragma unroll
-        for (int v = 0; v < WAVES; ++v) o += join[v][h * (DH + 4) + d];
+        for (int v = 0; v < WAVES; ++v) o += lds.join[v][h * (DH + 4) + d];
         if (whole) {
             float hm = NEG_INF, hl = 0.0f;
 #pragma unroll
@@ -303,6 +348,10 @@ __global__ __launch_bounds__(64 * WAVES) void attn_fp4_chunk_kernel(const kda_at
     }
 }
 
+// Blocks that run at once at head dimension 128: four to each of 256 CUs.
+constexpr int RUN = 1024;
+static_assert(RUN <= MAX_SPREAD, "the join holds a weight for each chunk of a sequence");
+
 template <int DT, int DH>
 hipError_t run_fp4(const kda_attn_fp4_args &f, const Plan &p, float *acc, float *ml, int32_t *err, hipStream_t st) {
     const kda_attn_args &a = f.attn;
@@ -322,9 +371,14 @@ template <int DT> hipError_t run_fp4_dt(const kda_attn_fp4_args &f, const Plan &
 }  // namespace
 }  // namespace attn
 
+size_t attn_fp4_workspace(int64_t B, int64_t hq, int64_t hkv, int64_t dh, int64_t width, int64_t page) {
+    const attn::Plan p = attn::plan(B, hq, hkv, width, page, attn::RUN);
+    return p.join ? (size_t)p.slots * hq * (dh + 2) * sizeof(float) : 0;
+}
+
 hipError_t launch_attn_decode_fp4(const kda_attn_fp4_args &f, float *ws, int32_t *err, hipStream_t st) {
     const kda_attn_args &a = f.attn;
-    const attn::Plan p = attn::plan(a.num_seqs, a.q_heads, a.kv_heads, a.table_width, a.page_size);
+    const attn::Plan p = attn::plan(a.num_seqs, a.q_heads, a.kv_heads, a.table_width, a.page_size, attn::RUN);
     float *ml = ws ? ws + (size_t)p.slots * a.q_heads * a.head_dim : nullptr;
     if (a.dtype == KDA_DTYPE_BF16) return attn::run_fp4_dt<KDA_DTYPE_BF16>(f, p, ws, ml, err, st);
     return attn::run_fp4_dt<KDA_DTYPE_F16>(f, p, ws, ml, err, st);

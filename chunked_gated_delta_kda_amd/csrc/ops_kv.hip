@@ -62,13 +62,6 @@ __device__ __forceinline__ void check_batch(const Batch &b, int32_t *err) {
     if (bad) atomicOr(err, KDA_DEVERR_CU_SEQLENS);
 }
 
-template <int DT> __device__ __forceinline__ void load8(const void *p, int64_t at, float (&x)[8]) {
-    using E = typename Elem<DT>::type;
-    typedef E E8 __attribute__((ext_vector_type(8)));
-    const E8 r = *reinterpret_cast<const E8 *>((const E *)p + at);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)r[i];
-}
 template <int DT> __device__ __forceinline__ void store8(void *p, int64_t at, const float (&x)[8]) {
     using E = typename Elem<DT>::type;
     typedef E E8 __attribute__((ext_vector_type(8)));
@@ -78,58 +71,58 @@ template <int DT> __device__ __forceinline__ void store8(void *p, int64_t at, co
     *reinterpret_cast<E8 *>((E *)p + at) = r;
 }
 
-// How 8 elements of a head are rotated.
+template <int DT> using Row8 = typename Elem<DT>::type __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ u32x4 raw8(const void *p, int64_t at) { return *reinterpret_cast<const u32x4 *>((const uint16_t *)p + at); }
+
+// How 8 elements of a head are rotated: x_i c_i + y_i s_i with y the elements they are paired with, half a rotation away or
+// their neighbours, and the sign of either in s.
 struct Turn {
-    enum Kind { NONE, FIRST, SECOND, PAIRS } kind;      // FIRST, SECOND: of pairs (i, i + rot / 2)
-    int other;          // where the elements lie that they are paired with
-    float c[8], s[8];   // PAIRS: four of each
+    bool on;
+    int other;          // where the paired elements lie (their own place: neighbours)
+    float c[8], s[8];
 };
 
-__device__ __forceinline__ Turn turn_of(const kda_kv_args &a, int pos, int e) {
-    Turn r;
+__device__ __forceinline__ void turn_of(const kda_kv_args &a, int e, Turn &r) {
     const int d = 8 * e, half = a.rot_dim / 2;
-    r.other = d;
-    if (!a.rope || d >= a.rot_dim) {
-        r.kind = Turn::NONE;
-        return r;
-    }
+    r.on = a.rope && d < a.rot_dim;
+    r.other = !r.on || a.interleaved ? d : d < half ? d + half : d - half;
+}
+
+__device__ __forceinline__ void angles_of(const kda_kv_args &a, int pos, int d, Turn &r) {
+    const int half = a.rot_dim / 2;
     const float *row = a.rope + (int64_t)pos * a.rot_dim;
     if (a.interleaved) {
-        r.kind = Turn::PAIRS;
+        const f32x4 c = *reinterpret_cast<const f32x4 *>(row + d / 2), s = *reinterpret_cast<const f32x4 *>(row + half + d / 2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r.c[i] = row[d / 2 + i], r.s[i] = row[half + d / 2 + i];
-        return r;
-    }
-    r.kind = d < half ? Turn::FIRST : Turn::SECOND;
-    const int at = d < half ? d : d - half;
-    r.other = d < half ? d + half : d - half;
+        for (int i = 0; i < 8; ++i) r.c[i] = c[i / 2], r.s[i] = i & 1 ? s[i / 2] : -s[i / 2];
+    } else {
+        const int at = d < half ? d : d - half;
+        const float sign = d < half ? -1.0f : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.c[i] = row[at + i], r.s[i] = row[half + at + i];
-    return r;
-}
-
-// x c -+ y s. F double: rounded once from 64 bits (the products of a 16-bit and a 32-bit number are exact there), so that
-// which side of a border of the 4-bit codes a value falls on does not hang on the order of roundings.
-template <class F> __device__ __forceinline__ float turned(float x, float c, float y, float s) {
-    if constexpr (sizeof(F) == 8) return (float)__builtin_fma((F)x, (F)c, (F)y * (F)s);
-    else return __builtin_fmaf(x, c, y * s);
-}
-
-template <int DT, class F> __device__ __forceinline__ void rotated(const Turn &r, const void *p, int64_t row, int d, float (&x)[8]) {
-    load8<DT>(p, row + d, x);
-    if (r.kind == Turn::PAIRS) {
+        for (int n = 0; n < 2; ++n) {
+            const f32x4 c = *reinterpret_cast<const f32x4 *>(row + at + 4 * n), s = *reinterpret_cast<const f32x4 *>(row + half + at + 4 * n);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float u = x[2 * i], v = x[2 * i + 1];
-            x[2 * i] = turned<F>(u, r.c[i], -v, r.s[i]);
-            x[2 * i + 1] = turned<F>(v, r.c[i], u, r.s[i]);
+            for (int i = 0; i < 4; ++i) r.c[4 * n + i] = c[i], r.s[4 * n + i] = sign * s[i];
         }
-    } else if (r.kind != Turn::NONE) {
-        float y[8];
-        load8<DT>(p, row + r.other, y);
-        const float sign = r.kind == Turn::FIRST ? -1.0f : 1.0f;
+    }
+}
+
+// F double: rounded once from 64 bits (the products of a 16-bit and a 32-bit number are exact there), so that which side of
+// a border of the 4-bit codes a value falls on does not hang on the order of roundings.
+template <int DT, class F> __device__ __forceinline__ void rotated(bool on, bool neighbours, const Turn &r, u32x4 own, u32x4 other, float (&x)[8]) {
+    const Row8<DT> u = __builtin_bit_cast(Row8<DT>, own);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = turned<F>(x[i], r.c[i], sign * y[i], r.s[i]);
+    for (int i = 0; i < 8; ++i) x[i] = (float)u[i];
+    if (!on) return;
+    if (neighbours) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) other[i] = own[i] << 16 | own[i] >> 16;
+    }
+    const Row8<DT> v = __builtin_bit_cast(Row8<DT>, other);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(F) == 8) x[i] = (float)__builtin_fma((F)x[i], (F)r.c[i], (F)(float)v[i] * (F)r.s[i]);
+        else x[i] = __builtin_fmaf(x[i], r.c[i], (float)v[i] * r.s[i]);
     }
 }
 
@@ -165,7 +158,10 @@ template <int DT> __device__ __forceinline__ uint32_t to_fp4(const float (&x)[8]
     return e;
 }
 
-// A block takes one new token; its threads 8 elements of a head each, head after head: queries, keys, values.
+// A block takes one new token; its threads 8 elements of a head each, head after head: queries, keys, values. The rows
+// of AHEAD heads are asked for before the token's place is looked up: the look-ups (sequence, length, page, angles) wait
+// for one another, and the rows with them otherwise.
+constexpr int AHEAD = 3;
 template <int DT, int DH, bool FOUR>
 __global__ __launch_bounds__(THREADS) void kv_append_kernel(const kda_kv_args a, int32_t *err) {
     constexpr int LANES = DH / 8, HEADS = THREADS / LANES;      // of a head; heads at a time
@@ -173,6 +169,27 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(const kda_kv_args a,
     if (blockIdx.x == 0) check_batch(batch, err);
     const int t = blockIdx.x;
     if (t >= a.total_tokens) return;
+    const int e = threadIdx.x % LANES, d = 8 * e, slots = a.q_heads + 2 * a.kv_heads;
+    Turn turn;
+    turn_of(a, e, turn);
+    const bool neighbours = a.interleaved;
+    u32x4 own[AHEAD], other[AHEAD];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) {
+            const int h = h0 + n * HEADS;
+            if (h >= slots) continue;
+            const void *p = a.v;
+            int64_t row = t * a.v_stride + (h - a.q_heads - a.kv_heads) * a.v_head_stride;
+            int paired = d;
+            if (h < a.q_heads) p = a.q, row = t * a.q_stride + h * a.q_head_stride, paired = turn.other;
+            else if (h < a.q_heads + a.kv_heads) p = a.k, row = t * a.k_stride + (h - a.q_heads) * a.k_head_stride, paired = turn.other;
+            own[n] = raw8(p, row + d);
+            if (!neighbours) other[n] = raw8(p, row + paired);
+        }
+    };
+    const int first = threadIdx.x / LANES;
+    load(first);
     int seq, left, past;
     batch.find(t, seq, left, past);
     if (!left) return;
@@ -181,38 +198,42 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(const kda_kv_args a,
     const int64_t pos = (int64_t)len - left;
     int page = -1;
     const bool inside = len > 0 && pos >= 0 && pos < (int64_t)a.table_width * a.page_size && (!a.rope || pos < a.max_positions);
-    if (inside) page = a.block_table[(int64_t)seq * a.table_stride + pos / a.page_size];
+    if (inside) {
+        page = a.block_table[(int64_t)seq * a.table_stride + pos / a.page_size];
+        if (turn.on) angles_of(a, (int)pos, d, turn);
+    }
     if (page < 0 || page >= a.num_pages) {
         if (err && threadIdx.x == 0) atomicOr(err, KDA_DEVERR_PAGES);
         return;
     }
     const int at = (int)(pos % a.page_size);
-    const int e = threadIdx.x % LANES, d = 8 * e;
-    const Turn turn = turn_of(a, (int)pos, e);
-    const Turn none = {Turn::NONE, d, {}, {}};
-    const int slots = a.q_heads + 2 * a.kv_heads;
-    for (int h = threadIdx.x / LANES; h < slots; h += HEADS) {
-        float x[8];
-        if (h < a.q_heads) {
-            rotated<DT, float>(turn, a.q, (int64_t)t * a.q_stride + (int64_t)h * a.q_head_stride, d, x);
-            store8<DT>(a.q_out, ((int64_t)t * a.q_heads + h) * DH + d, x);
-            continue;
-        }
-        const bool key = h < a.q_heads + a.kv_heads;
-        const int c = h - a.q_heads - (key ? 0 : a.kv_heads);
-        if (key) rotated<DT, std::conditional_t<FOUR, double, float>>(turn, a.k, (int64_t)t * a.k_stride + (int64_t)c * a.k_head_stride, d, x);
-        else rotated<DT, float>(none, a.v, (int64_t)t * a.v_stride + (int64_t)c * a.v_head_stride, d, x);
-        void *cache = key ? a.k_cache : a.v_cache;
-        const int64_t row = key ? page * a.k_page_stride + at * a.k_token_stride + c * a.k_cache_head_stride
-                                : page * a.v_page_stride + at * a.v_token_stride + c * a.v_cache_head_stride;
-        if constexpr (!FOUR) store8<DT>(cache, row + d, x);
-        else {
-            uint32_t code;
-            const uint32_t s = to_fp4<DT>(x, code);
-            *reinterpret_cast<uint32_t *>((uint8_t *)cache + row + d / 2) = code;
-            uint8_t *scale = key ? a.k_scale + page * a.k_scale_page_stride + at * a.k_scale_token_stride + c * a.k_scale_head_stride
-                                 : a.v_scale + page * a.v_scale_page_stride + at * a.v_scale_token_stride + c * a.v_scale_head_stride;
-            if (e % 4 == 0) scale[e / 4] = (uint8_t)s;
+    for (int h0 = first; h0 < slots; h0 += AHEAD * HEADS) {
+        if (h0 != first) load(h0);
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) {
+            const int h = h0 + n * HEADS;
+            if (h >= slots) continue;
+            float x[8];
+            if (h < a.q_heads) {
+                rotated<DT, float>(turn.on, neighbours, turn, own[n], other[n], x);
+                store8<DT>(a.q_out, ((int64_t)t * a.q_heads + h) * DH + d, x);
+                continue;
+            }
+            const bool key = h < a.q_heads + a.kv_heads;
+            const int c = h - a.q_heads - (key ? 0 : a.kv_heads);
+            rotated<DT, std::conditional_t<FOUR, double, float>>(key && turn.on, neighbours, turn, own[n], other[n], x);
+            void *cache = key ? a.k_cache : a.v_cache;
+            const int64_t row = key ? page * a.k_page_stride + at * a.k_token_stride + c * a.k_cache_head_stride
+                                    : page * a.v_page_stride + at * a.v_token_stride + c * a.v_cache_head_stride;
+            if constexpr (!FOUR) store8<DT>(cache, row + d, x);
+            else {
+                uint32_t code;
+                const uint32_t s = to_fp4<DT>(x, code);
+                *reinterpret_cast<uint32_t *>((uint8_t *)cache + row + d / 2) = code;
+                uint8_t *scale = key ? a.k_scale + page * a.k_scale_page_stride + at * a.k_scale_token_stride + c * a.k_scale_head_stride
+                                     : a.v_scale + page * a.v_scale_page_stride + at * a.v_scale_token_stride + c * a.v_scale_head_stride;
+                if (e % 4 == 0) scale[e / 4] = (uint8_t)s;
+            }
         }
     }
 }

@@ -30,6 +30,7 @@ hipError_t launch_ssm_bwd(const kda_ssm_args &a, const kda_ssm_grads &g, float *
 size_t attn_workspace(int64_t B, int64_t hq, int64_t hkv, int64_t dh, int64_t width, int64_t page);
 hipError_t launch_attn_decode(const kda_attn_args &a, float *ws, int32_t *err, hipStream_t st);
 // the same over a cache of 4 bits (ops_attn_fp4.hip)
+size_t attn_fp4_workspace(int64_t B, int64_t hq, int64_t hkv, int64_t dh, int64_t width, int64_t page);
 hipError_t launch_attn_decode_fp4(const kda_attn_fp4_args &f, float *ws, int32_t *err, hipStream_t st);
 
 // writer of the paged cache, read-back of the 4-bit one (ops_kv.hip)

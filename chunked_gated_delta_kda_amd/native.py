@@ -23,7 +23,7 @@ EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_noalloc", "kda_workspace_bytes", "k
            "kda_ssm_fwd", "kda_ssm_workspace_bytes", "kda_ssm_decode",
            "kda_ssm_bwd", "kda_ssm_bwd_workspace_bytes",
            "kda_attn_decode", "kda_attn_workspace_bytes",
-           "kda_attn_decode_fp4", "kda_kv_append", "kda_kv_read_fp4",
+           "kda_attn_decode_fp4", "kda_attn_fp4_workspace_bytes", "kda_kv_append", "kda_kv_read_fp4",
            "kda_lin_fwd", "kda_lin_workspace_bytes", "kda_lin_decode", "kda_lin_bwd", "kda_lin_bwd_workspace_bytes",
            "kda_device_errors", "kda_status_string", "kda_version")
 #: KDA_DEVERR_* bits of the device error word
@@ -202,6 +202,8 @@ def load_library(path=LIB_PATH):
     lib.kda_attn_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_attn_decode_fp4.argtypes = [ctypes.POINTER(KdaAttnFp4Args), vp, vp, ctypes.c_size_t]
     lib.kda_attn_decode_fp4.restype = ctypes.c_int
+    lib.kda_attn_fp4_workspace_bytes.argtypes = [i32] * 6
+    lib.kda_attn_fp4_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_kv_append.argtypes = [ctypes.POINTER(KdaKvArgs), vp]
     lib.kda_kv_append.restype = ctypes.c_int
     lib.kda_kv_read_fp4.argtypes = [ctypes.POINTER(KdaKvReadArgs), vp]

@@ -170,7 +170,7 @@ def attn_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
             out = like(q, q.shape)
         if lse is None and return_lse:
             lse = like(q, (B, hq), torch.float32)
-        workspace, wp, wn = scratch(workspace, lib.kda_attn_workspace_bytes(B, hq, hkv, dh, width, page), q)
+        workspace, wp, wn = scratch(workspace, lib.kda_attn_fp4_workspace_bytes(B, hq, hkv, dh, width, page), q)
         args = native.KdaAttnFp4Args(native.KdaAttnArgs(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
             ptr(lse), *strides, B, hq, hkv, dh, pages, page, width, DTYPES[q.dtype],

@@ -80,6 +80,8 @@ def check_kv_append_args(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqle
         if rope.dim() != 2 or rope.shape[0] < 1 or rope.shape[1] % 16 or not 16 <= rope.shape[1] <= s.dh:
             raise ValueError(f"rope: expected fp32 [positions, rotated elements], a multiple of 16 up to {s.dh}, got {tuple(rope.shape)}")
         dense("rope", rope, torch.float32, rope.shape, dev)
+        if rope.data_ptr() % 16:
+            raise ValueError("rope: expected a base aligned to 16 bytes")
         s.positions, s.rot = rope.shape
     s.strides = strides + cache + scales + [table]
     return s

@@ -495,7 +495,7 @@ int kda_attn_decode(const kda_attn_args *args, void *stream, void *workspace, si
  * and head_dim / 32 bytes of scales, one for every KDA_FP4_GROUP elements: s stands for 2^(s - 127), 255 for
  * NaN. Codes are [num_pages, page_size, kv_heads, head_dim / 2], scales [num_pages, page_size, kv_heads, head_dim / 32],
  * rows contiguous, any other strides (in bytes): those of codes multiples of 16 on a base aligned to 16, those of
- * scales multiples of head_dim / 32 on a base aligned to that. Rows of one head that lie next to each other in a page
+ * scales multiples of head_dim / 32 on a base aligned to that; kda_attn_decode_fp4 takes page and token strides under 2^32. Rows of one head that lie next to each other in a page
  * ([num_pages, kv_heads, page_size, ..]) suit the memory best.
  */
 #define KDA_FP4_GROUP 32
@@ -510,9 +510,11 @@ typedef struct kda_attn_fp4_args {
 /*
  * kda_attn_decode_fp4 -- kda_attn_decode over a cache of 4 bits, in the arithmetic of a cache of q's type that holds the
  * values that the codes stand for (each of them is exact in bf16 and, between 2^-24 and 65504, in fp16: larger ones are
- * infinite there). Values that are not finite make their elements of the output infinite or NaN. Workspace, limits, errors and
- * the rest as kda_attn_decode; the workspace is of kda_attn_workspace_bytes() bytes.
+ * infinite there). Values that are not finite make their elements of the output infinite or NaN. Limits, errors and
+ * the rest as kda_attn_decode; the workspace is of kda_attn_fp4_workspace_bytes() bytes.
  */
+size_t kda_attn_fp4_workspace_bytes(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                    int32_t table_width, int32_t page_size);
 int kda_attn_decode_fp4(const kda_attn_fp4_args *args, void *stream, void *workspace, size_t workspace_bytes);
 
 typedef struct kda_kv_args {
@@ -556,8 +558,8 @@ typedef struct kda_kv_args {
  * seq_lens 0 is an empty slot: its rows are passed over. Rows that would lie before position 0 (n > L), past the
  * sequence's row of the table, past the table of rotations or on a page outside the cache are left out
  * (KDA_DEVERR_PAGES). Rows that are left out or padding leave q_out as it was. Two sequences whose table rows name one
- * page must not append to the same place of it. Rows of q, k, v and of a cache of dtype are read and written 16 bytes at a
- * time: bases aligned to 16 bytes, strides multiples of 8 elements, else KDA_ERR_UNSUPPORTED; rows of the caches must not
+ * page must not append to the same place of it. Rows of q, k, v, rope and of a cache of dtype are read and written 16 bytes
+ * at a time: bases aligned to 16 bytes, strides multiples of 8 elements, else KDA_ERR_UNSUPPORTED; rows of the caches must not
  * overlap (KDA_ERR_SHAPE). Captured calls stay right when lengths, pages, offsets and table entries change. Limits:
  * total_tokens <= 2^27, table_width * page_size <= 2^30, heads <= 65535.
  */

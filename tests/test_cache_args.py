@@ -175,7 +175,7 @@ def test_append_abi_refusals(lib, four):
     call = lambda **kw: lib.kda_kv_append(ctypes.byref(kv_args(four, **kw)), None)  # noqa: E731
     assert lib.kda_kv_append(None, None) == 1
     for kw in (dict(dtype=0), dict(dtype=3), dict(head_dim=96), dict(rot_dim=24), dict(rot_dim=0), dict(rot_dim=144),
-               dict(interleaved=2), dict(k_stride=260), dict(q_head_stride=4), dict(k=MB + 8), dict(q_out=4 * MB + 2),
+               dict(interleaved=2), dict(k_stride=260), dict(q_head_stride=4), dict(k=MB + 8), dict(q_out=4 * MB + 2), dict(rope=5 * MB + 4),
                dict(k_cache=16 * MB + 8), dict(v_token_stride=132)):
         assert call(**kw) == 3, kw
     for kw in (dict(num_seqs=0), dict(total_tokens=-1), dict(kv_heads=0), dict(q_heads=0), dict(q_heads=-1), dict(q_heads=65536),
@@ -219,13 +219,14 @@ def test_attn_fp4_abi_refusals(lib):
                dict(v_scale_token_stride=6)):
         assert call(**kw) == 3, kw
     for kw in (dict(num_seqs=0), dict(q_heads=7), dict(kv_heads=0), dict(num_pages=0), dict(table_width=0), dict(table_stride=63),
-               dict(k_head_stride=-16), dict(k_scale_page_stride=-4), dict(num_seqs=1 << 17)):
+               dict(k_head_stride=-16), dict(k_scale_page_stride=-4), dict(num_seqs=1 << 17), dict(k_page_stride=1 << 32),
+               dict(v_scale_token_stride=1 << 32)):
         assert call(**kw) == 2, kw
     for name in ("q", "k_cache", "v_cache", "block_table", "seq_lens", "out", "k_scale", "v_scale"):
         assert call(**{name: None}) == 1, name
     for kw in (dict(out=1 * MB), dict(out=16 * MB), dict(lse=50 * MB), dict(lse=49 * MB), dict(out=60 * MB), dict(lse=61 * MB)):
         assert call(**kw) == 7, kw
-    need = lib.kda_attn_workspace_bytes(3, 8, 2, 128, 64, 16)
+    need = lib.kda_attn_fp4_workspace_bytes(3, 8, 2, 128, 64, 16)
     assert need > 0 and call(n=need - 1) == 4
 
 
