@@ -238,7 +238,22 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(const kda_kv_args a,
     }
 }
 
-// A block takes TOKENS rows of the packed result.
+// Eight values of codes w times the scale s.
+template <int DT> __device__ __forceinline__ u32x4 values_of(uint32_t w, uint32_t scale) {
+    const float s = __uint_as_float(scale << 23);
+    if constexpr (DT == KDA_DTYPE_BF16)
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+    else
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3))};
+}
+
+// A block takes TOKENS rows of the packed result, their look-ups (sequence, page, codes) side by side.
 constexpr int TOKENS = 4;
 template <int DT, int DH>
 __global__ __launch_bounds__(THREADS) void kv_read_fp4_kernel(const kda_kv_read_args a, int32_t *err) {
@@ -246,41 +261,43 @@ __global__ __launch_bounds__(THREADS) void kv_read_fp4_kernel(const kda_kv_read_
     using E = typename Elem<DT>::type;
     const Batch batch = {a.cu_seqlens, a.num_seqs, a.total_tokens};
     if (blockIdx.x == 0) check_batch(batch, err);
-    const int e = threadIdx.x % LANES;
-    for (int t = blockIdx.x * TOKENS; t < a.total_tokens && t < (blockIdx.x + 1) * TOKENS; ++t) {
-        int seq, left, past;
-        batch.find(t, seq, left, past);
-        if (!left) continue;
-        int page = -1;
-        if (past < (int64_t)a.table_width * a.page_size) page = a.block_table[(int64_t)seq * a.table_stride + past / a.page_size];
-        const bool there = page >= 0 && page < a.num_pages;
-        if (!there && err && threadIdx.x == 0) atomicOr(err, KDA_DEVERR_PAGES);
-        const int at = past % a.page_size;
-        for (int h = threadIdx.x / LANES; h < 2 * a.kv_heads; h += HEADS) {
-            const bool key = h < a.kv_heads;
-            const int c = key ? h : h - a.kv_heads;
-            u32x4 r = {0, 0, 0, 0};
-            if (there) {
-                const uint8_t *cache = key ? (const uint8_t *)a.k_cache + page * a.k_page_stride + at * a.k_token_stride + c * a.k_head_stride
-                                           : (const uint8_t *)a.v_cache + page * a.v_page_stride + at * a.v_token_stride + c * a.v_head_stride;
-                const uint8_t *scale = key ? a.k_scale + page * a.k_scale_page_stride + at * a.k_scale_token_stride + c * a.k_scale_head_stride
-                                           : a.v_scale + page * a.v_scale_page_stride + at * a.v_scale_token_stride + c * a.v_scale_head_stride;
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(cache + 4 * e);
-                const float s = __uint_as_float((uint32_t)scale[e / 4] << 23);
-                if constexpr (DT == KDA_DTYPE_BF16)
-                    r = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
-                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
-                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
-                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
-                else
-                    r = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
-                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
-                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
-                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3))};
+    const int e = threadIdx.x % LANES, t0 = blockIdx.x * TOKENS;
+    int left[TOKENS], place[TOKENS], page[TOKENS];
+    bool there[TOKENS], bad = false;
+#pragma unroll
+    for (int n = 0; n < TOKENS; ++n) {
+        int seq = 0, past = 0;
+        left[n] = 0, page[n] = -1;
+        if (t0 + n < a.total_tokens) batch.find(t0 + n, seq, left[n], past);
+        if (left[n] && past < (int64_t)a.table_width * a.page_size) page[n] = a.block_table[(int64_t)seq * a.table_stride + past / a.page_size];
+        place[n] = past % a.page_size;
+    }
+#pragma unroll
+    for (int n = 0; n < TOKENS; ++n) {
+        there[n] = page[n] >= 0 && page[n] < a.num_pages;
+        bad |= left[n] && !there[n];
+    }
+    if (bad && err && threadIdx.x == 0) atomicOr(err, KDA_DEVERR_PAGES);
+    for (int h = threadIdx.x / LANES; h < 2 * a.kv_heads; h += HEADS) {
+        const bool key = h < a.kv_heads;
+        const int64_t c = key ? h : h - a.kv_heads;
+        const uint8_t *cache = key ? (const uint8_t *)a.k_cache + c * a.k_head_stride : (const uint8_t *)a.v_cache + c * a.v_head_stride;
+        const uint8_t *scale = key ? a.k_scale + c * a.k_scale_head_stride : a.v_scale + c * a.v_scale_head_stride;
+        const int64_t to_page = key ? a.k_page_stride : a.v_page_stride, to_token = key ? a.k_token_stride : a.v_token_stride;
+        const int64_t sc_page = key ? a.k_scale_page_stride : a.v_scale_page_stride, sc_token = key ? a.k_scale_token_stride : a.v_scale_token_stride;
+        uint32_t w[TOKENS], s[TOKENS];
+#pragma unroll
+        for (int n = 0; n < TOKENS; ++n) {
+            w[n] = s[n] = 0;
+            if (there[n]) {
+                w[n] = *reinterpret_cast<const uint32_t *>(cache + page[n] * to_page + place[n] * to_token + 4 * e);
+                s[n] = scale[page[n] * sc_page + place[n] * sc_token + e / 4];
             }
-            E *to = (E *)(key ? a.k : a.v) + ((int64_t)t * a.kv_heads + c) * DH + 8 * e;
-            *reinterpret_cast<u32x4 *>(to) = r;
         }
+        E *to = (E *)(key ? a.k : a.v) + ((int64_t)t0 * a.kv_heads + c) * DH + 8 * e;
+#pragma unroll
+        for (int n = 0; n < TOKENS; ++n)
+            if (left[n]) *reinterpret_cast<u32x4 *>(to + (int64_t)n * a.kv_heads * DH) = values_of<DT>(w[n], s[n]);
     }
 }
 
