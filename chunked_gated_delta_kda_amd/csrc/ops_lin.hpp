@@ -47,20 +47,24 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // Nothing is moved over this place: without such places reads are taken so far ahead that their registers spill.
 __device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
+// Two fp32 numbers rounded to bf16, in one word.
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const f32x2 x = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+}
+
 // 8 fp32 numbers as N bf16 numbers each: each the rounding of what those before it leave.
 template <int N> __device__ __forceinline__ void split(const float (&x)[8], u32x4 (&to)[N]) {
-    float r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = x[i];
+    for (int i = 0; i < 4; ++i) {
+        float a = x[2 * i], b = x[2 * i + 1];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        bf16x8 h;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = (__bf16)r[i];
-        to[n] = __builtin_bit_cast(u32x4, h);
-        if (n + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] -= (float)h[i];
+        for (int n = 0; n < N; ++n) {
+            const uint32_t w = pack(a, b);
+            to[n][i] = w;
+            if (n + 1 < N) a -= __uint_as_float(w << 16), b -= __uint_as_float(w & 0xffff0000u);
         }
     }
 }
@@ -91,13 +95,16 @@ __device__ __forceinline__ u32x4 read16(Buffer b, uint32_t at, uint32_t more = 0
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, __builtin_amdgcn_readfirstlane((int)more), 0));
 }
 
-// One chunk of rows in LDS, 16 bytes between them: LDS serves 256 bytes at once, and neither one 16-byte unit of 16 rows
-// (row_operand) nor halves of every fourth unit of 8 rows (key_operand) meet in a bank.
+// One chunk of rows in LDS. LDS serves 256 bytes at once; 16-byte reads of 64 lanes go in groups of lanes 0-3, 12-15, 20-27
+// and the like, which are units of 8 rows in one lane group g and of the other 8 in its neighbour (row_operand), transposing
+// ones in halves of the wave, halves of four units of 8 rows (key_operand). 16 bytes between rows and 64 more
+// between every four keep both from meeting in a bank at 128 columns.
 template <int NP, int D> struct Tile {
-    static constexpr int ROW = D + 8;
-    uint16_t x[NP][C * ROW];
+    static constexpr int ROW = D + 8, FOUR = 4 * ROW + (D == 128 ? 32 : 0);      // elements of a row, of four
+    uint16_t x[NP][C / 4 * FOUR];
+    static __device__ __forceinline__ int at(int row) { return (row >> 2) * FOUR + (row & 3) * ROW; }
     __device__ __forceinline__ void put(int plane, int row, int unit, u32x4 e) {
-        *reinterpret_cast<u32x4 *>(&x[plane][row * ROW + 8 * unit]) = e;
+        *reinterpret_cast<u32x4 *>(&x[plane][at(row) + 8 * unit]) = e;
     }
 };
 
@@ -155,14 +162,14 @@ template <int DT, int D, int NT> struct Stage {
 //  * tokens of two tiles of pairs: slot 8 g + s is token 4 g + s for s < 4, 16 + 4 g + s - 4 else (value_operand reads
 //    values in that order);
 //  * key elements of two tiles of a state: lane group g's rows 4 g .. + 3 of tiles 2 s and 2 s + 1 are the halves of unit
-//    s + K / 32 g of a key row (the first half in tile 2 s where g is even, in the other where it is odd: state_operand),
+//    s + K / 32 g of a key row (the first half in tile 2 s where g < 2, in the other elsewhere: state_operand),
 //    which row_operand reads at once.
-template <int KD> __device__ __forceinline__ int key_element(int t, int g) { return 8 * ((t >> 1) + KD / 32 * g) + 4 * ((g ^ t) & 1); }
+template <int KD> __device__ __forceinline__ int key_element(int t, int g) { return 8 * ((t >> 1) + KD / 32 * g) + 4 * ((g >> 1 ^ t) & 1); }
 
 // of row 16 t + i, units s + D / 32 g
 template <int NP, int D> __device__ __forceinline__ u32x4 row_operand(const Tile<NP, D> &m, int plane, int t, int s) {
     const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    return *reinterpret_cast<const u32x4 *>(&m.x[plane][(16 * t + i) * m.ROW + 8 * (s + D / 32 * g)]);
+    return *reinterpret_cast<const u32x4 *>(&m.x[plane][m.at(i) + 4 * t * m.FOUR + 8 * (s + D / 32 * g)]);
 }
 
 // A transposing read hands the 16 lanes of a row of 16 columns (each lane's address: 4 columns of row lane / 4) a column of 4
@@ -170,23 +177,23 @@ template <int NP, int D> __device__ __forceinline__ u32x4 row_operand(const Tile
 template <int NP, int D> __device__ __forceinline__ u32x4 turned(const uint16_t *p) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * Tile<NP, D>::ROW));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * Tile<NP, D>::FOUR));
     const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
     return u32x4{x[0], x[1], y[0], y[1]};
 }
 // of the key element that tile t has in row i, rows 32 s ..
 template <int NP, int D> __device__ __forceinline__ u32x4 key_operand(const Tile<NP, D> &m, int plane, int t, int s) {
     const int i = threadIdx.x & 15, row = 4 * ((threadIdx.x & 63) >> 4) + (i >> 2);
-    return turned<NP, D>(&m.x[plane][(32 * s + row) * m.ROW + key_element<D>(t, i & 3)]);
+    return turned<NP, D>(&m.x[plane][m.at(row) + 8 * s * m.FOUR + key_element<D>(t, i & 3)]);
 }
 // of value element 16 t + i, rows 32 s ..
 template <int NP, int D> __device__ __forceinline__ u32x4 value_operand(const Tile<NP, D> &m, int plane, int t, int s) {
     const int i = threadIdx.x & 15, row = 4 * ((threadIdx.x & 63) >> 4) + (i >> 2);
-    return turned<NP, D>(&m.x[plane][(32 * s + row) * m.ROW + 16 * t + 4 * (i & 3)]);
+    return turned<NP, D>(&m.x[plane][m.at(row) + 8 * s * m.FOUR + 16 * t + 4 * (i & 3)]);
 }
 // of the wave's column i of the state, key elements as row_operand(s) has them; before it is split
 template <int KD> __device__ __forceinline__ void state_operand(const f32x4 (&S)[KD / 16], int s, float (&x)[8]) {
-    const bool odd = threadIdx.x & 16;
+    const bool odd = threadIdx.x & 32;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         x[r] = odd ? S[2 * s + 1][r] : S[2 * s][r];
