@@ -96,9 +96,8 @@ __device__ __forceinline__ u32x4 read16(Buffer b, uint32_t at, uint32_t more = 0
 }
 
 // One chunk of rows in LDS. LDS serves 256 bytes at once; 16-byte reads of 64 lanes go in groups of lanes 0-3, 12-15, 20-27
-// and the like, which are units of 8 rows in one lane group g and of the other 8 in its neighbour (row_operand), transposing
-// ones in halves of the wave, halves of four units of 8 rows (key_operand). 16 bytes between rows and 64 more
-// between every four keep both from meeting in a bank at 128 columns.
+// and the like, which are units of 8 rows in one lane group g and of the other 8 in its neighbour (row_operand): 16 bytes
+// between rows and 64 more between every four keep them from meeting in a bank at 128 columns.
 template <int NP, int D> struct Tile {
     static constexpr int ROW = D + 8, FOUR = 4 * ROW + (D == 128 ? 32 : 0);      // elements of a row, of four
     uint16_t x[NP][C / 4 * FOUR];
@@ -162,9 +161,8 @@ template <int DT, int D, int NT> struct Stage {
 //  * tokens of two tiles of pairs: slot 8 g + s is token 4 g + s for s < 4, 16 + 4 g + s - 4 else (value_operand reads
 //    values in that order);
 //  * key elements of two tiles of a state: lane group g's rows 4 g .. + 3 of tiles 2 s and 2 s + 1 are the halves of unit
-//    s + K / 32 g of a key row (the first half in tile 2 s where g < 2, in the other elsewhere: state_operand),
-//    which row_operand reads at once.
-template <int KD> __device__ __forceinline__ int key_element(int t, int g) { return 8 * ((t >> 1) + KD / 32 * g) + 4 * ((g >> 1 ^ t) & 1); }
+//    s + K / 32 g of a key row, which row_operand reads at once.
+template <int KD> __device__ __forceinline__ int key_element(int t, int g) { return 8 * ((t >> 1) + KD / 32 * g) + 4 * (t & 1); }
 
 // of row 16 t + i, units s + D / 32 g
 template <int NP, int D> __device__ __forceinline__ u32x4 row_operand(const Tile<NP, D> &m, int plane, int t, int s) {
@@ -191,16 +189,6 @@ template <int NP, int D> __device__ __forceinline__ u32x4 value_operand(const Ti
     const int i = threadIdx.x & 15, row = 4 * ((threadIdx.x & 63) >> 4) + (i >> 2);
     return turned<NP, D>(&m.x[plane][m.at(row) + 8 * s * m.FOUR + 16 * t + 4 * (i & 3)]);
 }
-// of the wave's column i of the state, key elements as row_operand(s) has them; before it is split
-template <int KD> __device__ __forceinline__ void state_operand(const f32x4 (&S)[KD / 16], int s, float (&x)[8]) {
-    const bool odd = threadIdx.x & 32;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        x[r] = odd ? S[2 * s + 1][r] : S[2 * s][r];
-        x[4 + r] = odd ? S[2 * s][r] : S[2 * s + 1][r];
-    }
-}
-
 // What a chunk's tokens are multiplied by. Sums of decays are formed in 64 bits; G_i is kept as a whole number and
 // a rest of at most 1/2 (base 2), so that differences lose nothing where the sums are large.
 struct __attribute__((aligned(16))) Clock {
@@ -309,39 +297,70 @@ template <bool REV> struct Chunks {
     }
 };
 
-// S <- total S + sum_j k_j (up_j v_j)^T over a chunk, for the wave's columns. v's operands as the second product wants them.
-template <int NP, int KD>
-__device__ __forceinline__ void update(f32x4 (&S)[KD / 16], const Tile<NP, KD> &k, const u32x4 (&v)[NP][2], const Clock &clock) {
+// up_j v_j of the wave's column, tokens 32 s ..; v's operands as the second product wants them
+template <int NP> __device__ __forceinline__ void weighted(const u32x4 (&v)[NP][2], const Clock &clock, int s, float (&x)[8]) {
     const int g = (threadIdx.x & 63) >> 4;
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(&clock.up[32 * s + 4 * g]);
+    const f32x4 b = *reinterpret_cast<const f32x4 *>(&clock.up[32 * s + 16 + 4 * g]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float e = 0.0f;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const uint32_t word = v[p][s][i / 2];
+            const float f = __uint_as_float(i & 1 ? word & 0xffff0000u : word << 16);
+            e = p ? e + f : f;
+        }
+        x[i] = e * (i < 4 ? a[i & 3] : b[i & 3]);
+    }
+}
+// S += sum_j k_j w_j^T for those pairs of parts p of k and n of w that take(p, n) names, w's tokens 32 s ..
+template <int NP, int KD, int N, class F>
+__device__ __forceinline__ void add_products(f32x4 (&S)[KD / 16], const Tile<NP, KD> &k, const u32x4 (&w)[N], int s, F take) {
+#pragma unroll
+    for (int kt = 0; kt < KD / 16; kt += 2) {
+        u32x4 row[2][NP];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) row[t][p] = key_operand(k, p, kt + t, s);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (take(p, n)) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) S[kt + t] = mma(row[t][p], w[n], S[kt + t]);
+                }
+        hold();
+    }
+}
+// S <- total S + sum_j k_j (up_j v_j)^T over a chunk, for the wave's columns, up_j v_j in N parts
+template <int NP, int KD, int N>
+__device__ __forceinline__ void update(f32x4 (&S)[KD / 16], const Tile<NP, KD> &k, const u32x4 (&v)[NP][2], const Clock &clock) {
     const float total = clock.total;
 #pragma unroll
     for (int kt = 0; kt < KD / 16; ++kt) S[kt] *= total;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const f32x4 a = *reinterpret_cast<const f32x4 *>(&clock.up[32 * s + 4 * g]);
-        const f32x4 b = *reinterpret_cast<const f32x4 *>(&clock.up[32 * s + 16 + 4 * g]);
         float x[8];
+        weighted<NP>(v, clock, s, x);
+        u32x4 w[N];
+        split<N>(x, w);
+        add_products<NP, KD>(S, k, w, s, [](int p, int n) { return p + n < N; });
+    }
+}
+// the third part of those sums, where two have been taken (a pass of its own, for a few chunks: its registers are not held
+// through the first)
+template <int NP, int KD>
+__device__ __forceinline__ void refine(f32x4 (&S)[KD / 16], const Tile<NP, KD> &k, const u32x4 (&v)[NP][2], const Clock &clock) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float e = 0.0f;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const uint32_t word = v[p][s][i / 2];
-                const float f = __uint_as_float(i & 1 ? word & 0xffff0000u : word << 16);
-                e = p ? e + f : f;
-            }
-            x[i] = e * (i < 4 ? a[i & 3] : b[i & 3]);
-        }
+    for (int s = 0; s < 2; ++s) {
+        float x[8];
+        weighted<NP>(v, clock, s, x);
         u32x4 w[3];
         split<3>(x, w);
-#pragma unroll
-        for (int kt = 0; kt < KD / 16; ++kt) {
-            u32x4 row[NP];
-#pragma unroll
-            for (int p = 0; p < NP; ++p) row[p] = key_operand(k, p, kt, s);
-            pairs<NP, 3, 3>([&](int p, int n) { S[kt] = mma(row[p], w[n], S[kt]); });
-            if (kt % 4 == 3) hold();
-        }
+        add_products<NP, KD>(S, k, w, s, [](int p, int n) { return p + n == 2; });
     }
 }
 
@@ -453,7 +472,7 @@ template <int DT, int KD, int VD, bool REV> __device__ __forceinline__ void own_
         if (n + 1 < count) load(n + 1);
         u32x4 v[NP][2];
         value_operands(L.v, wave, v);
-        update<NP, KD>(S, L.k, v, L.clock[n & 1]);
+        update<NP, KD, 3>(S, L.k, v, L.clock[n & 1]);
         if (wave == 0 && n + 1 < count) sum += tick<REV>(L.clock[(n + 1) & 1], g, 1.0f, a.up);
     }
     store_state<KD, VD>(S, a.state + ((int64_t)seg * b.H + h) * (KD * VD), wave);
@@ -621,15 +640,19 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
 #pragma unroll
         for (int s = 0; s < KD / 32; ++s) {
             float x[8];
-            state_operand<KD>(S, s, x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = S[2 * s][r], x[4 + r] = S[2 * s + 1][r];
             u32x4 part[IN];
             split<IN>(x, part);
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                u32x4 qq[NP];
+            for (int it = 0; it < 4; it += 2) {     // (products into one result wait for each other: two in turn)
+                u32x4 qq[2][NP];
 #pragma unroll
-                for (int p = 0; p < NP; ++p) qq[p] = row_operand(L.q, p, it, s);
-                pairs<IN, NP, IN>([&](int x, int y) { acc[it] = mma(part[x], qq[y], acc[it]); });
+                for (int p = 0; p < NP; ++p) qq[0][p] = row_operand(L.q, p, it, s), qq[1][p] = row_operand(L.q, p, it + 1, s);
+                pairs<IN, NP, IN>([&](int x, int y) {
+                    acc[it] = mma(part[x], qq[0][y], acc[it]);
+                    acc[it + 1] = mma(part[x], qq[1][y], acc[it + 1]);
+                });
             }
             hold();
         }
@@ -673,7 +696,12 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
         }
         hold();
         leave = c.leave;
-        if (!leave || (c.close && a.fin)) update<NP, KD>(S, L.k, v, clock);
+        // exact where the state ends in fp32: a final state (that of the part), gradients of decays
+        if (!leave || (c.close && a.fin)) {
+            update<NP, KD, DOT ? 3 : 2>(S, L.k, v, clock);
+            if constexpr (!DOT)
+                if (c.close && a.fin) refine<NP, KD>(S, L.k, v, clock);
+        }
         if constexpr (!DOT)
             if (leave && c.close && a.fin) store_state<KD, VD>(S, a.fin + ((int64_t)c.seq * b.H + h) * SIZE, wave);
         if (wave == 0) tick<REV>(L.clock[turn ^ 1], decay, a.in_scale, a.up_scale);
