@@ -13,6 +13,8 @@
 // and put to 0, so that nothing outlives a reset.
 #include "ops_lin.hpp"
 
+#include <type_traits>
+
 namespace kda {
 namespace ops {
 namespace lin {
@@ -32,21 +34,32 @@ __global__ __launch_bounds__(JOIN_THREADS) void lin_bwd_join_kernel(const Batch 
     else join<SIZE>(b, y, yf, true);
 }
 
-template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_dq_kernel(const Batch b, const Walk a, int32_t *err) {
-    __shared__ WalkLds<DT, KD, VD> lds;
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS<VD>);
-    walk<DT, KD, VD, false, true>(b, a, lds);
-}
-template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_dv_kernel(const Batch b, const Walk a) {
-    __shared__ WalkLds<DT, KD, VD> lds;
-    walk<DT, KD, VD, true, false>(b, a, lds);
-}
-template <int DT, int KD, int VD>
-__global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_dk_kernel(const Batch b, const Walk a) {
-    __shared__ WalkLds<DT, KD, VD> lds;
-    walk<DT, KD, VD, true, true>(b, a, lds);
+// The three walks, by blockIdx.z, the longer ones first: side by side they fill what each leaves of the chip (8192 tokens of 16
+// heads in segments of 512: 138 us, one after the other 175). dq's and dk's states lie turned and take a wave for every 16 key
+// columns, dv's for every 16 value columns: where these differ, dv's has a launch of its own.
+enum { DQ, DK, DV };
+template <int DT, int KD, int VD, int FIRST, int LAST> struct WalksLds {
+    static constexpr int NT = FIRST == DV ? THREADS<VD> : THREADS<KD>, A_SIMD = FIRST == DV ? WAVES_A_SIMD<DT, VD> : WAVES_A_SIMD<DT, KD>;
+    typedef WalkLds<DT, VD, KD> Turned;
+    typedef WalkLds<DT, KD, VD> Straight;
+    union {
+        typename std::conditional<FIRST == DV, Straight, Turned>::type t;
+        typename std::conditional<LAST == DV, Straight, Turned>::type s;
+    };
+};
+template <int DT, int KD, int VD, int FIRST, int LAST>
+__global__ __launch_bounds__((WalksLds<DT, KD, VD, FIRST, LAST>::NT), (WalksLds<DT, KD, VD, FIRST, LAST>::A_SIMD)) void lin_walks_kernel(
+    const Batch b, const Walk dq, const Walk dk, const Walk dv, int32_t *err) {
+    typedef WalksLds<DT, KD, VD, FIRST, LAST> Lds;
+    static_assert(FIRST == DV || LAST != DV || KD == VD, "one number of waves for all");
+    __shared__ Lds lds;
+    const int which = FIRST + blockIdx.z;
+    if (which == DQ && blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, Lds::NT);
+    if constexpr (FIRST == DQ) {
+        if (which == DQ) return walk<DT, VD, KD, false, true>(b, dq, lds.t);
+        if (which == DK) return walk<DT, VD, KD, true, true>(b, dk, lds.t);
+    }
+    if constexpr (LAST == DV) walk<DT, KD, VD, true, false>(b, dv, lds.s);
 }
 
 // ---------------------------------------------------------------- gradients of the decays
@@ -89,20 +102,28 @@ __device__ __forceinline__ float row_suffix(float x) {
     return x;
 }
 
-constexpr int DECAY_THREADS = 256;
+// A block takes a segment of one head, four chunks at a time, four waves each: a wave the pairs with 16 of the tokens i. (A
+// wave a chunk left two waves a SIMD to wait for their operands: 58 us for 8192 tokens of 16 heads, now @.)
+constexpr int DECAY_WAVES = 16, DECAY_THREADS = 64 * DECAY_WAVES;
+struct DecayLds {
+    Clock clocks[4];
+    float part[DECAY_WAVES], border[4], sums[4][4];
+    float inside[4][C];         // of chunk and token: what passes it within its 16 tokens i
+    float rows[4][4][C];        // of chunk, 16 tokens i, token j: W summed over the i
+};
 
-// A block takes a segment of one head, four chunks at a time, a wave each.
 template <int DT, int KD, int VD>
 __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b, const Decays a) {
     constexpr int NP = PLANES<DT>, SIZE = KD * VD;
-    __shared__ Clock clocks[4];
-    __shared__ float part[4], border[4], sums[4][4];
+    __shared__ DecayLds L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    // its chunk and its tokens i (four waves of a SIMD, which have most pairs at 3, have one of each)
+    const int turn = wave >> 2, it = (wave + turn) & 3;
     const int seg = blockIdx.x, h = blockIdx.y;
     const Offsets o = b.offsets();
     const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
     Chunks<false> chunks(o, s0, s1);
-    Clock &clock = clocks[wave];
+    Clock &clock = L.clocks[turn];
     float all = 0.0f, F = 0.0f;
 #pragma unroll 1
     for (;;) {
@@ -113,7 +134,7 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
             const Chunk c = chunks.next();
             if (!c.len) break;
             ++count;
-            if (n == wave) own = c;
+            if (n == turn) own = c;
             if (!c.enter) continue;
             // what passes the first border of a part: the block together
             enters |= 1 << n;
@@ -129,102 +150,112 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
             }
             sum = wave_sum(sum);
             __syncthreads();
-            if (lane == 0) part[wave] = sum;
+            if (lane == 0) L.part[wave] = sum;
             __syncthreads();
-            if (threadIdx.x == 0) border[n] = (part[0] + part[1]) + (part[2] + part[3]);
+            if (wave == 0) {
+                sum = row_suffix(L.part[i]);
+                if (lane == 0) L.border[n] = sum;
+            }
         }
         if (!count) break;
-        const bool there = lane < own.len;
+        const bool there = it == 0 && lane < own.len;
         const int64_t at = (int64_t)(own.first + lane) * b.H + h;
-        const float u = there ? a.u[at] : 0.0f, w = there ? a.w[at] : 0.0f;
-        tick<false>(clock, b.decay(own.first, own.len, h), 1.0f, 1.0f);
-        {
+        float u = 0.0f, w = 0.0f;
+        if (it == 0) {
+            if (there) u = a.u[at], w = a.w[at];
+            tick<false>(clock, b.decay(own.first, own.len, h), 1.0f, 1.0f);
             const float su = wave_sum(u), sw = wave_sum(w), size = wave_sum(__builtin_fabsf(u));
-            if (lane == 0) sums[wave][0] = su, sums[wave][1] = sw, sums[wave][2] = clock.total, sums[wave][3] = size;
+            if (lane == 0) L.sums[turn][0] = su, L.sums[turn][1] = sw, L.sums[turn][2] = clock.total, L.sums[turn][3] = size;
         }
         __syncthreads();
         float mine = 0.0f;      // what passes all of the wave's chunk
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             if (n >= count) break;
-            if (enters >> n & 1) F = border[n];
-            float c = F - sums[n][0];
-            if (sums[n][2] < 0x1p-24f && __builtin_fabsf(c) < 0x1p-16f * sums[n][3]) c = 0.0f;
-            if (n == wave) mine = c;
-            F = c + sums[n][1];
+            if (enters >> n & 1) F = L.border[n];
+            float c = F - L.sums[n][0];
+            if (L.sums[n][2] < 0x1p-24f && __builtin_fabsf(c) < 0x1p-16f * L.sums[n][3]) c = 0.0f;
+            if (n == turn) mine = c;
+            F = c + L.sums[n][1];
         }
         // W: rows tokens j, columns tokens i > j. Summed over i from each token on, then over the j before it: nothing is subtracted.
-        float inside[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // of token 16 it + i
-        float later[4][4];                              // over the tiles of i behind
+        float inside = 0.0f;        // of token 16 it + i
+        const int ti = 16 * it + i;
+        const float wi = clock.whole[ti], ri = clock.rest[ti];
+#pragma unroll 1
+        for (int jt = 0; jt <= it; ++jt) {
+            if (16 * it >= own.len) break;
+            const int tj = 16 * jt + i;
+            f32x4 qk = {0, 0, 0, 0}, dv = {0, 0, 0, 0};
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt)
+            for (int s = 0; s < KD / 32; ++s) {
+                u32x4 x[NP], y[NP];
+                global_operand<DT>(a.k, h, own.first + tj, tj < own.len, 32 * s + 8 * g, x);
+                global_operand<DT>(a.q, h, own.first + ti, ti < own.len, 32 * s + 8 * g, y);
+                pairs<NP, NP, 4>([&](int m, int k) { qk = mma(x[m], y[k], qk); });
+            }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) later[jt][r] = 0.0f;
+            for (int s = 0; s < VD / 32; ++s) {
+                u32x4 x[NP], y[NP];
+                global_operand<DT>(a.v, h, own.first + tj, tj < own.len, 32 * s + 8 * g, x);
+                global_operand<DT>(a.d_out, h, own.first + ti, ti < own.len, 32 * s + 8 * g, y);
+                pairs<NP, NP, 4>([&](int m, int k) { dv = mma(x[m], y[k], dv); });
+            }
+            const f32x4 wj = *reinterpret_cast<const f32x4 *>(&clock.whole[16 * jt + 4 * g]);
+            const f32x4 rj = *reinterpret_cast<const f32x4 *>(&clock.rest[16 * jt + 4 * g]);
 #pragma unroll
-        for (int it = 3; it >= 0; --it) {
-            if (16 * it >= own.len) continue;
-            const int ti = 16 * it + i;
-            const float wi = clock.whole[ti], ri = clock.rest[ti];
-#pragma unroll
-            for (int jt = 0; jt < 4; ++jt) {
-                if (jt > it) continue;
-                const int tj = 16 * jt + i;
-                f32x4 qk = {0, 0, 0, 0}, dv = {0, 0, 0, 0};
-#pragma unroll
-                for (int s = 0; s < KD / 32; ++s) {
-                    u32x4 x[NP], y[NP];
-                    global_operand<DT>(a.k, h, own.first + tj, tj < own.len, 32 * s + 8 * g, x);
-                    global_operand<DT>(a.q, h, own.first + ti, ti < own.len, 32 * s + 8 * g, y);
-                    pairs<NP, NP, 4>([&](int m, int k) { qk = mma(x[m], y[k], qk); });
-                }
-#pragma unroll
-                for (int s = 0; s < VD / 32; ++s) {
-                    u32x4 x[NP], y[NP];
-                    global_operand<DT>(a.v, h, own.first + tj, tj < own.len, 32 * s + 8 * g, x);
-                    global_operand<DT>(a.d_out, h, own.first + ti, ti < own.len, 32 * s + 8 * g, y);
-                    pairs<NP, NP, 4>([&](int m, int k) { dv = mma(x[m], y[k], dv); });
-                }
-                const f32x4 wj = *reinterpret_cast<const f32x4 *>(&clock.whole[16 * jt + 4 * g]);
-                const f32x4 rj = *reinterpret_cast<const f32x4 *>(&clock.rest[16 * jt + 4 * g]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = 16 * jt + 4 * g + r;
-                    const float x = qk[r] * dv[r] * exp2_f((wi - wj[r]) + (ri - rj[r])) * a.scale;
-                    const float from = row_suffix(j < ti ? x : 0.0f) + later[jt][r];
-                    inside[it] += j < ti ? from : 0.0f;
-                    later[jt][r] = __shfl(from, lane & 48);     // of the tile's first token
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int j = 16 * jt + 4 * g + r;
+                const float x = qk[r] * dv[r] * exp2_f((wi - wj[r]) + (ri - rj[r])) * a.scale;
+                const float from = row_suffix(j < ti ? x : 0.0f);
+                inside += j < ti ? from : 0.0f;
+                if (i == 0) L.rows[turn][it][j] = from;
             }
         }
-        // lane t: the tokens' own sums, u from t on, w before t
-        float dg = 0.0f;
+        inside = swap16_add(inside, inside);
+        inside = swap32_add(inside, inside);
+        if (g == 0) L.inside[turn][ti] = inside;
+        __syncthreads();
+        if (it == 0) {
+            // lane t: what passes within its 16 tokens i, from those behind, u from t on, w before t
+            float dg = L.inside[turn][lane], from = u, upto = w, behind[3];
+            float sum = 0.0f;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            float x = swap16_add(inside[it], inside[it]);
-            x = swap32_add(x, x);
-            if (g == it) dg = x;
-        }
-        float from = u, upto = w;
+            for (int n = 3; n > 0; --n) {       // to tokens from 16 n on
+                if (16 * n < own.len) sum += g <= n ? L.rows[turn][n][lane] : 0.0f;
+                behind[n - 1] = sum;
+            }
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const float x = __shfl_down(from, d), y = __shfl_up(upto, d);
-            if (lane + d < 64) from += x;
-            if (lane >= d) upto += y;
+            for (int d = 1; d < 64; d *= 2) {
+                const float x = __shfl_down(from, d), y = __shfl_up(upto, d);
+                if (lane + d < 64) from += x;
+                if (lane >= d) upto += y;
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    const float z = __shfl_up(behind[n], d);
+                    if (lane >= d) behind[n] += z;
+                }
+            }
+            // (before t: what the lane before holds; the last tokens have none behind)
+            const float y0 = __shfl_up(behind[0], 1), y1 = __shfl_up(behind[1], 1), y2 = __shfl_up(behind[2], 1), before = __shfl_up(upto, 1);
+            if (lane && g < 3) dg += g == 0 ? y0 : g == 1 ? y1 : y2;
+            dg += from + (lane ? before : 0.0f) + mine;
+            if (there) {
+                if (a.per_head) all += dg;
+                else a.dg[at] = dg;
+            }
         }
-        const float before = __shfl_up(upto, 1);
-        dg += from + (lane ? before : 0.0f) + mine;
-        if (there) {
-            if (a.per_head) all += dg;
-            else a.dg[at] = dg;
-        }
-        __syncthreads();        // border and sums are read
+        __syncthreads();        // all of it is read
     }
     if (a.per_head) {
         all = wave_sum(all);
         __syncthreads();
-        if (lane == 0) part[wave] = all;
+        if (lane == 0) L.part[wave] = all;
         __syncthreads();
-        if (threadIdx.x == 0) a.dg[(int64_t)seg * b.H + h] = (part[0] + part[1]) + (part[2] + part[3]);
+        if (wave == 0) {
+            all = row_suffix(L.part[i]);
+            if (lane == 0) a.dg[(int64_t)seg * b.H + h] = all;
+        }
     }
 }
 
@@ -244,7 +275,7 @@ struct Plan {
 };
 Plan plan(int64_t T, int64_t H, int64_t S, int64_t size, bool per_head, bool own_d_init) {
     Plan p;
-    p.seg = segment(T, H, 512, C);
+    p.seg = segment(T, H, 256, C);
     p.segs = (int)ceil_div(T > 0 ? T : 1, p.seg);
     p.state = p.segs > 1 ? (size_t)p.segs * H * size : 0;
     p.factor = p.segs > 1 ? (size_t)p.segs * H : 0;
@@ -278,11 +309,13 @@ template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, con
     const Walk wq = {d, v, k, r.dq, x, a.initial_state, nullptr, a.scale, a.scale, 1.0f, q, u};
     const Walk wv = {k, q, d, r.dv, y, r.d_final_state, d_init, a.scale, 1.0f, a.scale, none, nullptr};
     const Walk wk = {v, d, q, r.dk, y, r.d_final_state, nullptr, a.scale, 1.0f, a.scale, k, w};
-    lin_dq_kernel<DT, VD, KD><<<grid, THREADS<KD>, 0, st>>>(b, wq, err);
-    if ((e = hipGetLastError())) return e;
-    lin_dv_kernel<DT, KD, VD><<<grid, THREADS<VD>, 0, st>>>(b, wv);
-    if ((e = hipGetLastError())) return e;
-    lin_dk_kernel<DT, VD, KD><<<grid, THREADS<KD>, 0, st>>>(b, wk);
+    if constexpr (KD == VD) {
+        lin_walks_kernel<DT, KD, VD, DQ, DV><<<dim3(grid.x, grid.y, 3), THREADS<KD>, 0, st>>>(b, wq, wk, wv, err);
+    } else {
+        lin_walks_kernel<DT, KD, VD, DQ, DK><<<dim3(grid.x, grid.y, 2), THREADS<KD>, 0, st>>>(b, wq, wk, wv, err);
+        if ((e = hipGetLastError())) return e;
+        lin_walks_kernel<DT, KD, VD, DV, DV><<<grid, THREADS<VD>, 0, st>>>(b, wq, wk, wv, err);
+    }
     if ((e = hipGetLastError())) return e;
     const Decays dec = {q, k, v, d, x, y, a.initial_state, d_init, u, w, a.g_per_head ? sums : r.dg, a.scale, a.g_per_head};
     lin_decay_kernel<DT, KD, VD><<<grid, DECAY_THREADS, 0, st>>>(b, dec);
