@@ -78,19 +78,39 @@ __device__ __forceinline__ float wave_sum(float x) {
     for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
     return x;
 }
-// operand: 8 elements of a row, as bf16 parts
-template <int DT> __device__ __forceinline__ void global_operand(const Role &s, int h, int t, bool there, int at, u32x4 (&to)[PLANES<DT>]) {
-    u32x4 r = {0, 0, 0, 0};
-    if (there) r = *reinterpret_cast<const u32x4 *>((const uint16_t *)s.p + (int64_t)t * s.row + (int64_t)h * s.head + at);
-    if constexpr (DT == KDA_DTYPE_BF16) to[0] = r;
-    else {
-        typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-        const f16x8 e = __builtin_bit_cast(f16x8, r);
-        float v[8];
+// 16 rows of a chunk as operands: lane (i, g) has elements 32 s + 8 g .. of row i
+template <int DT, int D> struct Sixteen {
+    u32x4 r[D / 32];
+    __device__ __forceinline__ void load(const Rows &s, const Chunk &c, int first) {
+        const Buffer b = s.from(c.first, c.len, D);
+        const int row = first + (threadIdx.x & 15);
+        const uint32_t at = row < c.len ? row * s.row + (threadIdx.x & 48) : OUTSIDE;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
-        split<2>(v, to);
+        for (int n = 0; n < D / 32; ++n) r[n] = read16(b, at, 64 * n);
     }
+    __device__ __forceinline__ void operand(int n, u32x4 (&to)[PLANES<DT>]) const {
+        if constexpr (DT == KDA_DTYPE_BF16) to[0] = r[n];
+        else {
+            typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+            const f16x8 e = __builtin_bit_cast(f16x8, r[n]);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
+            split<2>(v, to);
+        }
+    }
+};
+template <int DT, int D> __device__ __forceinline__ f32x4 products(const Sixteen<DT, D> &a, const Sixteen<DT, D> &b) {
+    constexpr int NP = PLANES<DT>;
+    f32x4 c = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        u32x4 x[NP], y[NP];
+        a.operand(s, x);
+        b.operand(s, y);
+        pairs<NP, NP, 4>([&](int m, int k) { c = mma(x[m], y[k], c); });
+    }
+    return c;
 }
 
 // sums over a row's lanes from each lane on: four steps to the right
@@ -114,7 +134,7 @@ struct DecayLds {
 
 template <int DT, int KD, int VD>
 __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b, const Decays a) {
-    constexpr int NP = PLANES<DT>, SIZE = KD * VD;
+    constexpr int SIZE = KD * VD;
     __shared__ DecayLds L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
     // its chunk and its tokens i (four waves of a SIMD, which have most pairs at 3, have one of each)
@@ -125,16 +145,35 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
     Chunks<false> chunks(o, s0, s1);
     Clock &clock = L.clocks[turn];
     float all = 0.0f, F = 0.0f;
+    // the wave's chunk of the next four, and what it reads of it first
+    const Rows rq(a.q, h), rk(a.k, h), rv(a.v, h), rd(a.d_out, h);
+    Chunk own;
+    Sixteen<DT, KD> q, k;
+    Sixteen<DT, VD> d, v;
+    float u, w, decay;
+    auto fetch = [&]() {
+        Chunks<false> ahead = chunks;
+        own = Chunk{0, 0, 0, false, false, false, false};
+#pragma unroll 1
+        for (int n = 0; n <= turn; ++n) own = ahead.next();
+        u = w = decay = 0.0f;
+        if (it == 0) {
+            const int64_t at = (int64_t)(own.first + lane) * b.H + h;
+            if (lane < own.len) u = a.u[at], w = a.w[at];
+            decay = b.decay(own.first, own.len, h);
+        }
+        q.load(rq, own, 16 * it), d.load(rd, own, 16 * it);
+        k.load(rk, own, 0), v.load(rv, own, 0);
+    };
+    fetch();
 #pragma unroll 1
     for (;;) {
-        Chunk own = {0, 0, 0, false, false, false, false};
         int enters = 0, count = 0;
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
             const Chunk c = chunks.next();
             if (!c.len) break;
             ++count;
-            if (n == turn) own = c;
             if (!c.enter) continue;
             // what passes the first border of a part: the block together
             enters |= 1 << n;
@@ -149,9 +188,9 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
                 }
             }
             sum = wave_sum(sum);
-            __syncthreads();
+            lds_barrier();
             if (lane == 0) L.part[wave] = sum;
-            __syncthreads();
+            lds_barrier();
             if (wave == 0) {
                 sum = row_suffix(L.part[i]);
                 if (lane == 0) L.border[n] = sum;
@@ -160,14 +199,12 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
         if (!count) break;
         const bool there = it == 0 && lane < own.len;
         const int64_t at = (int64_t)(own.first + lane) * b.H + h;
-        float u = 0.0f, w = 0.0f;
         if (it == 0) {
-            if (there) u = a.u[at], w = a.w[at];
-            tick<false>(clock, b.decay(own.first, own.len, h), 1.0f, 1.0f);
+            tick<false>(clock, decay, 1.0f, 1.0f);
             const float su = wave_sum(u), sw = wave_sum(w), size = wave_sum(__builtin_fabsf(u));
             if (lane == 0) L.sums[turn][0] = su, L.sums[turn][1] = sw, L.sums[turn][2] = clock.total, L.sums[turn][3] = size;
         }
-        __syncthreads();
+        lds_barrier();
         float mine = 0.0f;      // what passes all of the wave's chunk
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -185,22 +222,8 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
 #pragma unroll 1
         for (int jt = 0; jt <= it; ++jt) {
             if (16 * it >= own.len) break;
-            const int tj = 16 * jt + i;
-            f32x4 qk = {0, 0, 0, 0}, dv = {0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < KD / 32; ++s) {
-                u32x4 x[NP], y[NP];
-                global_operand<DT>(a.k, h, own.first + tj, tj < own.len, 32 * s + 8 * g, x);
-                global_operand<DT>(a.q, h, own.first + ti, ti < own.len, 32 * s + 8 * g, y);
-                pairs<NP, NP, 4>([&](int m, int k) { qk = mma(x[m], y[k], qk); });
-            }
-#pragma unroll
-            for (int s = 0; s < VD / 32; ++s) {
-                u32x4 x[NP], y[NP];
-                global_operand<DT>(a.v, h, own.first + tj, tj < own.len, 32 * s + 8 * g, x);
-                global_operand<DT>(a.d_out, h, own.first + ti, ti < own.len, 32 * s + 8 * g, y);
-                pairs<NP, NP, 4>([&](int m, int k) { dv = mma(x[m], y[k], dv); });
-            }
+            const f32x4 qk = products(k, q), dv = products(v, d);
+            if (jt < it) k.load(rk, own, 16 * jt + 16), v.load(rv, own, 16 * jt + 16);
             const f32x4 wj = *reinterpret_cast<const f32x4 *>(&clock.whole[16 * jt + 4 * g]);
             const f32x4 rj = *reinterpret_cast<const f32x4 *>(&clock.rest[16 * jt + 4 * g]);
 #pragma unroll
@@ -215,14 +238,17 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
         inside = swap16_add(inside, inside);
         inside = swap32_add(inside, inside);
         if (g == 0) L.inside[turn][ti] = inside;
-        __syncthreads();
+        const int len = own.len;
+        const float own_u = u, own_w = w;
+        fetch();
+        lds_barrier();
         if (it == 0) {
             // lane t: what passes within its 16 tokens i, from those behind, u from t on, w before t
-            float dg = L.inside[turn][lane], from = u, upto = w, behind[3];
+            float dg = L.inside[turn][lane], from = own_u, upto = own_w, behind[3];
             float sum = 0.0f;
 #pragma unroll
             for (int n = 3; n > 0; --n) {       // to tokens from 16 n on
-                if (16 * n < own.len) sum += g <= n ? L.rows[turn][n][lane] : 0.0f;
+                if (16 * n < len) sum += g <= n ? L.rows[turn][n][lane] : 0.0f;
                 behind[n - 1] = sum;
             }
 #pragma unroll
@@ -245,13 +271,13 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
                 else a.dg[at] = dg;
             }
         }
-        __syncthreads();        // all of it is read
+        lds_barrier();        // all of it is read
     }
     if (a.per_head) {
         all = wave_sum(all);
-        __syncthreads();
+        lds_barrier();
         if (lane == 0) L.part[wave] = all;
-        __syncthreads();
+        lds_barrier();
         if (wave == 0) {
             all = row_suffix(L.part[i]);
             if (lane == 0) a.dg[(int64_t)seg * b.H + h] = all;
