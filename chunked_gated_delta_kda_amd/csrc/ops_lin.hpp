@@ -374,7 +374,12 @@ template <int NP, int VD> __device__ __forceinline__ void value_operands(const T
 // A state of KD x VD between memory and the wave's columns. TURNED: memory holds it as [VD][KD]. p NULL: zeros.
 template <int KD, int VD, bool TURNED> __device__ __forceinline__ void load_state(f32x4 (&S)[KD / 16], const float *p, int wave) {
     const uint32_t i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    const Buffer b = buffer(p, p ? 4 * KD * VD : 0);
+    if (!p) {
+#pragma unroll
+        for (int kt = 0; kt < KD / 16; ++kt) S[kt] = f32x4{0, 0, 0, 0};
+        return;
+    }
+    const Buffer b = buffer(p, 4 * KD * VD);
 #pragma unroll
     for (int kt = 0; kt < KD / 16; ++kt) {
         const uint32_t k = key_element<KD>(kt & 1, g);
@@ -539,7 +544,7 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
     const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
     constexpr int SIZE = KD * VD;
     // empty sequences, spread over the segments: what enters them leaves them
-    if (a.fin && b.cu) {
+    if (a.fin && (b.cu || !b.T)) {
         for (int n0 = seg * 64; n0 < b.N; n0 += b.segs * 64) {
             const int n = n0 + lane;
             uint64_t none = __ballot(n < b.N && o.at(n) >= o.at(n + 1));
@@ -722,7 +727,7 @@ template <int DT, int VD> constexpr int WAVES_A_SIMD = (PLANES<DT> == 1 ? 2 : 1)
 // Tokens of a segment: short enough for `blocks` blocks (segments x heads) where the batch has the chunks for it.
 inline int segment(int64_t T, int64_t H, int64_t blocks, int64_t least) {
     const int64_t want = ceil_div(T * H, blocks);
-    const int64_t len = ceil_div(want, C) * C;
+    const int64_t len = ceil_div(want < T ? want : T, C) * C;
     return (int)(len < least ? least : len);
 }
 

@@ -394,3 +394,132 @@ def test_caller_workspace_and_buffers():
     assert all(torch.equal(got[n], mine[n]) for n in got)
     with pytest.raises(native.KdaError):
         kda.lin_bwd(**d, d_out=out, workspace=ws[:-4])
+
+
+def test_no_tokens_without_offsets():
+    """One sequence of no tokens: the final state is the initial one, and its gradient goes straight through."""
+    import chunked_gated_delta_kda_amd as kda
+
+    d = make([0], 3, 64, 128, "bf16", 30)
+    d["cu_seqlens"] = None
+    fin = torch.full_like(d["initial_state"], float("nan"))
+    out, fin = kda.lin_fwd(**d, final_state=fin, check=True)
+    assert out.shape == (0, 3, 128) and torch.equal(fin, d["initial_state"])
+    _, none = kda.lin_fwd(**dict(d, initial_state=None), final_state=torch.full_like(fin, float("nan")))
+    assert not none.any()
+    for fixed in (False, True):
+        g = d["g"] if not fixed else torch.full((3,), -0.1, device="cuda")
+        got = kda.lin_bwd(**dict(d, g=g), d_out=out, d_final_state=fin)
+        assert torch.equal(got["d_initial_state"], fin) and not got["dg"].any() and got["dg"].shape == g.shape
+
+
+def test_shared_rows_and_rows_far_apart():
+    """Keys that all heads share (stride 0), a query that all tokens share, and values as far apart as they may lie (rows past
+    2^32 bytes): the same results as copies, bit by bit."""
+    import chunked_gated_delta_kda_amd as kda
+
+    T, H, D, far = 200, 4, 128, 1 << 24
+    d = make([90, 110], H, D, D, "bf16", 31)
+    d["k"] = d["k"][:, :1].expand(T, H, D)
+    d["q"] = d["q"][:1].expand(T, H, D)
+    wide = torch.empty(T * far, dtype=torch.bfloat16, device="cuda").view(T, far)[:, far - H * D:].unflatten(1, (H, D))
+    wide.copy_(d["v"])
+    apart = dict(d, v=wide)
+    copies = {n: t.clone(memory_format=torch.contiguous_format) for n, t in d.items()}
+    do = torch.randn(T, H, D, generator=torch.Generator().manual_seed(32)).to(torch.bfloat16).cuda()
+    for a, b in zip(kda.lin_fwd(**apart, check=True), kda.lin_fwd(**copies)):
+        assert torch.equal(a, b)
+    a, b = kda.lin_bwd(**apart, d_out=do), kda.lin_bwd(**copies, d_out=do)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    tok = lambda x: [x[n][:1] for n in ("q", "k", "v", "g")]  # noqa: E731
+    assert torch.equal(kda.lin_decode(*tok(apart))[0], kda.lin_decode(*tok(copies))[0])
+
+
+def test_a_long_prompt_is_its_parts():
+    """65536 tokens in one call and in four that hand on their states, and the gradients likewise: whole results to what
+    fp32 states and one rounding of the outputs leave."""
+    import chunked_gated_delta_kda_amd as kda
+
+    n, part, H = 65536, 16384, 2
+    d = make([n], H, 128, 128, "bf16", 33, slope=0.002)
+    d.pop("cu_seqlens")
+    do = torch.randn(n, H, 128, generator=torch.Generator().manual_seed(34)).to(torch.bfloat16).cuda()
+    out, fin = kda.lin_fwd(**d)
+    whole = kda.lin_bwd(**d, d_out=do)
+    states, outs = [d["initial_state"]], []
+    cut = lambda i: {x: d[x][i * part:(i + 1) * part] for x in ("q", "k", "v", "g")}  # noqa: E731
+    for i in range(4):
+        o, s = kda.lin_fwd(**cut(i), initial_state=states[-1])
+        outs.append(o)
+        states.append(s)
+    near("out", np64(torch.cat(outs)), np64(out), 2.0 ** -8)
+    near("final", np64(states[-1]), np64(fin), 2.0 ** -19)
+    grads, back = [], None
+    for i in (3, 2, 1, 0):
+        grads.insert(0, kda.lin_bwd(**cut(i), d_out=do[i * part:(i + 1) * part], initial_state=states[i], d_final_state=back))
+        back = grads[0]["d_initial_state"]
+    for name in ("dq", "dk", "dv"):
+        near(name, np64(torch.cat([x[name] for x in grads])), np64(whole[name]), 2.0 ** -8)
+    near("dg", np64(torch.cat([x["dg"] for x in grads])), np64(whole["dg"]), 2.0 ** -18)
+    near("d_initial_state", np64(back), np64(whole["d_initial_state"]), 2.0 ** -19)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams side by side, each with workspaces of its own."""
+    import chunked_gated_delta_kda_amd as kda
+
+    jobs = [make([3000, 200], 8, 128, 128, "bf16", 35), make([1500], 12, 64, 128, "fp16", 36)]
+    dos = [torch.randn(j["v"].shape, generator=torch.Generator().manual_seed(37)).to(j["v"].dtype).cuda() for j in jobs]
+    run = lambda j, do: [*kda.lin_fwd(**j), *kda.lin_bwd(**j, d_out=do).values()]  # noqa: E731
+    want = [run(j, do) for j, do in zip(jobs, dos)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = []
+    for _ in range(5):
+        for j, do, s in zip(jobs, dos, streams):
+            with torch.cuda.stream(s):
+                got.append(run(j, do))
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i % 2])), i
+
+
+def test_a_captured_token_of_a_hybrid_block():
+    """What one token of a model of both kinds of layers runs: a step of the linear attention, new keys and values into a 4-bit
+    cache, attention over it; captured once, replayed while inputs and lengths change, every replay against eager calls."""
+    import chunked_gated_delta_kda_amd as kda
+
+    B, H, hq, hkv, D, page, W = 4, 4, 8, 2, 128, 16, 6
+    g = torch.Generator().manual_seed(38)
+    half = torch.arange(W * page)[:, None] * 10000.0 ** (-torch.arange(0, D, 2) / D)
+    rope = torch.cat([half.cos(), half.sin()], 1).float().cuda()
+    table = torch.randperm(B * W, generator=g).to(torch.int32).view(B, W).cuda()
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    x = torch.zeros(B, 3 * H * D, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(B, (hq + 2 * hkv) * D, dtype=torch.bfloat16, device="cuda")
+    decay = -0.1 * torch.rand(H, generator=g).cuda()
+
+    def step(state, cache, outs=(None, None, None)):
+        q, k, v = (t.unflatten(1, (H, D)) for t in x.chunk(3, 1))
+        o, _ = kda.lin_decode(q, k, v, decay, None, state, out=outs[0])
+        q, k, v = (t.unflatten(1, (-1, D)) for t in y.split([hq * D, hkv * D, hkv * D], 1))
+        kc, vc, ks, vs = cache
+        q = kda.kv_append(k, v, kc, vc, table, lens, rope=rope, q=q, k_scale=ks, v_scale=vs, q_out=outs[1])
+        return o, q, kda.attn_decode_fp4(q, kc, vc, ks, vs, table, lens, out=outs[2])
+
+    state = lambda: torch.zeros(B, H, D, D, device="cuda")  # noqa: E731
+    cache = lambda: kda.kv_cache_fp4(B * W, page, hkv, D)  # noqa: E731
+    outs = [t.clone() for t in step(state(), cache())]
+    mine, theirs, sm, st = cache(), cache(), state(), state()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(sm, mine, outs)
+    for i in range(12):
+        lens.copy_(torch.tensor([i + 1, i + 30, i + 60, 0 if i % 4 == 3 else i + 2], dtype=torch.int32))
+        x.copy_(torch.randn(x.shape, generator=g))
+        y.copy_(torch.randn(y.shape, generator=g))
+        graph.replay()
+        want = step(st, theirs, [None, outs[1].clone(), None])
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), i
+        assert torch.equal(sm, st) and all(torch.equal(a, b) for a, b in zip(mine, theirs)), i
