@@ -21,10 +21,14 @@ def _by8(name, t, dev):
         inner = shape[-1]
         strides = [shape[1] * inner, inner] if len(shape) == 3 else [shape[1] * shape[2] * inner, shape[2] * inner, inner]
         bad = False
+    elif len(shape) == 3:       # (written out: a loop over dimensions takes longer than all else here)
+        a, b, inner = t.stride()
+        strides = [a if shape[0] > 1 else 0, b if shape[1] > 1 else 0]
+        bad = inner != 1 or (strides[0] | strides[1]) & 7
     else:
-        last = len(shape) - 1
-        strides = [s if n > 1 else 0 for n, s in zip(shape[:last], t.stride())]
-        bad = t.stride(last) != 1 or any(s % 8 for s in strides)
+        a, b, c, inner = t.stride()
+        strides = [a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, c if shape[2] > 1 else 0]
+        bad = inner != 1 or (strides[0] | strides[1] | strides[2]) & 7
     if bad or t.data_ptr() % 16 or t.get_device() != dev:
         fail(name, t, "rows of contiguous elements, strides that are multiples of 8, a base aligned to 16 bytes", dev)
     return strides
@@ -130,11 +134,12 @@ def check_cache_fp4(name, code, scale, dh, dev, shape=None):
     if scale.dtype is not torch.uint8 or ss[:3] != cs[:3] or ss[3:] != (per,) or scale.get_device() != dev:
         fail(f"{name}_scale", scale, f"uint8 {(*cs[:3], per)}", dev)
     both = []
-    for what, t, unit, base in ((f"{name}_cache", code, 16, 16), (f"{name}_scale", scale, per, per)):
-        shape, strides = t.shape, t.stride()
-        if strides[3] != 1 or t.data_ptr() % base or any(s % unit for n, s in zip(shape[:3], strides) if n > 1):
-            fail(what, t, f"contiguous rows, strides that are multiples of {unit} bytes, a base aligned to {base}", dev)
-        both.append([s if n > 1 else 0 for n, s in zip(shape[:3], strides)])
+    for what, t, unit in ((f"{name}_cache", code, 16), (f"{name}_scale", scale, per)):
+        a, b, c, inner = t.stride()
+        strides = [a if cs[0] > 1 else 0, b if cs[1] > 1 else 0, c if cs[2] > 1 else 0]
+        if inner != 1 or t.data_ptr() % unit or (strides[0] | strides[1] | strides[2]) % unit:      # (units are powers of two)
+            fail(what, t, f"contiguous rows, strides that are multiples of {unit} bytes, a base aligned to {unit}", dev)
+        both.append(strides)
     return both
 
 
