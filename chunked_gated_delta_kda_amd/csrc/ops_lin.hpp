@@ -658,6 +658,7 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
                     acc[it] = mma(part[x], qq[0][y], acc[it]);
                     acc[it + 1] = mma(part[x], qq[1][y], acc[it + 1]);
                 });
+                if constexpr (DOT) hold();
             }
             hold();
         }
