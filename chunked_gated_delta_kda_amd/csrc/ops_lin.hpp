@@ -485,14 +485,14 @@ template <int DT, int KD, int VD, bool REV> __device__ __forceinline__ void own_
 }
 
 // ---------------------------------------------------------------- join
-// state[s] <- what leaves segment s (backwards: what it hands to the one before), in the order of the segments.
+// state[s] <- what leaves segment s (backwards: what it hands to the one before), in the order of the segments. Each step waits
+// for the one before, so that AHEAD segments' states are asked for at once.
 constexpr int JOIN_THREADS = 256;
-template <int SIZE> __device__ __forceinline__ void join(const Batch &b, float *state, const float *factor, bool rev) {
+template <int SIZE, int AHEAD> __device__ __forceinline__ void join_by(const Batch &b, float *state, const float *factor, bool rev) {
     const int h = blockIdx.y, x = blockIdx.x * JOIN_THREADS + threadIdx.x;
     float c = 0.0f;
     const int64_t step = (int64_t)b.H * SIZE;
     float *p = state + (int64_t)h * SIZE + x;
-    constexpr int AHEAD = 8;
     for (int n0 = 0; n0 < b.segs - 1; n0 += AHEAD) {
         float u[AHEAD], f[AHEAD];
 #pragma unroll
@@ -509,6 +509,11 @@ template <int SIZE> __device__ __forceinline__ void join(const Batch &b, float *
             }
         }
     }
+}
+// Few segments: 8 ahead (16 segments of 16 heads, both ways, 6.7 us for 8.3), more: 32 (64 of 8 heads 14 us for 20).
+template <int SIZE> __device__ __forceinline__ void join(const Batch &b, float *state, const float *factor, bool rev) {
+    if (b.segs <= 16) join_by<SIZE, 8>(b, state, factor, rev);
+    else join_by<SIZE, 32>(b, state, factor, rev);
 }
 
 // ---------------------------------------------------------------- the walk
@@ -724,6 +729,9 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
 
 // The second argument of launch bounds, waves a SIMD: two blocks on a CU where LDS holds them.
 template <int DT, int VD> constexpr int WAVES_A_SIMD = (PLANES<DT> == 1 ? 2 : 1) * WAVES<VD> / 4;
+
+// Blocks that run at once on 256 CUs: two a CU where LDS holds them.
+template <int DT, int KD, int VD> constexpr int RUN = 256 * (2 * sizeof(WalkLds<DT, KD, VD>) <= 160 * 1024 ? 2 : 1);
 
 // Tokens of a segment: short enough for `blocks` blocks (segments x heads) where the batch has the chunks for it.
 inline int segment(int64_t T, int64_t H, int64_t blocks, int64_t least) {
