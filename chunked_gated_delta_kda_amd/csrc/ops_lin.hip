@@ -13,8 +13,9 @@ __global__ __launch_bounds__(THREADS<VD>, WAVES<VD> / 2) void lin_state_kernel(c
     own_state<DT, KD, VD, false>(b, a, lds);
 }
 
-template <int SIZE> __global__ __launch_bounds__(JOIN_THREADS) void lin_join_kernel(const Batch b, float *state, const float *factor) {
-    join<SIZE>(b, state, factor, false);
+template <int SIZE, int AHEAD>
+__global__ __launch_bounds__(JOIN_THREADS) void lin_join_kernel(const Batch b, float *state, const float *factor) {
+    join<SIZE, AHEAD>(b, state, factor, false);
 }
 
 template <int DT, int KD, int VD>
@@ -96,7 +97,9 @@ template <int DT, int KD, int VD> hipError_t forward(const kda_lin_args &a, floa
         const Own own = {k, v, a.initial_state, ws, factor, 1.0f};
         lin_state_kernel<DT, KD, VD><<<grid, THREADS<VD>, 0, st>>>(b, own);
         if (hipError_t e = hipGetLastError()) return e;
-        lin_join_kernel<KD * VD><<<dim3(KD * VD / JOIN_THREADS, (unsigned)a.heads), JOIN_THREADS, 0, st>>>(b, ws, factor);
+        const dim3 join(KD * VD / JOIN_THREADS, (unsigned)a.heads);
+        if (far_ahead(p.segs)) lin_join_kernel<KD * VD, 32><<<join, JOIN_THREADS, 0, st>>>(b, ws, factor);
+        else lin_join_kernel<KD * VD, 8><<<join, JOIN_THREADS, 0, st>>>(b, ws, factor);
         if (hipError_t e = hipGetLastError()) return e;
     }
     const Walk w = {q, k, v, a.out, ws, a.initial_state, a.final_state, a.scale, a.scale, 1.0f, {nullptr, 0, 0}, nullptr};

@@ -488,7 +488,7 @@ template <int DT, int KD, int VD, bool REV> __device__ __forceinline__ void own_
 // state[s] <- what leaves segment s (backwards: what it hands to the one before), in the order of the segments. Each step waits
 // for the one before, so that AHEAD segments' states are asked for at once.
 constexpr int JOIN_THREADS = 256;
-template <int SIZE, int AHEAD> __device__ __forceinline__ void join_by(const Batch &b, float *state, const float *factor, bool rev) {
+template <int SIZE, int AHEAD> __device__ __forceinline__ void join(const Batch &b, float *state, const float *factor, bool rev) {
     const int h = blockIdx.y, x = blockIdx.x * JOIN_THREADS + threadIdx.x;
     float c = 0.0f;
     const int64_t step = (int64_t)b.H * SIZE;
@@ -510,11 +510,8 @@ template <int SIZE, int AHEAD> __device__ __forceinline__ void join_by(const Bat
         }
     }
 }
-// Few segments: 8 ahead (16 segments of 16 heads, both ways, 6.7 us for 8.3), more: 32 (64 of 8 heads 14 us for 20).
-template <int SIZE> __device__ __forceinline__ void join(const Batch &b, float *state, const float *factor, bool rev) {
-    if (b.segs <= 16) join_by<SIZE, 8>(b, state, factor, rev);
-    else join_by<SIZE, 32>(b, state, factor, rev);
-}
+// Few segments: 8 ahead (2 x 16 segments of 16 heads 6.7 us for 8.3), more: 32 (64 of 8 heads 14 us for 20).
+inline bool far_ahead(int segs) { return segs > 16; }
 
 // ---------------------------------------------------------------- the walk
 struct Walk {

@@ -28,10 +28,10 @@ __global__ __launch_bounds__(THREADS<VD>, WAVES<VD> / 2) void lin_bwd_state_kern
     else own_state<DT, KD, VD, true>(b, y, lds);
 }
 
-template <int SIZE>
+template <int SIZE, int AHEAD>
 __global__ __launch_bounds__(JOIN_THREADS) void lin_bwd_join_kernel(const Batch b, float *x, const float *xf, float *y, const float *yf) {
-    if (blockIdx.z == 0) join<SIZE>(b, x, xf, false);
-    else join<SIZE>(b, y, yf, true);
+    if (blockIdx.z == 0) join<SIZE, AHEAD>(b, x, xf, false);
+    else join<SIZE, AHEAD>(b, y, yf, true);
 }
 
 // The three walks, by blockIdx.z, the longer ones first: side by side they fill what each leaves of the chip (8192 tokens of 16
@@ -330,7 +330,9 @@ template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, con
         const Own ox = {k, v, a.initial_state, x, xf, 1.0f}, oy = {q, d, r.d_final_state, y, yf, a.scale};
         lin_bwd_state_kernel<DT, KD, VD><<<dim3(grid.x, grid.y, 2), THREADS<VD>, 0, st>>>(b, ox, oy);
         if ((e = hipGetLastError())) return e;
-        lin_bwd_join_kernel<KD * VD><<<dim3(KD * VD / JOIN_THREADS, grid.y, 2), JOIN_THREADS, 0, st>>>(b, x, xf, y, yf);
+        const dim3 join(KD * VD / JOIN_THREADS, grid.y, 2);
+        if (far_ahead(p.segs)) lin_bwd_join_kernel<KD * VD, 32><<<join, JOIN_THREADS, 0, st>>>(b, x, xf, y, yf);
+        else lin_bwd_join_kernel<KD * VD, 8><<<join, JOIN_THREADS, 0, st>>>(b, x, xf, y, yf);
         if ((e = hipGetLastError())) return e;
     }
     // dq on X^T, dk on Y^T: their states' rows are value elements
