@@ -14,6 +14,9 @@
 //    part of a key at once (16 bytes of a row of 128) and needs one scale for it (two in rows of 256).
 //  * Scales of 32 keys and 32 values come with one load, a lane each, and go through LDS to the lanes that need
 //    them; the conversion reads the exponent's bits of its scale operand only, so a scale is one rotation of its word.
+// Measured: 1 x 65536 tokens, 32 heads over 8 of 128 (71 MB) 22.9 us, 3.1 TB/s, and the join 7.9 (16 bits: 46-54); 64 skewed
+// sequences, 32 heads over 4, fp16 (97 MB) 30.4, 3.2 TB/s; 64 x 4096 tokens (285 MB) 52, 5.5 TB/s. What is short of
+// memory's rate is the time in which a block begins and ends: its first pages, keys and values wait for one another.
 #include <type_traits>
 
 #include "ops_attn.hpp"
@@ -348,7 +351,7 @@ __global__ __launch_bounds__(64 * WAVES, (DH == 256 ? 2 : 4)) void attn_fp4_chun
     }
 }
 
-// Blocks that run at once at head dimension 128: four to each of 256 CUs.
+// Blocks that run at once at head dimension 128: four to each of 256 CUs. Tokens are spread over as many.
 constexpr int RUN = 1024;
 static_assert(RUN <= MAX_SPREAD, "the join holds a weight for each chunk of a sequence");
 

