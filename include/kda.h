@@ -495,8 +495,8 @@ int kda_attn_decode(const kda_attn_args *args, void *stream, void *workspace, si
  * and head_dim / 32 bytes of scales, one for every KDA_FP4_GROUP elements: s stands for 2^(s - 127), 255 for
  * NaN. Codes are [num_pages, page_size, kv_heads, head_dim / 2], scales [num_pages, page_size, kv_heads, head_dim / 32],
  * rows contiguous, any other strides (in bytes): those of codes multiples of 16 on a base aligned to 16, those of
- * scales multiples of head_dim / 32 on a base aligned to that; kda_attn_decode_fp4 takes page and token strides under 2^32. Rows of one head that lie next to each other in a page
- * ([num_pages, kv_heads, page_size, ..]) suit the memory best.
+ * scales multiples of head_dim / 32 on a base aligned to that; kda_attn_decode_fp4 takes page and token strides under
+ * 2^32. Rows of one head that lie next to each other in a page ([num_pages, kv_heads, page_size, ..]) suit the memory best.
  */
 #define KDA_FP4_GROUP 32
 
@@ -552,10 +552,10 @@ typedef struct kda_kv_args {
  * kda_attn_decode_fp4 reads: the j-th of the n new rows of a sequence with seq_lens = L cached tokens lies at position
  * p = L - n + j. Keys (and q) are rotated on the way: with c and s the cosine and sine of rope's row p for the i-th pair,
  * (x, y) becomes (x c - y s, y c + x s), in fp32, rounded once; keys that go into 4 bits are rotated in 64 bits and
- * rounded to fp32 before that. 4 bits: the scale of 32 elements is 2^(floor(log2 max) - 2), twice that where max is over 1.75
- * times its power of two, within 2^-126 and the power of two that keeps 6 times the scale in dtype; codes are
- * rounded to nearest, halfway cases to the even code, at most 6; a group with an infinity or a NaN is stored as NaN. A sequence with
- * seq_lens 0 is an empty slot: its rows are passed over. Rows that would lie before position 0 (n > L), past the
+ * rounded to fp32 before that. 4 bits: the scale of 32 elements is 2^(floor(log2 max) - 2), twice that where max is
+ * over 1.75 times its power of two, within 2^-126 and the power of two that keeps 6 times the scale in dtype; codes
+ * are rounded to nearest, halfway cases to the even code, at most 6; a group with an infinity or a NaN is stored as
+ * NaN. A sequence with seq_lens 0 is an empty slot: its rows are passed over. Rows that would lie before position 0 (n > L), past the
  * sequence's row of the table, past the table of rotations or on a page outside the cache are left out
  * (KDA_DEVERR_PAGES). Rows that are left out or padding leave q_out as it was. Two sequences whose table rows name one
  * page must not append to the same place of it. Rows of q, k, v, rope and of a cache of dtype are read and written 16 bytes
