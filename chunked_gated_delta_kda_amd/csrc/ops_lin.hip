@@ -79,17 +79,20 @@ struct Plan {
 };
 // A block a segment and head, as many as run at once: 8192 tokens of 32 heads in bf16 (two blocks a CU) 135 us with 512, 146 with
 // 256, 158 with 1024; 9442 ragged ones of 5 in fp16 (one a CU) 51 us with 256, 62 with 512.
-constexpr int MOST = 512;
-Plan plan(int64_t T, int64_t H, int64_t blocks) {
+// Few chunks are walked one after another, which takes one launch for three (us a call, 2 | 64 heads: 128 tokens 12.8 | 12.9 for 19.5 | 19.9,
+// 256 tokens 19.4 | 21.0 for 19.5 | 29.9, 512 tokens, which stay with three, 35.4 | 37.2 for 19.3 | 47.4).
+constexpr int MOST = 512, FEW = 4;
+Plan plan(int64_t T, int64_t H, int64_t chunks, int64_t blocks) {
     Plan p;
-    p.seg = segment(T, H, blocks, C);
+    p.seg = chunks <= FEW ? FEW * C : segment(T, H, blocks, C);
     p.segs = (int)ceil_div(T > 0 ? T : 1, p.seg);
     return p;
 }
 
 template <int DT, int KD, int VD> hipError_t forward(const kda_lin_args &a, float *ws, int32_t *err, hipStream_t st) {
     static_assert(RUN<DT, KD, VD> <= MOST, "the workspace holds the states of as many segments");
-    const Plan p = plan(a.total_tokens, a.heads, RUN<DT, KD, VD>);
+    const int64_t chunks = ceil_div(a.total_tokens, C) + a.num_seqs - 1;      // at most
+    const Plan p = plan(a.total_tokens, a.heads, chunks, RUN<DT, KD, VD>);
     const Batch b = {a.cu_seqlens, a.g, a.g_per_head ? 0 : a.heads, a.num_seqs, a.total_tokens, a.heads, p.seg, p.segs, turns(a.num_seqs, p.segs)};
     const Role q = {a.q, a.q_stride, a.q_head_stride}, k = {a.k, a.k_stride, a.k_head_stride}, v = {a.v, a.v_stride, a.v_head_stride};
     const dim3 grid((unsigned)p.segs, (unsigned)a.heads);
@@ -126,7 +129,7 @@ template <int DT> hipError_t decode_dt(const kda_lin_args &a, hipStream_t st) {
 }  // namespace lin
 
 size_t lin_workspace(int64_t T, int64_t H, int64_t KD, int64_t VD) {
-    const lin::Plan p = lin::plan(T, H, lin::MOST);      // (fewer blocks: fewer segments)
+    const lin::Plan p = lin::plan(T, H, lin::FEW + 1, lin::MOST);      // (fewer blocks, few chunks: fewer segments)
     return p.segs > 1 ? (size_t)p.segs * H * (KD * VD + 1) * sizeof(float) : 0;
 }
 

@@ -485,6 +485,20 @@ def test_a_long_prompt_is_its_parts():
     near("d_initial_state", np64(back), np64(whole["d_initial_state"]), 2.0 ** -19)
 
 
+def test_few_chunks_and_many_sequences_in_as_many_tokens():
+    """256 tokens as one sequence, as four and as 256, with no more workspace than is asked for."""
+    import chunked_gated_delta_kda_amd as kda
+    from chunked_gated_delta_kda_amd import native
+
+    need = native.load_library().kda_lin_workspace_bytes(256, 3, 128, 128)
+    for lengths in ([256], [64] * 4, [65, 63, 128], [1] * 256):
+        d = make(lengths, 3, 128, 128, "bf16", 42)
+        ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        out, fin = check_forward(d, lengths, "bf16", check=True, workspace=ws)
+        again, fagain = kda.lin_fwd(**d)
+        assert torch.equal(out, again) and torch.equal(fin, fagain)
+
+
 def test_two_calls_at_once():
     """Calls on two streams side by side, each with workspaces of its own."""
     import chunked_gated_delta_kda_amd as kda
