@@ -22,7 +22,8 @@ template <int DT, int KD, int VD>
 __global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_walk_kernel(const Batch b, const Walk a, int32_t *err) {
     __shared__ WalkLds<DT, KD, VD> lds;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS<VD>);
-    walk<DT, KD, VD, false, false>(b, a, lds);
+    const int seg = (int)blockIdx.x / b.turns;
+    walk<DT, KD, VD, false, false>(b, a, Place{seg, (int)blockIdx.y, (int)blockIdx.x - seg * b.turns, (int)blockIdx.x, (int)gridDim.x, 0}, lds);
 }
 
 // One token of each sequence: S <- e^g S + k v^T, out = scale S^T q. The state is read and written once; a block takes one
@@ -106,7 +107,7 @@ template <int DT, int KD, int VD> hipError_t forward(const kda_lin_args &a, floa
         else lin_join_kernel<KD * VD, 8><<<join, JOIN_THREADS, 0, st>>>(b, ws, factor);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    const Walk w = {q, k, v, a.out, ws, a.initial_state, a.final_state, a.scale, a.scale, 1.0f, {nullptr, 0, 0}, nullptr};
+    const Walk w = {q, k, v, a.out, ws, a.initial_state, a.final_state, a.scale, a.scale, 1.0f, {nullptr, 0, 0}, nullptr, nullptr, nullptr, nullptr};
     lin_walk_kernel<DT, KD, VD><<<dim3(grid.x * b.turns, grid.y), THREADS<VD>, 0, st>>>(b, w, err);
     return hipGetLastError();
 }

@@ -431,6 +431,21 @@ template <int KD, int VD> __device__ __forceinline__ void store_state(const f32x
             __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[kt][r]), b, 4 * (key_element<KD>(kt & 1, g) * VD + 16 * wave + i),
                                                   4 * VD * (8 * (kt >> 1) + r), 0);
 }
+// The same as lanes hold it, 16 bytes of each after the other's.
+template <int KD, int VD> __device__ __forceinline__ void store_lanes(const f32x4 (&S)[KD / 16], float *p, int wave) {
+    const Buffer b = buffer(p, 4 * KD * VD);
+#pragma unroll
+    for (int kt = 0; kt < KD / 16; ++kt)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[kt]), b, 4 * KD * 16 * wave + 16 * (threadIdx.x & 63), 1024 * kt, 0);
+}
+// One of either form (lanes, or [VD][KD]). p NULL: zeros.
+template <int KD, int VD> __device__ __forceinline__ void load_either(f32x4 (&S)[KD / 16], const float *p, int wave, bool lanes) {
+    const uint32_t i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    const uint32_t at = lanes ? 16 * (threadIdx.x & 63) : 4 * (i * KD + key_element<KD>(0, g)), step = lanes ? 1024 : 16;
+    const Buffer b = buffer(p, p ? 4 * KD * VD : 0);
+#pragma unroll
+    for (int kt = 0; kt < KD / 16; ++kt) S[kt] = __builtin_bit_cast(f32x4, read16(b, 4 * KD * 16 * wave + at, kt * step));
+}
 
 // The batch and its segments.
 struct Batch {
@@ -550,6 +565,9 @@ inline bool far_ahead(int segs) { return segs > 16; }
 // has 4 neighbouring key elements of a column, which is what the products with the state and into it want (no state
 // passes through LDS, no wave needs another's). A chunk's rows come through LDS, the next chunk's are on their way in
 // registers meanwhile. The pairs' weights, which all waves need, are made by 8 of them once, as operands.
+//
+// The gradients of decays need what passes all of a chunk, e^G <X, Y> with X the state that enters it and Y the gradient of the one that
+// leaves: the walk for dk, from the end, leaves Y where the one for dq, which holds X, reads it.
 struct Walk {
     Role q, k, v;
     void *out;              // [T, H, VD], contiguous
@@ -558,7 +576,15 @@ struct Walk {
     float *fin;             // what leaves it, or NULL (not with DOT, whose states lie turned in memory)
     float pair_scale, in_scale, up_scale;
     Role e;                 // DOT: rows that the part of the result from the state that enters is multiplied with; states are [VD][KD]
-    float *dot;             // DOT: [T, H]
+    float *dot;             // DOT: [T, H]; forwards with what passes all of a chunk at its last token
+    float *between;         // DOT: states [blocks of the launch, seg / C], as lanes hold them, that enter chunks from the ones behind them, which
+                            // the walk from the end writes and the one forwards reads
+    const float *end, *last; // DOT forwards: the states that enter segments from behind [segs, H, KD, VD], and sequences [N, H, KD, VD] or NULL
+};
+// Which walk of a launch a block does: its segment and head, its turn among the blocks that share the segment, its place
+// among the blocks of the head and their number, its place in the launch.
+struct Place {
+    int seg, h, turn, at, of, block;
 };
 
 // The pairs' weights go in as two parts.
@@ -568,22 +594,31 @@ template <int DT, int KD, int VD> struct WalkLds {
     Tile<PLANES<DT>, VD> v;
     u32x4 pair[4][2][PARTS][64];      // operands of the pairs' weights: 16 columns (tokens i), 32 tokens j, part, lane
     Clock clock[2];
-    float dots[WAVES<VD>][C];
+    float dots[WAVES<VD>][C], passing[WAVES<VD>];
 };
 
+// sums over a row's lanes from each lane on: four steps to the right
+__device__ __forceinline__ float row_suffix(float x) {
+    x += dpp_f<0x101>(x);       // the lane one to the right (0 past the row's end), then two, four, eight
+    x += dpp_f<0x102>(x);
+    x += dpp_f<0x104>(x);
+    x += dpp_f<0x108>(x);
+    return x;
+}
+
 template <int DT, int KD, int VD, bool REV, bool DOT>
-__device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, KD, VD> &L) {
+__device__ __forceinline__ void walk(const Batch &b, const Walk &a, const Place &place, WalkLds<DT, KD, VD> &L) {
     constexpr int NP = PLANES<DT>, NT = THREADS<VD>, NW = WAVES<VD>, IN = DOT ? 3 : 2;      // IN: parts of the state in its product with q
     using E = typename Elem<DT>::type;
     typedef E E4 __attribute__((ext_vector_type(4)));
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-    const int seg = (int)blockIdx.x / b.turns, h = blockIdx.y;
+    const int seg = place.seg, h = place.h;
     const Offsets o = b.offsets();
     const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
     constexpr int SIZE = KD * VD;
     // empty sequences, spread over the segments: what enters them leaves them
     if (a.fin && (b.cu || !b.T)) {
-        for (int64_t n0 = (int64_t)blockIdx.x * 64; n0 < b.N; n0 += (int64_t)gridDim.x * 64) {
+        for (int64_t n0 = (int64_t)place.at * 64; n0 < b.N; n0 += (int64_t)place.of * 64) {
             const int n = (int)n0 + lane;
             uint64_t none = __ballot(n < b.N && o.at(n) >= o.at(n + 1));
             while (none) {
@@ -598,7 +633,7 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
     }
     const Rows rq(a.q, h), rk(a.k, h), rv(a.v, h), re(a.e, h);
     float *const dots = DOT ? a.dot + h : nullptr;
-    Chunks<REV> chunks(o, s0, s1, b.turns, (int)blockIdx.x - seg * b.turns);
+    Chunks<REV> chunks(o, s0, s1, b.turns, place.turn);
     Stage<DT, KD, NT> sq, sk;
     Stage<DT, VD, NT> sv;
     float decay = 0.0f;
@@ -613,9 +648,17 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
             float sum = L.dots[0][threadIdx.x];
 #pragma unroll
             for (int w = 1; w < NW; ++w) sum += L.dots[w][threadIdx.x];
+            if (!REV && (int)threadIdx.x == len - 1) {
+                float pass = L.passing[0];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) pass += L.passing[w];
+                sum += pass;
+            }
             (dots + (uint64_t)(uint32_t)first * (uint32_t)b.H)[threadIdx.x * (uint32_t)b.H] = sum;
         }
     };
+    // (only the last chunk of a part may be short: no two others begin in the same 64 tokens of the segment)
+    auto between = [&](const Chunk &c) { return a.between + ((int64_t)place.block * (b.seg / C) + (c.first - s0) / C) * SIZE; };
     Chunk c = chunks.next();
     int before_first = 0, before_len = 0, turn = 0;
     load(c);
@@ -630,13 +673,31 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, WalkLds<DT, 
         do {
         const Chunk then = chunks.next();
         const Clock &clock = L.clock[turn];
+        f32x4 Y[DOT && !REV ? KD / 16 : 1];
+        if constexpr (DOT && !REV)
+            load_either<KD, VD>(Y, !c.leave ? between(c) : !c.close ? a.end + ((int64_t)(seg + 1) * b.H + h) * SIZE
+                                          : a.last ? a.last + ((int64_t)c.seq * b.H + h) * SIZE : nullptr, wave, !c.leave);
         lds_barrier();
         if constexpr (DOT) put_dots(before_first, before_len);
         sq.store(L.q);
         sk.store(L.k);
         sv.store(L.v);
         lds_barrier();
+        if constexpr (DOT && !REV) {
+            const float total = clock.total;
+            float pass = 0.0f;
+#pragma unroll
+            for (int kt = 0; kt < KD / 16; ++kt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) pass = __builtin_fmaf(total * S[kt][r], Y[kt][r], pass);
+            pass = swap16_add(pass, pass);
+            pass = row_suffix(swap32_add(pass, pass));
+            if (lane == 0) L.passing[wave] = pass;
+            hold();
+        }
         load(then);
+        if constexpr (DOT && REV)       // (after the loads, which would wait for it)
+            if (!c.enter) store_lanes<KD, VD>(S, between(c), wave);
         // weights of the pairs: columns 16 tokens i, rows 32 tokens j, an operand a wave (two of four waves' each)
 #pragma unroll 1
         for (int f = wave; f < 8; f += NW) {

@@ -1,16 +1,15 @@
 // ops_lin_bwd.hip -- gradients of the linear attention with a decay for each head (ops_lin.hpp).
 //
-// With X the state that enters a chunk and Y the gradient of the one that leaves it, three walks give dq (forwards on X),
-// dv and dk (backwards on Y), and on the way u_i = q_i . (part of dq_i from X), w_j = k_j . (part of dk_j from Y).
+// With X the state that enters a chunk and Y the gradient of the one that leaves it, three walks give dv and dk (backwards on
+// Y), then dq (forwards on X), and on the way u_i = q_i . (part of dq_i from X), w_j = k_j . (part of dk_j from Y).
 // A decay's gradient is what passes it, from tokens before t to tokens from t on:
 //
-//   dg_t = sum_{j < t <= i} W_ij + sum_{i >= t} u_i + sum_{j < t} w_j + c,   W_ij = scale e^{G_i - G_j} (q_i . k_j) (do_i . v_j)
+//   dg_t = sum_{j < t <= i} W_ij + sum_{i >= t} u_i + sum_{j < t} w_j + e^G <X, Y>,   W_ij = scale e^{G_i - G_j} (q_i . k_j) (do_i . v_j)
 //
-// over the chunk, with c what passes all of it: F, what passes its first border (<X, Y> there, formed at a segment's
-// border or a sequence's), less the chunk's u; c plus the chunk's w pass the next border. That is the only subtraction, over
-// the chunks of a segment: pairs of a token with itself, which outweigh all else where decays are short, never enter,
-// and where a chunk leaves less than 2^-24 of a state and c is under 2^-16 of its u's sizes, c is what rounding left of that difference
-// and put to 0, so that nothing outlives a reset.
+// over the chunk, the last term what passes all of it. Nothing is subtracted: pairs of a token with itself, which outweigh
+// all else where decays are short, never enter, nor does what ends before t or begins behind it, which may be larger by any factor (tokens of
+// other sizes, resets). The walk for dk leaves Y at each border of chunks inside a segment for the one for dq, which holds X there: 1 KB for
+// a token and head of 128 x 128, written and read once, SLOTS bytes at a time.
 //
 // 8 x 1024 tokens of 16 heads of 128 x 128 in bf16 (261 MB in and out: 49 us of memory): states both ways 27 us, joins 7, walks 137, decays
 // 43; 200 in all. The walks are bound as the forward's is, with three parts where they lead to a decay's gradient.
@@ -37,40 +36,40 @@ __global__ __launch_bounds__(JOIN_THREADS) void lin_bwd_join_kernel(const Batch 
     else join<SIZE, AHEAD>(b, y, yf, true);
 }
 
-// The three walks, by blockIdx.z, the longer ones first: side by side they fill what each leaves of the chip (8192 tokens of 16
-// heads in segments of 512: 138 us, one after the other 175). dq's and dk's states lie turned and take a wave for every 16 key
-// columns, dv's for every 16 value columns: where these differ, dv's has a launch of its own.
+// Walks of one launch, by blockIdx.z: side by side they fill what each leaves of the chip. dq's and dk's states lie turned and take a
+// wave for every 16 key columns, dv's for every 16 value columns: where these differ, dv's has a launch of its own.
 enum { DQ, DK, DV };
-template <int DT, int KD, int VD, int FIRST, int LAST> struct WalksLds {
-    static constexpr int NT = FIRST == DV ? THREADS<VD> : THREADS<KD>, A_SIMD = FIRST == DV ? WAVES_A_SIMD<DT, VD> : WAVES_A_SIMD<DT, KD>;
-    typedef WalkLds<DT, VD, KD> Turned;
-    typedef WalkLds<DT, KD, VD> Straight;
-    union {
-        typename std::conditional<FIRST == DV, Straight, Turned>::type t;
-        typename std::conditional<LAST == DV, Straight, Turned>::type s;
-    };
-};
-template <int DT, int KD, int VD, int FIRST, int LAST>
-__global__ __launch_bounds__((WalksLds<DT, KD, VD, FIRST, LAST>::NT), (WalksLds<DT, KD, VD, FIRST, LAST>::A_SIMD)) void lin_walks_kernel(
-    const Batch b, const Walk dq, const Walk dk, const Walk dv, int32_t *err) {
-    typedef WalksLds<DT, KD, VD, FIRST, LAST> Lds;
-    static_assert(FIRST == DV || LAST != DV || KD == VD, "one number of waves for all");
-    __shared__ Lds lds;
-    const int which = FIRST + blockIdx.z;
-    if (which == DQ && blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, Lds::NT);
-    if constexpr (FIRST == DQ) {
-        if (which == DQ) return walk<DT, VD, KD, false, true>(b, dq, lds.t);
-        if (which == DK) return walk<DT, VD, KD, true, true>(b, dk, lds.t);
+template <int DT, int KD, int VD, int W> struct One {
+    static constexpr int NT = W == DV ? THREADS<VD> : THREADS<KD>, A_SIMD = W == DV ? WAVES_A_SIMD<DT, VD> : WAVES_A_SIMD<DT, KD>;
+    typedef typename std::conditional<W == DV, WalkLds<DT, KD, VD>, WalkLds<DT, VD, KD>>::type Lds;
+    static __device__ __forceinline__ void run(const Batch &b, const Walk &a, const Place &p, Lds &lds) {
+        if constexpr (W == DV) walk<DT, KD, VD, true, false>(b, a, p, lds);
+        else walk<DT, VD, KD, W == DK, true>(b, a, p, lds);
     }
-    if constexpr (LAST == DV) walk<DT, KD, VD, true, false>(b, dv, lds.s);
+};
+// Blocks take the segments of one head after another, from block `first` of all on.
+template <int DT, int KD, int VD, int W, int V>
+__global__ __launch_bounds__((One<DT, KD, VD, W>::NT), (One<DT, KD, VD, W>::A_SIMD)) void lin_walks_kernel(
+    const Batch b, const Walk w, const Walk v, int64_t first, int32_t *err) {
+    typedef One<DT, KD, VD, W> A;
+    typedef One<DT, KD, VD, V> B;
+    static_assert(A::NT == B::NT, "one number of waves for both");
+    __shared__ union {
+        typename A::Lds a;
+        typename B::Lds b;
+    } lds;
+    const int64_t n = first + blockIdx.x;
+    const int h = (int)(n / b.segs), seg = (int)(n - (int64_t)h * b.segs);
+    const Place p = {seg, h, 0, seg, b.segs, (int)blockIdx.x};
+    if (err && n == 0 && blockIdx.z == 0) check_offsets(b.offsets(), err, threadIdx.x, A::NT);
+    if (blockIdx.z == 0) return A::run(b, w, p, lds.a);
+    if constexpr (V != W) B::run(b, v, p, lds.b);
 }
 
 // ---------------------------------------------------------------- gradients of the decays
 struct Decays {
     Role q, k, v, d_out;
-    const float *x, *y;         // joined states and gradients
-    const float *init, *d_init; // of sequences, or both NULL
-    const float *u, *w;         // [T, H]
+    const float *u, *w;         // [T, H]; u with what passes all of a chunk at its last token
     float *dg;                  // [T, H], or partial sums [segs, H]
     float scale;
     int per_head;
@@ -116,28 +115,18 @@ template <int DT, int D> __device__ __forceinline__ f32x4 products(const Sixteen
     return c;
 }
 
-// sums over a row's lanes from each lane on: four steps to the right
-__device__ __forceinline__ float row_suffix(float x) {
-    x += dpp_f<0x101>(x);       // the lane one to the right (0 past the row's end), then two, four, eight
-    x += dpp_f<0x102>(x);
-    x += dpp_f<0x104>(x);
-    x += dpp_f<0x108>(x);
-    return x;
-}
-
 // A block takes a segment of one head, four chunks at a time, four waves each: a wave the pairs with 16 of the tokens i. (A
 // wave a chunk left two waves a SIMD to wait for their operands: 58 us for 8192 tokens of 16 heads, now 44.)
 constexpr int DECAY_WAVES = 16, DECAY_THREADS = 64 * DECAY_WAVES;
 struct DecayLds {
     Clock clocks[4];
-    float part[DECAY_WAVES], border[4], sums[4][4];
+    float part[DECAY_WAVES];
     float inside[4][C];         // of chunk and token: what passes it within its 16 tokens i
     float rows[4][4][C];        // of chunk, 16 tokens i, token j: W summed over the i
 };
 
 template <int DT, int KD, int VD>
 __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b, const Decays a) {
-    constexpr int SIZE = KD * VD;
     __shared__ DecayLds L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
     // its chunk and its tokens i (four waves of a SIMD, which have most pairs at 3, have one of each)
@@ -147,7 +136,7 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
     const int s0 = seg * b.seg, s1 = s0 + b.seg < b.T ? s0 + b.seg : b.T;
     Chunks<false> chunks(o, s0, s1);
     Clock &clock = L.clocks[turn];
-    float all = 0.0f, F = 0.0f;
+    float all = 0.0f;
     // the wave's chunk of the next four, and what it reads of it first
     const Rows rq(a.q, h), rk(a.k, h), rv(a.v, h), rd(a.d_out, h);
     Chunk own;
@@ -171,53 +160,14 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
     fetch();
 #pragma unroll 1
     for (;;) {
-        int enters = 0, count = 0;
+        int count = 0;
 #pragma unroll 1
-        for (int n = 0; n < 4; ++n) {
-            const Chunk c = chunks.next();
-            if (!c.len) break;
-            ++count;
-            if (!c.enter) continue;
-            // what passes the first border of a part: the block together
-            enters |= 1 << n;
-            const float *x = nullptr, *y = nullptr;
-            if (!c.open) x = a.x + ((int64_t)(seg - 1) * b.H + h) * SIZE, y = a.y + ((int64_t)seg * b.H + h) * SIZE;
-            else if (a.init) x = a.init + ((int64_t)c.seq * b.H + h) * SIZE, y = a.d_init + ((int64_t)c.seq * b.H + h) * SIZE;
-            float sum = 0.0f;
-            if (x) {
-                for (int e = 4 * threadIdx.x; e < SIZE; e += 4 * DECAY_THREADS) {
-                    const f32x4 p = *reinterpret_cast<const f32x4 *>(x + e), q = *reinterpret_cast<const f32x4 *>(y + e);
-                    sum += (p[0] * q[0] + p[1] * q[1]) + (p[2] * q[2] + p[3] * q[3]);
-                }
-            }
-            sum = wave_sum(sum);
-            lds_barrier();
-            if (lane == 0) L.part[wave] = sum;
-            lds_barrier();
-            if (wave == 0) {
-                sum = row_suffix(L.part[i]);
-                if (lane == 0) L.border[n] = sum;
-            }
-        }
+        while (count < 4 && chunks.next().len) ++count;
         if (!count) break;
         const bool there = it == 0 && lane < own.len;
         const int64_t at = (int64_t)(own.first + lane) * b.H + h;
-        if (it == 0) {
-            tick<false>(clock, decay, 1.0f, 1.0f);
-            const float su = wave_sum(u), sw = wave_sum(w), size = wave_sum(__builtin_fabsf(u));
-            if (lane == 0) L.sums[turn][0] = su, L.sums[turn][1] = sw, L.sums[turn][2] = clock.total, L.sums[turn][3] = size;
-        }
+        if (it == 0) tick<false>(clock, decay, 1.0f, 1.0f);
         lds_barrier();
-        float mine = 0.0f;      // what passes all of the wave's chunk
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            if (n >= count) break;
-            if (enters >> n & 1) F = L.border[n];
-            float c = F - L.sums[n][0];
-            if (L.sums[n][2] < 0x1p-24f && __builtin_fabsf(c) < 0x1p-16f * L.sums[n][3]) c = 0.0f;
-            if (n == turn) mine = c;
-            F = c + L.sums[n][1];
-        }
         // W: rows tokens j, columns tokens i > j. Summed over i from each token on, then over the j before it: nothing is subtracted.
         float inside = 0.0f;        // of token 16 it + i
         const int ti = 16 * it + i;
@@ -268,7 +218,7 @@ __global__ __launch_bounds__(DECAY_THREADS) void lin_decay_kernel(const Batch b,
             // (before t: what the lane before holds; the last tokens have none behind)
             const float y0 = __shfl_up(behind[0], 1), y1 = __shfl_up(behind[1], 1), y2 = __shfl_up(behind[2], 1), before = __shfl_up(upto, 1);
             if (lane && g < 3) dg += g == 0 ? y0 : g == 1 ? y1 : y2;
-            dg += from + (lane ? before : 0.0f) + mine;
+            dg += from + (lane ? before : 0.0f);
             if (there) {
                 if (a.per_head) all += dg;
                 else a.dg[at] = dg;
@@ -298,24 +248,33 @@ __global__ __launch_bounds__(64) void lin_decay_sum_kernel(const float *part, fl
 }
 
 // ---------------------------------------------------------------- host
+// States that the walk for dk hands on take this many bytes at most; larger batches are walked a range of blocks at a time.
+constexpr size_t SLOTS = (size_t)1 << 30;
+constexpr int LONGEST = 64;      // chunks of a segment: at 128 x 128, SLOTS holds the states of 256 such segments
 struct Plan {
     int seg, segs;
-    size_t state, factor, token, d_init, sums;     // elements of the parts of the workspace
+    int64_t blocks, most;     // segments and heads; of them in a launch
+    size_t state, factor, token, d_init, sums, between;     // elements of the parts of the workspace (d_init: room that callers' sizes count)
 };
-// 256 blocks of each walk: three of them run side by side. 8192 tokens of 16 heads in all (us, 170 blocks | 256 | 340 | 512):
-// 266 | 236 | 287 | 272, as longer segments have fewer states to write, join and read.
+// 256 blocks of each walk at least. 8192 tokens of 16 heads in all (us, 256 blocks | 352 | 512 | 688): 280 | 354 | 326 | 369, as
+// longer segments have fewer states to write, join and read (65536 of 8: 1066 | 1106 | 1002 | 1100).
 Plan plan(int64_t T, int64_t H, int64_t S, int64_t size, bool per_head, bool own_d_init) {
     Plan p;
     p.seg = segment(T, H, 256, C);
+    if (p.seg > LONGEST * C) p.seg = LONGEST * C;
     p.segs = (int)ceil_div(T > 0 ? T : 1, p.seg);
+    p.blocks = (int64_t)p.segs * H;
+    const int64_t per = p.seg / C, fit = (int64_t)(SLOTS / (size * sizeof(float))) / per;
+    p.most = p.seg == C || fit > p.blocks ? p.blocks : fit;
     p.state = p.segs > 1 ? (size_t)p.segs * H * size : 0;
     p.factor = p.segs > 1 ? (size_t)p.segs * H : 0;
     p.token = (size_t)T * H;
     p.d_init = own_d_init ? (size_t)S * H * size : 0;
     p.sums = per_head ? (size_t)p.segs * H : 0;
+    p.between = p.seg > C ? (size_t)(p.most * per * size) : 0;
     return p;
 }
-inline size_t elements(const Plan &p) { return 2 * p.state + p.d_init + 2 * p.factor + 2 * p.token + p.sums; }
+inline size_t elements(const Plan &p) { return 2 * p.state + p.d_init + p.between + 2 * p.factor + 2 * p.token + p.sums; }
 
 template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, const kda_lin_grads &r, float *ws, int32_t *err, hipStream_t st) {
     const bool own_d_init = a.initial_state && !r.d_initial_state;
@@ -324,9 +283,8 @@ template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, con
     const Role q = {a.q, a.q_stride, a.q_head_stride}, k = {a.k, a.k_stride, a.k_head_stride}, v = {a.v, a.v_stride, a.v_head_stride};
     const Role d = {r.d_out, r.d_out_stride, r.d_out_head_stride}, none = {nullptr, 0, 0};
     // 16-byte pieces first
-    float *x = ws, *y = x + p.state, *di = y + p.state, *xf = di + p.d_init, *yf = xf + p.factor, *u = yf + p.factor, *w = u + p.token,
-          *sums = w + p.token;
-    float *d_init = own_d_init ? di : r.d_initial_state;
+    float *x = ws, *y = x + p.state, *between = y + p.state + p.d_init, *xf = between + p.between, *yf = xf + p.factor, *u = yf + p.factor,
+          *w = u + p.token, *sums = w + p.token;
     const dim3 grid((unsigned)p.segs, (unsigned)a.heads);
     hipError_t e;
     if (p.segs > 1) {
@@ -339,18 +297,23 @@ template <int DT, int KD, int VD> hipError_t backward(const kda_lin_args &a, con
         if ((e = hipGetLastError())) return e;
     }
     // dq on X^T, dk on Y^T: their states' rows are value elements
-    const Walk wq = {d, v, k, r.dq, x, a.initial_state, nullptr, a.scale, a.scale, 1.0f, q, u};
-    const Walk wv = {k, q, d, r.dv, y, r.d_final_state, d_init, a.scale, 1.0f, a.scale, none, nullptr};
-    const Walk wk = {v, d, q, r.dk, y, r.d_final_state, nullptr, a.scale, 1.0f, a.scale, k, w};
-    if constexpr (KD == VD) {
-        lin_walks_kernel<DT, KD, VD, DQ, DV><<<dim3(grid.x, grid.y, 3), THREADS<KD>, 0, st>>>(b, wq, wk, wv, err);
-    } else {
-        lin_walks_kernel<DT, KD, VD, DQ, DK><<<dim3(grid.x, grid.y, 2), THREADS<KD>, 0, st>>>(b, wq, wk, wv, err);
+    const Walk wq = {d, v, k, r.dq, x, a.initial_state, nullptr, a.scale, a.scale, 1.0f, q, u, between, y, r.d_final_state};
+    const Walk wv = {k, q, d, r.dv, y, r.d_final_state, r.d_initial_state, a.scale, 1.0f, a.scale, none, nullptr, nullptr, nullptr, nullptr};
+    const Walk wk = {v, d, q, r.dk, y, r.d_final_state, nullptr, a.scale, 1.0f, a.scale, k, w, between, nullptr, nullptr};
+    for (int64_t first = 0; first < p.blocks; first += p.most) {
+        const unsigned n = (unsigned)(p.blocks - first < p.most ? p.blocks - first : p.most);
+        if constexpr (KD == VD) {
+            lin_walks_kernel<DT, KD, VD, DK, DV><<<dim3(n, 1, 2), THREADS<KD>, 0, st>>>(b, wk, wv, first, err);
+        } else {
+            lin_walks_kernel<DT, KD, VD, DK, DK><<<n, THREADS<KD>, 0, st>>>(b, wk, wk, first, err);
+            if ((e = hipGetLastError())) return e;
+            lin_walks_kernel<DT, KD, VD, DV, DV><<<n, THREADS<VD>, 0, st>>>(b, wv, wv, first, nullptr);
+        }
         if ((e = hipGetLastError())) return e;
-        lin_walks_kernel<DT, KD, VD, DV, DV><<<grid, THREADS<VD>, 0, st>>>(b, wq, wk, wv, err);
+        lin_walks_kernel<DT, KD, VD, DQ, DQ><<<n, THREADS<KD>, 0, st>>>(b, wq, wq, first, nullptr);
+        if ((e = hipGetLastError())) return e;
     }
-    if ((e = hipGetLastError())) return e;
-    const Decays dec = {q, k, v, d, x, y, a.initial_state, d_init, u, w, a.g_per_head ? sums : r.dg, a.scale, a.g_per_head};
+    const Decays dec = {q, k, v, d, u, w, a.g_per_head ? sums : r.dg, a.scale, a.g_per_head};
     lin_decay_kernel<DT, KD, VD><<<grid, DECAY_THREADS, 0, st>>>(b, dec);
     if ((e = hipGetLastError())) return e;
     if (a.g_per_head) {

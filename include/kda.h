@@ -646,9 +646,11 @@ typedef struct kda_lin_grads {
 /*
  * kda_lin_bwd -- gradients of kda_lin_fwd with respect to every input, from d_out and d_final_state (args->out and
  * args->final_state are ignored). Needs nothing that the forward computed. Sums run in a fixed order: the same results from run to
- * run. workspace: kda_lin_bwd_workspace_bytes() bytes of device memory, or NULL: then the library allocates it
- * stream-ordered on `stream`. Where initial_state is given and d_initial_state is not, the workspace holds it
- * (need_d_initial_state 0; 1 where initial_state is NULL).
+ * run. dg_t is the sum of what passes token t and of nothing else, so that it is as exact as fp32 sums of that size are, whatever
+ * the rest of the sequence holds; it is 0 where nothing passes (a reset). workspace: kda_lin_bwd_workspace_bytes() bytes of device memory, or
+ * NULL: then the library allocates it stream-ordered on `stream`. It holds states of chunks inside segments, up to 1 GiB of them (1 KB for a
+ * token and head of 128 x 128 up to there). Where initial_state is given and d_initial_state is not, the workspace has room for
+ * it (need_d_initial_state 0; 1 where initial_state is NULL).
  */
 size_t kda_lin_bwd_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t heads, int32_t key_dim, int32_t value_dim,
                                    int32_t g_per_head, int32_t need_d_initial_state);
