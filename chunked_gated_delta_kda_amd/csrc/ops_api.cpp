@@ -229,22 +229,42 @@ int check_scales(const Scales &s, int64_t sb) {
     return s.p ? KDA_OK : KDA_ERR_NULL;
 }
 
-// whether no two rows of a cache that is written share a byte: each stride steps over what the smaller ones span
-bool apart(const Scales &c, int64_t pages, int64_t page_size, int64_t heads, int64_t row) {
-    struct Dim {
-        int64_t size, stride;
-    } d[] = {{pages, c.page}, {page_size, c.token}, {heads, c.head}};
-    for (int i = 0; i < 3; ++i)
-        for (int j = 0; j < 2; ++j)
-            if (d[j].stride > d[j + 1].stride) std::swap(d[j], d[j + 1]);
-    int64_t spanned = row;
-    for (const Dim &x : d) {
-        if (x.size == 1) continue;
-        if (x.stride < spanned) return false;
-        spanned += (x.size - 1) * x.stride;
+// The rows of a cache, in bytes: its dimensions of more than one entry, by falling stride, and what a dimension's entries (at the end
+// a row) span.
+struct Layout {
+    const char *p;
+    int dims = 0;
+    int64_t size[3], stride[3], span[4];
+    Layout(const Scales &c, int64_t pages, int64_t page_size, int64_t heads, int64_t row, int64_t es) : p((const char *)c.p) {
+        const int64_t n[] = {pages, page_size, heads}, s[] = {c.page, c.token, c.head};
+        for (int i = 0; i < 3; ++i) {
+            if (n[i] == 1) continue;
+            int at = dims++;
+            for (; at > 0 && stride[at - 1] < s[i] * es; --at) size[at] = size[at - 1], stride[at] = stride[at - 1];
+            size[at] = n[i], stride[at] = s[i] * es;
+        }
+        span[dims] = row * es;
+        for (int i = dims - 1; i >= 0; --i) span[i] = span[i + 1] + (size[i] - 1) * stride[i];
     }
-    return true;
-}
+    // whether no two of its rows share a byte: each stride steps over what the smaller ones span
+    bool apart() const {
+        for (int i = 0; i < dims; ++i)
+            if (stride[i] < span[i + 1]) return false;
+        return true;
+    }
+    // Whether rows of two layouts with rows apart may share a byte, b's part from dimension `d` on lying `off` bytes behind this one's. Where
+    // their parts meet and their strides are the same, the few entries' distances that keep them together decide; where
+    // strides differ, they are taken to share.
+    bool shares(const Layout &b, int64_t off, int d = 0) const {
+        if (off >= span[d] || -off >= b.span[d]) return false;
+        if (d == dims) return true;
+        if (stride[d] != b.stride[d]) return true;
+        const int64_t near = -off / stride[d];
+        for (int64_t i = near - 2; i <= near + 2; ++i)      // entry of b less entry of this one
+            if (i > -size[d] && i < b.size[d] && shares(b, off + i * stride[d], d + 1)) return true;
+        return false;
+    }
+};
 
 // ---------------------------------------------------------------- linear attention
 bool lin_dim(int64_t d) { return d == 64 || d == 128; }
@@ -507,9 +527,12 @@ int kda_kv_append(const kda_kv_args *args, void *stream) {
             if (const int rc = check_scales(s, sb)) return rc;
     if (!a.block_table || !a.seq_lens || (a.total_tokens > 0 && (!a.k || !a.v || (a.q && !a.q_out)))) return KDA_ERR_NULL;
     if (!by16(a.k) || !by16(a.v) || !by16(a.q) || !by16(a.q_out) || !by16(a.rope)) return KDA_ERR_UNSUPPORTED;
-    for (int i = 0; i < 2; ++i)
-        if (!apart(caches[i], a.num_pages, a.page_size, a.kv_heads, row) || (four && !apart(sc[i], a.num_pages, a.page_size, a.kv_heads, sb)))
-            return KDA_ERR_SHAPE;
+    const int64_t ces = four ? 1 : 2;
+    const Layout written[] = {{caches[0], a.num_pages, a.page_size, a.kv_heads, row, ces}, {caches[1], a.num_pages, a.page_size, a.kv_heads, row, ces},
+                              {sc[0], a.num_pages, a.page_size, a.kv_heads, sb, 1}, {sc[1], a.num_pages, a.page_size, a.kv_heads, sb, 1}};
+    const int buffers = four ? 4 : 2;
+    for (int i = 0; i < buffers; ++i)
+        if (!written[i].apart()) return KDA_ERR_SHAPE;
     const int64_t T = a.total_tokens, es = 2;
     auto rows3 = [&](const void *p, int64_t stride, int64_t head, int64_t heads) {
         return span(T > 0 ? p : nullptr, ((T - 1) * stride + (heads - 1) * head + a.head_dim) * es);
@@ -518,7 +541,6 @@ int kda_kv_append(const kda_kv_args *args, void *stream) {
                        rows3(a.q, a.q_stride, a.q_head_stride, a.q_heads), span(a.rope, (int64_t)a.max_positions * a.rot_dim * 4),
                        span(a.cu_seqlens, ((int64_t)a.num_seqs + 1) * 4),
                        span(a.block_table, (((int64_t)a.num_seqs - 1) * a.table_stride + a.table_width) * 4), span(a.seq_lens, (int64_t)a.num_seqs * 4)};
-    // (caches that are slices of one tensor interleave: their spans may meet)
     const Span out[] = {span(a.q_out, T * a.q_heads * a.head_dim * es),
                         cache_span(caches[0].p, a.num_pages, a.page_size, a.kv_heads, caches[0].page, caches[0].token, caches[0].head, row, four ? 1 : 2),
                         cache_span(caches[1].p, a.num_pages, a.page_size, a.kv_heads, caches[1].page, caches[1].token, caches[1].head, row, four ? 1 : 2),
@@ -529,7 +551,10 @@ int kda_kv_append(const kda_kv_args *args, void *stream) {
             if (meet(i, o)) return KDA_ERR_ALIAS;
     for (int i = 1; i < 5; ++i)
         if (meet(out[0], out[i])) return KDA_ERR_ALIAS;
-    if (a.k_cache == a.v_cache || (four && a.k_scale == a.v_scale)) return KDA_ERR_ALIAS;
+    // (caches that are slices of one tensor interleave: their spans may meet, their rows may not)
+    for (int i = 0; i < buffers; ++i)
+        for (int j = 0; j < i; ++j)
+            if (written[j].shares(written[i], written[i].p - written[j].p)) return KDA_ERR_ALIAS;
     return launched(kda::ops::launch_kv_append(a, kda::device_error_word(), (hipStream_t)stream));
 }
 

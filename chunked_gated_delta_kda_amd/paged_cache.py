@@ -100,6 +100,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, ro
     the last offset are padding), or None: one row for each of N = T sequences; rope: fp32 [positions, R], R a multiple of 16 up to
     Dh, R/2 cosines and R/2 sines of each position, or None for no rotation; interleaved: neighbouring elements turn
     together, else i and i + R/2; the elements behind R stay; q: [T, Hq, Dh], rotated likewise; q_out: buffer for it or None.
+    Caches and scales may be slices of one tensor that lie between each other, but share no bytes.
     check: as in fwd; rows that do not fit the table, the cache or the table of rotations are left out and raise.
     Returns the rotated q [T, Hq, Dh] (None without q); rows that are padding or left out are not written there, nor in the
     cache. A tensor that the call allocates belongs to its stream.

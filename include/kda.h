@@ -559,9 +559,10 @@ typedef struct kda_kv_args {
  * sequence's row of the table, past the table of rotations or on a page outside the cache are left out
  * (KDA_DEVERR_PAGES). Rows that are left out or padding leave q_out as it was. Two sequences whose table rows name one
  * page must not append to the same place of it. Rows of q, k, v, rope and of a cache of dtype are read and written 16 bytes
- * at a time: bases aligned to 16 bytes, strides multiples of 8 elements, else KDA_ERR_UNSUPPORTED; rows of the caches must not
- * overlap (KDA_ERR_SHAPE). Captured calls stay right when lengths, pages, offsets and table entries change. Limits:
- * total_tokens <= 2^27, table_width * page_size <= 2^30, heads <= 65535.
+ * at a time: bases aligned to 16 bytes, strides multiples of 8 elements, else KDA_ERR_UNSUPPORTED; rows of a cache must not
+ * overlap (KDA_ERR_SHAPE), nor those of two of the caches and scales (KDA_ERR_ALIAS): where they lie between each other, as slices of one
+ * tensor do, strides are the same from the largest on until they part. Captured calls stay right when lengths, pages, offsets
+ * and table entries change. Limits: total_tokens <= 2^27, table_width * page_size <= 2^30, heads <= 65535.
  */
 int kda_kv_append(const kda_kv_args *args, void *stream);
 

@@ -249,3 +249,49 @@ def test_read_abi_refusals(lib):
         assert call(**{name: None}) == 1, name
     for kw in (dict(k=61 * MB), dict(k=16 * MB), dict(v=49 * MB), dict(v=51 * MB), dict(k=50 * MB)):
         assert call(**kw) == 7, kw
+
+
+@pytest.mark.parametrize("kw", [
+    dict(v_cache=16 * MB + 4096), dict(v_cache=16 * MB - 4096),                 # a page on, a page back
+    dict(v_cache=16 * MB + 256), dict(k_cache=32 * MB + 16 * 256),              # a token's row on
+    dict(v_cache=16 * MB + 128),                                                # a head's
+    dict(v_cache=16 * MB + 4096 * 9 * 2), dict(v_cache=16 * MB - (4096 * 9 * 2 + 15 * 512 + 256 + 240)),      # only the last page, the last bytes
+    dict(v_cache=16 * MB + 8192 * 2, k_page_stride=8192, v_page_stride=8192),   # pages of a wider tensor, the same halves
+    dict(v_cache=16 * MB + 512, v_page_stride=8192, v_token_stride=512),        # strides that differ
+])
+def test_caches_that_share_bytes_are_refused(lib, kw):
+    assert lib.kda_kv_append(ctypes.byref(kv_args(False, **kw)), None) == 7
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k_scale=16 * MB), dict(v_scale=32 * MB + 64), dict(k_scale=32 * MB), dict(v_scale=16 * MB + 2048 * 9 + 15 * 128 + 64 + 60),
+    dict(v_scale=48 * MB + 4), dict(v_scale=48 * MB + 8), dict(v_cache=16 * MB + 2048), dict(v_cache=16 * MB + 64),
+])
+def test_4_bit_caches_that_share_bytes_are_refused(lib, kw):
+    assert lib.kda_kv_append(ctypes.byref(kv_args(True, **kw)), None) == 7
+
+
+def test_caches_between_each_other(lib):
+    """Two caches at random in one another's gaps, byte by byte: sharing bytes is refused, and nothing else where strides are
+    the same. (Only where no GPU would run what is accepted.)"""
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls would run")
+    g = np.random.Generator(np.random.PCG64(3))
+    seen = {True: 0, False: 0}
+    for _ in range(600):
+        n = dict(zip(("page", "token", "cache_head"), (int(x) for x in g.integers(1, 4, 3))))
+        order, at, st = list(g.permutation(list(n))), 64 * int(g.integers(1, 4)), {}
+        for name in order[::-1]:
+            st[name] = at
+            at = at * n[name] + 64 * int(g.integers(0, 3))
+        shift = 64 * int(g.integers(-at // 64 - 1, at // 64 + 2))
+        rows = lambda base: {base + a * st["page"] + b * st["token"] + c * st["cache_head"] + e  # noqa: E731
+                             for a in range(n["page"]) for b in range(n["token"]) for c in range(n["cache_head"]) for e in range(64)}
+        share = bool(rows(0) & rows(shift))
+        kw = {f"{x}_{name}_stride": s for x in "kv" for name, s in st.items()}
+        kw.update(head_dim=64, rot_dim=64, k_head_stride=64, k_cache=16 * MB, v_cache=16 * MB + 2 * shift, num_pages=n["page"],
+                  page_size=n["token"], kv_heads=n["cache_head"])
+        code = lib.kda_kv_append(ctypes.byref(kv_args(False, **kw)), None)
+        assert (code == 7) == share, (n, st, shift, code)
+        seen[share] += 1
+    assert min(seen.values()) > 100
