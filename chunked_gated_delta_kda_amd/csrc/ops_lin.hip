@@ -23,7 +23,13 @@ __global__ __launch_bounds__(THREADS<VD>, (WAVES_A_SIMD<DT, VD>)) void lin_walk_
     __shared__ WalkLds<DT, KD, VD> lds;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(b.offsets(), err, threadIdx.x, THREADS<VD>);
     const int seg = (int)blockIdx.x / b.turns;
-    walk<DT, KD, VD, false, false>(b, a, Place{seg, (int)blockIdx.y, (int)blockIdx.x - seg * b.turns, (int)blockIdx.x, (int)gridDim.x, 0}, lds);
+    const Place place = {seg, (int)blockIdx.y, (int)blockIdx.x - seg * b.turns, (int)blockIdx.x, (int)gridDim.x, 0};
+    if (__syncthreads_or(walk<DT, KD, VD, false, false>(b, a, place, lds))) {      // a value was not finite
+        // (other strides as far as the compiler knows: rows' places that it keeps for this walk through the first cost that 5%)
+        Walk again = a;
+        asm volatile("" : "+s"(again.q.row), "+s"(again.k.row), "+s"(again.v.row));
+        walk<DT, KD, VD, false, false, true>(b, again, place, lds);
+    }
 }
 
 // One token of each sequence: S <- e^g S + k v^T, out = scale S^T q. The state is read and written once; a block takes one

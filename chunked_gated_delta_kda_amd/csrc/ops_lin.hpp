@@ -140,6 +140,17 @@ template <int DT, int D, int NT> struct Stage {
         for (int n = 0; n < N; ++n)      // (rows that lie over each other, strides of 0, are cut off as well)
             r[n] = read16(b, (int)row + ROWS * n < len ? at : OUTSIDE, ROWS * n * s.row);
     }
+    // whether this lane has an infinity or a NaN
+    __device__ __forceinline__ bool not_finite() const {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        constexpr unsigned short INF = DT == KDA_DTYPE_BF16 ? 0x7f80 : 0x7c00;
+        u16x2 top = {0, 0};
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, r[n][i] & 0x7fff7fffu));
+        return top[0] >= INF || top[1] >= INF;
+    }
     __device__ __forceinline__ void store(Tile<PLANES<DT>, D> &t) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -595,7 +606,24 @@ template <int DT, int KD, int VD> struct WalkLds {
     u32x4 pair[4][2][PARTS][64];      // operands of the pairs' weights: 16 columns (tokens i), 32 tokens j, part, lane
     Clock clock[2];
     float dots[WAVES<VD>][C], passing[WAVES<VD>];
+    int from[VD];       // PICKED: the first token of the chunk whose value in a column is not finite, C for none
 };
+
+// Puts values that are not finite to 0 in LDS, and notes where each column has its first. A thread takes a column.
+template <int NP, int VD> __device__ __forceinline__ void take_out(Tile<NP, VD> &v, int (&from)[VD]) {
+    if (threadIdx.x < VD) {
+        int first = C;
+#pragma unroll 1
+        for (int t = C - 1; t >= 0; --t) {
+            const int at = v.at(t) + threadIdx.x;
+            if ((v.x[0][at] & 0x7f80) != 0x7f80) continue;      // (as bf16: the first part of an fp16 value is infinite or NaN where that is)
+            first = t;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) v.x[p][at] = 0;
+        }
+        from[threadIdx.x] = first;
+    }
+}
 
 // sums over a row's lanes from each lane on: four steps to the right
 __device__ __forceinline__ float row_suffix(float x) {
@@ -606,8 +634,10 @@ __device__ __forceinline__ float row_suffix(float x) {
     return x;
 }
 
-template <int DT, int KD, int VD, bool REV, bool DOT>
-__device__ __forceinline__ void walk(const Batch &b, const Walk &a, const Place &place, WalkLds<DT, KD, VD> &L) {
+// Returns whether this wave has met a value that is not finite (not with DOT or REV). Such a value makes NaN of its column in tokens of its chunk
+// before it, whose weights for it are 0: a walk that is PICKED takes them out and puts NaN where they reach.
+template <int DT, int KD, int VD, bool REV, bool DOT, bool PICKED = false>
+__device__ __forceinline__ bool walk(const Batch &b, const Walk &a, const Place &place, WalkLds<DT, KD, VD> &L) {
     constexpr int NP = PLANES<DT>, NT = THREADS<VD>, NW = WAVES<VD>, IN = DOT ? 3 : 2;      // IN: parts of the state in its product with q
     using E = typename Elem<DT>::type;
     typedef E E4 __attribute__((ext_vector_type(4)));
@@ -661,6 +691,7 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, const Place 
     auto between = [&](const Chunk &c) { return a.between + ((int64_t)place.block * (b.seg / C) + (c.first - s0) / C) * SIZE; };
     Chunk c = chunks.next();
     int before_first = 0, before_len = 0, turn = 0;
+    bool met = false;
     load(c);
     if (wave == 0) tick<REV>(L.clock[0], decay, a.in_scale, a.up_scale);
 #pragma unroll 1
@@ -682,7 +713,12 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, const Place 
         sq.store(L.q);
         sk.store(L.k);
         sv.store(L.v);
+        if constexpr (!REV && !DOT && !PICKED) met |= __any(sv.not_finite());
         lds_barrier();
+        if constexpr (PICKED) {
+            take_out(L.v, L.from);
+            lds_barrier();
+        }
         if constexpr (DOT && !REV) {
             const float total = clock.total;
             float pass = 0.0f;
@@ -790,6 +826,19 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, const Place 
                 for (int n = 0; n < PARTS; ++n) part[n] = L.pair[it][s][n][lane];
                 pairs<NP, PARTS, 2>([&](int x, int y) { acc[it] = mma(v[x][s], part[y], acc[it]); });
             }
+        if constexpr (PICKED) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int from = L.from[16 * wave + 4 * g + r];
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+                    if (16 * it + i >= from) acc[it][r] = __builtin_nanf("");
+            }
+            if (L.from[16 * wave + i] < C) {
+#pragma unroll
+                for (int kt = 0; kt < KD / 16; ++kt) S[kt] = f32x4{} + __builtin_nanf("");
+            }
+        }
         const uint32_t out_row = 2 * (uint32_t)(b.H * VD);
         const Buffer out = buffer((char *)a.out + ((int64_t)c.first * b.H + h) * (2 * VD), (c.len - 1) * out_row + 2 * VD);
 #pragma unroll
@@ -819,6 +868,7 @@ __device__ __forceinline__ void walk(const Batch &b, const Walk &a, const Place 
         lds_barrier();
         put_dots(before_first, before_len);
     }
+    return met;
 }
 
 // The second argument of launch bounds, waves a SIMD: two blocks on a CU where LDS holds them.

@@ -76,8 +76,8 @@ def lin_fwd(q, k, v, g, scale=None, cu_seqlens=None, initial_state=None, output_
     8 elements (slices of a projection are read in place); g: fp32 natural-log decays, [T, H] from the data or [H] fixed for each
     head, meant to be 0 or less (-inf forgets what was before); scale: 1/sqrt(K) by default; cu_seqlens: int32 [S+1] on the device or
     None (one sequence); initial_state: fp32 [S, H, K, V] or None (zeros); out, final_state: caller buffers or
-    None. final_state must not overlap initial_state (lin_decode updates in place). An input that is not finite makes its head
-    of its sequence infinite or NaN, from up to 63 tokens before it on. check: as in fwd.
+    None. final_state must not overlap initial_state (lin_decode updates in place). Inputs that are not finite make what hangs on
+    them infinite or NaN, and nothing before them. check: as in fwd.
     Returns (out [T, H, V] of q's dtype, final_state fp32 [S, H, K, V] or None). Tensors that the call allocates
     belong to its stream.
     """

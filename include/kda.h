@@ -618,10 +618,10 @@ typedef struct kda_lin_args {
  *
  * with S from initial_state and final_state the last S. g_t is meant to be 0 or less; -infinity (anything under -2839)
  * forgets all that was before. Chunks of 64 tokens go through matrix instructions; states and the gradients of g
- * are as exact as fp32 sums are, the outputs lose about 2^-16 beside their rounding to dtype. An input that is not
- * finite makes its head of its sequence infinite or NaN, from up to 63 tokens before it on; no other head or sequence. Rows are read 16
- * bytes at a time: bases aligned to 16 bytes, strides multiples of 8 elements, else KDA_ERR_UNSUPPORTED; states are
- * aligned to 16 bytes too. Segments of the time axis run side by side, their states joined in the workspace:
+ * are as exact as fp32 sums are, the outputs lose about 2^-16 beside their rounding to dtype. Where an input is not finite, what
+ * hangs on it is infinite or NaN: of q its token, of v its element from its token on, of k and g their head of their sequence from
+ * their token on; nothing before. (Gradients: their head of their sequence.) Rows are read 16 bytes at a time: bases
+ * aligned to 16 bytes, strides multiples of 8 elements, else KDA_ERR_UNSUPPORTED; states are aligned to 16 bytes too. Segments of the time axis run side by side, their states joined in the workspace:
  * kda_lin_workspace_bytes() bytes of device memory, or NULL: then the library allocates it stream-ordered on `stream`. The
  * same results from run to run. Limits: total_tokens <= 2^27, heads <= 65535, num_seqs * heads <= 2^27. final_state must not
  * overlap initial_state.
