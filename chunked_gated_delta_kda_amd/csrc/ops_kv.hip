@@ -9,8 +9,9 @@
 // Bound by memory: each row is read and written once. A thread has 8 neighbouring elements of one head (16 bytes) and
 // goes from head to head of its token with the same 8 cosines and sines in registers; the elements that they are
 // paired with come through the cache, which the neighbouring lanes fill. Measured at heads of 128: 8192 ragged tokens of 32 + 4 + 4
-// heads in fp16 (170 MB) 37 us, 4.5 TB/s; 8192 of 32 + 8 + 8 into 4 bits (176 MB) 45 us, 3.9 TB/s (the rotation of
-// keys in 64 bits and the codes); 256 tokens 4.5 us, latency.
+// heads in fp16 (170 MB) 37 us, 4.5 TB/s; 8192 of 32 + 8 + 8 into 4 bits (176 MB) 45 us, 3.9 TB/s: 59% of its waves' cycles are
+// waits, with five waves a SIMD (96 registers) and look-ups that wait for each other (sequence, length, page, angles); vector
+// instructions of all kinds take 22 us, the rotation of keys in 64 bits under 1 of them; 256 tokens 4.5 us, latency.
 #include <type_traits>
 
 #include "ops_common.hpp"
@@ -162,8 +163,11 @@ template <int DT> __device__ __forceinline__ uint32_t to_fp4(const float (&x)[8]
 
 // A block takes one new token; its threads 8 elements of a head each, head after head: queries, keys, values. The rows
 // of AHEAD heads are asked for before the token's place is looked up: the look-ups (sequence, length, page, angles) wait
-// for one another, and the rows with them otherwise: 8192 tokens of 32 + 8 + 8 heads of 128 into 4 bits 49 us for 67. Registers
-// are held to what 6 waves a SIMD leave each, 5 for 4 bits (37 us for 39 with 8192 ragged tokens, 45 for 48): fewer spill.
+// for one another, and the rows with them otherwise: 8192 tokens of 32 + 8 + 8 heads of 128 into 4 bits 49 us for 67. What is left of
+// a token with more rows than that is asked for in turn. 2 | 3 | 4 ahead for 8192 tokens (us in 16, in 4 bits): 32 + 8 + 8 heads of 128 47, 50 |
+// 46, 46 | 75, 69; 64 + 8 + 8 69, 75 | 73, 73 | 119, 108; 32 + 8 + 8 of 256 82, 88 | 86, 86 | 139, 117; 16 + 2 + 2 of 256 40, 45 | 38, 41 |
+// 68, 63 (spills). Registers are held to what 6 waves a SIMD leave each, 5 for 4 bits (37 us for 39 with 8192 ragged tokens, 45 for
+// 48): fewer spill.
 constexpr int AHEAD = 3;
 template <int DT, int DH, bool FOUR>
 __global__ __launch_bounds__(THREADS, (FOUR ? 5 : 6)) void kv_append_kernel(const kda_kv_args a, int32_t *err) {

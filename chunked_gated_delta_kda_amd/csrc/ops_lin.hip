@@ -84,10 +84,10 @@ __global__ __launch_bounds__(DECODE_THREADS) void lin_decode_kernel(const kda_li
 struct Plan {
     int seg, segs;
 };
-// A block a segment and head, as many as run at once: 8192 tokens of 32 heads in bf16 (two blocks a CU) 135 us with 512, 146 with
-// 256, 158 with 1024; 9442 ragged ones of 5 in fp16 (one a CU) 51 us with 256, 62 with 512.
-// Few chunks are walked one after another, which takes one launch for three (us a call, 2 | 64 heads: 128 tokens 12.8 | 12.9 for 19.5 | 19.9,
-// 256 tokens 19.4 | 21.0 for 19.5 | 29.9, 512 tokens, which stay with three, 35.4 | 37.2 for 19.3 | 47.4).
+// A block a segment and head, as many as run at once: 8192 tokens of 32 heads in bf16 (two blocks a CU) 131 us with 512, 135 with
+// 256, 150 with 1024; 9442 ragged ones of 5 in fp16 (one a CU) 48 us with 256, 59 with 512.
+// Few chunks are walked one after another, which takes one launch for three (us a call, 2 | 64 heads: 128 tokens 15.2 | 15.4 for 21.0 | 21.6,
+// 256 tokens 20.8 | 22.5 for 21.3 | 31.4, 512 tokens, which stay with three, 37.0 | 39.2 for 21.4 | 49.7).
 constexpr int MOST = 512, FEW = 4;
 Plan plan(int64_t T, int64_t H, int64_t chunks, int64_t blocks) {
     Plan p;

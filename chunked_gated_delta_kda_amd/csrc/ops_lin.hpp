@@ -18,9 +18,9 @@
 // bf16's exponents hold fp16's), and what is computed in fp32 as two (2^-17 of it is lost; where it ends in a 16-bit output) or three
 // (2^-25; where it ends in fp32: states and gradients of decays). States themselves stay in fp32 registers.
 //
-// 8192 tokens of 32 heads of 128 x 128 in bf16 (268 MB in and out: 51 us of memory): states of segments 40 us, join 15,
-// walk 80. In the walk matrix instructions (84 a wave and chunk, 16 cycles each) and vector ones (334, for splits, decays
-// and conversions) take 18 us each, one beside the other where the two waves and two blocks of a SIMD allow; the phases of a
+// 8192 tokens of 32 heads of 128 x 128 in bf16 (268 MB in and out: 51 us of memory): states of segments 39 us, join 15,
+// walk 81. In the walk matrix instructions (79 a wave and chunk, 16 cycles each) take 17 us, vector ones (377, for splits, decays
+// and conversions) 20, LDS 21: no unit is full. They meet where the two waves and two blocks of a SIMD allow; the phases of a
 // chunk, between barriers, keep them from meeting more often. Without its loads it takes 82% of the time, without the update 74%.
 #pragma once
 
@@ -885,8 +885,8 @@ inline int segment(int64_t T, int64_t H, int64_t blocks, int64_t least) {
 }
 
 // Blocks that share the parts of a segment in the forward's walk: more than one where segments hold many. Of 32 heads, 64 single
-// tokens (us, with states) 67 for 388, 64 beside a prompt of 4096 223 for 505; 16 heads, 512 sequences of 16 tokens, which fill the card
-// without, 284 for 278 (109 for 92 without states). 4 blocks leave 297 of the 505, 16 the same 222.
+// tokens (us, with states) 68 for 401, 64 beside a prompt of 4096 223 for 507; 16 heads, 512 sequences of 16 tokens, which fill the card
+// without, 270 for 266 (110 for 89 without states). 4 blocks leave 294 of the 507, 16 the same 223.
 inline int turns(int64_t S, int64_t segs) {
     const int64_t most = 8, parts = ceil_div(S, segs);
     return (int)(parts < 2 ? 1 : parts < most ? parts : most);

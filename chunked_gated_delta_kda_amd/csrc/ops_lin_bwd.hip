@@ -11,8 +11,9 @@
 // other sizes, resets). The walk for dk leaves Y at each border of chunks inside a segment for the one for dq, which holds X there: 1 KB for
 // a token and head of 128 x 128, written and read once, SLOTS bytes at a time.
 //
-// 8 x 1024 tokens of 16 heads of 128 x 128 in bf16 (261 MB in and out: 49 us of memory): states both ways 27 us, joins 7, walks 137, decays
-// 43; 200 in all. The walks are bound as the forward's is, with three parts where they lead to a decay's gradient.
+// 8 x 1024 tokens of 16 heads of 128 x 128 in bf16 (261 MB in and out: 49 us of memory): states both ways 27 us, joins 7, walks for dk and
+// dv 112, for dq 90, decays 37; 266 in all. The walks are bound as the forward's is, with three parts where they lead to a
+// decay's gradient; the one for dq, a block a CU, waits 66% of its waves' cycles. The states handed on (117 MB each way) take 38 us of them.
 #include "ops_lin.hpp"
 
 #include <type_traits>
@@ -36,7 +37,8 @@ __global__ __launch_bounds__(JOIN_THREADS) void lin_bwd_join_kernel(const Batch 
     else join<SIZE, AHEAD>(b, y, yf, true);
 }
 
-// Walks of one launch, by blockIdx.z: side by side they fill what each leaves of the chip. dq's and dk's states lie turned and take a
+// Walks of one launch, by blockIdx.z: side by side they fill what each leaves of the chip (dv beside dk and then dq 112 + 90 us, dk and
+// then dv beside dq 98 + 117). dq's and dk's states lie turned and take a
 // wave for every 16 key columns, dv's for every 16 value columns: where these differ, dv's has a launch of its own.
 enum { DQ, DK, DV };
 template <int DT, int KD, int VD, int W> struct One {
@@ -116,7 +118,7 @@ template <int DT, int D> __device__ __forceinline__ f32x4 products(const Sixteen
 }
 
 // A block takes a segment of one head, four chunks at a time, four waves each: a wave the pairs with 16 of the tokens i. (A
-// wave a chunk left two waves a SIMD to wait for their operands: 58 us for 8192 tokens of 16 heads, now 44.)
+// wave a chunk left two waves a SIMD to wait for their operands: a third more time. Now 37 us for 8192 tokens of 16 heads.)
 constexpr int DECAY_WAVES = 16, DECAY_THREADS = 64 * DECAY_WAVES;
 struct DecayLds {
     Clock clocks[4];
