@@ -60,13 +60,15 @@ def check(d, lengths, kind, do, df):
     return got
 
 
-# lengths, heads, K, V, type, g of [H], initial state: segments of 192 tokens (three chunks), of 64 of the fewest, of all
+# lengths, heads, K, V, type, g of [H], initial state: segments of two to eleven chunks, sequences of one segment and of several
 CASES = [
     ([700], 64, 128, 128, "bf16", False, True),
     ([5, 300, 0, 1, 63, 200, 131], 64, 64, 128, "fp16", False, True),
     ([190, 510], 64, 128, 64, "bf16", True, False),
     ([150, 50], 300, 64, 64, "fp16", False, True),
     ([400], 96, 64, 64, "bf16", True, True),
+    ([1100], 160, 64, 64, "bf16", False, True),
+    ([90, 0, 610], 128, 64, 128, "fp16", False, True),
 ]
 IDS = lambda c: f"{len(c[0])}x{max(c[0])}h{c[1]}k{c[2]}v{c[3]}{c[4]}{'f' if c[5] else ''}{'i' if c[6] else ''}"  # noqa: E731
 
